@@ -1,0 +1,95 @@
+// Device-side helpers of the mixture-of-experts operators: row types, vector
+// loads and stores, and group bounds.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace sgemm {
+namespace ex {
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+// Rounds to nearest even.
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+    return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) {
+    return __float2half_rn(x);
+}
+
+// N values loaded and stored at once (N * sizeof(T) is 2 .. 16 bytes, the
+// address a multiple of it).
+template <class T, int N>
+struct alignas(sizeof(T) * N) Pack {
+    T v[N];
+};
+
+template <class T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T *p) {
+    return *reinterpret_cast<const Pack<T, N> *>(p);
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &x) {
+    *reinterpret_cast<Pack<T, N> *>(p) = x;
+}
+
+// First row of group e (e = experts: one past the last group's end), limited
+// to 0 .. rows; group 0 starts at row 0 whatever offsets[0] holds.
+__device__ __forceinline__ int group_start(const int32_t *offsets, int e, int rows) {
+    if (e == 0) return 0;
+    const int o = __ldg(offsets + e);
+    return o < 0 ? 0 : (o > rows ? rows : o);
+}
+
+// A run of rows [begin, end) of group `group` (group = experts: rows outside
+// every group).
+struct RowTile {
+    int group, begin, end;
+};
+
+// Tile `tile` of the rows cut into tiles of `size` rows that do not cross
+// groups, groups in order and the rows past the last group as one more; group
+// = -1 when there are fewer tiles. Called by a full warp: 32 groups a step.
+__device__ __forceinline__ RowTile row_tile_of(const int32_t *offsets, int experts, int rows, int size, int tile) {
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    int base = 0;
+    for (int e0 = 0; e0 <= experts; e0 += 32) {
+        const int e = e0 + lane;
+        const int begin = e <= experts ? group_start(offsets, e, rows) : 0;
+        const int end = e < experts ? max(begin, group_start(offsets, e + 1, rows)) : (e == experts ? rows : 0);
+        const int tiles = (end - begin + size - 1) / size;
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        const unsigned has = __ballot_sync(0xffffffffu, tile < base + sum);
+        if (has) {
+            const int src = __ffs(has) - 1;
+            const int first = __shfl_sync(0xffffffffu, base + sum - tiles, src);
+            const int b = __shfl_sync(0xffffffffu, begin, src), f = __shfl_sync(0xffffffffu, end, src);
+            const int at = b + (tile - first) * size;
+            return RowTile{e0 + src, at, min(at + size, f)};
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return RowTile{-1, 0, 0};
+}
+
+}  // namespace ex
+}  // namespace sgemm

@@ -1,0 +1,147 @@
+// One product per group of rows, any type, alignment and form, on the CUDA
+// cores:
+//
+//     C[s] = A[s] op(B[e(s)])                     (rows)
+//     C[e] = sum over s in group e of A[s]^T B[s]  (wgrad)
+//
+// The group bounds are read on the device, so no call waits for the host. A
+// block makes one 64 x 64 tile of C with 16 x 16 threads, 4 x 4 sums each,
+// in fp32 from 64 x 16 tiles in shared memory; every product in fp32.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "experts_common.cuh"
+#include "experts_internal.h"
+
+namespace sgemm {
+namespace ex {
+namespace {
+
+constexpr int TILE = 64, DEPTH = 16, GEMM_THREADS = 256;
+
+struct SimpleArgs {
+    bool wgrad, trans;
+    int rows, experts;
+    int64_t M, N, K;
+    const int32_t *offsets;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb, strideB;
+    void *C;
+    int64_t ldc, strideC;
+    int tiles_n;
+};
+
+// rows: blockIdx.x = row tile * tiles_n + column tile. wgrad: the same over a
+// matrix's tiles, blockIdx.y the group.
+template <class T>
+__global__ void __launch_bounds__(GEMM_THREADS) grouped_simple_kernel(const SimpleArgs a) {
+    __shared__ float As[DEPTH][TILE + 1], Bs[DEPTH][TILE + 1];
+    const int tid = static_cast<int>(threadIdx.x);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x % a.tiles_n) * TILE;
+    const int mt = static_cast<int>(blockIdx.x / a.tiles_n);
+    // op(A)[m][k] at A + m * am + k * ak, op(B)[k][n] at B + k * bk + n * bn.
+    const T *A = static_cast<const T *>(a.A), *B = static_cast<const T *>(a.B);
+    T *C = static_cast<T *>(a.C);
+    int64_t m_count, k_count, am, ak, bk, bn;
+    if (a.wgrad) {
+        const int e = static_cast<int>(blockIdx.y);
+        const int begin = group_start(a.offsets, e, a.rows);
+        const int end = max(begin, group_start(a.offsets, e + 1, a.rows));
+        k_count = end - begin;
+        am = 1, ak = a.lda, bk = a.ldb, bn = 1;
+        m_count = min(static_cast<int64_t>(TILE), a.M - static_cast<int64_t>(mt) * TILE);
+        A += begin * a.lda + static_cast<int64_t>(mt) * TILE;
+        B += begin * a.ldb;
+        C += e * a.strideC + static_cast<int64_t>(mt) * TILE * a.ldc;
+    } else {
+        const RowTile rt = row_tile_of(a.offsets, a.experts, a.rows, TILE, mt);
+        if (rt.group < 0) return;
+        m_count = rt.end - rt.begin;
+        k_count = rt.group < a.experts ? a.K : 0;
+        am = a.lda, ak = 1, bk = a.trans ? 1 : a.ldb, bn = a.trans ? a.ldb : 1;
+        A += rt.begin * a.lda;
+        if (rt.group < a.experts) B += rt.group * a.strideB;
+        C += rt.begin * a.ldc;
+    }
+    const int64_t n_count = min(static_cast<int64_t>(TILE), a.N - n0);
+    B += n0 * bn;
+    float sum[4][4] = {};
+    const int ty = tid >> 4, tx = tid & 15;
+    for (int64_t k0 = 0; k0 < k_count; k0 += DEPTH) {
+        // Threads run along the operand's contiguous direction.
+#pragma unroll
+        for (int i = 0; i < TILE * DEPTH / GEMM_THREADS; ++i) {
+            const int x = tid + i * GEMM_THREADS;
+            const int m = ak == 1 ? x / DEPTH : x % TILE, ka = ak == 1 ? x % DEPTH : x / TILE;
+            As[ka][m] = m < m_count && k0 + ka < k_count ? to_f32(A[m * am + (k0 + ka) * ak]) : 0.0f;
+            const int n = bk == 1 ? x / DEPTH : x % TILE, kb = bk == 1 ? x % DEPTH : x / TILE;
+            Bs[kb][n] = n < n_count && k0 + kb < k_count ? to_f32(B[n * bn + (k0 + kb) * bk]) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+            float x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = As[k][ty + 16 * i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = Bs[k][tx + 16 * i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(x[i], y[j], sum[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (ty + 16 * i < m_count && tx + 16 * j < n_count)
+                C[(ty + 16 * i) * a.ldc + n0 + tx + 16 * j] = from_f32<T>(sum[i][j]);
+}
+
+int simple_launch(const GroupedProblem &p, cudaStream_t stream, int *launches) {
+    SimpleArgs a{};
+    a.wgrad = p.wgrad;
+    a.trans = p.transB == SGEMM_OP_T;
+    a.rows = static_cast<int>(p.rows);
+    a.experts = static_cast<int>(p.experts);
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.offsets = p.offsets;
+    a.A = p.A;
+    a.lda = p.lda;
+    a.B = p.B;
+    a.ldb = p.ldb;
+    a.strideB = p.strideB;
+    a.C = p.C;
+    a.ldc = p.ldc;
+    a.strideC = p.strideC;
+    const int64_t tiles_n = (p.N + TILE - 1) / TILE;
+    // Every group may end in a part of a tile.
+    const int64_t tiles_m = p.wgrad ? (p.M + TILE - 1) / TILE : (p.rows + TILE - 1) / TILE + p.experts;
+    if (tiles_n > INT32_MAX / tiles_m) return SGEMM_ERR_UNSUPPORTED;
+    a.tiles_n = static_cast<int>(tiles_n);
+    const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n), p.wgrad ? static_cast<unsigned>(p.experts) : 1u);
+    if (p.type == SGEMM_TYPE_F32)
+        grouped_simple_kernel<float><<<grid, GEMM_THREADS, 0, stream>>>(a);
+    else if (p.type == SGEMM_TYPE_BF16)
+        grouped_simple_kernel<__nv_bfloat16><<<grid, GEMM_THREADS, 0, stream>>>(a);
+    else
+        grouped_simple_kernel<__half><<<grid, GEMM_THREADS, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    ++*launches;
+    return SGEMM_OK;
+}
+
+}  // namespace
+
+int grouped_launch(const GroupedProblem &p, const DeviceInfo &, cudaStream_t stream, int *launches) {
+    return simple_launch(p, stream, launches);
+}
+
+}  // namespace ex
+}  // namespace sgemm

@@ -1,0 +1,552 @@
+// Sort of (token, choice) pairs by expert and the row copies that go with it:
+// gather, weighted combine and their gradients.
+//
+// Sort. With key(p) = ids[p] where that is an expert and E otherwise, the
+// slot of pair p is
+//
+//     slot(p) = #{p' : key(p') < key(p)} + #{p' < p : key(p') = key(p)},
+//
+// a stable counting sort: a histogram, its exclusive sum, and ranks among
+// equals. Warps own contiguous ranges of pairs, 32 at a time; equal keys of
+// one step find each other by a warp match, so ranks need no atomics and the
+// order is the pairs' own.
+//
+// Row copies. With w the weights, s(t, j) the slots and d the row width
+//
+//     gather        xs[s(t,j)] = x[t]
+//     combine       y[t]  = sum_j w[t,j] h[s(t,j)]
+//     its gradient  dh[s(t,j)] = w[t,j] dy[t],  dw[t,j] = <dy[t], h[s(t,j)]>
+//
+// All three are bound by memory: one thread holds 16 bytes of a token's row
+// and goes through the token's choices, so x, dy and every row of h are read
+// once and every output is written once, without atomics.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "experts_common.cuh"
+#include "experts_internal.h"
+
+namespace sgemm {
+namespace ex {
+namespace {
+
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_MAX_WARPS = SORT_THREADS / 32;
+// Counters of one block: one row of experts + 1 per counting warp.
+constexpr int SORT_SMEM_INTS = 48 * 1024;
+// Pairs that one block sorts alone.
+constexpr int64_t SORT_SINGLE = 8192;
+// Pairs per block and table entries of the two-kernel form.
+constexpr int64_t SORT_PER_BLOCK = 2048;
+constexpr int64_t SORT_TABLE = 64 * 1024;
+constexpr int64_t SORT_BLOCKS = 152;  // one per SM of a GB300
+
+template <class Id>
+__device__ __forceinline__ int key_of(const Id *ids, int64_t p, int experts) {
+    const Id id = __ldg(ids + p);
+    return id < 0 || id >= experts ? experts : static_cast<int>(id);
+}
+
+// Pairs [begin, end) of block `block` of `blocks`.
+__device__ __forceinline__ void block_range(int64_t pairs, int block, int blocks, int64_t *begin, int64_t *end) {
+    const int64_t per = ((pairs + blocks - 1) / blocks + 31) / 32 * 32;
+    *begin = min(per * block, pairs);
+    *end = min(*begin + per, pairs);
+}
+
+// Table row `blockIdx.x`: how many pairs of this block have each key.
+template <class Id>
+__global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const Id *ids, int64_t pairs, int experts,
+                                                                  int32_t *table) {
+    extern __shared__ int32_t count[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    for (int e = threadIdx.x; e <= experts; e += SORT_THREADS) count[e] = 0;
+    __syncthreads();
+    int64_t begin, end;
+    block_range(pairs, blockIdx.x, gridDim.x, &begin, &end);
+    for (int64_t p = begin + threadIdx.x; p < end; p += SORT_THREADS) atomicAdd(count + key_of(ids, p, experts), 1);
+    __syncthreads();
+    int32_t *row = table + static_cast<int64_t>(blockIdx.x) * (experts + 1);
+    for (int e = threadIdx.x; e <= experts; e += SORT_THREADS) row[e] = count[e];
+}
+
+// Exclusive sum over x[0 .. n-1] in place by the whole block; `part` holds 33
+// values.
+__device__ __forceinline__ void block_exclusive_sum(int32_t *x, int n, int32_t *part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int carry = 0;
+    for (int i0 = 0; i0 < n; i0 += SORT_THREADS) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        const int v = i < n ? x[i] : 0;
+        int s = v;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += o;
+        }
+        if (lane == 31) part[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            const int w = part[lane];
+            int t = w;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, t, d);
+                if (lane >= d) t += o;
+            }
+            part[lane] = t - w;
+            if (lane == 31) part[32] = t;
+        }
+        __syncthreads();
+        if (i < n) x[i] = carry + part[warp] + s - v;
+        carry += part[32];
+        __syncthreads();
+    }
+}
+
+// Slots of this block's pairs. gridDim.x == 1: the whole sort; otherwise the
+// table of sort_count_kernel gives the pairs of each key in every block.
+// Shared memory: `warps` rows of experts + 1 counters, one row of group
+// starts, 33 partial sums.
+template <class Id>
+__global__ void __launch_bounds__(SORT_THREADS) sort_rank_kernel(const Id *ids, int64_t pairs, int experts, int warps,
+                                                                 const int32_t *table, int32_t *offsets,
+                                                                 int32_t *order, int32_t *slot) {
+    extern __shared__ int32_t smem[];
+    const int keys = experts + 1;
+    const int blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+    int32_t *start = smem + warps * keys, *part = start + keys;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < warps * keys; i += SORT_THREADS) smem[i] = 0;
+    for (int i = threadIdx.x; i < keys; i += SORT_THREADS) start[i] = 0;
+    __syncthreads();
+
+    int64_t begin, end;
+    block_range(pairs, block, blocks, &begin, &end);
+    const int64_t per = ((end - begin + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t w0 = min(begin + per * warp, end), w1 = min(w0 + per, end);
+    int32_t *mine = smem + warp * keys;
+    if (warp < warps) {
+        for (int64_t p0 = w0; p0 < w1; p0 += 32) {
+            const bool in = p0 + lane < w1;
+            const int key = in ? key_of(ids, p0 + lane, experts) : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            if (in && lane == __ffs(same) - 1) mine[key] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    // Per key: counts before each warp in the block, and the total over all
+    // blocks in `start`.
+    if (blocks == 1) {
+        for (int e = threadIdx.x; e < keys; e += SORT_THREADS) {
+            int sum = 0;
+            for (int w = 0; w < warps; ++w) {
+                const int v = smem[w * keys + e];
+                smem[w * keys + e] = sum;
+                sum += v;
+            }
+            start[e] = sum;
+        }
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int parts = max(1, SORT_THREADS / keys);
+        // Warp 0's row takes the pairs of earlier blocks on top of the counts
+        // before warp 0, which are none: fold it in by adding after the loop.
+        for (int i = threadIdx.x; i < parts * keys; i += SORT_THREADS) {
+            const int e = i % keys;
+            int all = 0, before = 0;
+#pragma unroll 8
+            for (int b = i / keys; b < blocks; b += parts) {
+                const int v = __ldcg(table + static_cast<int64_t>(b) * keys + e);
+                all += v;
+                before += b < block ? v : 0;
+            }
+            atomicAdd(start + e, all);
+            atomicAdd(smem + e, before);
+        }
+        __syncthreads();
+        // Row 0 holds count(warp 0) + pairs of earlier blocks; their sum is
+        // where warp 1 starts, so the exclusive sum needs count(warp 0) alone:
+        // recovered from the block's own table row.
+        for (int e = threadIdx.x; e < keys; e += SORT_THREADS) {
+            int rest = 0;
+            for (int w = 1; w < warps; ++w) rest += smem[w * keys + e];
+            const int own0 = __ldcg(table + static_cast<int64_t>(block) * keys + e) - rest;
+            int sum = smem[e] - own0;
+            smem[e] = sum;
+            sum += own0;
+            for (int w = 1; w < warps; ++w) {
+                const int v = smem[w * keys + e];
+                smem[w * keys + e] = sum;
+                sum += v;
+            }
+        }
+    }
+    __syncthreads();
+    block_exclusive_sum(start, keys, part);
+    if (block == 0)
+        for (int e = threadIdx.x; e < keys; e += SORT_THREADS) offsets[e] = start[e];
+    if (warp < warps) {
+        for (int64_t p0 = w0; p0 < w1; p0 += 32) {
+            const int64_t p = p0 + lane;
+            const bool in = p < w1;
+            const int key = in ? key_of(ids, p, experts) : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            const int leader = __ffs(same) - 1;
+            int base = 0;
+            if (in && lane == leader) {
+                base = start[key] + mine[key];
+                mine[key] += __popc(same);
+            }
+            base = __shfl_sync(0xffffffffu, base, leader);
+            if (in) {
+                const int s = base + __popc(same & ((1u << lane) - 1u));
+                slot[p] = s;
+                order[s] = static_cast<int32_t>(p);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// ------------------------------------------------------------------ row copies
+
+// Threads of a block: tx along the row, ty tokens.
+constexpr int ROW_THREADS = 256;
+
+struct RowArgs {
+    int64_t tokens;
+    int top_k, experts;
+    int64_t vecs;   // vectors in a row
+    int64_t pairs;  // tokens * top_k
+    const int32_t *slot, *offsets;
+};
+
+// Slots below this bound belong to an expert.
+__device__ __forceinline__ int kept_end(const RowArgs &a) {
+    const int o = __ldg(a.offsets + a.experts);
+    return static_cast<int>(max(int64_t(0), min(int64_t(o), a.pairs)));
+}
+
+// xs[slot[t][j]] = x[t]: a copy of V bytes a thread, so no types.
+template <class V>
+__global__ void __launch_bounds__(ROW_THREADS) gather_kernel(const RowArgs a, const char *x, int64_t ldx, char *xs,
+                                                             int64_t ldxs) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.tokens) return;
+    const int end = kept_end(a);
+    const int32_t *slot = a.slot + t * a.top_k;
+    for (int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c < a.vecs;
+         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+        const V v = *reinterpret_cast<const V *>(x + t * ldx + c * static_cast<int64_t>(sizeof(V)));
+        for (int j = 0; j < a.top_k; ++j) {
+            const int s = __ldg(slot + j);
+            if (static_cast<unsigned>(s) >= a.pairs) continue;
+            *reinterpret_cast<V *>(xs + s * ldxs + c * static_cast<int64_t>(sizeof(V))) = s < end ? v : V{};
+        }
+    }
+}
+
+// Choices whose rows a thread has in flight at once.
+constexpr int CHOICES = 8;
+
+template <class T, int N, bool WEIGHTED>
+__global__ void __launch_bounds__(ROW_THREADS) combine_kernel(const RowArgs a, const T *h, int64_t ldh,
+                                                              const float *weights, T *y, int64_t ldy) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.tokens) return;
+    const int end = kept_end(a);
+    for (int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c < a.vecs;
+         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+        float sum[N] = {};
+        for (int j0 = 0; j0 < a.top_k; j0 += CHOICES) {
+            Pack<T, N> rows[CHOICES];
+            float w[CHOICES];
+            bool kept[CHOICES];
+#pragma unroll
+            for (int j = 0; j < CHOICES; ++j) {
+                kept[j] = false;
+                if (j0 + j >= a.top_k) continue;
+                const int s = __ldg(a.slot + t * a.top_k + j0 + j);
+                kept[j] = s >= 0 && s < end;
+                if (!kept[j]) continue;
+                if (WEIGHTED) w[j] = __ldg(weights + t * a.top_k + j0 + j);
+                rows[j] = load_pack<T, N>(h + s * ldh + c * N);
+            }
+#pragma unroll
+            for (int j = 0; j < CHOICES; ++j) {
+                if (!kept[j]) continue;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    sum[i] = WEIGHTED ? fmaf(w[j], to_f32(rows[j].v[i]), sum[i]) : sum[i] + to_f32(rows[j].v[i]);
+            }
+        }
+        Pack<T, N> out;
+#pragma unroll
+        for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(sum[i]);
+        store_pack(y + t * ldy + c * N, out);
+    }
+}
+
+// blockDim.x (a multiple of 32) threads share a token and go over its whole
+// row, so the dot products end in the block.
+template <class T, int N>
+__global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs a, const T *dy, int64_t lddy,
+                                                                   const T *h, int64_t ldh, const float *weights,
+                                                                   T *dh, int64_t lddh, float *dweights) {
+    __shared__ float part[ROW_THREADS / 32][CHOICES];
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool in = t < a.tokens;
+    const int end = kept_end(a);
+    const int lane = threadIdx.x & 31;
+    const int warp = static_cast<int>((threadIdx.y * blockDim.x + threadIdx.x) >> 5);
+    const int warps = static_cast<int>(blockDim.x >> 5);  // of one token
+    for (int j0 = 0; j0 < a.top_k; j0 += CHOICES) {
+        float dot[CHOICES] = {};
+        float w[CHOICES];
+        int s[CHOICES];  // -1: past top_k or not a slot; >= end: dropped
+#pragma unroll
+        for (int j = 0; j < CHOICES; ++j) {
+            s[j] = -1;
+            w[j] = 0.0f;
+            if (!in || j0 + j >= a.top_k) continue;
+            s[j] = __ldg(a.slot + t * a.top_k + j0 + j);
+            if (s[j] < 0 || s[j] >= a.pairs) s[j] = -1;
+            w[j] = __ldg(weights + t * a.top_k + j0 + j);
+        }
+        if (in) {
+            for (int64_t c = threadIdx.x; c < a.vecs; c += blockDim.x) {
+                const Pack<T, N> g = load_pack<T, N>(dy + t * lddy + c * N);
+                Pack<T, N> rows[CHOICES];
+#pragma unroll
+                for (int j = 0; j < CHOICES; ++j)
+                    if (s[j] >= 0 && s[j] < end) rows[j] = load_pack<T, N>(h + s[j] * ldh + c * N);
+#pragma unroll
+                for (int j = 0; j < CHOICES; ++j) {
+                    if (s[j] < 0) continue;
+                    Pack<T, N> out;
+                    if (s[j] < end) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            dot[j] = fmaf(to_f32(g.v[i]), to_f32(rows[j].v[i]), dot[j]);
+                            out.v[i] = from_f32<T>(w[j] * to_f32(g.v[i]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(0.0f);
+                    }
+                    store_pack(dh + s[j] * lddh + c * N, out);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CHOICES; ++j) {
+            if (j0 + j >= a.top_k) break;
+            float d = dot[j];
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (lane == 0) part[warp][j] = d;
+        }
+        __syncthreads();
+        if (in && threadIdx.x < CHOICES && j0 + static_cast<int>(threadIdx.x) < a.top_k) {
+            float d = 0.0f;
+            for (int i = 0; i < warps; ++i) d += part[threadIdx.y * warps + i][threadIdx.x];
+            dweights[t * a.top_k + j0 + threadIdx.x] = d;
+        }
+        __syncthreads();
+    }
+}
+
+// Largest power of two (at most 16) that divides every address and row
+// stride, in bytes.
+int vector_bytes(int64_t size, int64_t width, const void *p0, int64_t ld0, const void *p1, int64_t ld1,
+                 const void *p2 = nullptr, int64_t ld2 = 0) {
+    const uint64_t all = reinterpret_cast<uint64_t>(p0) | reinterpret_cast<uint64_t>(p1) |
+                         reinterpret_cast<uint64_t>(p2) |
+                         static_cast<uint64_t>((width | ld0 | ld1 | ld2) * size) | 16u;
+    return static_cast<int>(all & (~all + 1));
+}
+
+// Block shape: tx threads along a row of `vecs` vectors, the smallest power
+// of two from 32 to 256 that covers it.
+dim3 row_block(int64_t vecs) {
+    unsigned tx = 32;
+    while (tx < ROW_THREADS && tx < vecs) tx *= 2;
+    return dim3(tx, ROW_THREADS / tx);
+}
+
+// One block per blockDim.y tokens and up to 64 pieces of a row.
+bool row_grid(const Route &r, int64_t vecs, dim3 block, bool split_row, dim3 *grid) {
+    const int64_t x = (r.tokens + block.y - 1) / block.y;
+    int64_t y = split_row ? (vecs + block.x - 1) / block.x : 1;
+    if (y > 64) y = 64;
+    if (x > INT32_MAX) return false;
+    *grid = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+    return true;
+}
+
+RowArgs row_args(const Route &r, int64_t vecs) {
+    return RowArgs{r.tokens, static_cast<int>(r.top_k), static_cast<int>(r.experts), vecs, r.tokens * r.top_k,
+                   r.slot,   r.offsets};
+}
+
+int launched(int *launches) {
+    if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    ++*launches;
+    return SGEMM_OK;
+}
+
+template <class Id>
+int sort_typed(const Id *ids, int64_t pairs, int experts, int32_t *offsets, int32_t *order, int32_t *slot,
+               int32_t *workspace, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (dev.device < 0 || dev.device >= 64) return SGEMM_ERR_DEVICE;
+    const int keys = experts + 1;
+    const int table_blocks = sort_blocks(pairs, experts);
+    const int blocks = table_blocks > 0 ? table_blocks : 1;
+    const int64_t per = (pairs + blocks - 1) / blocks;
+    // Two steps of 32 pairs per warp before another warp counts.
+    int warps = static_cast<int>((per + 63) / 64);
+    const int fit = (SORT_SMEM_INTS - keys - 33) / keys;
+    if (warps > fit) warps = fit;
+    if (warps > SORT_MAX_WARPS) warps = SORT_MAX_WARPS;
+    if (warps < 1) warps = 1;
+    const size_t smem = static_cast<size_t>(warps * keys + keys + 33) * sizeof(int32_t);
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(sort_rank_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 SORT_SMEM_INTS * 4) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    if (table_blocks > 0) {
+        sort_count_kernel<Id><<<blocks, SORT_THREADS, keys * sizeof(int32_t), stream>>>(ids, pairs, experts,
+                                                                                        workspace);
+        const int rc = launched(launches);
+        if (rc != SGEMM_OK) return rc;
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(SORT_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = table_blocks > 0 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, sort_rank_kernel<Id>, ids, pairs, experts, warps,
+                           static_cast<const int32_t *>(workspace), offsets, order, slot) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    ++*launches;
+    return SGEMM_OK;
+}
+
+template <class T, int N>
+int combine_typed(const Route &r, const void *h, int64_t ldh, const float *weights, void *y, int64_t ldy,
+                  cudaStream_t stream, int *launches) {
+    const int64_t vecs = r.width / N;
+    const dim3 block = row_block(vecs);
+    dim3 grid;
+    if (!row_grid(r, vecs, block, true, &grid)) return SGEMM_ERR_UNSUPPORTED;
+    const RowArgs a = row_args(r, vecs);
+    if (weights)
+        combine_kernel<T, N, true><<<grid, block, 0, stream>>>(a, static_cast<const T *>(h), ldh, weights,
+                                                               static_cast<T *>(y), ldy);
+    else
+        combine_kernel<T, N, false><<<grid, block, 0, stream>>>(a, static_cast<const T *>(h), ldh, nullptr,
+                                                                static_cast<T *>(y), ldy);
+    return launched(launches);
+}
+
+template <class T, int N>
+int combine_grad_typed(const Route &r, const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                       const float *weights, void *dh, int64_t lddh, float *dweights, cudaStream_t stream,
+                       int *launches) {
+    const int64_t vecs = r.width / N;
+    const dim3 block = row_block(vecs);
+    dim3 grid;
+    if (!row_grid(r, vecs, block, false, &grid)) return SGEMM_ERR_UNSUPPORTED;
+    combine_grad_kernel<T, N><<<grid, block, 0, stream>>>(row_args(r, vecs), static_cast<const T *>(dy), lddy,
+                                                          static_cast<const T *>(h), ldh, weights,
+                                                          static_cast<T *>(dh), lddh, dweights);
+    return launched(launches);
+}
+
+// f(T{}, N) for the row type and the values a thread moves at once.
+template <class F>
+int for_type(int type, int bytes, F &&f) {
+    if (type == SGEMM_TYPE_F32) {
+        if (bytes == 16) return f(float{}, std::integral_constant<int, 4>{});
+        if (bytes == 8) return f(float{}, std::integral_constant<int, 2>{});
+        return f(float{}, std::integral_constant<int, 1>{});
+    }
+    if (type == SGEMM_TYPE_BF16) {
+        if (bytes == 16) return f(__nv_bfloat16{}, std::integral_constant<int, 8>{});
+        if (bytes >= 4) return f(__nv_bfloat16{}, std::integral_constant<int, 2>{});
+        return f(__nv_bfloat16{}, std::integral_constant<int, 1>{});
+    }
+    if (bytes == 16) return f(__half{}, std::integral_constant<int, 8>{});
+    if (bytes >= 4) return f(__half{}, std::integral_constant<int, 2>{});
+    return f(__half{}, std::integral_constant<int, 1>{});
+}
+
+}  // namespace
+
+int sort_blocks(int64_t pairs, int64_t experts) {
+    if (pairs <= SORT_SINGLE) return 0;
+    int64_t b = (pairs + SORT_PER_BLOCK - 1) / SORT_PER_BLOCK;
+    const int64_t table = SORT_TABLE / (experts + 1);
+    if (b > table) b = table;
+    if (b > SORT_BLOCKS) b = SORT_BLOCKS;
+    return b < 2 ? 2 : static_cast<int>(b);
+}
+
+int sort_launch(const void *ids, int id_bits, int64_t pairs, int64_t experts, int32_t *offsets, int32_t *order,
+                int32_t *slot, int32_t *workspace, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const int e = static_cast<int>(experts);
+    if (id_bits == 64)
+        return sort_typed(static_cast<const int64_t *>(ids), pairs, e, offsets, order, slot, workspace, dev, stream,
+                          launches);
+    return sort_typed(static_cast<const int32_t *>(ids), pairs, e, offsets, order, slot, workspace, dev, stream,
+                      launches);
+}
+
+int gather_launch(int type, const Route &r, const void *x, int64_t ldx, void *xs, int64_t ldxs, const DeviceInfo &,
+                  cudaStream_t stream, int *launches) {
+    const int64_t size = type_size(type);
+    const int vb = vector_bytes(size, r.width, x, ldx, xs, ldxs);
+    const int64_t vecs = r.width * size / vb;
+    const dim3 block = row_block(vecs);
+    dim3 grid;
+    if (!row_grid(r, vecs, block, true, &grid)) return SGEMM_ERR_UNSUPPORTED;
+    const RowArgs a = row_args(r, vecs);
+    const char *in = static_cast<const char *>(x);
+    char *out = static_cast<char *>(xs);
+    switch (vb) {
+        case 16: gather_kernel<uint4><<<grid, block, 0, stream>>>(a, in, ldx * size, out, ldxs * size); break;
+        case 8: gather_kernel<uint2><<<grid, block, 0, stream>>>(a, in, ldx * size, out, ldxs * size); break;
+        case 4: gather_kernel<uint32_t><<<grid, block, 0, stream>>>(a, in, ldx * size, out, ldxs * size); break;
+        default: gather_kernel<uint16_t><<<grid, block, 0, stream>>>(a, in, ldx * size, out, ldxs * size); break;
+    }
+    return launched(launches);
+}
+
+int combine_launch(int type, const Route &r, const void *h, int64_t ldh, const float *weights, void *y, int64_t ldy,
+                   const DeviceInfo &, cudaStream_t stream, int *launches) {
+    return for_type(type, vector_bytes(type_size(type), r.width, h, ldh, y, ldy), [&](auto t, auto n) {
+        return combine_typed<decltype(t), decltype(n)::value>(r, h, ldh, weights, y, ldy, stream, launches);
+    });
+}
+
+int combine_grad_launch(int type, const Route &r, const void *dy, int64_t lddy, const void *h, int64_t ldh,
+                        const float *weights, void *dh, int64_t lddh, float *dweights, const DeviceInfo &,
+                        cudaStream_t stream, int *launches) {
+    return for_type(type, vector_bytes(type_size(type), r.width, dy, lddy, h, ldh, dh, lddh), [&](auto t, auto n) {
+        return combine_grad_typed<decltype(t), decltype(n)::value>(r, dy, lddy, h, ldh, weights, dh, lddh, dweights,
+                                                                   stream, launches);
+    });
+}
+
+}  // namespace ex
+}  // namespace sgemm

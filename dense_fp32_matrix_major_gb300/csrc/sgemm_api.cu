@@ -273,6 +273,8 @@ int current_device(DeviceInfo *info) {
     return g_dev.status[dev];
 }
 
+void note_launches(int launches) { g_last_launches.store(launches); }
+
 }  // namespace sgemm
 
 using sgemm::Problem;
