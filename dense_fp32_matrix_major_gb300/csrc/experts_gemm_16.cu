@@ -1,0 +1,583 @@
+// Products per expert in bf16 and fp16 on SM pairs (tcgen05, cta_group::2):
+//
+//     rows   C[s] = A[s] op(B[e(s)])                  s in group e
+//     wgrad  C[e] = sum over s in group e of A[s]^T B[s]
+//
+// Bound by the tensor pipe where groups are long, by reading B where they are
+// short. Products of two 16-bit values are exact in fp32 and are summed in
+// fp32 in tensor memory; a value is rounded once, when C is written.
+//
+// Two CTAs on two SMs of a cluster make one 256 x 256 tile of C: each stages
+// 128 rows of A and 128 columns of B per 64-deep k-block, and one MMA of 256
+// x 256 x 16 issued by the even CTA reads both halves, so either operand
+// crosses each SM's shared memory once for 256 columns or rows. Two
+// accumulators of 256 columns fill tensor memory: the epilogue empties one
+// while the tensor core fills the other.
+//
+// Groups. The bounds are read on the device. Tiles never cross groups; the
+// workers (one CTA pair each) take the tiles of the groups in order, round
+// robin, each role of a worker walking the group bounds for itself. Along
+// rows a tile may reach past its group's end: those rows of A belong to the
+// next group, change only rows of C that are not written, and cost nothing
+// else. In wgrad the rows are the summed direction: the part of the last
+// k-block that lies past the group's end is zeroed in shared memory, in both
+// operands (a NaN of the next group times zero would stay), before the MMA
+// may read it.
+//
+// Layouts. An operand whose summed direction is contiguous in memory (A of
+// rows, B of op = T) is staged K-major, otherwise MN-major, both in 128-byte
+// swizzled rows as TMA writes them; the MMA takes either, so nothing is
+// transposed.
+//
+// Roles in each CTA (7 warps): warp 0 loads (TMA, 6 stages), warp 1 of the
+// even CTA issues the MMAs, warps 2-5 write C (one per quarter of tensor
+// memory's lanes: round to 16 bits, 32 x 64 chunks through shared memory,
+// TMA stores; rows of a chunk that crosses the group's end, and C that TMA
+// cannot address, with per-thread stores), warp 6 zeroes wgrad's tails. The
+// loads of both CTAs complete on the even CTA's barriers. Every wait is
+// bounded in time.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "experts_common.cuh"
+#include "experts_internal.h"
+#include "tc_common.cuh"
+
+namespace sgemm {
+namespace ex {
+namespace {
+
+using namespace tc;
+
+namespace g16 {
+
+constexpr int PM = 256, PN = 256, HM = 128, HN = 128;  // tile of a pair, this CTA's share of the operands
+constexpr int KB = 64;                                 // k-block: 64 values = 128 bytes
+constexpr int STAGES = 6;
+constexpr int A_BYTES = HM * KB * 2, B_BYTES = HN * KB * 2, STAGE = A_BYTES + B_BYTES;
+constexpr int BOX = 64 * 128;  // bytes of a 64 x 64 MN-major box
+constexpr int CHUNK = 32 * 128;  // 32 rows x 64 columns of C
+constexpr int C0 = STAGES * STAGE;
+constexpr int EPI_WARPS = 4, TAIL_WARP = 6, THREADS = 7 * 32;
+constexpr int BAR0 = C0 + EPI_WARPS * 2 * CHUNK;
+constexpr int SMEM_BYTES = BAR0 + 256 + 1024;
+// mbarriers
+constexpr int FULL = 0, EMPTY = FULL + STAGES, TAIL = EMPTY + STAGES, ACC_FULL = TAIL + STAGES,
+              ACC_EMPTY = ACC_FULL + 2, DRAIN = ACC_EMPTY + 2, NBARS = DRAIN + 1;
+static_assert(NBARS * 8 + 24 <= 256, "barrier block");
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(STAGE % 1024 == 0 && C0 % 1024 == 0, "1024-byte aligned swizzled buffers");
+
+}  // namespace g16
+
+struct Args16 {
+    int rows, experts;
+    int64_t M, N, K;  // M: wgrad only
+    const int32_t *offsets;
+    void *C;
+    int64_t ldc, strideC;
+    int tiles_m, tiles_n;  // tiles_m: wgrad only
+    int c_tma;
+    int bf16;
+    uint32_t idesc;
+    uint64_t timeout_ns;
+    int *watchdog;
+};
+
+enum Form { ROWS_N, ROWS_T, WGRAD };
+
+// One tile: rows [row0, row_end) of C (of matrix `item` in wgrad) from column
+// n0 on, summed over k_blocks k-blocks that start at row k0 (wgrad).
+struct Unit {
+    int group, row0, row_end, n0, k0, k_rows, k_blocks;
+};
+
+// Calls f(unit) for the tiles of worker `index` of `count`, in order.
+template <Form FORM, class F>
+__device__ __forceinline__ void for_each_tile(const Args16 &a, volatile int *abort_flag, int index, int count, F &&f) {
+    if (FORM == WGRAD) {
+        const int per = a.tiles_m * a.tiles_n;
+        const int64_t total = static_cast<int64_t>(per) * a.experts;
+        for (int64_t u = index; u < total; u += count) {
+            if (*abort_flag) return;
+            const int e = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<int64_t>(e) * per);
+            const int begin = group_start(a.offsets, e, a.rows);
+            const int end = max(begin, group_start(a.offsets, e + 1, a.rows));
+            f(Unit{e, r / a.tiles_n * g16::PM, static_cast<int>(a.M), r % a.tiles_n * g16::PN, begin, end - begin,
+                   (end - begin + g16::KB - 1) / g16::KB});
+        }
+    } else {
+        const int k_blocks = static_cast<int>((a.K + g16::KB - 1) / g16::KB);
+        int e = 0, begin = 0, base = 0;
+        int next = a.experts > 0 ? group_start(a.offsets, 1, a.rows) : a.rows;
+        int end = max(begin, next);
+        int tiles = (end - begin + g16::PM - 1) / g16::PM;
+        for (int64_t u = index;; u += count) {
+            if (*abort_flag) return;
+            const int rt = static_cast<int>(u / a.tiles_n);
+            while (rt >= base + tiles) {
+                if (e == a.experts) return;
+                base += tiles;
+                ++e;
+                begin = next;
+                next = e < a.experts ? group_start(a.offsets, e + 1, a.rows) : a.rows;
+                end = max(begin, next);
+                tiles = (end - begin + g16::PM - 1) / g16::PM;
+            }
+            f(Unit{e, begin + (rt - base) * g16::PM, end, static_cast<int>(u % a.tiles_n) * g16::PN, 0, 0,
+                   e < a.experts ? k_blocks : 0});
+        }
+    }
+}
+
+// TMA load into this CTA's shared memory that completes its bytes on the
+// mbarrier at shared::cluster address `bar` (of either CTA of the pair).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+        "{%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+    return r;
+}
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle:
+// boxes of 64 values x 64 k (rows of 128 bytes, one k each). Leading offset:
+// from one box of 64 values to the next; stride offset: from 8 k to the next 8.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(g16::BOX >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ void mma16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <Form FORM>
+__global__ void __launch_bounds__(g16::THREADS, 1)
+    grouped16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Args16 a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + g16::BAR0);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + g16::NBARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + g16::NBARS + 1);
+    const uint32_t signal_word = smem_u32(bars + g16::NBARS + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < g16::STAGES; ++s) {
+            mbar_init(bar(g16::FULL + s), 1);
+            mbar_init(bar(g16::EMPTY + s), 1);
+            mbar_init(bar(g16::TAIL + s), 1);
+        }
+        for (int d = 0; d < 2; ++d) {
+            mbar_init(bar(g16::ACC_FULL + d), 1);
+            mbar_init(bar(g16::ACC_EMPTY + d), 2 * g16::EPI_WARPS);
+        }
+        mbar_init(bar(g16::DRAIN), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    }
+    __syncthreads();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ loads
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+                const int m0 = u.row0 + g16::HM * static_cast<int>(rank), n0 = u.n0 + g16::HN * static_cast<int>(rank);
+                for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
+                    const int s = static_cast<int>(it % g16::STAGES);
+                    if (!mbar_wait<true>(bar(g16::EMPTY + s), ((it / g16::STAGES) & 1) ^ 1, a, abort_flag,
+                                         WD_PRODUCER)) {
+                        ok = false;
+                        return;
+                    }
+                    const uint32_t sa = base + static_cast<uint32_t>(s * g16::STAGE), sb = sa + g16::A_BYTES;
+                    const bool tail = FORM == WGRAD && (kb + 1) * g16::KB > u.k_rows;
+                    uint32_t to;
+                    if (tail) {
+                        // Each CTA's own barrier; its tail warp signals the even CTA's.
+                        to = map_to_cta(bar(g16::TAIL + s), rank);
+                        mbar_arrive_expect_tx(bar(g16::TAIL + s), g16::STAGE);
+                    } else {
+                        to = map_to_cta(bar(g16::FULL + s), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(bar(g16::FULL + s), 2 * g16::STAGE);
+                    }
+                    const int k = kb * g16::KB;
+                    if (FORM == WGRAD) {
+                        tma_load_pair(sa, &tmA, m0, u.k0 + k, 0, to);
+                        tma_load_pair(sa + g16::BOX, &tmA, m0 + 64, u.k0 + k, 0, to);
+                        tma_load_pair(sb, &tmB, n0, u.k0 + k, 0, to);
+                        tma_load_pair(sb + g16::BOX, &tmB, n0 + 64, u.k0 + k, 0, to);
+                    } else {
+                        tma_load_pair(sa, &tmA, k, m0, 0, to);
+                        if (FORM == ROWS_T) {
+                            tma_load_pair(sb, &tmB, k, n0, u.group, to);
+                        } else {
+                            tma_load_pair(sb, &tmB, n0, k, u.group, to);
+                            tma_load_pair(sb + g16::BOX, &tmB, n0 + 64, k, u.group, to);
+                        }
+                    }
+                }
+            });
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------------- MMA
+        if (rank == 0) {
+            const bool leader = elect_one();
+            uint32_t it = 0, units = 0;
+            bool ok = true;
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+                if (u.k_blocks == 0 || !ok) return;
+                const uint32_t d = units & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::ACC_EMPTY + d), ((units >> 1) & 1) ^ 1, a,
+                                                             abort_flag, WD_MMA_ACC));
+                tc_fence_after();
+                const uint32_t dt = tmem_base + d * g16::PN;
+                for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
+                    const int s = static_cast<int>(it % g16::STAGES);
+                    ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::FULL + s), (it / g16::STAGES) & 1, a,
+                                                                 abort_flag, WD_MMA_FULL));
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t sa = base + static_cast<uint32_t>(s * g16::STAGE), sb = sa + g16::A_BYTES;
+                    const uint64_t da = FORM == WGRAD ? mn_desc(sa) : sw128_desc(sa);
+                    const uint64_t db = FORM == ROWS_T ? sw128_desc(sb) : mn_desc(sb);
+                    // 16 values of k further: 32 bytes along a K-major row, 16
+                    // rows of 128 bytes in an MN-major box.
+                    constexpr uint64_t step_a = (FORM == WGRAD ? 16 * 128 : 32) >> 4;
+                    constexpr uint64_t step_b = (FORM == ROWS_T ? 32 : 16 * 128) >> 4;
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < g16::KB / 16; ++ks)
+                            mma16_pair(dt, da + ks * step_a, db + ks * step_b, a.idesc, kb > 0 || ks > 0);
+                        tc_commit2(bar(g16::EMPTY + s));
+                    }
+                    __syncwarp();
+                }
+                if (leader && ok) tc_commit2(bar(g16::ACC_FULL + d));
+                __syncwarp();
+                ++units;
+            });
+            if (leader) tc_commit2(bar(g16::DRAIN));
+            __syncwarp();
+            if (lane == 0) {
+                const bool was_aborted = *abort_flag != 0;
+                if (!mbar_wait<true>(bar(g16::DRAIN), 0, a, abort_flag, WD_DRAIN) && was_aborted) {
+                    const uint64_t t0 = global_timer();
+                    while (!mbar_try_wait<true>(bar(g16::DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
+                    }
+                }
+            }
+        }
+    } else if (warp == g16::TAIL_WARP) {
+        // ---------------------------------------------- tails of the summed rows
+        if (FORM == WGRAD) {
+            uint32_t it = 0, uses = 0;  // bit s: parity of the tails staged in stage s so far
+            bool ok = true;
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+                if (!ok || u.k_blocks == 0) return;
+                const int left = u.k_rows % g16::KB;
+                it += static_cast<uint32_t>(u.k_blocks);
+                if (left == 0) return;
+                const int s = static_cast<int>((it - 1) % g16::STAGES);
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(bar(g16::TAIL + s), (uses >> s) & 1, a, abort_flag, WD_PRODUCER));
+                if (!ok) return;
+                uses ^= 1u << s;
+                const uint32_t st = base + static_cast<uint32_t>(s * g16::STAGE);
+                // Rows left .. 63 of each of the four boxes, 16 bytes a lane.
+                const int vecs = (g16::KB - left) * 8;
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b)
+                    for (int i = lane; i < vecs; i += 32)
+                        st_shared_v4(st + static_cast<uint32_t>(b * g16::BOX + left * 128 + i * 16), 0.0f, 0.0f, 0.0f,
+                                     0.0f);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(bar(g16::FULL + s), 4);
+                    else
+                        st_async_signal(signal_word, bar(g16::FULL + s), 0);
+                }
+                __syncwarp();
+            });
+        }
+    } else {
+        // --------------------------------------------------------------- epilogue
+        const int q = warp & 3;  // quarter of tensor memory's lanes
+        const uint32_t stage0 = base + g16::C0 + static_cast<uint32_t>((warp - 2) * 2 * g16::CHUNK);
+        uint32_t units = 0, chunks = 0;
+        bool ok = true;
+        for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+            if (!ok) return;
+            const bool summed = u.k_blocks > 0;
+            const uint32_t d = units & 1;
+            if (summed) {
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::ACC_FULL + d), (units >> 1) & 1, a, abort_flag,
+                                                             WD_EPILOGUE));
+                if (!ok) return;
+                tc_fence_after();
+                ++units;
+            }
+            const int row0 = u.row0 + g16::HM * static_cast<int>(rank) + 32 * q;
+            const int rows = min(32, u.row_end - row0);  // may be negative
+            const uint32_t dt = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + d * g16::PN;
+            const int item = FORM == WGRAD ? u.group : 0;
+#pragma unroll 1
+            for (int ch = 0; ch < g16::PN / 64; ++ch) {
+                const int col0 = u.n0 + 64 * ch;
+                const bool wanted = rows > 0 && col0 < a.N;  // uniform over the warp
+                uint32_t v[32];
+                if (summed && wanted) {
+                    float x[32];
+                    tmem_load32(dt + static_cast<uint32_t>(64 * ch), x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = pack16(x[2 * j], x[2 * j + 1], a.bf16);
+                    tmem_load32(dt + static_cast<uint32_t>(64 * ch + 32), x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[16 + j] = pack16(x[2 * j], x[2 * j + 1], a.bf16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0;
+                }
+                if (summed && ch == g16::PN / 64 - 1) {
+                    // The accumulator is out of tensor memory.
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(bar(g16::ACC_EMPTY + d), 0);
+                }
+                if (!wanted) continue;
+                const uint32_t buf = stage0 + (chunks & 1) * g16::CHUNK;
+                ++chunks;
+                // The store that read this buffer two chunks ago is done reading.
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_shared_v4(buf + sw128_offset(lane, j), __uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                 __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                if (a.c_tma && rows == 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&tmC, col0, row0, item, buf);
+                } else {
+                    // Row by row, the lanes along the row.
+                    __syncwarp();
+                    uint16_t *c = static_cast<uint16_t *>(a.C) + item * a.strideC + static_cast<int64_t>(row0) * a.ldc +
+                                  col0;
+                    const int cols = static_cast<int>(min(static_cast<int64_t>(64), a.N - col0));
+                    for (int r = 0; r < rows; ++r, c += a.ldc) {
+                        const uint32_t w = __float_as_uint(ld_shared_f32(buf + sw128_offset(r, lane >> 2) +
+                                                                         static_cast<uint32_t>((lane & 3) * 4)));
+                        if (2 * lane < cols) c[2 * lane] = static_cast<uint16_t>(w);
+                        if (2 * lane + 1 < cols) c[2 * lane + 1] = static_cast<uint16_t>(w >> 16);
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) bulk_commit();  // one group per chunk, empty or not
+            }
+        });
+        if (lane == 0) bulk_wait<0>();
+    }
+
+    // The odd CTA's tensor memory is written by the even CTA's MMAs: wait for
+    // them to drain before the pair releases it. After a wait that gave up,
+    // loads may still be on their way: leave them time to land.
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        const uint64_t t0 = global_timer();
+        while (global_timer() - t0 < 10000000ull) {
+        }
+    }
+    if (rank != 0 && threadIdx.x == 0) {
+        if (!mbar_wait<true>(bar(g16::DRAIN), 0, a, abort_flag, WD_DRAIN)) {
+            const uint64_t t0 = global_timer();
+            while (!mbar_try_wait<true>(bar(g16::DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+constexpr int kMaxDevices = 64;
+std::once_flag g_once[kMaxDevices][3];
+cudaError_t g_err[kMaxDevices][3];
+int g_clusters[kMaxDevices][3];
+
+// Whether a tensor map can describe `items` matrices of rows x ld 16-bit
+// values, `stride` apart.
+bool mappable(const void *p, int64_t rows, int64_t ld, int64_t items, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 &&
+           (items == 1 || (stride % 8 == 0 && stride >= rows * ld));
+}
+
+template <Form FORM>
+int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    auto kernel = grouped16_kernel<FORM>;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(g16::THREADS);
+    cfg.dynamicSmemBytes = g16::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    std::call_once(g_once[dev.device][FORM], [&] {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g16::SMEM_BYTES);
+        int n = 0;
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t q = cfg;
+            q.gridDim = dim3(2 * (dev.sm_count / 2));
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
+        }
+        g_err[dev.device][FORM] = e;
+        g_clusters[dev.device][FORM] = n;
+    });
+    const int clusters = g_clusters[dev.device][FORM];
+    int *flag = watchdog_flag_device_ptr();
+    if (g_err[dev.device][FORM] != cudaSuccess || clusters < 1 || !flag) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    const CUtensorMapDataType type =
+        p.type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    alignas(64) CUtensorMap mapA{}, mapB{}, mapC{};
+    const int64_t strideB = p.experts > 1 ? p.strideB : 0, strideC = p.experts > 1 ? p.strideC : 0;
+    bool ok;
+    if (FORM == WGRAD) {
+        ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.M, p.lda, 1, 0, 64, g16::KB, sw) &&
+             encode_map_typed(&mapB, type, 2, p.B, p.rows, p.N, p.ldb, 1, 0, 64, g16::KB, sw);
+    } else {
+        ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.K, p.lda, 1, 0, g16::KB, g16::HM, sw) &&
+             (FORM == ROWS_T ? encode_map_typed(&mapB, type, 2, p.B, p.N, p.K, p.ldb, p.experts, strideB, g16::KB,
+                                                g16::HN, sw)
+                             : encode_map_typed(&mapB, type, 2, p.B, p.K, p.N, p.ldb, p.experts, strideB, 64,
+                                                g16::KB, sw));
+    }
+    if (!ok) return SGEMM_ERR_LAUNCH;
+    const bool c_tma =
+        (FORM == WGRAD ? mappable(p.C, p.M, p.ldc, p.experts, p.strideC) : mappable(p.C, p.rows, p.ldc, 1, 0)) &&
+        (FORM == WGRAD ? encode_map_typed(&mapC, type, 2, p.C, p.M, p.N, p.ldc, p.experts, strideC, 64, 32, sw)
+                       : encode_map_typed(&mapC, type, 2, p.C, p.rows, p.N, p.ldc, 1, 0, 64, 32, sw));
+    if (!c_tma) mapC = mapA;  // not read by the kernel
+
+    Args16 a{};
+    a.rows = static_cast<int>(p.rows);
+    a.experts = static_cast<int>(p.experts);
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.offsets = p.offsets;
+    a.C = p.C;
+    a.ldc = p.ldc;
+    a.strideC = p.strideC;
+    const int64_t tiles_n = (p.N + g16::PN - 1) / g16::PN;
+    const int64_t tiles_m = FORM == WGRAD ? (p.M + g16::PM - 1) / g16::PM : 1;
+    if (tiles_n * tiles_m > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+    a.tiles_n = static_cast<int>(tiles_n);
+    a.tiles_m = static_cast<int>(tiles_m);
+    a.c_tma = c_tma ? 1 : 0;
+    a.bf16 = p.type == SGEMM_TYPE_BF16 ? 1 : 0;
+    // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B
+    // fp16 (0) or bf16 (1) in bits 7-9 and 10-12, bit 15 / 16: A / B MN-major,
+    // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+    const uint32_t t = a.bf16 ? 1u : 0u;
+    a.idesc = (1u << 4) | (t << 7) | (t << 10) | (FORM == WGRAD ? 1u << 15 : 0u) | (FORM == ROWS_T ? 0u : 1u << 16) |
+              (static_cast<uint32_t>(g16::PN >> 3) << 17) | (static_cast<uint32_t>(g16::PM >> 4) << 24);
+    a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
+    a.watchdog = flag;
+    // Every group may end in a part of a tile, and so may the rest.
+    const int64_t units = FORM == WGRAD ? tiles_m * tiles_n * p.experts
+                                        : ((p.rows + g16::PM - 1) / g16::PM + p.experts) * tiles_n;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
+    if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    ++*launches;
+    return SGEMM_OK;
+}
+
+}  // namespace
+
+// Operands that tensor maps can describe: 16-byte aligned bases and rows,
+// sizes that fit their coordinates.
+bool grouped16_supports(const GroupedProblem &p) {
+    const int64_t lim = INT32_MAX / 2;
+    return p.type != SGEMM_TYPE_F32 && p.rows > 0 && (p.wgrad || p.K > 0) && p.rows < lim && p.M < lim && p.N < lim &&
+           p.K < lim && mappable(p.A, p.rows, p.lda, 1, 0) &&
+           (p.wgrad ? mappable(p.B, p.rows, p.ldb, 1, 0)
+                    : mappable(p.B, p.transB == SGEMM_OP_T ? p.N : p.K, p.ldb, p.experts, p.strideB));
+}
+
+int grouped16_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
+    if (p.wgrad) return launch16<WGRAD>(p, dev, stream, launches);
+    return p.transB == SGEMM_OP_T ? launch16<ROWS_T>(p, dev, stream, launches)
+                                  : launch16<ROWS_N>(p, dev, stream, launches);
+}
+
+}  // namespace ex
+}  // namespace sgemm

@@ -1098,22 +1098,28 @@ int launch_tma(const Problem &p, const DeviceInfo &dev, int sk_mode, cudaStream_
 
 namespace tc {
 
-// A batch of row-major rows x cols fp32 matrices as a rank-3 tensor map (see
+// A batch of row-major rows x cols matrices as a rank-3 tensor map (see
 // tc_common.cuh).
-bool encode_map(CUtensorMap *map, const float *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t batch,
-                int64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+bool encode_map_typed(CUtensorMap *map, CUtensorMapDataType type, int64_t size, const void *ptr, int64_t rows,
+                      int64_t cols, int64_t ld, int64_t batch, int64_t stride, uint32_t box_cols, uint32_t box_rows,
+                      CUtensorMapSwizzle swizzle) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const int64_t items = stride == 0 ? 1 : batch;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(items)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * sizeof(float),
-                                   static_cast<cuuint64_t>(stride == 0 ? ld * rows : stride) * sizeof(float)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size),
+                                   static_cast<cuuint64_t>((stride == 0 ? ld * rows : stride) * size)};
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float *>(ptr), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(map, type, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_map(CUtensorMap *map, const float *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t batch,
+                int64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    return encode_map_typed(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(float), ptr, rows, cols, ld, batch, stride,
+                            box_cols, box_rows, swizzle);
 }
 
 }  // namespace tc

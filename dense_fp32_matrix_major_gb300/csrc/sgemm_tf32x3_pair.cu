@@ -129,47 +129,6 @@ static_assert(SLOT % 1024 == 0 && RAW0 % 1024 == 0 && R0 % 1024 == 0, "1024-byte
 
 }  // namespace pr
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    cluster_arrive();
-    cluster_wait();
-}
-
-// Arrive on the mbarrier at this CTA's shared offset `bar` in CTA `cta` of
-// the cluster, releasing this thread's prior writes at cluster scope.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t cta) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(cta));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
-}
-
-// st.async of a 4-byte word into CTA `cta`'s shared memory at this CTA's
-// offset `word`, completing 4 bytes of transactions on the mbarrier at offset
-// `bar` there. The completion has release semantics at cluster scope (this
-// thread's prior writes, and those it has observed, are visible to a thread
-// that sees the phase complete) and the issuing thread does not wait for it.
-__device__ __forceinline__ void st_async_signal(uint32_t word, uint32_t bar, uint32_t cta) {
-    uint32_t rw, rb;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rw) : "r"(word), "r"(cta));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(bar), "r"(cta));
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(rw), "r"(0u),
-                 "r"(rb)
-                 : "memory");
-}
-
 // One 256 x 128 x 8 product of the pair: A (128 rows per CTA) from TMEM, B
 // (64 columns per CTA) from shared memory.
 __device__ __forceinline__ void tc_mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t accumulate) {
@@ -180,16 +139,6 @@ __device__ __forceinline__ void tc_mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         " tcgen05.mma.cta_group::2.kind::tf32 [%0], [%1], %2, %3, p;\n"
         "}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(pr::kIdesc2), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive on the mbarrier at offset `bar` of both CTAs once the pair's MMAs
-// issued so far have completed.
-__device__ __forceinline__ void tc_commit2(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            bar),
-        "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 

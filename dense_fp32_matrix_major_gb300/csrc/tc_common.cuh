@@ -198,10 +198,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for the phase with the given parity to complete, within the time
-// limit; false if the limit passed or another role already aborted.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Args &a, volatile int *abort_flag,
-                                          int code) {
+// limit; false if the limit passed or another role already aborted. The
+// kernel's arguments give the limit (timeout_ns) and the flag (watchdog).
+template <bool CLUSTER = false, class KernelArgs>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const KernelArgs &a,
+                                          volatile int *abort_flag, int code) {
     if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = global_timer();
     for (uint32_t n = 1;; ++n) {
@@ -823,12 +824,69 @@ __device__ __forceinline__ void for_each_unit(const Args &a, volatile int *abort
     for_each_unit_of(a, abort_flag, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), f);
 }
 
+// ------------------------------------------------------- CTA pairs (clusters of two)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+
+// Arrive on the mbarrier at this CTA's shared offset `bar` in CTA `cta` of
+// the cluster, releasing this thread's prior writes at cluster scope.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t cta) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(cta));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+// st.async of a 4-byte word into CTA `cta`'s shared memory at this CTA's
+// offset `word`, completing 4 bytes of transactions on the mbarrier at offset
+// `bar` there. The completion has release semantics at cluster scope (this
+// thread's prior writes, and those it has observed, are visible to a thread
+// that sees the phase complete) and the issuing thread does not wait for it.
+__device__ __forceinline__ void st_async_signal(uint32_t word, uint32_t bar, uint32_t cta) {
+    uint32_t rw, rb;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rw) : "r"(word), "r"(cta));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(bar), "r"(cta));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(rw), "r"(0u),
+                 "r"(rb)
+                 : "memory");
+}
+
+// Arrive on the mbarrier at offset `bar` of both CTAs once the pair's MMAs
+// issued so far have completed.
+__device__ __forceinline__ void tc_commit2(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 // Host side, defined with the kernels in sgemm_tf32x3.cu: a rank-3 tensor
 // map over a batch of row-major rows x cols fp32 matrices with row stride ld
 // and item stride `stride` (elements; 0 = one matrix shared by all items),
 // boxes of box_cols x box_rows x 1, out-of-range elements read as zero.
 bool encode_map(CUtensorMap *map, const float *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t batch,
                 int64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+// The same for elements of another type of `size` bytes.
+bool encode_map_typed(CUtensorMap *map, CUtensorMapDataType type, int64_t size, const void *ptr, int64_t rows,
+                      int64_t cols, int64_t ld, int64_t batch, int64_t stride, uint32_t box_cols, uint32_t box_rows,
+                      CUtensorMapSwizzle swizzle);
 
 }  // namespace tc
 }  // namespace sgemm
