@@ -91,5 +91,63 @@ __device__ __forceinline__ RowTile row_tile_of(const int32_t *offsets, int exper
     return RowTile{-1, 0, 0};
 }
 
+// The tiles of C of one product per group: rows of C (C[s] = A[s] op(B[e]))
+// or one matrix per group (wgrad, C[e] = A_e^T B_e).
+struct GroupTiles {
+    const int32_t *offsets;
+    int rows, experts;
+    int64_t M, K;          // wgrad: rows of a matrix; otherwise the summed length
+    int tiles_m, tiles_n;  // tiles_m: wgrad only
+};
+
+// One tile: rows [row0, row_end) of C (of the group's matrix in wgrad; at most
+// a tile of them) from column n0 on, summed over k_blocks k-blocks; in wgrad
+// those are the k_rows rows of A and B from k0 on. group = experts: rows of C
+// outside every group, nothing to sum.
+struct GroupTile {
+    int group, row0, row_end, n0, k0, k_rows, k_blocks;
+};
+
+// Calls f(tile) for the tiles (TM x TN, k-blocks of TK) of worker `index` of
+// `count`, groups in order, columns before rows, round robin. Every thread of
+// a worker walks the same sequence.
+template <bool WGRAD, int TM, int TN, int TK, class F>
+__device__ __forceinline__ void for_each_group_tile(const GroupTiles &a, volatile int *abort_flag, int index, int count,
+                                                    F &&f) {
+    if (WGRAD) {
+        const int per = a.tiles_m * a.tiles_n;
+        const int64_t total = static_cast<int64_t>(per) * a.experts;
+        for (int64_t u = index; u < total; u += count) {
+            if (*abort_flag) return;
+            const int e = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<int64_t>(e) * per);
+            const int begin = group_start(a.offsets, e, a.rows);
+            const int end = max(begin, group_start(a.offsets, e + 1, a.rows));
+            f(GroupTile{e, r / a.tiles_n * TM, static_cast<int>(a.M), r % a.tiles_n * TN, begin, end - begin,
+                        (end - begin + TK - 1) / TK});
+        }
+    } else {
+        const int k_blocks = static_cast<int>((a.K + TK - 1) / TK);
+        int e = 0, begin = 0, base = 0;
+        int next = group_start(a.offsets, 1, a.rows);
+        int end = max(begin, next);
+        int tiles = (end - begin + TM - 1) / TM;
+        for (int64_t u = index;; u += count) {
+            if (*abort_flag) return;
+            const int rt = static_cast<int>(u / a.tiles_n);
+            while (rt >= base + tiles) {
+                if (e == a.experts) return;
+                base += tiles;
+                ++e;
+                begin = next;
+                next = e < a.experts ? group_start(a.offsets, e + 1, a.rows) : a.rows;
+                end = max(begin, next);
+                tiles = (end - begin + TM - 1) / TM;
+            }
+            f(GroupTile{e, begin + (rt - base) * TM, end, static_cast<int>(u % a.tiles_n) * TN, 0, 0,
+                        e < a.experts ? k_blocks : 0});
+        }
+    }
+}
+
 }  // namespace ex
 }  // namespace sgemm

@@ -140,6 +140,7 @@ int simple_launch(const GroupedProblem &p, cudaStream_t stream, int *launches) {
 }  // namespace
 
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (grouped_f32_supports(p)) return grouped_f32_launch(p, dev, stream, launches);
     if (grouped16_supports(p)) return grouped16_launch(p, dev, stream, launches);
     return simple_launch(p, stream, launches);
 }

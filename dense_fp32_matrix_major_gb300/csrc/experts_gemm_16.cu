@@ -75,12 +75,10 @@ static_assert(STAGE % 1024 == 0 && C0 % 1024 == 0, "1024-byte aligned swizzled b
 }  // namespace g16
 
 struct Args16 {
-    int rows, experts;
-    int64_t M, N, K;  // M: wgrad only
-    const int32_t *offsets;
+    GroupTiles tiles;
+    int64_t N;
     void *C;
     int64_t ldc, strideC;
-    int tiles_m, tiles_n;  // tiles_m: wgrad only
     int c_tma;
     int bf16;
     uint32_t idesc;
@@ -90,48 +88,9 @@ struct Args16 {
 
 enum Form { ROWS_N, ROWS_T, WGRAD };
 
-// One tile: rows [row0, row_end) of C (of matrix `item` in wgrad) from column
-// n0 on, summed over k_blocks k-blocks that start at row k0 (wgrad).
-struct Unit {
-    int group, row0, row_end, n0, k0, k_rows, k_blocks;
-};
-
-// Calls f(unit) for the tiles of worker `index` of `count`, in order.
 template <Form FORM, class F>
 __device__ __forceinline__ void for_each_tile(const Args16 &a, volatile int *abort_flag, int index, int count, F &&f) {
-    if (FORM == WGRAD) {
-        const int per = a.tiles_m * a.tiles_n;
-        const int64_t total = static_cast<int64_t>(per) * a.experts;
-        for (int64_t u = index; u < total; u += count) {
-            if (*abort_flag) return;
-            const int e = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<int64_t>(e) * per);
-            const int begin = group_start(a.offsets, e, a.rows);
-            const int end = max(begin, group_start(a.offsets, e + 1, a.rows));
-            f(Unit{e, r / a.tiles_n * g16::PM, static_cast<int>(a.M), r % a.tiles_n * g16::PN, begin, end - begin,
-                   (end - begin + g16::KB - 1) / g16::KB});
-        }
-    } else {
-        const int k_blocks = static_cast<int>((a.K + g16::KB - 1) / g16::KB);
-        int e = 0, begin = 0, base = 0;
-        int next = a.experts > 0 ? group_start(a.offsets, 1, a.rows) : a.rows;
-        int end = max(begin, next);
-        int tiles = (end - begin + g16::PM - 1) / g16::PM;
-        for (int64_t u = index;; u += count) {
-            if (*abort_flag) return;
-            const int rt = static_cast<int>(u / a.tiles_n);
-            while (rt >= base + tiles) {
-                if (e == a.experts) return;
-                base += tiles;
-                ++e;
-                begin = next;
-                next = e < a.experts ? group_start(a.offsets, e + 1, a.rows) : a.rows;
-                end = max(begin, next);
-                tiles = (end - begin + g16::PM - 1) / g16::PM;
-            }
-            f(Unit{e, begin + (rt - base) * g16::PM, end, static_cast<int>(u % a.tiles_n) * g16::PN, 0, 0,
-                   e < a.experts ? k_blocks : 0});
-        }
-    }
+    for_each_group_tile<FORM == WGRAD, g16::PM, g16::PN, g16::KB>(a.tiles, abort_flag, index, count, f);
 }
 
 // TMA load into this CTA's shared memory that completes its bytes on the
@@ -232,7 +191,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
                 const int m0 = u.row0 + g16::HM * static_cast<int>(rank), n0 = u.n0 + g16::HN * static_cast<int>(rank);
                 for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                     const int s = static_cast<int>(it % g16::STAGES);
@@ -276,7 +235,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
             const bool leader = elect_one();
             uint32_t it = 0, units = 0;
             bool ok = true;
-            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
                 if (u.k_blocks == 0 || !ok) return;
                 const uint32_t d = units & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::ACC_EMPTY + d), ((units >> 1) & 1) ^ 1, a,
@@ -324,7 +283,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
         if (FORM == WGRAD) {
             uint32_t it = 0, uses = 0;  // bit s: parity of the tails staged in stage s so far
             bool ok = true;
-            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+            for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
                 if (!ok || u.k_blocks == 0) return;
                 const int left = u.k_rows % g16::KB;
                 it += static_cast<uint32_t>(u.k_blocks);
@@ -359,7 +318,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
         const uint32_t stage0 = base + g16::C0 + static_cast<uint32_t>((warp - 2) * 2 * g16::CHUNK);
         uint32_t units = 0, chunks = 0;
         bool ok = true;
-        for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Unit &u) {
+        for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
             if (!ok) return;
             const bool summed = u.k_blocks > 0;
             const uint32_t d = units & 1;
@@ -524,20 +483,20 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     if (!c_tma) mapC = mapA;  // not read by the kernel
 
     Args16 a{};
-    a.rows = static_cast<int>(p.rows);
-    a.experts = static_cast<int>(p.experts);
-    a.M = p.M;
     a.N = p.N;
-    a.K = p.K;
-    a.offsets = p.offsets;
     a.C = p.C;
     a.ldc = p.ldc;
     a.strideC = p.strideC;
     const int64_t tiles_n = (p.N + g16::PN - 1) / g16::PN;
     const int64_t tiles_m = FORM == WGRAD ? (p.M + g16::PM - 1) / g16::PM : 1;
     if (tiles_n * tiles_m > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
-    a.tiles_n = static_cast<int>(tiles_n);
-    a.tiles_m = static_cast<int>(tiles_m);
+    a.tiles = GroupTiles{p.offsets,
+                         static_cast<int>(p.rows),
+                         static_cast<int>(p.experts),
+                         p.wgrad ? p.M : 0,
+                         p.K,
+                         static_cast<int>(tiles_m),
+                         static_cast<int>(tiles_n)};
     a.c_tma = c_tma ? 1 : 0;
     a.bf16 = p.type == SGEMM_TYPE_BF16 ? 1 : 0;
     // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B

@@ -1,0 +1,180 @@
+// Products per expert in fp32: launcher of the tensor-core SGEMM kernel on SM
+// pairs (tf32x3_pair.cuh) over row groups. Accuracy and the treatment of
+// infinities and NaN are that kernel's.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "experts_internal.h"
+#include "tf32x3_pair.cuh"
+
+namespace sgemm {
+namespace ex {
+namespace {
+
+constexpr int kMaxDevices = 64;
+std::once_flag g_once[kMaxDevices][6];
+cudaError_t g_err[kMaxDevices][6];
+int g_clusters[kMaxDevices][6];
+
+// The library's rule for one product: from here on operands that tensor maps
+// cannot describe are first copied into aligned rows (a pass over memory),
+// below it the kernel loads them itself with 4-byte copies.
+constexpr double COPY_FROM = 1.25 * 1073741824.0;
+
+template <bool VEC_C, bool TA, bool TB, PairUnits UNITS>
+int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
+           int *launches) {
+    auto kernel = tf32x3_pair_kernel<VEC_C, TA, TB, UNITS>;
+    constexpr bool WG = UNITS == GROUP_WGRAD;
+    constexpr int idx = (VEC_C ? 3 : 0) + (WG ? 2 : TB ? 1 : 0);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(pr::THREADS);
+    cfg.dynamicSmemBytes = pr::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    std::call_once(g_once[dev.device][idx], [&] {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pr::SMEM_BYTES);
+        int n = 0;
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t c = cfg;
+            c.gridDim = dim3(2 * (dev.sm_count / 2));
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &c);
+        }
+        g_err[dev.device][idx] = e;
+        g_clusters[dev.device][idx] = n;
+    });
+    const int clusters = g_clusters[dev.device][idx];
+    int *flag = watchdog_flag_device_ptr();
+    if (g_err[dev.device][idx] != cudaSuccess || clusters < 1 || !flag) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    alignas(64) CUtensorMap mapA{}, mapB{}, mapC{};
+    if (!cpa) {
+        const bool ok =
+            WG ? encode_map(&mapA, q.A, p.rows, p.M, q.lda, 1, 0, 32, 32, sw) &&
+                     encode_map(&mapB, q.B, p.rows, p.N, q.ldb, 1, 0, pr::HN, BK, plain)
+               : encode_map(&mapA, q.A, p.rows, p.K, q.lda, 1, 0, BK, pr::HM, sw) &&
+                     (TB ? encode_map(&mapB, q.B, p.N, p.K, q.ldb, p.experts, q.strideB, BK, pr::HN, sw)
+                         : encode_map(&mapB, q.B, p.K, p.N, q.ldb, p.experts, q.strideB, pr::HN, BK, plain));
+        if (!ok) return SGEMM_ERR_LAUNCH;
+    }
+    const int64_t c_rows = WG ? p.M : p.rows, c_items = WG ? p.experts : 1, c_stride = c_items > 1 ? p.strideC : 0;
+    const bool c_tma = VEC_C && tma_operand_ok(q.C, p.ldc, c_stride, c_rows, c_items) &&
+                       encode_map(&mapC, q.C, c_rows, p.N, p.ldc, c_items, c_stride, 32, 32, sw);
+    if (!c_tma) mapC = mapA;  // not read by the kernel
+
+    const int64_t tiles_n = (p.N + pr::PN - 1) / pr::PN, tiles_m = WG ? (p.M + pr::PM - 1) / pr::PM : 1;
+    if (tiles_m * tiles_n > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+    Args a{};
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.A = q.A;
+    a.lda = q.lda;
+    a.B = q.B;
+    a.ldb = q.ldb;
+    a.strideB = q.strideB;
+    a.C = q.C;
+    a.ldc = p.ldc;
+    a.strideC = c_stride;
+    a.cpa = cpa ? 1 : 0;
+    a.ta = TA ? 1 : 0;
+    a.tb = TB ? 1 : 0;
+    a.c_tma = c_tma ? 1 : 0;
+    a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
+    a.watchdog = flag;
+    const GroupTiles gt{p.offsets,
+                        static_cast<int>(p.rows),
+                        static_cast<int>(p.experts),
+                        WG ? p.M : 0,
+                        p.K,
+                        static_cast<int>(tiles_m),
+                        static_cast<int>(tiles_n)};
+    // Every group may end in a part of a tile, and so may the rest.
+    const int64_t units =
+        WG ? tiles_m * tiles_n * p.experts : ((p.rows + pr::PM - 1) / pr::PM + p.experts) * tiles_n;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
+    if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a, gt) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    ++*launches;
+    return SGEMM_OK;
+}
+
+template <bool VEC_C>
+int launch_form(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
+                int *launches) {
+    if (p.wgrad) return launch<VEC_C, true, false, GROUP_WGRAD>(p, q, cpa, dev, stream, launches);
+    return p.transB == SGEMM_OP_T ? launch<VEC_C, false, true, GROUP_ROWS>(p, q, cpa, dev, stream, launches)
+                                  : launch<VEC_C, false, false, GROUP_ROWS>(p, q, cpa, dev, stream, launches);
+}
+
+}  // namespace
+
+// Sizes that fit tensor map coordinates, and a sum to make.
+bool grouped_f32_supports(const GroupedProblem &p) {
+    const int64_t lim = INT32_MAX / 2;
+    return p.type == SGEMM_TYPE_F32 && p.rows > 0 && p.rows < lim && p.M < lim && p.N < lim && p.K < lim &&
+           (p.wgrad || p.K > 0);
+}
+
+int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
+    // The operands as the library's single product describes them: A stored
+    // rows x M and B rows x N, summed along the rows, or A rows x K and one B
+    // per group.
+    Problem q{};
+    q.M = p.M;
+    q.N = p.N;
+    q.K = p.K;
+    q.A = static_cast<const float *>(p.A);
+    q.lda = p.lda;
+    q.B = static_cast<const float *>(p.B);
+    q.ldb = p.ldb;
+    q.C = static_cast<float *>(p.C);
+    q.ldc = p.ldc;
+    q.transA = p.wgrad ? SGEMM_OP_T : SGEMM_OP_N;
+    q.transB = p.wgrad ? SGEMM_OP_N : p.transB;
+    q.batch = p.wgrad ? 1 : p.experts;
+    q.strideB = q.batch > 1 ? p.strideB : 0;
+    const int64_t b_rows = q.transB == SGEMM_OP_T ? q.N : q.K;
+    bool cpa = !tma_operand_ok(q.A, q.lda, 0, p.rows, 1) || !tma_operand_ok(q.B, q.ldb, q.strideB, b_rows, q.batch);
+    float *scratch = nullptr;
+    if (cpa && static_cast<double>(p.rows) * static_cast<double>(p.wgrad ? p.M : p.K) * static_cast<double>(p.N) >=
+                   COPY_FROM) {
+        const size_t bytes = repack_bytes(q);
+        scratch = scratch_alloc(dev, bytes, stream);
+        if (scratch) {
+            Problem copied;
+            const int rc = repack_into(q, dev, scratch, bytes, stream, &copied, launches);
+            if (rc != SGEMM_OK) {
+                scratch_free(scratch, stream);
+                return rc;
+            }
+            q = copied;
+            cpa = false;
+        }
+    }
+    const bool vec_c = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0 &&
+                       (!p.wgrad || p.experts == 1 || p.strideC % 4 == 0);
+    const int rc = vec_c ? launch_form<true>(p, q, cpa, dev, stream, launches)
+                         : launch_form<false>(p, q, cpa, dev, stream, launches);
+    scratch_free(scratch, stream);
+    return rc;
+}
+
+}  // namespace ex
+}  // namespace sgemm

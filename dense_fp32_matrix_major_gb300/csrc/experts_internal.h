@@ -51,6 +51,9 @@ struct GroupedProblem {
     int64_t ldc, strideC;
 };
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
+// fp32 on SM pairs (experts_gemm_f32.cu).
+bool grouped_f32_supports(const GroupedProblem &p);
+int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 // bf16 and fp16 on SM pairs (experts_gemm_16.cu).
 bool grouped16_supports(const GroupedProblem &p);
 int grouped16_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);

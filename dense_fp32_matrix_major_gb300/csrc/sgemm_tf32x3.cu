@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1) tf32x3_kernel(const Args a) {
                                 st_shared_v4(cs + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2],
                                              v[4 * j + 3]);
                             __syncwarp();
-                            store_staged_rows(a, cs, a.C + at.item * a.strideC, m0 + q * 32, n0 + ch * 32, atomic);
+                            store_staged_rows(a, cs, a.C + at.item * a.strideC, a.M, m0 + q * 32, n0 + ch * 32, atomic);
                             __syncwarp();  // the chunk is read before the next one is written
                         }
                     } else {

@@ -667,15 +667,15 @@ __device__ __forceinline__ void store_chunk_regs(const Args &a, float *crow, int
 // step with the lanes along the row, so that each warp store covers 128
 // contiguous bytes whatever C's alignment: C = act(alpha * v + beta * C +
 // bias) for a whole tile, C += alpha * v with atomics for a tile split along
-// K. Rows from M and columns from N on are skipped. Called by all 32 lanes
+// K. Rows from m_end and columns from N on are skipped. Called by all 32 lanes
 // after the chunk is complete in shared memory (__syncwarp).
-__device__ __forceinline__ void store_staged_rows(const Args &a, uint32_t rc, float *citem, int64_t row0,
-                                                  int64_t col0, bool atomic) {
+__device__ __forceinline__ void store_staged_rows(const Args &a, uint32_t rc, float *citem, int64_t m_end,
+                                                  int64_t row0, int64_t col0, bool atomic) {
     const int lane = static_cast<int>(threadIdx.x & 31);
     // Parameters in registers: the shared-memory loads below are ordered
     // against all memory, so fields read through `a` would be reloaded on
     // every row.
-    const int64_t M = a.M, ldc = a.ldc, col = col0 + lane;
+    const int64_t M = m_end, ldc = a.ldc, col = col0 + lane;
     const bool col_ok = col < a.N;
     const bool fused = a.ep && !atomic;
     const int bias_kind = fused ? a.bias_kind : SGEMM_BIAS_NONE, act = a.act;
