@@ -251,32 +251,37 @@ __global__ void __launch_bounds__(ROW_THREADS) gather_kernel(const RowArgs a, co
 // Choices whose rows a thread has in flight at once.
 constexpr int CHOICES = 8;
 
-template <class T, int N, bool WEIGHTED>
+// FITS: top_k is at most CH, and a thread reads its token's slots once.
+template <class T, int N, bool WEIGHTED, int CH, bool FITS>
 __global__ void __launch_bounds__(ROW_THREADS) combine_kernel(const RowArgs a, const T *h, int64_t ldh,
                                                               const float *weights, T *y, int64_t ldy) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.tokens) return;
     const int end = kept_end(a);
+    int s[CH];  // -1: dropped
+    float w[CH];
+    auto choices = [&](int j0) {  // all slots, then all rows: two waits for memory, not two a choice
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int at = min(j0 + j, a.top_k - 1);
+            s[j] = __ldg(a.slot + t * a.top_k + at);
+            w[j] = WEIGHTED ? __ldg(weights + t * a.top_k + at) : 1.0f;
+            if (j0 + j >= a.top_k || s[j] >= end) s[j] = -1;
+        }
+    };
+    if (FITS) choices(0);
     for (int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c < a.vecs;
          c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
         float sum[N] = {};
-        for (int j0 = 0; j0 < a.top_k; j0 += CHOICES) {
-            Pack<T, N> rows[CHOICES];
-            float w[CHOICES];
-            bool kept[CHOICES];
+        for (int j0 = 0; j0 < (FITS ? 1 : a.top_k); j0 += CH) {
+            if (!FITS) choices(j0);
+            Pack<T, N> rows[CH];
 #pragma unroll
-            for (int j = 0; j < CHOICES; ++j) {
-                kept[j] = false;
-                if (j0 + j >= a.top_k) continue;
-                const int s = __ldg(a.slot + t * a.top_k + j0 + j);
-                kept[j] = s >= 0 && s < end;
-                if (!kept[j]) continue;
-                if (WEIGHTED) w[j] = __ldg(weights + t * a.top_k + j0 + j);
-                rows[j] = load_pack<T, N>(h + s * ldh + c * N);
-            }
+            for (int j = 0; j < CH; ++j)
+                if (s[j] >= 0) rows[j] = load_pack<T, N>(h + s[j] * ldh + c * N);
 #pragma unroll
-            for (int j = 0; j < CHOICES; ++j) {
-                if (!kept[j]) continue;
+            for (int j = 0; j < CH; ++j) {
+                if (s[j] < 0) continue;
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     sum[i] = WEIGHTED ? fmaf(w[j], to_f32(rows[j].v[i]), sum[i]) : sum[i] + to_f32(rows[j].v[i]);
@@ -289,8 +294,34 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_kernel(const RowArgs a, c
     }
 }
 
+// Sums CHOICES = 8 values over the lanes of a warp: at each of three steps a
+// lane keeps half of its values and adds the partner's, so 9 exchanges in
+// place of 40. Lane l ends with the value whose number has the lane's bits 16, 8
+// and 4 as 4, 2 and 1.
+__device__ __forceinline__ float warp_sum8(const float (&v)[CHOICES]) {
+    const int lane = threadIdx.x & 31;
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        const float keep = up ? v[i + 4] : v[i], give = up ? v[i] : v[i + 4];
+        a[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        const float keep = up ? a[i + 2] : a[i], give = up ? a[i] : a[i + 2];
+        b[i] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+    }
+    const bool up = lane & 4;
+    float s = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+
 // blockDim.x (a multiple of 32) threads share a token and go over its whole
-// row, so the dot products end in the block.
+// row, so the dot products end in the block: in the warp when it has the
+// token to itself.
 template <class T, int N>
 __global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs a, const T *dy, int64_t lddy,
                                                                    const T *h, int64_t ldh, const float *weights,
@@ -340,19 +371,18 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < CHOICES; ++j) {
-            if (j0 + j >= a.top_k) break;
-            float d = dot[j];
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (lane == 0) part[warp][j] = d;
+        const float d = warp_sum8(dot);
+        const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+        if (warps == 1) {
+            if (in && (lane & 3) == 0 && j0 + j < a.top_k) dweights[t * a.top_k + j0 + j] = d;
+            continue;
         }
+        if ((lane & 3) == 0) part[warp][j] = d;
         __syncthreads();
         if (in && threadIdx.x < CHOICES && j0 + static_cast<int>(threadIdx.x) < a.top_k) {
-            float d = 0.0f;
-            for (int i = 0; i < warps; ++i) d += part[threadIdx.y * warps + i][threadIdx.x];
-            dweights[t * a.top_k + j0 + threadIdx.x] = d;
+            float sum = 0.0f;
+            for (int i = 0; i < warps; ++i) sum += part[threadIdx.y * warps + i][threadIdx.x];
+            dweights[t * a.top_k + j0 + threadIdx.x] = sum;
         }
         __syncthreads();
     }
@@ -374,6 +404,12 @@ dim3 row_block(int64_t vecs) {
     unsigned tx = 32;
     while (tx < ROW_THREADS && tx < vecs) tx *= 2;
     return dim3(tx, ROW_THREADS / tx);
+}
+
+// A warp per token where that fills the GPU: slots are read once a token, dot
+// products end in the warp, and its loads of several rows at once keep it busy.
+dim3 token_block(const Route &r, int64_t vecs, const DeviceInfo &dev) {
+    return r.tokens >= 16 * dev.sm_count ? dim3(32, ROW_THREADS / 32) : row_block(vecs);
 }
 
 // One block per blockDim.y tokens and up to 64 pieces of a row.
@@ -442,29 +478,33 @@ int sort_typed(const Id *ids, int64_t pairs, int experts, int32_t *offsets, int3
     return SGEMM_OK;
 }
 
-template <class T, int N>
+template <class T, int N, bool WEIGHTED>
 int combine_typed(const Route &r, const void *h, int64_t ldh, const float *weights, void *y, int64_t ldy,
-                  cudaStream_t stream, int *launches) {
+                  const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     const int64_t vecs = r.width / N;
-    const dim3 block = row_block(vecs);
+    const dim3 block = token_block(r, vecs, dev);
     dim3 grid;
-    if (!row_grid(r, vecs, block, true, &grid)) return SGEMM_ERR_UNSUPPORTED;
+    if (!row_grid(r, vecs, block, block.x > 32, &grid)) return SGEMM_ERR_UNSUPPORTED;
     const RowArgs a = row_args(r, vecs);
-    if (weights)
-        combine_kernel<T, N, true><<<grid, block, 0, stream>>>(a, static_cast<const T *>(h), ldh, weights,
-                                                               static_cast<T *>(y), ldy);
+    const T *in = static_cast<const T *>(h);
+    T *out = static_cast<T *>(y);
+    if (r.top_k <= 2)
+        combine_kernel<T, N, WEIGHTED, 2, true><<<grid, block, 0, stream>>>(a, in, ldh, weights, out, ldy);
+    else if (r.top_k <= 4)
+        combine_kernel<T, N, WEIGHTED, 4, true><<<grid, block, 0, stream>>>(a, in, ldh, weights, out, ldy);
+    else if (r.top_k <= CHOICES)
+        combine_kernel<T, N, WEIGHTED, CHOICES, true><<<grid, block, 0, stream>>>(a, in, ldh, weights, out, ldy);
     else
-        combine_kernel<T, N, false><<<grid, block, 0, stream>>>(a, static_cast<const T *>(h), ldh, nullptr,
-                                                                static_cast<T *>(y), ldy);
+        combine_kernel<T, N, WEIGHTED, CHOICES, false><<<grid, block, 0, stream>>>(a, in, ldh, weights, out, ldy);
     return launched(launches);
 }
 
 template <class T, int N>
 int combine_grad_typed(const Route &r, const void *dy, int64_t lddy, const void *h, int64_t ldh,
-                       const float *weights, void *dh, int64_t lddh, float *dweights, cudaStream_t stream,
-                       int *launches) {
+                       const float *weights, void *dh, int64_t lddh, float *dweights, const DeviceInfo &dev,
+                       cudaStream_t stream, int *launches) {
     const int64_t vecs = r.width / N;
-    const dim3 block = row_block(vecs);
+    const dim3 block = token_block(r, vecs, dev);
     dim3 grid;
     if (!row_grid(r, vecs, block, false, &grid)) return SGEMM_ERR_UNSUPPORTED;
     combine_grad_kernel<T, N><<<grid, block, 0, stream>>>(row_args(r, vecs), static_cast<const T *>(dy), lddy,
@@ -533,18 +573,21 @@ int gather_launch(int type, const Route &r, const void *x, int64_t ldx, void *xs
 }
 
 int combine_launch(int type, const Route &r, const void *h, int64_t ldh, const float *weights, void *y, int64_t ldy,
-                   const DeviceInfo &, cudaStream_t stream, int *launches) {
+                   const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     return for_type(type, vector_bytes(type_size(type), r.width, h, ldh, y, ldy), [&](auto t, auto n) {
-        return combine_typed<decltype(t), decltype(n)::value>(r, h, ldh, weights, y, ldy, stream, launches);
+        using T = decltype(t);
+        constexpr int N = decltype(n)::value;
+        return weights ? combine_typed<T, N, true>(r, h, ldh, weights, y, ldy, dev, stream, launches)
+                       : combine_typed<T, N, false>(r, h, ldh, weights, y, ldy, dev, stream, launches);
     });
 }
 
 int combine_grad_launch(int type, const Route &r, const void *dy, int64_t lddy, const void *h, int64_t ldh,
-                        const float *weights, void *dh, int64_t lddh, float *dweights, const DeviceInfo &,
+                        const float *weights, void *dh, int64_t lddh, float *dweights, const DeviceInfo &dev,
                         cudaStream_t stream, int *launches) {
     return for_type(type, vector_bytes(type_size(type), r.width, dy, lddy, h, ldh, dh, lddh), [&](auto t, auto n) {
         return combine_grad_typed<decltype(t), decltype(n)::value>(r, dy, lddy, h, ldh, weights, dh, lddh, dweights,
-                                                                   stream, launches);
+                                                                   dev, stream, launches);
     });
 }
 
