@@ -141,7 +141,10 @@ int simple_launch(const GroupedProblem &p, cudaStream_t stream, int *launches) {
 
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     if (grouped_f32_supports(p)) return grouped_f32_launch(p, dev, stream, launches);
-    if (grouped16_supports(p)) return grouped16_launch(p, dev, stream, launches);
+    if (grouped16_supports(p)) {
+        const int rc = grouped16_launch(p, dev, stream, launches);
+        if (rc != SGEMM_ERR_UNSUPPORTED) return rc;  // no memory for copies: nothing was enqueued
+    }
     return simple_launch(p, stream, launches);
 }
 

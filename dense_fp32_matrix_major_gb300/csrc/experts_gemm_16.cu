@@ -519,23 +519,117 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     return SGEMM_OK;
 }
 
+bool a_mappable(const GroupedProblem &p) { return mappable(p.A, p.rows, p.lda, 1, 0); }
+
+int64_t b_rows(const GroupedProblem &p) { return p.wgrad ? p.rows : p.transB == SGEMM_OP_T ? p.N : p.K; }
+int64_t b_cols(const GroupedProblem &p) { return p.wgrad ? p.N : p.transB == SGEMM_OP_T ? p.K : p.N; }
+
+bool b_mappable(const GroupedProblem &p) {
+    return p.wgrad ? mappable(p.B, p.rows, p.ldb, 1, 0) : mappable(p.B, b_rows(p), p.ldb, p.experts, p.strideB);
+}
+
+// Copies of operands whose rows are not 16-byte aligned, in rows of a multiple
+// of 8 values. Lanes along a row; a block takes whole rows in turn.
+struct CopyRows {
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t rows, cols, ld_src, ld_dst, items, stride_src;
+};
+
+__global__ void __launch_bounds__(256) copy_rows_kernel(const CopyRows j) {
+    const int64_t total = j.rows * j.items;
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < total;
+         r += static_cast<int64_t>(gridDim.x) * 8) {
+        const int64_t item = r / j.rows, row = r - item * j.rows;
+        const uint16_t *s = j.src + item * j.stride_src + row * j.ld_src;
+        uint16_t *d = j.dst + r * j.ld_dst;
+        for (int64_t c0 = lane; c0 < j.cols; c0 += 32 * 8) {
+            uint16_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c0 + 32 * i < j.cols ? __ldg(s + c0 + 32 * i) : uint16_t(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i < j.cols) d[c0 + 32 * i] = v[i];
+        }
+    }
+}
+
+// Bytes of the copies that p needs (0: none).
+size_t copy_bytes(const GroupedProblem &p) {
+    int64_t n = 0;
+    if (!a_mappable(p)) n += p.rows * (((p.wgrad ? p.M : p.K) + 7) / 8 * 8);
+    if (!b_mappable(p)) n += b_rows(p) * ((b_cols(p) + 7) / 8 * 8) * (p.wgrad ? 1 : p.experts);
+    return static_cast<size_t>(n) * 2 + 512;
+}
+
+// Enqueues the copies into `scratch` and describes the copied operands in *q.
+int copy_operands(const GroupedProblem &p, uint16_t *scratch, const DeviceInfo &dev, cudaStream_t stream,
+                  GroupedProblem *q, int *launches) {
+    *q = p;
+    uint16_t *next = scratch;
+    auto copy = [&](const CopyRows &j) {
+        const int64_t blocks = (j.rows * j.items + 7) / 8, most = 8LL * dev.sm_count;
+        copy_rows_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream>>>(j);
+        if (cudaGetLastError() != cudaSuccess) return false;
+        ++*launches;
+        return true;
+    };
+    if (!a_mappable(p)) {
+        const int64_t cols = p.wgrad ? p.M : p.K, ld = (cols + 7) / 8 * 8;
+        if (!copy(CopyRows{static_cast<const uint16_t *>(p.A), next, p.rows, cols, p.lda, ld, 1, 0}))
+            return SGEMM_ERR_LAUNCH;
+        q->A = next;
+        q->lda = ld;
+        next += (p.rows * ld + 127) / 128 * 128;
+    }
+    if (!b_mappable(p)) {
+        const int64_t rows = b_rows(p), cols = b_cols(p), ld = (cols + 7) / 8 * 8, items = p.wgrad ? 1 : p.experts;
+        if (!copy(CopyRows{static_cast<const uint16_t *>(p.B), next, rows, cols, p.ldb, ld, items, p.strideB}))
+            return SGEMM_ERR_LAUNCH;
+        q->B = next;
+        q->ldb = ld;
+        q->strideB = rows * ld;
+    }
+    return SGEMM_OK;
+}
+
+int launch_form(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (p.wgrad) return launch16<WGRAD>(p, dev, stream, launches);
+    return p.transB == SGEMM_OP_T ? launch16<ROWS_T>(p, dev, stream, launches)
+                                  : launch16<ROWS_N>(p, dev, stream, launches);
+}
+
 }  // namespace
 
-// Operands that tensor maps can describe: 16-byte aligned bases and rows,
-// sizes that fit their coordinates.
+// Sizes that fit tensor map coordinates, and a sum to make. Operands whose rows
+// are not 16-byte aligned are copied first where that is estimated to take
+// less time than the CUDA-core kernel, which copies nothing: that one makes
+// about 25 TFLOP/s and no k-step of 16 in less than 0.6 us; the copies move
+// about 5 TB/s, and launches and a short product take 20 us.
 bool grouped16_supports(const GroupedProblem &p) {
     const int64_t lim = INT32_MAX / 2;
-    return p.type != SGEMM_TYPE_F32 && p.rows > 0 && (p.wgrad || p.K > 0) && p.rows < lim && p.M < lim && p.N < lim &&
-           p.K < lim && mappable(p.A, p.rows, p.lda, 1, 0) &&
-           (p.wgrad ? mappable(p.B, p.rows, p.ldb, 1, 0)
-                    : mappable(p.B, p.transB == SGEMM_OP_T ? p.N : p.K, p.ldb, p.experts, p.strideB));
+    if (p.type == SGEMM_TYPE_F32 || p.rows <= 0 || (!p.wgrad && p.K <= 0) || p.rows >= lim || p.M >= lim ||
+        p.N >= lim || p.K >= lim)
+        return false;
+    if (a_mappable(p) && b_mappable(p)) return true;
+    const double s = static_cast<double>(p.rows), m = static_cast<double>(p.wgrad ? p.M : p.K),
+                 n = static_cast<double>(p.N);
+    const double depth = p.wgrad ? s / static_cast<double>(p.experts) : m;
+    const double cores = 2.0 * s * m * n / 25e6, steps = depth / 16 * 0.6;
+    return 2.0 * static_cast<double>(copy_bytes(p)) / 5e6 + 20.0 < (cores > steps ? cores : steps);
 }
 
 int grouped16_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
-    if (p.wgrad) return launch16<WGRAD>(p, dev, stream, launches);
-    return p.transB == SGEMM_OP_T ? launch16<ROWS_T>(p, dev, stream, launches)
-                                  : launch16<ROWS_N>(p, dev, stream, launches);
+    if (a_mappable(p) && b_mappable(p)) return launch_form(p, dev, stream, launches);
+    float *scratch = scratch_alloc(dev, copy_bytes(p), stream);
+    if (!scratch) return SGEMM_ERR_UNSUPPORTED;
+    GroupedProblem q;
+    int rc = copy_operands(p, reinterpret_cast<uint16_t *>(scratch), dev, stream, &q, launches);
+    if (rc == SGEMM_OK) rc = launch_form(q, dev, stream, launches);
+    scratch_free(scratch, stream);
+    return rc;
 }
 
 }  // namespace ex

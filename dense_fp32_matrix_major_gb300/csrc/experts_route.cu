@@ -35,9 +35,9 @@ constexpr int SORT_MAX_WARPS = SORT_THREADS / 32;
 // Counters of one block: one row of experts + 1 per counting warp.
 constexpr int SORT_SMEM_INTS = 48 * 1024;
 // Pairs that one block sorts alone.
-constexpr int64_t SORT_SINGLE = 8192;
+constexpr int64_t SORT_SINGLE = 2048;
 // Pairs per block and table entries of the two-kernel form.
-constexpr int64_t SORT_PER_BLOCK = 2048;
+constexpr int64_t SORT_PER_BLOCK = 1024;
 constexpr int64_t SORT_TABLE = 64 * 1024;
 constexpr int64_t SORT_BLOCKS = 152;  // one per SM of a GB300
 
@@ -104,6 +104,26 @@ __device__ __forceinline__ void block_exclusive_sum(int32_t *x, int n, int32_t *
     }
 }
 
+// Calls f(key, p) for the pairs [w0, w1) of a warp in steps of 32, all lanes
+// together (key -1 past the end). Up to HELD steps' keys are loaded at once,
+// before the first is used.
+constexpr int HELD = 8;
+template <class Id, class F>
+__device__ __forceinline__ void for_keys(const Id *ids, int64_t w0, int64_t w1, int experts, F &&f) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t p0 = w0; p0 < w1; p0 += 32 * HELD) {
+        int key[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int64_t p = p0 + 32 * i + lane;
+            key[i] = p < w1 ? key_of(ids, p, experts) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (p0 + 32 * i < w1) f(key[i], p0 + 32 * i + lane);
+    }
+}
+
 // Slots of this block's pairs. gridDim.x == 1: the whole sort; otherwise the
 // table of sort_count_kernel gives the pairs of each key in every block.
 // Shared memory: `warps` rows of experts + 1 counters, one row of group
@@ -127,13 +147,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_rank_kernel(const Id *ids, 
     const int64_t w0 = min(begin + per * warp, end), w1 = min(w0 + per, end);
     int32_t *mine = smem + warp * keys;
     if (warp < warps) {
-        for (int64_t p0 = w0; p0 < w1; p0 += 32) {
-            const bool in = p0 + lane < w1;
-            const int key = in ? key_of(ids, p0 + lane, experts) : -1;
+        for_keys(ids, w0, w1, experts, [&](int key, int64_t) {
             const unsigned same = __match_any_sync(0xffffffffu, key);
-            if (in && lane == __ffs(same) - 1) mine[key] += __popc(same);
+            if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
             __syncwarp();
-        }
+        });
     }
     __syncthreads();
     // Per key: counts before each warp in the block, and the total over all
@@ -188,25 +206,22 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_rank_kernel(const Id *ids, 
     if (block == 0)
         for (int e = threadIdx.x; e < keys; e += SORT_THREADS) offsets[e] = start[e];
     if (warp < warps) {
-        for (int64_t p0 = w0; p0 < w1; p0 += 32) {
-            const int64_t p = p0 + lane;
-            const bool in = p < w1;
-            const int key = in ? key_of(ids, p, experts) : -1;
+        for_keys(ids, w0, w1, experts, [&](int key, int64_t p) {
             const unsigned same = __match_any_sync(0xffffffffu, key);
             const int leader = __ffs(same) - 1;
             int base = 0;
-            if (in && lane == leader) {
+            if (key >= 0 && lane == leader) {
                 base = start[key] + mine[key];
                 mine[key] += __popc(same);
             }
             base = __shfl_sync(0xffffffffu, base, leader);
-            if (in) {
+            if (key >= 0) {
                 const int s = base + __popc(same & ((1u << lane) - 1u));
                 slot[p] = s;
                 order[s] = static_cast<int32_t>(p);
             }
             __syncwarp();
-        }
+        });
     }
 }
 

@@ -29,34 +29,54 @@
 // NaN in 16-bit x would turn the subtraction into NaN; rows of x that hold
 // one are recomputed with scalar arithmetic.
 //
-// Work. A block takes 16 * row_tiles rows of q; its 8 warps are row_tiles
-// tiles times 8 / row_tiles interleaved shares of k, joined in shared memory.
-// A warp's step is 16 rows x 128 k; the q of its next two steps are on their
-// way before x is staged and while a step is multiplied.
+// Work. One block per SM goes through units of R = 16 .. 128 rows of q times
+// all of k. A producer warp streams q into a ring in shared memory by TMA
+// (stages of 32 KB, boxes of 128 bytes x R rows in the 128-byte swizzle, some
+// 100 KB on their way per SM); 16 warps each take two steps of a stage, 16 rows
+// x 128 k each, side by side, and add up their shares of k at the end of a unit. x is laid out
+// either by every block for itself, once, and stays in shared memory, or,
+// where it is too large for that, by a small kernel before this one, and is
+// streamed with q. The swizzle lets a quad's lanes read 64 contiguous bytes of
+// a row without bank conflicts if the rows of a quarter warp are four (groups
+// of 128) or two apart, so row g of a matrix instruction is row_of(g) of a tile.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "experts_common.cuh"
 #include "experts_internal.h"
+#include "tc_common.cuh"
 
 namespace sgemm {
 namespace ex {
 namespace {
 
-constexpr int W4_THREADS = 256;
-constexpr int W4_WARPS = W4_THREADS / 32;
-constexpr int W4_ROWS = 8;    // rows of x that share a pass
-constexpr int STEP = 128;     // values of k per warp step
-constexpr int AHEAD = 2;      // steps whose weights are on their way
-constexpr int TURN = 4;       // steps between fetches of scales (width 128)
+constexpr int CONSUMERS = 16;                      // warps
+constexpr int W4_THREADS = 32 * (CONSUMERS + 1);   // and the producer
+constexpr int W4_ROWS = 8;         // rows of x that share a pass
+constexpr int STEP = 128;          // values of k per warp step
+constexpr int PAIR = 2;            // steps of a warp in a stage
+constexpr int TURN = 2;            // stages between fetches of scales
+constexpr int Q_STAGE = 32 * 1024;
+constexpr int MAX_STAGES = 6;
+constexpr int SMEM_BYTES = 224 * 1024;      // of a block, at most
+constexpr int RESIDENT_ONE = 144 * 1024;    // x in shared memory: one row, eight rows
+constexpr int RESIDENT_EIGHT = 96 * 1024;
+constexpr int X_STAGE = 64 * 1024;          // x of a stage, at most, when it is streamed
+constexpr int PASSES = 256;                 // of one launch when x is streamed
 
 struct W4Args {
     int rows, experts;
     int64_t N, K;
     int groups;       // per row of q
     int group_shift;  // log2 of the group
-    int row_tiles;    // 16-row tiles per block: 1, 2, 4 or 8
-    int chunk_steps;  // steps of x staged at once, a multiple of the shares
+    int unit_rows;    // R
+    int units;        // ceil(N / R)
+    int stages;       // of the ring
+    int first_pass;
     int x_vector;     // rows of x in 16-byte pieces
     const int32_t *ids;
     const void *x;
@@ -67,6 +87,9 @@ struct W4Args {
     const uint8_t *zeros;
     void *y;
     int64_t ldy;
+    const uint8_t *prepared;  // streamed x
+    uint64_t timeout_ns;
+    int *watchdog;
 };
 
 // How a row type enters the matrix instruction: terms of x, the bits that q is
@@ -82,19 +105,19 @@ struct Operand<__nv_bfloat16> {
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0x43004300u;  // 128, 128 in bf16
     static constexpr float BASE = 128.0f, UNIT = 1.0f;
-    static constexpr int BLOCKS = 4;           // per SM
-    static constexpr int X_BYTES = 48 * 1024;  // shared memory for x
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&d);
     }
+    static __device__ __forceinline__ uint32_t twice(float) { return 0; }
     static __device__ __forceinline__ void split(__nv_bfloat16 x, uint16_t (&t)[1]) { t[0] = __bfloat16_as_ushort(x); }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    // d = a b + c
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                               float c1, float c2, float c3) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     }
 };
 
@@ -104,16 +127,15 @@ struct Operand<__half> {
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0;
     static constexpr float BASE = 0.0f, UNIT = 16777216.0f;  // an operand's q is q 2^-24
-    static constexpr int BLOCKS = 4;
-    static constexpr int X_BYTES = 48 * 1024;
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t) { return a; }
+    static __device__ __forceinline__ uint32_t twice(float) { return 0; }
     static __device__ __forceinline__ void split(__half x, uint16_t (&t)[1]) { t[0] = __half_as_ushort(x); }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                               float c1, float c2, float c3) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     }
 };
 
@@ -123,10 +145,13 @@ struct Operand<float> {
     static constexpr bool EXACT = true;
     static constexpr uint32_t ONE = Operand<__nv_bfloat16>::ONE;
     static constexpr float BASE = 0.0f, UNIT = 1.0f;
-    static constexpr int BLOCKS = 3;
-    static constexpr int X_BYTES = 72 * 1024;
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         return Operand<__nv_bfloat16>::minus(a, b);
+    }
+    // x twice in bf16 (a whole number below 256, so exact).
+    static __device__ __forceinline__ uint32_t twice(float x) {
+        const uint32_t b = __float_as_uint(x);
+        return __byte_perm(b, b, 0x3232);
     }
     // The top 16 bits of x are a bf16 (truncated, so it cannot overflow); what
     // is left is exact in fp32 and is cut the same way. Infinities and NaN go
@@ -145,54 +170,39 @@ struct Operand<float> {
         x -= __uint_as_float(bits & 0xFFFF0000u);
         t[2] = static_cast<uint16_t>(__float_as_uint(x) >> 16);
     }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        Operand<__nv_bfloat16>::mma(c, a, b0, b1);
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                               float c1, float c2, float c3) {
+        Operand<__nv_bfloat16>::mma(d, a, b0, b1, c0, c1, c2, c3);
     }
 };
 
-__device__ __forceinline__ float scale_at(const W4Args &a, int64_t i) {
-    if (a.scale_type == SGEMM_TYPE_F32) return __ldg(static_cast<const float *>(a.scales) + i);
-    const uint16_t h = __ldg(static_cast<const uint16_t *>(a.scales) + i);
-    return a.scale_type == SGEMM_TYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(h) << 16)
-                                           : __half2float(__ushort_as_half(h));
+// Scale i as it is stored, and its value. Apart, so that a scale that is
+// fetched ahead is not waited for before it is used.
+__device__ __forceinline__ uint32_t scale_bits(const W4Args &a, int64_t i) {
+    return a.scale_type == SGEMM_TYPE_F32 ? __ldg(static_cast<const uint32_t *>(a.scales) + i)
+                                          : __ldg(static_cast<const uint16_t *>(a.scales) + i);
 }
 
-// How the k of a step lie in a lane's four words, by the width of the groups.
-//   128: words 0 .. 3 are k = 32 t + 8 u: 16 bytes a lane, one group (or half
-//        of one) a step.
-//   64:  words 2 h, 2 h + 1 are k = 64 h + 16 t + 8 (u & 1): 8 bytes a lane
-//        for each 64 k, one group.
-//   32:  as 64, then lanes t and t ^ 2 exchange a word, so that word 2 h + b of
-//        all four lanes is the b-th 32 k of that half.
+__device__ __forceinline__ float scale_value(const W4Args &a, uint32_t bits) {
+    if (a.scale_type == SGEMM_TYPE_F16) return __half2float(__ushort_as_half(static_cast<uint16_t>(bits)));
+    return __uint_as_float(a.scale_type == SGEMM_TYPE_F32 ? bits : bits << 16);
+}
+
+__device__ __forceinline__ float scale_at(const W4Args &a, int64_t i) { return scale_value(a, scale_bits(a, i)); }
+
+// How the k of a step lie in a lane's four words, by the width of the groups
+// (lane t of a quad, word u, 8 k each):
+//   128: k = 32 t + 8 u: 16 bytes a lane, one group (or half of one) a step.
+//   64:  k = 64 (u / 2) + 16 t + 8 (u % 2): 8 bytes a lane for each 64 k, one
+//        group.
+//   32:  as 64, then lanes t and t ^ 2 exchange a word, so that word u of all
+//        four lanes is the u-th 32 k: k = 32 u + 16 (t % 2) + 8 (t / 2).
+
+// Row of a 16-row tile (of its first or second eight) that is row g of the
+// matrix instruction.
 template <int WIDTH>
-__device__ __forceinline__ int k_of(int u, int t) {
-    if (WIDTH == 128) return 32 * t + 8 * u;
-    if (WIDTH == 64) return 64 * (u >> 1) + 16 * t + 8 * (u & 1);
-    return 32 * u + 16 * (t & 1) + 8 * (t >> 1);
-}
-
-// BYTES bytes of a row of q at k (aligned: BYTES / 2 divides k and the row).
-template <int BYTES, bool ALIGNED>
-__device__ __forceinline__ void load_q(const uint8_t *row, int k, int K, uint32_t *w) {
-    if constexpr (ALIGNED && BYTES == 16) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(row + k / 2));
-    } else if constexpr (ALIGNED) {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(w[0]), "=r"(w[1])
-                     : "l"(row + k / 2));
-    } else {
-#pragma unroll
-        for (int i = 0; i < BYTES / 4; ++i) {
-            w[i] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int kk = k + 8 * i + 2 * b;
-                if (kk < K) w[i] |= static_cast<uint32_t>(__ldg(row + kk / 2)) << (8 * b);
-            }
-        }
-    }
+__device__ __forceinline__ int row_of(int g) {
+    return WIDTH == 128 ? (g >> 1) | ((g & 1) << 2) : ((2 * g) & 7) | (g >> 2);
 }
 
 // One step of a lane: 32 values of k of rows g and g + 8.
@@ -200,13 +210,21 @@ struct Weights {
     uint32_t lo[4], hi[4];
 };
 
-// Scales and zero points of rows g (low half of z) and g + 8 that a lane
-// fetched: for width 128 those of step t of four, otherwise those of the t-th
-// 32 values of one step.
-struct Scales {
-    float lo, hi;
-    uint32_t z;
+// Scales and zero points of rows g and g + 8 that a lane fetched, as stored:
+// for width 128 those of step t of four, otherwise those of the t-th 32 values
+// of one step.
+struct Raw {
+    uint32_t lo, hi, z_lo, z_hi;
 };
+
+struct Scales {
+    float lo, hi, z_lo, z_hi;
+};
+
+__device__ __forceinline__ Scales values_of(const W4Args &a, const Raw &r) {
+    return Scales{scale_value(a, r.lo), scale_value(a, r.hi), static_cast<float>(r.z_lo & 15u),
+                  static_cast<float>(r.z_hi & 15u)};
+}
 
 // y[r][n] with scalar arithmetic, for rows of x that hold infinities or NaN.
 template <class T>
@@ -221,387 +239,657 @@ __device__ __noinline__ float scalar_row(const W4Args &a, int64_t row, const T *
     return s;
 }
 
-template <class T, int WIDTH, bool ALIGNED>
-__global__ void __launch_bounds__(W4_THREADS, Operand<T>::BLOCKS) w4_kernel(const __grid_constant__ W4Args a) {
+// The rows of x of pass `pass`: eight consecutive ones, or, with ids, row
+// `pass` and the next seven of the same expert where an eighth of them starts
+// there. Returns their number (0: nothing to do) and the expert; called by the
+// whole block.
+struct Members {
+    int row[W4_ROWS];
+    int count;
+};
+
+__device__ __forceinline__ int find_members(const W4Args &a, int pass, Members *m, int *expert) {
+    *expert = 0;
+    if (!a.ids) {
+        const int r0 = pass * W4_ROWS;
+        if (threadIdx.x < W4_ROWS) m->row[threadIdx.x] = r0 + static_cast<int>(threadIdx.x);
+        __syncthreads();
+        return min(W4_ROWS, a.rows - r0);
+    }
+    const int e = __ldg(a.ids + pass);
+    *expert = e;
+    if (e < 0 || e >= a.experts) return 0;
+    const int threads = static_cast<int>(blockDim.x);
+    int before = 0;
+    for (int r0 = 0; r0 < pass; r0 += threads) {
+        const int i = r0 + static_cast<int>(threadIdx.x);
+        before += __syncthreads_count(i < pass && __ldg(a.ids + i) == e);
+    }
+    if (before % W4_ROWS != 0) return 0;
+    if (threadIdx.x < 32) {
+        const int lane = static_cast<int>(threadIdx.x);
+        int have = 0;
+        for (int r0 = pass; r0 < a.rows && have < W4_ROWS; r0 += 32) {
+            const bool mine = r0 + lane < a.rows && __ldg(a.ids + r0 + lane) == e;
+            const unsigned all = __ballot_sync(0xffffffffu, mine);
+            const int at = have + __popc(all & ((1u << lane) - 1u));
+            if (mine && at < W4_ROWS) m->row[at] = r0 + lane;
+            have += __popc(all);
+        }
+        if (lane == 0) m->count = min(have, W4_ROWS);
+    }
+    __syncthreads();
+    return m->count;
+}
+
+// Steps of K values of k, in pairs: the last may hold zeros only.
+__host__ __device__ __forceinline__ int64_t steps_of(int64_t K) { return (K + PAIR * STEP - 1) / (PAIR * STEP) * PAIR; }
+
+// A step of x as the matrix instructions read it: term, unit u, row, lane t, 8
+// values, then, where zero points are taken from the sums, the sums of x
+// over every 32 k (width 32), 64 or 128: group, row.
+template <class T, int WIDTH, int NB>
+struct XStep {
+    static constexpr int UNIT_BYTES = NB * 64, TERM_BYTES = 4 * UNIT_BYTES;
+    static constexpr int GROUPS = 128 / WIDTH;
+    static constexpr int SUMS = Operand<T>::TERMS * TERM_BYTES;  // where the sums start
+    static constexpr int BYTES = SUMS + (Operand<T>::EXACT ? 0 : (GROUPS * NB * 4 + 15) / 16 * 16);
+};
+
+// Lays out values 8 piece .. 8 piece + 7 of step `st` of row `row` of x as row r
+// of `to` (the step); zeros past the end of k. The 16 pieces of a step are 16
+// consecutive lanes, all of which call this.
+template <class T, int WIDTH, int NB>
+__device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, int piece, int r, bool in, uint8_t *to) {
     using Op = Operand<T>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int members[W4_ROWS];
-    __shared__ int member_count;
-    __shared__ int odd_row[W4_ROWS];  // the row holds an infinity or NaN (16-bit x)
+    using X = XStep<T, WIDTH, NB>;
+    // Which unit of which lane holds them.
+    const int u = WIDTH == 128 ? piece & 3 : WIDTH == 64 ? 2 * (piece >> 3) + (piece & 1) : piece >> 2;
+    const int t = WIDTH == 128 ? piece >> 2 : WIDTH == 64 ? (piece >> 1) & 3 : ((piece >> 1) & 1) + 2 * (piece & 1);
+    const int k = st * STEP + piece * 8, K = static_cast<int>(a.K);
+    Pack<T, 8> v;
+    if (in && a.x_vector && k + 8 <= K) {
+        constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < 8; j += PER) {
+            const Pack<T, PER> p = load_pack<T, PER>(x + k + j);
+#pragma unroll
+            for (int m = 0; m < PER; ++m) v.v[j + m] = p.v[m];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = in && k + j < K ? x[k + j] : from_f32<T>(0.0f);
+    }
+    uint32_t w[Op::TERMS][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint16_t x0[Op::TERMS], x1[Op::TERMS];
+        Op::split(v.v[j], x0);
+        Op::split(v.v[j + 4], x1);
+#pragma unroll
+        for (int m = 0; m < Op::TERMS; ++m) w[m][j] = x0[m] | (static_cast<uint32_t>(x1[m]) << 16);
+    }
+    if (in) {
+#pragma unroll
+        for (int m = 0; m < Op::TERMS; ++m)
+            *reinterpret_cast<uint4 *>(to + m * X::TERM_BYTES + u * X::UNIT_BYTES + r * 64 + t * 16) =
+                make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]);
+    }
+    if (!Op::EXACT) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += to_f32(v.v[j]);
+#pragma unroll
+        for (int d = 1; d < WIDTH / 8; d *= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (in && piece % (WIDTH / 8) == 0)
+            reinterpret_cast<float *>(to + X::SUMS)[piece / (WIDTH / 8) * NB + r] = s;
+    }
+}
+
+// Lays out x of pass blockIdx.y for streaming: a thread per 8 values.
+constexpr int PREPARE_THREADS = 256;
+template <class T, int WIDTH>
+__global__ void __launch_bounds__(PREPARE_THREADS) w4_prepare_kernel(const __grid_constant__ W4Args a, uint8_t *to) {
+    __shared__ Members members;
+    asm volatile("griddepcontrol.launch_dependents;");
+    int expert;
+    const int nb = find_members(a, a.first_pass + static_cast<int>(blockIdx.y), &members, &expert);
+    if (nb == 0) return;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * PREPARE_THREADS + threadIdx.x;
+    const int steps = static_cast<int>(steps_of(a.K));
+    const int st = static_cast<int>(i / (16 * W4_ROWS)), r = static_cast<int>(i / 16) % W4_ROWS;
+    const bool in = st < steps && r < nb;
+    lay_out_x<T, WIDTH, W4_ROWS>(
+        a, static_cast<const T *>(a.x) + (in ? members.row[r] * a.ldx : 0), in ? st : 0, static_cast<int>(i & 15), r, in,
+        to + (static_cast<int64_t>(blockIdx.y) * steps + (in ? st : 0)) * XStep<T, WIDTH, W4_ROWS>::BYTES);
+}
+
+// Untiled bulk copy global -> this block's shared memory (16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ float lds32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+
+// NB: rows of x laid out, 1 or 8. With one, all eight columns of the matrix
+// instruction are that row; with fewer than eight rows of x the rest of shared
+// memory is whatever it was. Columns do not mix, so only those of rows of x are
+// read out. STREAM: x comes with q from a.prepared.
+template <class T, int WIDTH, int NB, bool STREAM>
+__global__ void __launch_bounds__(W4_THREADS, 1)
+    w4_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ W4Args a) {
+    using Op = Operand<T>;
+    using X = XStep<T, WIDTH, NB>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Members members;
+    __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES];
+    __shared__ int abort_word;
+    volatile int *abort_flag = &abort_word;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int64_t n_first = static_cast<int64_t>(blockIdx.x) * 16 * a.row_tiles;
+    const uint32_t raw = tc::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const int K = static_cast<int>(a.K), steps = static_cast<int>(steps_of(a.K));
+    const int R = a.unit_rows, RT = R / 16, KS = PAIR * CONSUMERS / RT;  // row tiles and steps of a stage
+    const int per_unit = (steps + KS - 1) / KS;                   // stages of a unit
+    const uint32_t x_stage = STREAM ? static_cast<uint32_t>(KS * X::BYTES + 1023) / 1024 * 1024 : 0;
+    const uint32_t stage_bytes = Q_STAGE + x_stage;
+    // Behind the ring: the warps' sums of two units, x when it stays.
+    constexpr int PART = CONSUMERS * NB * 16;
+    float *part = reinterpret_cast<float *>(smem_raw + (base - raw) + a.stages * stage_bytes);
+    uint8_t *x_here = reinterpret_cast<uint8_t *>(part + 2 * PART);
     T *y = static_cast<T *>(a.y);
-    if (threadIdx.x < W4_ROWS) odd_row[threadIdx.x] = 0;
+    auto full = [&](int s) { return tc::smem_u32(bars + s); };
+    auto empty = [&](int s) { return tc::smem_u32(bars + MAX_STAGES + s); };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(empty(s), CONSUMERS);
+        }
+        abort_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
 
-    // Rows of x that this block serves: eight consecutive ones, or, with ids,
-    // this row and the next seven of the same expert where an eighth of them
-    // starts here.
-    int expert = 0, nb = 0;
-    if (!a.ids) {
-        const int r0 = static_cast<int>(blockIdx.y) * W4_ROWS;
-        nb = min(W4_ROWS, a.rows - r0);
-        if (threadIdx.x < W4_ROWS) members[threadIdx.x] = r0 + static_cast<int>(threadIdx.x);
-    } else {
-        const int r = static_cast<int>(blockIdx.y);
-        expert = __ldg(a.ids + r);
-        if (expert < 0 || expert >= a.experts) {
-            for (int64_t n = n_first + threadIdx.x; n < min(a.N, n_first + 16 * a.row_tiles); n += W4_THREADS)
-                y[r * a.ldy + n] = from_f32<T>(0.0f);
-            return;
-        }
-        int before = 0;
-        for (int r0 = 0; r0 < r; r0 += W4_THREADS) {
-            const int i = r0 + static_cast<int>(threadIdx.x);
-            before += __syncthreads_count(i < r && __ldg(a.ids + i) == expert);
-        }
-        if (before % W4_ROWS != 0) return;
-        if (warp == 0) {
-            int have = 0;
-            for (int r0 = r; r0 < a.rows && have < W4_ROWS; r0 += 32) {
-                const bool mine = r0 + lane < a.rows && __ldg(a.ids + r0 + lane) == expert;
-                const unsigned all = __ballot_sync(0xffffffffu, mine);
-                const int at = have + __popc(all & ((1u << lane) - 1u));
-                if (mine && at < W4_ROWS) members[at] = r0 + lane;
-                have += __popc(all);
-            }
-            if (lane == 0) member_count = min(have, W4_ROWS);
-        }
-        __syncthreads();
-        nb = member_count;
+    const int pass = a.first_pass + static_cast<int>(blockIdx.y);
+    int expert;
+    const int nb = find_members(a, pass, &members, &expert);
+    if (nb == 0) {
+        if (expert < 0 || expert >= a.experts)  // a row without an expert is zero
+            for (int64_t n = static_cast<int64_t>(blockIdx.x) * W4_THREADS + threadIdx.x; n < a.N;
+                 n += static_cast<int64_t>(gridDim.x) * W4_THREADS)
+                y[pass * a.ldy + n] = from_f32<T>(0.0f);
+        return;
     }
 
-    const int shares = W4_WARPS / a.row_tiles;
-    const int tile = warp / shares, share = warp % shares;
-    // Rows of q of this lane: n0 + g and n0 + g + 8; past the last row they
-    // repeat it and are not written.
-    const int64_t n0 = n_first + 16 * tile;
-    const int64_t row_lo = static_cast<int64_t>(expert) * a.N + min(n0 + g, a.N - 1);
-    const int64_t row_hi = static_cast<int64_t>(expert) * a.N + min(n0 + g + 8, a.N - 1);
-    const uint8_t *q_lo = a.q + row_lo * (a.K / 2), *q_hi = a.q + row_hi * (a.K / 2);
-    const int64_t g_lo = row_lo * a.groups, g_hi = row_hi * a.groups;
-    const int K = static_cast<int>(a.K);
-    const int steps = (K + STEP - 1) / STEP;
-    auto fetch = [&](int st, Weights &w) {
-        const int k = st * STEP;
-        if (k + STEP <= K || !ALIGNED) {  // whole, or checked byte by byte
-            if (WIDTH == 128) {
-                load_q<16, ALIGNED>(q_lo, k + 32 * t, K, w.lo);
-                load_q<16, ALIGNED>(q_hi, k + 32 * t, K, w.hi);
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    load_q<8, ALIGNED>(q_lo, k + 64 * h + 16 * t, K, w.lo + 2 * h);
-                    load_q<8, ALIGNED>(q_hi, k + 64 * h + 16 * t, K, w.hi + 2 * h);
-                }
-            }
-        } else {
-            // The last step of a K that is a multiple of 32: lanes past it get zeros.
-#pragma unroll
-            for (int u = 0; u < 4; ++u) w.lo[u] = w.hi[u] = 0;
-            if (WIDTH == 128) {
-                if (k + 32 * t < K) {
-                    load_q<16, ALIGNED>(q_lo, k + 32 * t, K, w.lo);
-                    load_q<16, ALIGNED>(q_hi, k + 32 * t, K, w.hi);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (k + 64 * h + 16 * t < K) {
-                        load_q<8, ALIGNED>(q_lo, k + 64 * h + 16 * t, K, w.lo + 2 * h);
-                        load_q<8, ALIGNED>(q_hi, k + 64 * h + 16 * t, K, w.hi + 2 * h);
+    if (warp == CONSUMERS) {
+        // ------------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint8_t *x_from = STREAM ? a.prepared + static_cast<int64_t>(blockIdx.y) * steps * X::BYTES : nullptr;
+            int slot = 0;
+            uint32_t phase = 0;
+            bool waited = !STREAM;
+            auto copy_x = [&](int to, int stage) {  // of stage `stage` of a unit
+                const int first = stage * KS, here = min(KS, steps - first);
+                bulk_load(base + to * stage_bytes + Q_STAGE, x_from + static_cast<int64_t>(first) * X::BYTES,
+                          static_cast<uint32_t>(here * X::BYTES), full(to));
+            };
+            // Stages of the first turn of the ring whose q is on its way while
+            // the kernel that lays out x runs.
+            int without_x = 0;
+            auto catch_up = [&] {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+                for (int i = 0; i < without_x; ++i) copy_x(i, i % per_unit);
+            };
+            for (int u = static_cast<int>(blockIdx.x); u < a.units; u += static_cast<int>(gridDim.x)) {
+                const int row = expert * static_cast<int>(a.N) + u * R;
+                for (int stage = 0; stage < per_unit; ++stage) {
+                    if (!waited && without_x == a.stages) catch_up();
+                    if (!tc::mbar_wait(empty(slot), phase ^ 1, a, abort_flag, tc::WD_PRODUCER)) return;
+                    const int boxes = min(KS / 2, (K / 2 - stage * KS * 64 + 127) / 128);
+                    const int here = min(KS, steps - stage * KS);
+                    tc::mbar_arrive_expect_tx(full(slot), static_cast<uint32_t>(boxes * R * 128) +
+                                                              (STREAM ? static_cast<uint32_t>(here * X::BYTES) : 0));
+                    for (int b = 0; b < boxes; ++b)
+                        tc::tma_load_3d(base + slot * stage_bytes + b * R * 128, &tmQ, stage * KS * 64 + b * 128, row, 0,
+                                        full(slot));
+                    if (STREAM) {
+                        if (waited)
+                            copy_x(slot, stage);
+                        else
+                            ++without_x;
                     }
+                    if (++slot == a.stages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
             }
+            if (!waited) catch_up();
         }
-    };
-    auto fetch_scales = [&](int k) {  // the groups that hold value k of both rows
-        Scales s;
-        s.lo = s.hi = 0.0f;
-        s.z = 0x00080008u;
-        if (k < K) {
+        return;
+    }
+
+    // ---------------------------------------------------------------------- consumers
+    const int rt = warp % RT, box = warp / RT;  // row tile, and pair of steps
+    const int ra = 16 * rt + row_of<WIDTH>(g);  // rows of the unit; the second eight: + 8
+    // Scales of the group that holds value k of the rows of unit u.
+    auto fetch_scales = [&](int u, int k) {
+        Raw s{0, 0, 8, 8};
+        if (u < a.units && k < K) {
+            const int64_t n0 = static_cast<int64_t>(u) * R + ra, row0 = static_cast<int64_t>(expert) * a.N;
+            const int64_t lo = (row0 + min(n0, a.N - 1)) * a.groups, hi = (row0 + min(n0 + 8, a.N - 1)) * a.groups;
             const int gi = k >> a.group_shift;
-            s.lo = scale_at(a, g_lo + gi);
-            s.hi = scale_at(a, g_hi + gi);
-            if (a.zeros)
-                s.z = (__ldg(a.zeros + g_lo + gi) & 15u) | (static_cast<uint32_t>(__ldg(a.zeros + g_hi + gi) & 15u) << 16);
+            s.lo = scale_bits(a, lo + gi);
+            s.hi = scale_bits(a, hi + gi);
+            if (a.zeros) {
+                s.z_lo = __ldg(a.zeros + lo + gi);
+                s.z_hi = __ldg(a.zeros + hi + gi);
+            }
         }
         return s;
     };
     // Width 128: a quad's lanes fetch the scales of a turn's four steps;
-    // otherwise each step's come with its weights.
-    auto turn_scales = [&](int i0) { return fetch_scales((share + (i0 + t) * shares) * STEP); };
-    static_assert(TURN == 4 && TURN % AHEAD == 0, "a quad's lanes fetch the scales of a turn");
-    Weights ring[AHEAD];
-    Scales of_step[AHEAD], turn{}, next{};
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        const int st = share + i * shares;
-        if (st < steps) fetch(st, ring[i]);
-        if (WIDTH < 128) of_step[i] = fetch_scales(st * STEP + 32 * t);
-    }
-    if (WIDTH == 128) next = turn_scales(0);
-
-    // A chunk of x in shared memory: term, step, unit u, row, lane t, 8 values
-    // (k_of); zeros past the end of k. Behind it the sums of x over every 32 k
-    // (width 32), 64 or 128: step, group, row.
-    constexpr int SUMS = 128 / WIDTH;  // per step
-    float *x_sums = reinterpret_cast<float *>(smem + static_cast<size_t>(Op::TERMS) * a.chunk_steps * 256 * nb);
-    auto stage = [&](int first_step) {
-        __syncthreads();
-        const int here = min(a.chunk_steps, steps - first_step);
-        const int per_row = here * 16, total = per_row * nb;
-        for (int i0 = 0; i0 < total; i0 += W4_THREADS) {
-            const int i = i0 + static_cast<int>(threadIdx.x);
-            const bool in_range = i < total;  // for whole sixteenths of a block
-            const int r = in_range ? i / per_row : 0, o = in_range ? i - r * per_row : 0;
-            const int st = o >> 4, piece = o & 15;
-            // Which unit of which lane holds values 8 piece .. 8 piece + 7.
-            const int u = WIDTH == 128 ? piece & 3 : WIDTH == 64 ? 2 * (piece >> 3) + (piece & 1) : piece >> 2;
-            const int tt = WIDTH == 128 ? piece >> 2
-                                        : WIDTH == 64 ? (piece >> 1) & 3 : ((piece >> 1) & 1) + 2 * (piece & 1);
-            const int k = first_step * STEP + o * 8;
-            T in[8];
-            if (in_range && a.x_vector && k + 8 <= K) {
-                const T *src = static_cast<const T *>(a.x) + members[r] * a.ldx + k;
-                constexpr int PER = 16 / sizeof(T);
-#pragma unroll
-                for (int j = 0; j < 8; j += PER) {
-                    const Pack<T, PER> v = load_pack<T, PER>(src + j);
-#pragma unroll
-                    for (int m = 0; m < PER; ++m) in[j + m] = v.v[m];
-                }
-            } else {
-                const T *src = static_cast<const T *>(a.x) + members[r] * a.ldx;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) in[j] = in_range && k + j < K ? src[k + j] : from_f32<T>(0.0f);
-            }
-            uint16_t v[Op::TERMS][8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint16_t terms[Op::TERMS];
-                Op::split(in[j], terms);
-#pragma unroll
-                for (int m = 0; m < Op::TERMS; ++m) v[m][(j & 3) * 2 + (j >> 2)] = terms[m];
-            }
-            if (in_range) {
-#pragma unroll
-                for (int m = 0; m < Op::TERMS; ++m) {
-                    uint4 w;
-                    w.x = v[m][0] | (static_cast<uint32_t>(v[m][1]) << 16);
-                    w.y = v[m][2] | (static_cast<uint32_t>(v[m][3]) << 16);
-                    w.z = v[m][4] | (static_cast<uint32_t>(v[m][5]) << 16);
-                    w.w = v[m][6] | (static_cast<uint32_t>(v[m][7]) << 16);
-                    reinterpret_cast<uint4 *>(smem)[((m * a.chunk_steps + st) * 4 + u) * nb * 4 + r * 4 + tt] = w;
-                }
-            }
-            if (!Op::EXACT) {
-                float s = 0.0f, odd = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s += to_f32(in[j]);
-                    odd = fmaf(to_f32(in[j]), 0.0f, odd);  // NaN for an infinity or NaN
-                }
-                if (odd != 0.0f) odd_row[r] = 1;
-#pragma unroll
-                for (int d = 1; d < WIDTH / 8; d *= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-                if (in_range && piece % (WIDTH / 8) == 0)
-                    x_sums[(st * SUMS + piece / (WIDTH / 8)) * W4_ROWS + r] = s;
-            }
-        }
-        __syncthreads();
+    // otherwise each step's, a turn ahead.
+    static_assert(PAIR * TURN == 4, "a quad's lanes fetch the scales of a turn");
+    Raw of_step[TURN][PAIR], next{};
+    Scales turn{};
+    auto fetch_turn = [&](int u, int stage0) {
+        if (WIDTH == 128) next = fetch_scales(u, ((stage0 + (t >> 1)) * KS + PAIR * box + (t & 1)) * STEP);
     };
+    auto fetch_stage = [&](int u, int stage, Raw (&s)[PAIR]) {
+        if (WIDTH < 128) {
+#pragma unroll
+            for (int h = 0; h < PAIR; ++h) s[h] = fetch_scales(u, (stage * KS + PAIR * box + h) * STEP + 32 * t);
+        }
+    };
+    const int u0 = static_cast<int>(blockIdx.x), du = static_cast<int>(gridDim.x);
+    fetch_turn(u0, 0);
+#pragma unroll
+    for (int j = 0; j < TURN; ++j) fetch_stage(u0, j, of_step[j]);
+
+    // x, once, when it stays here.
+    if (!STREAM) {
+        const int total = steps * 16 * NB;  // a sixteenth of a step of a row each
+        for (int i0 = 0; i0 < total; i0 += CONSUMERS * 32) {
+            const int i = i0 + static_cast<int>(threadIdx.x);
+            const int r = (i >> 4) % NB, st = (i >> 4) / NB;
+            const bool in = i < total && r < nb;
+            lay_out_x<T, WIDTH, NB>(a, static_cast<const T *>(a.x) + (in ? members.row[r] * a.ldx : 0), in ? st : 0, i & 15,
+                                    r, in, x_here + (in ? st : 0) * X::BYTES);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+    }
+    const uint32_t x_at0 = tc::smem_u32(x_here);
 
     float sum[4] = {};
-    auto multiply = [&](Weights &w, const Scales &sc, int j, int st) {  // st: step within the chunk
-        if (WIDTH == 32) {
-            // Word 2 h + 1 of lanes 0, 1 for word 2 h of lanes 2, 3.
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t sl = __shfl_xor_sync(0xffffffffu, t < 2 ? w.lo[2 * h + 1] : w.lo[2 * h], 2);
-                const uint32_t sh = __shfl_xor_sync(0xffffffffu, t < 2 ? w.hi[2 * h + 1] : w.hi[2 * h], 2);
-                if (t < 2) {
-                    w.lo[2 * h + 1] = sl;
-                    w.hi[2 * h + 1] = sh;
-                } else {
-                    w.lo[2 * h] = sl;
-                    w.hi[2 * h] = sh;
-                }
-            }
-        }
+    // Two steps side by side: their chains of products do not depend on each
+    // other.
+    auto multiply = [&](const Weights (&w)[PAIR], const Scales (&sc)[PAIR], int j, uint32_t x_step) {
         // One accumulator per chain of dependent products.
         constexpr int CHAINS = Op::TERMS == 1 ? 2 : Op::TERMS;
-        float c[CHAINS][4] = {};
-        float s_lo = 0.0f, s_hi = 0.0f;
-        uint32_t z = 0, z_lo = 0, z_hi = 0;
+        constexpr int PER_GROUP = WIDTH / 32;  // words of a group
+        float c[PAIR][CHAINS][4];
+        float s_lo[PAIR], s_hi[PAIR], z_lo[PAIR], z_hi[PAIR];
+        uint32_t zz_lo[PAIR], zz_hi[PAIR];
+        const uint32_t x_at = x_step + (NB == 1 ? t : lane) * 16;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (u % (WIDTH / 32) == 0) {  // a group starts
-                const int from = (lane & ~3) | (WIDTH == 128 ? j : u);
-                s_lo = __shfl_sync(0xffffffffu, sc.lo, from);
-                s_hi = __shfl_sync(0xffffffffu, sc.hi, from);
-                z = __shfl_sync(0xffffffffu, sc.z, from);
-                z_lo = Op::ONE | (z & 0xFFFFu) | (z << 16);
-                z_hi = Op::ONE | (z >> 16) | (z & 0xFFFF0000u);
-            }
-            uint4 xv[Op::TERMS];
+            if (u % PER_GROUP == 0) {  // a group starts
 #pragma unroll
-            for (int m = 0; m < Op::TERMS; ++m) {
-                xv[m] = make_uint4(0, 0, 0, 0);
-                if (g < nb)
-                    xv[m] = reinterpret_cast<const uint4 *>(
-                        smem)[((m * a.chunk_steps + st) * 4 + u) * nb * 4 + g * 4 + t];
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t f[4];
-                f[0] = ((w.lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                f[1] = ((w.hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                f[2] = ((w.lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
-                f[3] = ((w.hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
-                if (Op::EXACT) {
-                    f[0] = Op::minus(f[0], z_lo);
-                    f[1] = Op::minus(f[1], z_hi);
-                    f[2] = Op::minus(f[2], z_lo);
-                    f[3] = Op::minus(f[3], z_hi);
+                for (int h = 0; h < PAIR; ++h) {
+                    const int from = (lane & ~3) | (WIDTH == 128 ? PAIR * j + h : u);
+                    s_lo[h] = __shfl_sync(0xffffffffu, sc[h].lo, from);
+                    s_hi[h] = __shfl_sync(0xffffffffu, sc[h].hi, from);
+                    z_lo[h] = z_hi[h] = 8.0f;
+                    if (a.zeros) {
+                        z_lo[h] = __shfl_sync(0xffffffffu, sc[h].z_lo, from);
+                        z_hi[h] = __shfl_sync(0xffffffffu, sc[h].z_hi, from);
+                    }
+                    if (Op::EXACT) {
+                        zz_lo[h] = Op::twice(128.0f + z_lo[h]);
+                        zz_hi[h] = Op::twice(128.0f + z_hi[h]);
+                    }
                 }
+            }
+            uint4 xv[PAIR][Op::TERMS];
+#pragma unroll
+            for (int h = 0; h < PAIR; ++h)
 #pragma unroll
                 for (int m = 0; m < Op::TERMS; ++m)
-                    Op::mma(c[Op::TERMS == 1 ? half : m], f, half ? xv[m].z : xv[m].x, half ? xv[m].w : xv[m].y);
+                    xv[h][m] = lds128(x_at + h * X::BYTES + m * X::TERM_BYTES + u * X::UNIT_BYTES);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int h = 0; h < PAIR; ++h) {
+                    uint32_t f[4];
+                    f[0] = ((w[h].lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                    f[1] = ((w[h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                    f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                    f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                    if (Op::EXACT) {
+                        f[0] = Op::minus(f[0], zz_lo[h]);
+                        f[1] = Op::minus(f[1], zz_hi[h]);
+                        f[2] = Op::minus(f[2], zz_lo[h]);
+                        f[3] = Op::minus(f[3], zz_hi[h]);
+                    }
+#pragma unroll
+                    for (int m = 0; m < Op::TERMS; ++m) {
+                        float(&d)[4] = c[h][Op::TERMS == 1 ? half : m];
+                        const uint32_t b0 = half ? xv[h][m].z : xv[h][m].x, b1 = half ? xv[h][m].w : xv[h][m].y;
+                        if (u % PER_GROUP == 0 && (half == 0 || Op::TERMS == 1))  // the chain starts
+                            Op::mma(d, f, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                        else
+                            Op::mma(d, f, b0, b1, d[0], d[1], d[2], d[3]);
+                    }
+                }
             }
-            if ((u + 1) % (WIDTH / 32) == 0) {  // the group ends
-                float d[4];
+            if ((u + 1) % PER_GROUP == 0) {  // the group ends
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // small terms first
-                    d[i] = c[CHAINS - 1][i];
+                for (int h = 0; h < PAIR; ++h) {
+                    float d[4];
 #pragma unroll
-                    for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[m][i];
+                    for (int i = 0; i < 4; ++i) {  // small terms first
+                        d[i] = c[h][CHAINS - 1][i];
 #pragma unroll
-                    for (int m = 0; m < CHAINS; ++m) c[m][i] = 0.0f;
+                        for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                    }
+                    if (!Op::EXACT) {
+                        const uint32_t at = x_step + h * X::BYTES + X::SUMS + u / PER_GROUP * NB * 4;
+                        const float xs0 = lds32(NB == 1 ? at : at + 8 * t);
+                        const float xs1 = NB == 1 ? xs0 : lds32(at + 8 * t + 4);
+                        const float b_lo = -Op::BASE - z_lo[h], b_hi = -Op::BASE - z_hi[h];
+                        d[0] = fmaf(d[0], Op::UNIT, b_lo * xs0);
+                        d[1] = fmaf(d[1], Op::UNIT, b_lo * xs1);
+                        d[2] = fmaf(d[2], Op::UNIT, b_hi * xs0);
+                        d[3] = fmaf(d[3], Op::UNIT, b_hi * xs1);
+                    }
+                    sum[0] = fmaf(s_lo[h], d[0], sum[0]);
+                    sum[1] = fmaf(s_lo[h], d[1], sum[1]);
+                    sum[2] = fmaf(s_hi[h], d[2], sum[2]);
+                    sum[3] = fmaf(s_hi[h], d[3], sum[3]);
                 }
-                if (!Op::EXACT) {
-                    const float2 xs = *reinterpret_cast<const float2 *>(
-                        x_sums + (st * SUMS + u / (WIDTH / 32)) * W4_ROWS + 2 * t);
-                    const float b_lo = Op::BASE + static_cast<float>(z & 0xFFFFu);
-                    const float b_hi = Op::BASE + static_cast<float>(z >> 16);
-                    d[0] = fmaf(d[0], Op::UNIT, -b_lo * xs.x);
-                    d[1] = fmaf(d[1], Op::UNIT, -b_lo * xs.y);
-                    d[2] = fmaf(d[2], Op::UNIT, -b_hi * xs.x);
-                    d[3] = fmaf(d[3], Op::UNIT, -b_hi * xs.y);
-                }
-                sum[0] = fmaf(s_lo, d[0], sum[0]);
-                sum[1] = fmaf(s_lo, d[1], sum[1]);
-                sum[2] = fmaf(s_hi, d[2], sum[2]);
-                sum[3] = fmaf(s_hi, d[3], sum[3]);
             }
         }
     };
 
-    // Every warp goes through the same number of steps, so that all meet at
-    // the chunks; those past the end are not multiplied.
-    const int per_chunk = a.chunk_steps / shares;
-    const int count = (steps + shares - 1) / shares;
-    int in_chunk = 0, first_step = 0;
-    if (count > 0) stage(0);
-    for (int i0 = 0; i0 < count; i0 += TURN) {
-        if (WIDTH == 128) {
-            turn = next;
-            next = turn_scales(i0 + TURN);
-        }
-#pragma unroll
-        for (int j = 0; j < TURN; ++j) {
-            const int i = i0 + j;
-            if (i >= count) break;
-            if (in_chunk == per_chunk) {
-                in_chunk = 0;
-                first_step += a.chunk_steps;
-                stage(first_step);
+    // This lane's bytes of a stage.
+    const uint32_t q_row = static_cast<uint32_t>(box * R * 128 + ra * 128), turn_of = static_cast<uint32_t>(ra & 7);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool alive = true;  // after a wait that gave up the loops go on without waiting or multiplying
+    int parity = 0;
+    for (int u = u0; u < a.units; u += du, parity ^= 1) {
+        for (int stage0 = 0; stage0 < per_unit; stage0 += TURN) {
+            const bool last_turn = stage0 + TURN >= per_unit;
+            if (WIDTH == 128) {
+                turn = values_of(a, next);
+                fetch_turn(last_turn ? u + du : u, last_turn ? 0 : stage0 + TURN);
             }
-            const int st = share + i * shares, slot = j % AHEAD;
-            if (st < steps) multiply(ring[slot], WIDTH == 128 ? turn : of_step[slot], j, st - first_step);
-            const int ahead = st + AHEAD * shares;
-            if (ahead < steps) fetch(ahead, ring[slot]);
-            if (WIDTH < 128) of_step[slot] = fetch_scales(ahead * STEP + 32 * t);
-            ++in_chunk;
+#pragma unroll
+            for (int j = 0; j < TURN; ++j) {
+                const int stage = stage0 + j;
+                if (stage < per_unit) {
+                    if (alive)
+                        alive = __all_sync(0xffffffffu,
+                                           tc::mbar_wait(full(slot), phase, a, abort_flag, tc::WD_MMA_FULL));
+                    const int st = stage * KS + PAIR * box;
+                    if (alive && st < steps) {
+                        const uint32_t sq = base + slot * stage_bytes, at = sq + q_row;
+                        Weights w[PAIR];
+#pragma unroll
+                        for (int h = 0; h < PAIR; ++h) {
+                            if (WIDTH == 128) {
+                                const uint32_t c = ((4 * h + t) ^ turn_of) * 16;
+                                const uint4 lo = lds128(at + c), hi = lds128(at + 8 * 128 + c);
+                                w[h].lo[0] = lo.x, w[h].lo[1] = lo.y, w[h].lo[2] = lo.z, w[h].lo[3] = lo.w;
+                                w[h].hi[0] = hi.x, w[h].hi[1] = hi.y, w[h].hi[2] = hi.z, w[h].hi[3] = hi.w;
+                            } else {
+#pragma unroll
+                                for (int p = 0; p < 2; ++p) {
+                                    const uint32_t c = ((4 * h + 2 * p + (t >> 1)) ^ turn_of) * 16 + (t & 1) * 8;
+                                    uint2 lo = lds64(at + c), hi = lds64(at + 8 * 128 + c);
+                                    if (WIDTH == 32) {
+                                        // The second word of lanes 0, 1 for the first of lanes 2, 3.
+                                        const uint32_t sl = __shfl_xor_sync(0xffffffffu, t < 2 ? lo.y : lo.x, 2);
+                                        const uint32_t sh = __shfl_xor_sync(0xffffffffu, t < 2 ? hi.y : hi.x, 2);
+                                        lo = t < 2 ? make_uint2(lo.x, sl) : make_uint2(sl, lo.y);
+                                        hi = t < 2 ? make_uint2(hi.x, sh) : make_uint2(sh, hi.y);
+                                    }
+                                    w[h].lo[2 * p] = lo.x, w[h].lo[2 * p + 1] = lo.y;
+                                    w[h].hi[2 * p] = hi.x, w[h].hi[2 * p + 1] = hi.y;
+                                }
+                            }
+                        }
+                        const uint32_t x_step = STREAM ? sq + Q_STAGE + static_cast<uint32_t>(PAIR * box * X::BYTES)
+                                                       : x_at0 + static_cast<uint32_t>(st * X::BYTES);
+                        if (WIDTH == 128) {
+                            const Scales both[PAIR] = {turn, turn};
+                            multiply(w, both, j, x_step);
+                        } else {
+                            const Scales both[PAIR] = {values_of(a, of_step[j][0]), values_of(a, of_step[j][1])};
+                            multiply(w, both, j, x_step);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(empty(slot));
+                    if (++slot == a.stages) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                fetch_stage(last_turn ? u + du : u, last_turn ? j : stage + TURN, of_step[j]);
+            }
+        }
+        // Join the shares of the unit. Two buffers: a warp that writes the next
+        // unit's sums may meet one that still reads this unit's.
+        float *mine = part + parity * PART + warp * NB * 16;
+        const int n_lo = row_of<WIDTH>(g);
+        if (NB == 1) {
+            if (t == 0) {
+                mine[n_lo] = sum[0];
+                mine[n_lo + 8] = sum[2];
+            }
+        } else {
+            mine[(2 * t) * 16 + n_lo] = sum[0];
+            mine[(2 * t + 1) * 16 + n_lo] = sum[1];
+            mine[(2 * t) * 16 + n_lo + 8] = sum[2];
+            mine[(2 * t + 1) * 16 + n_lo + 8] = sum[3];
+        }
+        sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+        for (int i = threadIdx.x; i < R * nb; i += CONSUMERS * 32) {
+            const int r = i / R, n = i - r * R;
+            const float *from = part + parity * PART + ((n >> 4) * NB + r) * 16 + (n & 15);
+            float s = 0.0f;
+            for (int w = 0; w < CONSUMERS / RT; ++w) s += from[w * RT * NB * 16];
+            const int64_t row = static_cast<int64_t>(u) * R + n;
+            if (row >= a.N) continue;
+            if (!Op::EXACT && !(fabsf(s) <= 3.0e38f))
+                s = scalar_row(a, static_cast<int64_t>(expert) * a.N + row,
+                               static_cast<const T *>(a.x) + members.row[r] * a.ldx);
+            y[members.row[r] * a.ldy + row] = from_f32<T>(s);
         }
     }
-    // Join the shares: part[warp][row of x][16 rows of q].
-    __syncthreads();
-    float *part = reinterpret_cast<float *>(smem);
-    part[(warp * 8 + 2 * t) * 16 + g] = sum[0];
-    part[(warp * 8 + 2 * t + 1) * 16 + g] = sum[1];
-    part[(warp * 8 + 2 * t) * 16 + g + 8] = sum[2];
-    part[(warp * 8 + 2 * t + 1) * 16 + g + 8] = sum[3];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * a.row_tiles * nb; i += W4_THREADS) {
-        const int r = i / (16 * a.row_tiles), n = i - r * (16 * a.row_tiles);
-        if (n_first + n >= a.N) continue;
-        const int w0 = (n >> 4) * shares;
-        float s = 0.0f;
-        for (int w = 0; w < shares; ++w) s += part[((w0 + w) * 8 + r) * 16 + (n & 15)];
-        if (!Op::EXACT && odd_row[r])
-            s = scalar_row(a, static_cast<int64_t>(expert) * a.N + n_first + n,
-                           static_cast<const T *>(a.x) + members[r] * a.ldx);
-        y[members[r] * a.ldy + n_first + n] = from_f32<T>(s);
+    // After a wait that gave up, copies may still be on their way: leave them
+    // time to land.
+    if (*abort_flag) {
+        const uint64_t t0 = tc::global_timer();
+        while (tc::global_timer() - t0 < 10000000ull) {
+        }
     }
 }
 
-template <class T, int WIDTH, bool ALIGNED>
-int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    auto kernel = w4_kernel<T, WIDTH, ALIGNED>;
-    using Op = Operand<T>;
-    const int64_t passes = a.ids ? a.rows : (a.rows + W4_ROWS - 1) / W4_ROWS;
-    const int nb = a.rows < W4_ROWS ? a.rows : W4_ROWS;
-    // Passes with work in them, and rows of x in one, as far as the host knows.
-    const int64_t busy = a.ids && a.experts < passes ? a.experts : passes;
-    const int64_t share_x = a.rows / busy < 1 ? 1 : (a.rows / busy < W4_ROWS ? a.rows / busy : W4_ROWS);
-    // Rows of q per block: few give every SM its part, many pay once for x and
-    // for a block's start (about the time of 16 KB of q). The choice makes the
-    // busiest SM's bytes least, an SM with fewer blocks than it has room for
-    // counting as full: its warps are too few to keep it busy.
-    int tiles = 1;
-    int64_t least = INT64_MAX;
-    for (int t = 1; t <= W4_WARPS; t *= 2) {
-        const int64_t blocks = (a.N + 16 * t - 1) / (16 * t) * busy;
-        int64_t per_sm = (blocks + dev.sm_count - 1) / dev.sm_count;
-        if (per_sm < Op::BLOCKS) per_sm = Op::BLOCKS;
-        const int64_t cost = per_sm * (t * 8 * a.K + share_x * a.K * static_cast<int64_t>(sizeof(T)) + 16384);
-        if (cost < least) {
-            least = cost;
-            tiles = t;
+// Any K and alignment, without tensor maps or workspace: a warp per row of q,
+// scalar arithmetic.
+template <class T>
+__global__ void __launch_bounds__(256) w4_simple_kernel(const __grid_constant__ W4Args a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (n >= a.N) return;
+    for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+        const int e = a.ids ? __ldg(a.ids + r) : 0;
+        float s = 0.0f;
+        if (e >= 0 && e < a.experts) {
+            const int64_t row = static_cast<int64_t>(e) * a.N + n;
+            const T *x = static_cast<const T *>(a.x) + r * a.ldx;
+            for (int64_t k = 2 * lane; k < a.K; k += 64) {
+                const int64_t gi = row * a.groups + (k >> a.group_shift);
+                const int b = __ldg(a.q + row * (a.K / 2) + k / 2), z = a.zeros ? __ldg(a.zeros + gi) & 15 : 8;
+                const float w = scale_at(a, gi);
+                s = fmaf(static_cast<float>((b & 15) - z) * w, to_f32(x[k]), s);
+                s = fmaf(static_cast<float>((b >> 4) - z) * w, to_f32(x[k + 1]), s);
+            }
         }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (lane == 0) static_cast<T *>(a.y)[r * a.ldy + n] = from_f32<T>(s);
     }
-    a.row_tiles = tiles;
-    const int shares = W4_WARPS / tiles;
-    const int step_bytes = nb * 2 * Op::TERMS * STEP, sum_bytes = Op::EXACT ? 0 : 128 / WIDTH * W4_ROWS * 4;
-    const int64_t all = ((a.K + STEP - 1) / STEP + shares - 1) / shares * shares;
-    int64_t chunk = Op::X_BYTES / (step_bytes + sum_bytes) / shares * shares;
-    if (chunk > all) chunk = all;
-    a.chunk_steps = static_cast<int>(chunk);
-    a.x_vector = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-    size_t smem = static_cast<size_t>(chunk) * (step_bytes + sum_bytes);
-    if (smem < W4_WARPS * 8 * 16 * sizeof(float)) smem = W4_WARPS * 8 * 16 * sizeof(float);
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Op::X_BYTES) != cudaSuccess) {
-        cudaGetLastError();
-        return SGEMM_ERR_LAUNCH;
-    }
-    const int64_t gx = (a.N + 16 * tiles - 1) / (16 * tiles);
-    if (gx > INT32_MAX || passes > 65535) return SGEMM_ERR_UNSUPPORTED;
-    kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(passes)), W4_THREADS, smem, stream>>>(a);
+}
+
+template <class T>
+int launch_simple(const W4Args &a, cudaStream_t stream, int *launches) {
+    const int64_t gx = (a.N + 7) / 8;
+    if (gx > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
+    w4_simple_kernel<T><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(a.rows)), 256, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
     ++*launches;
     return SGEMM_OK;
 }
 
+template <class T, int WIDTH, int NB, bool STREAM>
+int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    auto kernel = w4_kernel<T, WIDTH, NB, STREAM>;
+    using X = XStep<T, WIDTH, NB>;
+    const int passes = static_cast<int>(a.ids ? a.rows : (a.rows + W4_ROWS - 1) / W4_ROWS);
+    const int64_t steps = steps_of(a.K);
+    // Passes with work in them: with ids, the experts that rows with ids drawn
+    // evenly would use (blocks of other passes end at once).
+    int64_t busy = passes;
+    if (a.ids) {
+        double unused = 1.0;
+        for (int r = 0; r < a.rows && r < 64 * a.experts; ++r) unused *= 1.0 - 1.0 / a.experts;
+        const int64_t used = static_cast<int64_t>(a.experts * (1.0 - unused) + 0.5);
+        if (used < busy) busy = used < 1 ? 1 : used;
+    }
+    // Rows of a unit: few give every SM its part, many need less of a streamed
+    // x and end less often (about a stage's time). The choice makes the
+    // busiest SM's bytes least.
+    int64_t least = INT64_MAX;
+    for (int R = 16; R <= 128; R *= 2) {
+        const int64_t KS = PAIR * CONSUMERS / (R / 16), x = STREAM ? KS * X::BYTES : 0;
+        if (x > X_STAGE) continue;
+        const int64_t units = (a.N + R - 1) / R * busy;
+        const int64_t cost = (units + dev.sm_count - 1) / dev.sm_count * ((steps + KS - 1) / KS + 1) * (Q_STAGE + x / 2);
+        if (cost < least) {
+            least = cost;
+            a.unit_rows = R;
+        }
+    }
+    a.units = static_cast<int>((a.N + a.unit_rows - 1) / a.unit_rows);
+    const int64_t KS = PAIR * CONSUMERS / (a.unit_rows / 16);
+    const int64_t stage = Q_STAGE + (STREAM ? (KS * X::BYTES + 1023) / 1024 * 1024 : 0);
+    const int64_t rest = 1024 + 2 * CONSUMERS * NB * 16 * 4 + (STREAM ? 0 : steps * X::BYTES);
+    int64_t stages = (SMEM_BYTES - rest) / stage;
+    if (stages > MAX_STAGES) stages = MAX_STAGES;
+    a.stages = static_cast<int>(stages);
+    a.x_vector = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+    a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
+    a.watchdog = watchdog_flag_device_ptr();
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    std::call_once(once[dev.device], [&] {
+        set[dev.device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    });
+    alignas(64) CUtensorMap map{};
+    if (!a.watchdog || set[dev.device] != cudaSuccess ||
+        !tc::encode_map_typed(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, a.experts * a.N, a.K / 2, a.K / 2, 1, 0, 128,
+                              static_cast<uint32_t>(a.unit_rows), CU_TENSOR_MAP_SWIZZLE_128B)) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    float *scratch = nullptr;
+    if (STREAM) {
+        const int64_t at_once = passes < PASSES ? passes : PASSES;
+        scratch = scratch_alloc(dev, static_cast<size_t>(at_once * steps * X::BYTES), stream);
+        if (!scratch) return launch_simple<T>(a, stream, launches);
+        a.prepared = reinterpret_cast<const uint8_t *>(scratch);
+    }
+    int64_t workers = dev.sm_count / busy;
+    if (workers < 1) workers = 1;
+    if (workers > a.units) workers = a.units;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(W4_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(rest + stages * stage);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = STREAM ? 1 : 0;
+    int rc = SGEMM_OK;
+    const int chunk = STREAM ? PASSES : passes;
+    for (a.first_pass = 0; a.first_pass < passes && rc == SGEMM_OK; a.first_pass += chunk) {
+        const int here = passes - a.first_pass < chunk ? passes - a.first_pass : chunk;
+        if (STREAM) {
+            const int64_t blocks = (steps * 16 * W4_ROWS + PREPARE_THREADS - 1) / PREPARE_THREADS;
+            w4_prepare_kernel<T, WIDTH><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(here)),
+                                          PREPARE_THREADS, 0, stream>>>(a, reinterpret_cast<uint8_t *>(scratch));
+            if (cudaGetLastError() != cudaSuccess) {
+                rc = SGEMM_ERR_LAUNCH;
+                break;
+            }
+            ++*launches;
+        }
+        cfg.gridDim = dim3(static_cast<unsigned>(workers), static_cast<unsigned>(here));
+        if (cudaLaunchKernelEx(&cfg, kernel, map, a) != cudaSuccess) {
+            cudaGetLastError();
+            rc = SGEMM_ERR_LAUNCH;
+            break;
+        }
+        ++*launches;
+    }
+    scratch_free(scratch, stream);
+    return rc;
+}
+
+template <class T, int WIDTH>
+int launch_width(const W4Args &a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const int64_t steps = steps_of(a.K);
+    if (a.rows == 1 && steps * XStep<T, WIDTH, 1>::BYTES <= RESIDENT_ONE)
+        return launch<T, WIDTH, 1, false>(a, dev, stream, launches);
+    if (steps * XStep<T, WIDTH, 8>::BYTES <= RESIDENT_EIGHT)
+        return launch<T, WIDTH, 8, false>(a, dev, stream, launches);
+    return launch<T, WIDTH, 8, true>(a, dev, stream, launches);
+}
+
 template <class T>
-int launch_type(const W4Args &a, int64_t group, bool aligned, const DeviceInfo &dev, cudaStream_t stream,
-                int *launches) {
-    if (group >= 128)
-        return aligned ? launch<T, 128, true>(a, dev, stream, launches)
-                       : launch<T, 128, false>(a, dev, stream, launches);
-    if (group == 64)
-        return aligned ? launch<T, 64, true>(a, dev, stream, launches) : launch<T, 64, false>(a, dev, stream, launches);
-    return aligned ? launch<T, 32, true>(a, dev, stream, launches) : launch<T, 32, false>(a, dev, stream, launches);
+int launch_type(const W4Args &a, int64_t group, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (dev.device < 0 || dev.device >= 64) return SGEMM_ERR_DEVICE;
+    // What a tensor map can describe: rows of q of a multiple of 16 bytes.
+    if (a.K % 32 != 0 || a.K == 0 || reinterpret_cast<uintptr_t>(a.q) % 16 != 0 || a.K > INT32_MAX / 2 ||
+        a.N > INT32_MAX / 2 / a.experts)
+        return launch_simple<T>(a, stream, launches);
+    if (group >= 128) return launch_width<T, 128>(a, dev, stream, launches);
+    return group == 64 ? launch_width<T, 64>(a, dev, stream, launches) : launch_width<T, 32>(a, dev, stream, launches);
 }
 
 }  // namespace
@@ -623,11 +911,9 @@ int w4_launch(const W4Problem &p, const DeviceInfo &dev, cudaStream_t stream, in
     a.zeros = p.zeros;
     a.y = p.y;
     a.ldy = p.ldy;
-    // Rows of q in 16-byte pieces.
-    const bool aligned = p.K % 32 == 0 && reinterpret_cast<uintptr_t>(p.q) % 16 == 0;
-    if (p.type == SGEMM_TYPE_F32) return launch_type<float>(a, p.group, aligned, dev, stream, launches);
-    if (p.type == SGEMM_TYPE_BF16) return launch_type<__nv_bfloat16>(a, p.group, aligned, dev, stream, launches);
-    return launch_type<__half>(a, p.group, aligned, dev, stream, launches);
+    if (p.type == SGEMM_TYPE_F32) return launch_type<float>(a, p.group, dev, stream, launches);
+    if (p.type == SGEMM_TYPE_BF16) return launch_type<__nv_bfloat16>(a, p.group, dev, stream, launches);
+    return launch_type<__half>(a, p.group, dev, stream, launches);
 }
 
 }  // namespace ex

@@ -24,7 +24,7 @@ from typing import NamedTuple
 
 import torch
 
-from .sgemm import SgemmError, _stream_handle, lib
+from .sgemm import SgemmError, lib
 
 SGEMM_TYPE_F32 = 0
 SGEMM_TYPE_BF16 = 1
@@ -63,6 +63,18 @@ class Routing(NamedTuple):
     offsets: torch.Tensor  # experts + 1, int32: group e holds slots offsets[e] .. offsets[e + 1] - 1
     order: torch.Tensor    # tokens * top_k, int32: the pair (token * top_k + choice) at each slot
     slot: torch.Tensor     # tokens x top_k, int32: the slot of each pair
+
+
+# The current stream's handle without a Stream object (which costs 3 us).
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_handle(stream, t):
+    """The stream's handle; the tensors' device must be the current one, which the library launches on."""
+    device = t.device.index
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 def _check(rc, what):
@@ -144,7 +156,7 @@ def sort(ids, experts, stream=None):
     space = _empty((need // 4,), torch.int32, device, stream) if need else None
     _check(lib.sgemm_experts_sort(ptr, 64 if ids.dtype == torch.int64 else 32, tokens, top_k, experts,
                                   offsets.data_ptr(), order.data_ptr(), slot.data_ptr(),
-                                  space.data_ptr() if need else 0, need, _stream_handle(stream)),
+                                  space.data_ptr() if need else 0, need, _stream_handle(stream, ids)),
            "sgemm_experts_sort")
     return Routing(offsets, order, slot)
 
@@ -162,7 +174,7 @@ def gather(x, routing, out=None, stream=None):
     if tuple(out.shape) != (tokens * top_k, width):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gather(code, tokens, top_k, experts, width, x.data_ptr(), ldx, slot, offsets,
-                                    out.data_ptr(), ldo, _stream_handle(stream)), "sgemm_experts_gather")
+                                    out.data_ptr(), ldo, _stream_handle(stream, x)), "sgemm_experts_gather")
     return out
 
 
@@ -181,7 +193,7 @@ def _combine(h, weights, routing, out, stream):
     if tuple(out.shape) != (tokens, width):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_combine(code, tokens, top_k, experts, width, h.data_ptr(), ldh, w, slot, offsets,
-                                     out.data_ptr(), ldo, _stream_handle(stream)), "sgemm_experts_combine")
+                                     out.data_ptr(), ldo, _stream_handle(stream, h)), "sgemm_experts_combine")
     return out
 
 
@@ -213,7 +225,7 @@ def combine_grad(dy, h, weights, routing, stream=None):
     dw = _empty((tokens, top_k), torch.float32, h.device, stream)
     _check(lib.sgemm_experts_combine_grad(code, tokens, top_k, experts, width, dy.data_ptr(), lddy, h.data_ptr(), ldh,
                                           w, slot, offsets, dh.data_ptr(), max(width, 1), dw.data_ptr(),
-                                          _stream_handle(stream)), "sgemm_experts_combine_grad")
+                                          _stream_handle(stream, h)), "sgemm_experts_combine_grad")
     return dh, dw
 
 
@@ -236,7 +248,7 @@ def gemm(a, b, offsets, out=None, *, transB=False, stream=None):
     if tuple(out.shape) != (rows, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gemm(code, int(transB), rows, N, K, E, off, a.data_ptr(), lda, b.data_ptr(), ldb, stride,
-                                  out.data_ptr(), ldo, _stream_handle(stream)), "sgemm_experts_gemm")
+                                  out.data_ptr(), ldo, _stream_handle(stream, a)), "sgemm_experts_gemm")
     return out
 
 
@@ -262,7 +274,7 @@ def gemm_wgrad(a, b, offsets, out=None, *, stream=None):
     if tuple(out.shape) != (E, M, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gemm_wgrad(code, rows, M, N, E, off, a.data_ptr(), lda, b.data_ptr(), ldb,
-                                        out.data_ptr(), ldo, stride, _stream_handle(stream)),
+                                        out.data_ptr(), ldo, stride, _stream_handle(stream, a)),
            "sgemm_experts_gemm_wgrad")
     return out
 
@@ -297,5 +309,5 @@ def w4_matvec(x, q, scales, *, group, zeros=None, ids=None, out=None, stream=Non
     if tuple(out.shape) != (rows, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_w4_matvec(code, rows, N, K, group, E, ip, x.data_ptr(), ldx, qp, sp, TYPES[scales.dtype], zp,
-                               out.data_ptr(), ldo, _stream_handle(stream)), "sgemm_w4_matvec")
+                               out.data_ptr(), ldo, _stream_handle(stream, x)), "sgemm_w4_matvec")
     return out
