@@ -110,8 +110,10 @@ struct GroupTile {
 
 // Calls f(tile) for the tiles (TM x TN, k-blocks of TK) of worker `index` of
 // `count`, groups in order, columns before rows, round robin. Every thread of
-// a worker walks the same sequence.
-template <bool WGRAD, int TM, int TN, int TK, class F>
+// a worker walks the same sequence. EVEN > 0: a group's rows are spread evenly
+// over its tiles, in multiples of EVEN rows, and row_end is the tile's;
+// otherwise every tile but the last has TM rows, and row_end is the group's.
+template <bool WGRAD, int TM, int TN, int TK, int EVEN = 0, class F>
 __device__ __forceinline__ void for_each_group_tile(const GroupTiles &a, volatile int *abort_flag, int index, int count,
                                                     F &&f) {
     if (WGRAD) {
@@ -143,8 +145,15 @@ __device__ __forceinline__ void for_each_group_tile(const GroupTiles &a, volatil
                 end = max(begin, next);
                 tiles = (end - begin + TM - 1) / TM;
             }
-            f(GroupTile{e, begin + (rt - base) * TM, end, static_cast<int>(u % a.tiles_n) * TN, 0, 0,
-                        e < a.experts ? k_blocks : 0});
+            const int n0 = static_cast<int>(u % a.tiles_n) * TN, kb = e < a.experts ? k_blocks : 0;
+            if (EVEN > 0) {
+                constexpr int STEP = EVEN > 0 ? EVEN : 1;
+                const int each = ((end - begin + tiles - 1) / tiles + STEP - 1) / STEP * STEP;
+                const int row0 = min(begin + (rt - base) * each, end);
+                f(GroupTile{e, row0, min(row0 + each, end), n0, 0, 0, row0 < end ? kb : 0});
+            } else {
+                f(GroupTile{e, begin + (rt - base) * TM, end, n0, 0, 0, kb});
+            }
         }
     }
 }

@@ -7,35 +7,39 @@
 // short. Products of two 16-bit values are exact in fp32 and are summed in
 // fp32 in tensor memory; a value is rounded once, when C is written.
 //
-// Two CTAs on two SMs of a cluster make one 256 x 256 tile of C: each stages
-// 128 rows of A and 128 columns of B per 64-deep k-block, and one MMA of 256
-// x 256 x 16 issued by the even CTA reads both halves, so either operand
-// crosses each SM's shared memory once for 256 columns or rows. Two
-// accumulators of 256 columns fill tensor memory: the epilogue empties one
-// while the tensor core fills the other.
+// Two CTAs on two SMs of a cluster make one 256 x n tile (n <= 256): each
+// stages 128 rows of the first operand and n / 2 of the second per 64-deep
+// k-block, and one MMA of 256 x n x 16 issued by the even CTA reads both
+// halves. Two accumulators of 256 columns fill tensor memory: the epilogue
+// empties one while the tensor core fills the other.
+//
+// rows: the first operand is op(B), the second A, so the 256 are columns of C
+// and the n rows: the MMA's width is the one that costs time by the step (32
+// here), so a group of 40 rows is charged 64 and not 256. A group's rows are
+// spread evenly over its tiles. wgrad: both are full width; the groups are the
+// summed direction.
 //
 // Groups. The bounds are read on the device. Tiles never cross groups; the
 // workers (one CTA pair each) take the tiles of the groups in order, round
-// robin, each role of a worker walking the group bounds for itself. Along
-// rows a tile may reach past its group's end: those rows of A belong to the
-// next group, change only rows of C that are not written, and cost nothing
-// else. In wgrad the rows are the summed direction: the part of the last
-// k-block that lies past the group's end is zeroed in shared memory, in both
-// operands (a NaN of the next group times zero would stay), before the MMA
-// may read it.
+// robin, each role of a worker walking the group bounds for itself. Rows
+// staged past a tile's end belong to the next and change only sums that are
+// not written. In wgrad the part of the last k-block that lies past the
+// group's end is zeroed in shared memory, in both operands (a NaN of the next
+// group times zero would stay), before the MMA may read it.
 //
 // Layouts. An operand whose summed direction is contiguous in memory (A of
 // rows, B of op = T) is staged K-major, otherwise MN-major, both in 128-byte
 // swizzled rows as TMA writes them; the MMA takes either, so nothing is
 // transposed.
 //
-// Roles in each CTA (7 warps): warp 0 loads (TMA, 6 stages), warp 1 of the
-// even CTA issues the MMAs, warps 2-5 write C (one per quarter of tensor
-// memory's lanes: round to 16 bits, 32 x 64 chunks through shared memory,
-// TMA stores; rows of a chunk that crosses the group's end, and C that TMA
-// cannot address, with per-thread stores), warp 6 zeroes wgrad's tails. The
-// loads of both CTAs complete on the even CTA's barriers. Every wait is
-// bounded in time.
+// Roles in each CTA (12 warps): warp 0 loads the first operand and warp 11 the
+// second (TMA), warp 1 of the even CTA issues the MMAs, warps 2-9 write C (two
+// per quarter of tensor memory's lanes), warp 10 zeroes wgrad's tails. rows: a lane holds one column of C;
+// neighbouring lanes exchange values so that a warp stores two rows of 64
+// contiguous bytes at a time, and rows past the group's end cost nothing.
+// wgrad: 32 x 64 chunks through shared memory and TMA stores (per-thread
+// stores for C that TMA cannot address). The loads of both CTAs complete on
+// the even CTA's barriers. Every wait is bounded in time.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -55,22 +59,24 @@ using namespace tc;
 
 namespace g16 {
 
-constexpr int PM = 256, PN = 256, HM = 128, HN = 128;  // tile of a pair, this CTA's share of the operands
+constexpr int PM = 256, PN = 256, HM = 128, HN = 128;  // largest tile of a pair, this CTA's share of the operands
 constexpr int KB = 64;                                 // k-block: 64 values = 128 bytes
-constexpr int STAGES = 6;
+constexpr int ROW_STEP = 32;                           // rows: a tile's rows are a multiple of it
 constexpr int A_BYTES = HM * KB * 2, B_BYTES = HN * KB * 2, STAGE = A_BYTES + B_BYTES;
-constexpr int BOX = 64 * 128;  // bytes of a 64 x 64 MN-major box
-constexpr int CHUNK = 32 * 128;  // 32 rows x 64 columns of C
-constexpr int C0 = STAGES * STAGE;
-constexpr int EPI_WARPS = 4, TAIL_WARP = 6, THREADS = 7 * 32;
-constexpr int BAR0 = C0 + EPI_WARPS * 2 * CHUNK;
-constexpr int SMEM_BYTES = BAR0 + 256 + 1024;
+constexpr int BOX = 64 * 128;    // bytes of a 64 x 64 MN-major box
+constexpr int CHUNK = 32 * 128;  // 32 rows x 64 columns of C (wgrad)
+constexpr int EPI_WARPS = 8, TAIL_WARP = 2 + EPI_WARPS, LOAD2_WARP = TAIL_WARP + 1, THREADS = (LOAD2_WARP + 1) * 32;
+// Stages of the ring; in wgrad the C chunks (two a warp) take the place of one.
+constexpr int MAX_STAGES = 6;
+constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
+constexpr int bar0(bool wgrad) { return stages(wgrad) * STAGE + (wgrad ? EPI_WARPS * 2 * CHUNK : 0); }
+constexpr int smem_bytes(bool wgrad) { return bar0(wgrad) + 256 + 1024; }
 // mbarriers
-constexpr int FULL = 0, EMPTY = FULL + STAGES, TAIL = EMPTY + STAGES, ACC_FULL = TAIL + STAGES,
+constexpr int FULL = 0, EMPTY = FULL + MAX_STAGES, TAIL = EMPTY + MAX_STAGES, ACC_FULL = TAIL + MAX_STAGES,
               ACC_EMPTY = ACC_FULL + 2, DRAIN = ACC_EMPTY + 2, NBARS = DRAIN + 1;
 static_assert(NBARS * 8 + 24 <= 256, "barrier block");
-static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert(STAGE % 1024 == 0 && C0 % 1024 == 0, "1024-byte aligned swizzled buffers");
+static_assert(smem_bytes(true) <= 232448 && smem_bytes(false) <= 232448, "shared memory per CTA");
+static_assert(STAGE % 1024 == 0, "1024-byte aligned swizzled buffers");
 
 }  // namespace g16
 
@@ -79,9 +85,10 @@ struct Args16 {
     int64_t N;
     void *C;
     int64_t ldc, strideC;
-    int c_tma;
+    int c_tma;    // wgrad: C through TMA
+    int c_pairs;  // rows: C in 4-byte stores
     int bf16;
-    uint32_t idesc;
+    uint32_t idesc;  // without N
     uint64_t timeout_ns;
     int *watchdog;
 };
@@ -90,7 +97,15 @@ enum Form { ROWS_N, ROWS_T, WGRAD };
 
 template <Form FORM, class F>
 __device__ __forceinline__ void for_each_tile(const Args16 &a, volatile int *abort_flag, int index, int count, F &&f) {
-    for_each_group_tile<FORM == WGRAD, g16::PM, g16::PN, g16::KB>(a.tiles, abort_flag, index, count, f);
+    if (FORM == WGRAD)
+        for_each_group_tile<true, g16::PM, g16::PN, g16::KB>(a.tiles, abort_flag, index, count, f);
+    else  // rows in tiles of up to PN, columns in tiles of PM
+        for_each_group_tile<false, g16::PN, g16::PM, g16::KB, g16::ROW_STEP>(a.tiles, abort_flag, index, count, f);
+}
+
+// rows: the MMA's width for a tile.
+__device__ __forceinline__ int width_of(const GroupTile &u) {
+    return (u.row_end - u.row0 + g16::ROW_STEP - 1) / g16::ROW_STEP * g16::ROW_STEP;
 }
 
 // TMA load into this CTA's shared memory that completes its bytes on the
@@ -101,6 +116,12 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
         "{%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// 128 columns x 64 k of an MN-major operand: two boxes of 64 columns.
+__device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap *map, int x, int k, int item, uint32_t bar) {
+    tma_load_pair(dst, map, x, k, item, bar);
+    tma_load_pair(dst + g16::BOX, map, x + 64, k, item, bar);
 }
 
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t cta) {
@@ -143,10 +164,12 @@ template <Form FORM>
 __global__ void __launch_bounds__(g16::THREADS, 1)
     grouped16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Args16 a) {
+    // rows: tmA op(B), tmB A in boxes of 128 rows, tmC A in boxes of 32 rows.
+    constexpr int STAGES = g16::stages(FORM == WGRAD);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + g16::BAR0);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + g16::bar0(FORM == WGRAD));
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + g16::NBARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + g16::NBARS + 1);
     const uint32_t signal_word = smem_u32(bars + g16::NBARS + 2);
@@ -156,7 +179,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < g16::STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar(g16::FULL + s), 1);
             mbar_init(bar(g16::EMPTY + s), 1);
             mbar_init(bar(g16::TAIL + s), 1);
@@ -186,17 +209,24 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == g16::LOAD2_WARP) {
         // ------------------------------------------------------------------ loads
+        const bool first = warp == 0;  // the first operand (and the barriers' bytes), or the second
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
             for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
-                const int m0 = u.row0 + g16::HM * static_cast<int>(rank), n0 = u.n0 + g16::HN * static_cast<int>(rank);
+                // wgrad: rows of the matrix and its columns; rows: columns of C and its rows.
+                const int half = FORM == WGRAD ? g16::HN : width_of(u) / 2;
+                const int m0 = (FORM == WGRAD ? u.row0 : u.n0) + g16::HM * static_cast<int>(rank);
+                const int n0 = (FORM == WGRAD ? u.n0 : u.row0) + half * static_cast<int>(rank);
+                // rows: one box of 128 rows (a box costs more time than the rows it
+                // reads in vain), of 32 where those are enough.
+                const bool small = FORM != WGRAD && half <= 32;
+                const uint32_t bytes = g16::A_BYTES + (small ? 32 * 128 : g16::B_BYTES);
                 for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
-                    const int s = static_cast<int>(it % g16::STAGES);
-                    if (!mbar_wait<true>(bar(g16::EMPTY + s), ((it / g16::STAGES) & 1) ^ 1, a, abort_flag,
-                                         WD_PRODUCER)) {
+                    const int s = static_cast<int>(it % STAGES);
+                    if (!mbar_wait<true>(bar(g16::EMPTY + s), ((it / STAGES) & 1) ^ 1, a, abort_flag, WD_PRODUCER)) {
                         ok = false;
                         return;
                     }
@@ -206,25 +236,24 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                     if (tail) {
                         // Each CTA's own barrier; its tail warp signals the even CTA's.
                         to = map_to_cta(bar(g16::TAIL + s), rank);
-                        mbar_arrive_expect_tx(bar(g16::TAIL + s), g16::STAGE);
+                        if (first) mbar_arrive_expect_tx(bar(g16::TAIL + s), bytes);
                     } else {
                         to = map_to_cta(bar(g16::FULL + s), 0);
-                        if (rank == 0) mbar_arrive_expect_tx(bar(g16::FULL + s), 2 * g16::STAGE);
+                        if (first && rank == 0) mbar_arrive_expect_tx(bar(g16::FULL + s), 2 * bytes);
                     }
                     const int k = kb * g16::KB;
-                    if (FORM == WGRAD) {
-                        tma_load_pair(sa, &tmA, m0, u.k0 + k, 0, to);
-                        tma_load_pair(sa + g16::BOX, &tmA, m0 + 64, u.k0 + k, 0, to);
-                        tma_load_pair(sb, &tmB, n0, u.k0 + k, 0, to);
-                        tma_load_pair(sb + g16::BOX, &tmB, n0 + 64, u.k0 + k, 0, to);
+                    if (first) {
+                        if (FORM == WGRAD)
+                            load_mn(sa, &tmA, m0, u.k0 + k, 0, to);
+                        else if (FORM == ROWS_T)
+                            tma_load_pair(sa, &tmA, k, m0, u.group, to);
+                        else
+                            load_mn(sa, &tmA, m0, k, u.group, to);
+                    } else if (FORM == WGRAD) {
+                        load_mn(sb, &tmB, n0, u.k0 + k, 0, to);
                     } else {
-                        tma_load_pair(sa, &tmA, k, m0, 0, to);
-                        if (FORM == ROWS_T) {
-                            tma_load_pair(sb, &tmB, k, n0, u.group, to);
-                        } else {
-                            tma_load_pair(sb, &tmB, n0, k, u.group, to);
-                            tma_load_pair(sb + g16::BOX, &tmB, n0 + 64, k, u.group, to);
-                        }
+                        if (!small) tma_load_pair(sb, &tmB, k, n0, 0, to);
+                        if (small) tma_load_pair(sb, &tmC, k, n0, 0, to);
                     }
                 }
             });
@@ -242,23 +271,25 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                                                              abort_flag, WD_MMA_ACC));
                 tc_fence_after();
                 const uint32_t dt = tmem_base + d * g16::PN;
+                const uint32_t idesc =
+                    a.idesc | (static_cast<uint32_t>((FORM == WGRAD ? g16::PN : width_of(u)) >> 3) << 17);
                 for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
-                    const int s = static_cast<int>(it % g16::STAGES);
-                    ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::FULL + s), (it / g16::STAGES) & 1, a,
+                    const int s = static_cast<int>(it % STAGES);
+                    ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::FULL + s), (it / STAGES) & 1, a,
                                                                  abort_flag, WD_MMA_FULL));
                     if (!ok) return;
                     tc_fence_after();
                     const uint32_t sa = base + static_cast<uint32_t>(s * g16::STAGE), sb = sa + g16::A_BYTES;
-                    const uint64_t da = FORM == WGRAD ? mn_desc(sa) : sw128_desc(sa);
-                    const uint64_t db = FORM == ROWS_T ? sw128_desc(sb) : mn_desc(sb);
+                    const uint64_t da = FORM == ROWS_T ? sw128_desc(sa) : mn_desc(sa);
+                    const uint64_t db = FORM == WGRAD ? mn_desc(sb) : sw128_desc(sb);
                     // 16 values of k further: 32 bytes along a K-major row, 16
                     // rows of 128 bytes in an MN-major box.
-                    constexpr uint64_t step_a = (FORM == WGRAD ? 16 * 128 : 32) >> 4;
-                    constexpr uint64_t step_b = (FORM == ROWS_T ? 32 : 16 * 128) >> 4;
+                    constexpr uint64_t step_a = (FORM == ROWS_T ? 32 : 16 * 128) >> 4;
+                    constexpr uint64_t step_b = (FORM == WGRAD ? 16 * 128 : 32) >> 4;
                     if (leader) {
 #pragma unroll
                         for (int ks = 0; ks < g16::KB / 16; ++ks)
-                            mma16_pair(dt, da + ks * step_a, db + ks * step_b, a.idesc, kb > 0 || ks > 0);
+                            mma16_pair(dt, da + ks * step_a, db + ks * step_b, idesc, kb > 0 || ks > 0);
                         tc_commit2(bar(g16::EMPTY + s));
                     }
                     __syncwarp();
@@ -288,7 +319,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                 const int left = u.k_rows % g16::KB;
                 it += static_cast<uint32_t>(u.k_blocks);
                 if (left == 0) return;
-                const int s = static_cast<int>((it - 1) % g16::STAGES);
+                const int s = static_cast<int>((it - 1) % STAGES);
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(bar(g16::TAIL + s), (uses >> s) & 1, a, abort_flag, WD_PRODUCER));
                 if (!ok) return;
@@ -314,8 +345,9 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
         }
     } else {
         // --------------------------------------------------------------- epilogue
-        const int q = warp & 3;  // quarter of tensor memory's lanes
-        const uint32_t stage0 = base + g16::C0 + static_cast<uint32_t>((warp - 2) * 2 * g16::CHUNK);
+        const int q = warp & 3, second = (warp - 2) >> 2;  // quarter of tensor memory's lanes, half of the columns
+        const uint32_t stage0 =
+            base + static_cast<uint32_t>(STAGES * g16::STAGE + (warp - 2) * 2 * g16::CHUNK);  // wgrad
         uint32_t units = 0, chunks = 0;
         bool ok = true;
         for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
@@ -329,12 +361,56 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                 tc_fence_after();
                 ++units;
             }
+            const uint32_t dt = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + d * g16::PN;
+            auto release = [&] {  // the accumulator is out of tensor memory (this warp's part)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(bar(g16::ACC_EMPTY + d), 0);
+            };
+            if (FORM != WGRAD) {
+                // Lanes are columns of C, accumulator columns its rows.
+                const int col = u.n0 + g16::HM * static_cast<int>(rank) + 32 * q + lane;
+                const int rows = u.row_end - u.row0;
+                uint16_t *c0 = static_cast<uint16_t *>(a.C) + static_cast<int64_t>(u.row0) * a.ldc;
+#pragma unroll 1
+                for (int r0 = 32 * second; r0 < rows; r0 += 64) {
+                    float x[32];
+                    if (summed) {
+                        tmem_load32(dt + static_cast<uint32_t>(r0), x);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+                    }
+                    if (a.c_pairs) {
+                        // Even lanes take row 2 j, odd lanes row 2 j + 1, of their own
+                        // and their neighbour's column.
+                        const bool odd = lane & 1;
+                        const int even_col = col & ~1;
+                        uint16_t *p = c0 + static_cast<int64_t>(r0 + (odd ? 1 : 0)) * a.ldc + even_col;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, p += 2 * a.ldc) {
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 1);
+                            const uint32_t v = odd ? pack16(got, x[2 * j + 1], a.bf16) : pack16(x[2 * j], got, a.bf16);
+                            if (r0 + 2 * j + (odd ? 1 : 0) >= rows || even_col >= a.N) continue;
+                            if (even_col + 1 < a.N)
+                                *reinterpret_cast<uint32_t *>(p) = v;
+                            else
+                                *p = static_cast<uint16_t>(v);
+                        }
+                    } else {
+                        uint16_t *p = c0 + static_cast<int64_t>(r0) * a.ldc + col;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += a.ldc)
+                            if (r0 + j < rows && col < a.N) *p = static_cast<uint16_t>(pack16(x[j], 0.0f, a.bf16));
+                    }
+                }
+                if (summed) release();
+                return;
+            }
             const int row0 = u.row0 + g16::HM * static_cast<int>(rank) + 32 * q;
             const int rows = min(32, u.row_end - row0);  // may be negative
-            const uint32_t dt = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + d * g16::PN;
-            const int item = FORM == WGRAD ? u.group : 0;
 #pragma unroll 1
-            for (int ch = 0; ch < g16::PN / 64; ++ch) {
+            for (int ch = 2 * second; ch < 2 * second + 2; ++ch) {
                 const int col0 = u.n0 + 64 * ch;
                 const bool wanted = rows > 0 && col0 < a.N;  // uniform over the warp
                 uint32_t v[32];
@@ -350,12 +426,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0;
                 }
-                if (summed && ch == g16::PN / 64 - 1) {
-                    // The accumulator is out of tensor memory.
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(bar(g16::ACC_EMPTY + d), 0);
-                }
+                if (summed && ch == 2 * second + 1) release();
                 if (!wanted) continue;
                 const uint32_t buf = stage0 + (chunks & 1) * g16::CHUNK;
                 ++chunks;
@@ -369,12 +440,12 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                 if (a.c_tma && rows == 32) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) tma_store_3d(&tmC, col0, row0, item, buf);
+                    if (lane == 0) tma_store_3d(&tmC, col0, row0, u.group, buf);
                 } else {
                     // Row by row, the lanes along the row.
                     __syncwarp();
-                    uint16_t *c = static_cast<uint16_t *>(a.C) + item * a.strideC + static_cast<int64_t>(row0) * a.ldc +
-                                  col0;
+                    uint16_t *c = static_cast<uint16_t *>(a.C) + u.group * a.strideC +
+                                  static_cast<int64_t>(row0) * a.ldc + col0;
                     const int cols = static_cast<int>(min(static_cast<int64_t>(64), a.N - col0));
                     for (int r = 0; r < rows; ++r, c += a.ldc) {
                         const uint32_t w = __float_as_uint(ld_shared_f32(buf + sw128_offset(r, lane >> 2) +
@@ -438,12 +509,12 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(g16::THREADS);
-    cfg.dynamicSmemBytes = g16::SMEM_BYTES;
+    cfg.dynamicSmemBytes = g16::smem_bytes(FORM == WGRAD);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     std::call_once(g_once[dev.device][FORM], [&] {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g16::SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g16::smem_bytes(FORM == WGRAD));
         int n = 0;
         if (e == cudaSuccess) {
             cudaLaunchConfig_t q = cfg;
@@ -465,22 +536,21 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     alignas(64) CUtensorMap mapA{}, mapB{}, mapC{};
     const int64_t strideB = p.experts > 1 ? p.strideB : 0, strideC = p.experts > 1 ? p.strideC : 0;
     bool ok;
+    bool c_tma = false;
     if (FORM == WGRAD) {
         ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.M, p.lda, 1, 0, 64, g16::KB, sw) &&
              encode_map_typed(&mapB, type, 2, p.B, p.rows, p.N, p.ldb, 1, 0, 64, g16::KB, sw);
+        c_tma = mappable(p.C, p.M, p.ldc, p.experts, p.strideC) &&
+                encode_map_typed(&mapC, type, 2, p.C, p.M, p.N, p.ldc, p.experts, strideC, 64, 32, sw);
+        if (!c_tma) mapC = mapA;  // not read by the kernel
     } else {
-        ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.K, p.lda, 1, 0, g16::KB, g16::HM, sw) &&
-             (FORM == ROWS_T ? encode_map_typed(&mapB, type, 2, p.B, p.N, p.K, p.ldb, p.experts, strideB, g16::KB,
-                                                g16::HN, sw)
-                             : encode_map_typed(&mapB, type, 2, p.B, p.K, p.N, p.ldb, p.experts, strideB, 64,
-                                                g16::KB, sw));
+        ok = (FORM == ROWS_T
+                  ? encode_map_typed(&mapA, type, 2, p.B, p.N, p.K, p.ldb, p.experts, strideB, g16::KB, g16::HM, sw)
+                  : encode_map_typed(&mapA, type, 2, p.B, p.K, p.N, p.ldb, p.experts, strideB, 64, g16::KB, sw)) &&
+             encode_map_typed(&mapB, type, 2, p.A, p.rows, p.K, p.lda, 1, 0, g16::KB, g16::HN, sw) &&
+             encode_map_typed(&mapC, type, 2, p.A, p.rows, p.K, p.lda, 1, 0, g16::KB, 32, sw);
     }
     if (!ok) return SGEMM_ERR_LAUNCH;
-    const bool c_tma =
-        (FORM == WGRAD ? mappable(p.C, p.M, p.ldc, p.experts, p.strideC) : mappable(p.C, p.rows, p.ldc, 1, 0)) &&
-        (FORM == WGRAD ? encode_map_typed(&mapC, type, 2, p.C, p.M, p.N, p.ldc, p.experts, strideC, 64, 32, sw)
-                       : encode_map_typed(&mapC, type, 2, p.C, p.rows, p.N, p.ldc, 1, 0, 64, 32, sw));
-    if (!c_tma) mapC = mapA;  // not read by the kernel
 
     Args16 a{};
     a.N = p.N;
@@ -498,18 +568,19 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
                          static_cast<int>(tiles_m),
                          static_cast<int>(tiles_n)};
     a.c_tma = c_tma ? 1 : 0;
+    a.c_pairs = reinterpret_cast<uintptr_t>(p.C) % 4 == 0 && p.ldc % 2 == 0;
     a.bf16 = p.type == SGEMM_TYPE_BF16 ? 1 : 0;
     // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B
     // fp16 (0) or bf16 (1) in bits 7-9 and 10-12, bit 15 / 16: A / B MN-major,
-    // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+    // N >> 3 in bits 17-22 (the kernel's), M >> 4 in bits 24-28.
     const uint32_t t = a.bf16 ? 1u : 0u;
-    a.idesc = (1u << 4) | (t << 7) | (t << 10) | (FORM == WGRAD ? 1u << 15 : 0u) | (FORM == ROWS_T ? 0u : 1u << 16) |
-              (static_cast<uint32_t>(g16::PN >> 3) << 17) | (static_cast<uint32_t>(g16::PM >> 4) << 24);
+    a.idesc = (1u << 4) | (t << 7) | (t << 10) | (FORM == ROWS_T ? 0u : 1u << 15) | (FORM == WGRAD ? 1u << 16 : 0u) |
+              (static_cast<uint32_t>(g16::PM >> 4) << 24);
     a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
     a.watchdog = flag;
     // Every group may end in a part of a tile, and so may the rest.
     const int64_t units = FORM == WGRAD ? tiles_m * tiles_n * p.experts
-                                        : ((p.rows + g16::PM - 1) / g16::PM + p.experts) * tiles_n;
+                                        : ((p.rows + g16::PN - 1) / g16::PN + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a) != cudaSuccess) {
         cudaGetLastError();
