@@ -13,11 +13,11 @@
 // halves. Two accumulators of 256 columns fill tensor memory: the epilogue
 // empties one while the tensor core fills the other.
 //
-// rows: the first operand is op(B), the second A, so the 256 are columns of C
-// and the n rows: the MMA's width is the one that costs time by the step (32
-// here), so a group of 40 rows is charged 64 and not 256. A group's rows are
-// spread evenly over its tiles. wgrad: both are full width; the groups are the
-// summed direction.
+// The MMA's width n is the side that costs time by the step (32 here). rows:
+// the first operand is op(B) and gives the columns of C, the second A and its
+// rows, so a group of 40 rows is charged 64 and not 256; a group's rows are
+// spread evenly over its tiles. wgrad: the first operand is A, the second B;
+// the groups are the summed direction.
 //
 // Groups. The bounds are read on the device. Tiles never cross groups; the
 // workers (one CTA pair each) take the tiles of the groups in order, round
@@ -34,12 +34,16 @@
 //
 // Roles in each CTA (12 warps): warp 0 loads the first operand and warp 11 the
 // second (TMA), warp 1 of the even CTA issues the MMAs, warps 2-9 write C (two
-// per quarter of tensor memory's lanes), warp 10 zeroes wgrad's tails. rows: a lane holds one column of C;
-// neighbouring lanes exchange values so that a warp stores two rows of 64
-// contiguous bytes at a time, and rows past the group's end cost nothing.
-// wgrad: 32 x 64 chunks through shared memory and TMA stores (per-thread
-// stores for C that TMA cannot address). The loads of both CTAs complete on
-// the even CTA's barriers. Every wait is bounded in time.
+// per quarter of tensor memory's lanes), warp 10 zeroes wgrad's tails. The loads
+// of both CTAs complete on the even CTA's barriers. Every wait is bounded.
+//
+// Writing C. wgrad, whose tiles are short (a group's rows) and many: a lane
+// holds a row, 32 x 64 chunks go through shared memory and TMA stores, about
+// 150 instructions for 2048 values. rows: a lane holds a column of C; eight
+// lanes exchange values so that a lane stores 16 bytes of a row, about 200
+// instructions for 1024 values, hidden behind the longer sums, and rows past
+// the group's end cost nothing. (The same way for wgrad: 365 us in place of 224
+// for 16384 rows, 32 experts, 2048 x 4096.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -61,18 +65,18 @@ namespace g16 {
 
 constexpr int PM = 256, PN = 256, HM = 128, HN = 128;  // largest tile of a pair, this CTA's share of the operands
 constexpr int KB = 64;                                 // k-block: 64 values = 128 bytes
-constexpr int ROW_STEP = 32;                           // rows: a tile's rows are a multiple of it
+constexpr int ROW_STEP = 32;                           // a tile's width is a multiple of it
 constexpr int A_BYTES = HM * KB * 2, B_BYTES = HN * KB * 2, STAGE = A_BYTES + B_BYTES;
 constexpr int BOX = 64 * 128;    // bytes of a 64 x 64 MN-major box
-constexpr int CHUNK = 32 * 128;  // 32 rows x 64 columns of C (wgrad)
 constexpr int EPI_WARPS = 8, TAIL_WARP = 2 + EPI_WARPS, LOAD2_WARP = TAIL_WARP + 1, THREADS = (LOAD2_WARP + 1) * 32;
+constexpr int CHUNK = 32 * 128;  // 32 rows x 64 columns of C (wgrad)
 // Stages of the ring; in wgrad the C chunks (two a warp) take the place of one.
-constexpr int MAX_STAGES = 6;
+constexpr int STAGES = 6;
 constexpr int stages(bool wgrad) { return wgrad ? 5 : 6; }
 constexpr int bar0(bool wgrad) { return stages(wgrad) * STAGE + (wgrad ? EPI_WARPS * 2 * CHUNK : 0); }
 constexpr int smem_bytes(bool wgrad) { return bar0(wgrad) + 256 + 1024; }
 // mbarriers
-constexpr int FULL = 0, EMPTY = FULL + MAX_STAGES, TAIL = EMPTY + MAX_STAGES, ACC_FULL = TAIL + MAX_STAGES,
+constexpr int FULL = 0, EMPTY = FULL + STAGES, TAIL = EMPTY + STAGES, ACC_FULL = TAIL + STAGES,
               ACC_EMPTY = ACC_FULL + 2, DRAIN = ACC_EMPTY + 2, NBARS = DRAIN + 1;
 static_assert(NBARS * 8 + 24 <= 256, "barrier block");
 static_assert(smem_bytes(true) <= 232448 && smem_bytes(false) <= 232448, "shared memory per CTA");
@@ -85,9 +89,8 @@ struct Args16 {
     int64_t N;
     void *C;
     int64_t ldc, strideC;
-    int c_tma;    // wgrad: C through TMA
-    int c_pairs;  // rows: C in 4-byte stores
-    int bf16;
+    int c_tma;  // wgrad: C through TMA
+    int c_vec;  // rows: C in 16-byte stores
     uint32_t idesc;  // without N
     uint64_t timeout_ns;
     int *watchdog;
@@ -99,13 +102,15 @@ template <Form FORM, class F>
 __device__ __forceinline__ void for_each_tile(const Args16 &a, volatile int *abort_flag, int index, int count, F &&f) {
     if (FORM == WGRAD)
         for_each_group_tile<true, g16::PM, g16::PN, g16::KB>(a.tiles, abort_flag, index, count, f);
-    else  // rows in tiles of up to PN, columns in tiles of PM
+    else
         for_each_group_tile<false, g16::PN, g16::PM, g16::KB, g16::ROW_STEP>(a.tiles, abort_flag, index, count, f);
 }
 
-// rows: the MMA's width for a tile.
-__device__ __forceinline__ int width_of(const GroupTile &u) {
-    return (u.row_end - u.row0 + g16::ROW_STEP - 1) / g16::ROW_STEP * g16::ROW_STEP;
+// The MMA's width: the tile's rows (rows) or columns (wgrad), rounded up.
+template <Form FORM>
+__device__ __forceinline__ int width_of(const Args16 &a, const GroupTile &u) {
+    const int n = FORM == WGRAD ? static_cast<int>(min(static_cast<int64_t>(g16::PN), a.N - u.n0)) : u.row_end - u.row0;
+    return (n + g16::ROW_STEP - 1) / g16::ROW_STEP * g16::ROW_STEP;
 }
 
 // TMA load into this CTA's shared memory that completes its bytes on the
@@ -118,10 +123,11 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
         : "memory");
 }
 
-// 128 columns x 64 k of an MN-major operand: two boxes of 64 columns.
-__device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap *map, int x, int k, int item, uint32_t bar) {
+// 64 k of an MN-major operand: one or two boxes of 64 columns.
+__device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap *map, int x, int k, int item, int boxes,
+                                        uint32_t bar) {
     tma_load_pair(dst, map, x, k, item, bar);
-    tma_load_pair(dst + g16::BOX, map, x + 64, k, item, bar);
+    if (boxes > 1) tma_load_pair(dst + g16::BOX, map, x + 64, k, item, bar);
 }
 
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t cta) {
@@ -151,8 +157,9 @@ __device__ __forceinline__ void mma16_pair(uint32_t d_tmem, uint64_t a_desc, uin
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
-    if (bf16) {
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if (BF16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
@@ -160,11 +167,47 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <Form FORM>
+// A 32 x 32 block of sums, lane = column, x[j] = row j, as 16-bit rows: v[i]
+// becomes columns 8 (lane / 8) .. + 7 of row 8 i + lane % 8. Three exchanges
+// between lanes, each pairing columns and halving rows.
+template <bool BF16>
+__device__ __forceinline__ void gather_rows(const float (&x)[32], int lane, uint32_t (&v)[4][4]) {
+    const bool b1 = lane & 2, b2 = lane & 4;
+    // Of rows 2 j (low halves) and 2 j + 1 of this lane's and its neighbour's
+    // column: even lanes take row 2 j, odd lanes row 2 j + 1.
+    const uint32_t halves = lane & 1 ? 0x3276u : 0x5410u;
+    uint32_t one[16];  // rows 2 j + lane % 2, two columns
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t own = pack16<BF16>(x[2 * j], x[2 * j + 1]);
+        one[j] = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), halves);
+    }
+    uint32_t two[8][2];  // rows 4 i + lane % 4, four columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t own = b1 ? one[2 * i + 1] : one[2 * i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? one[2 * i] : one[2 * i + 1], 2);
+        two[i][0] = b1 ? got : own;
+        two[i][1] = b1 ? own : got;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t own = b2 ? two[2 * i + 1][c] : two[2 * i][c];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b2 ? two[2 * i][c] : two[2 * i + 1][c], 4);
+            v[i][c] = b2 ? got : own;
+            v[i][2 + c] = b2 ? own : got;
+        }
+    }
+}
+
+template <Form FORM, bool BF16>
 __global__ void __launch_bounds__(g16::THREADS, 1)
     grouped16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Args16 a) {
-    // rows: tmA op(B), tmB A in boxes of 128 rows, tmC A in boxes of 32 rows.
+    // tmA, tmB: the first and second operand. tmC: wgrad: C; rows: the second
+    // operand in boxes of 32 rows (tmB: 128).
     constexpr int STAGES = g16::stages(FORM == WGRAD);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -216,14 +259,15 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
             uint32_t it = 0;
             bool ok = true;
             for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const GroupTile &u) {
-                // wgrad: rows of the matrix and its columns; rows: columns of C and its rows.
-                const int half = FORM == WGRAD ? g16::HN : width_of(u) / 2;
+                const int half = width_of<FORM>(a, u) / 2;
                 const int m0 = (FORM == WGRAD ? u.row0 : u.n0) + g16::HM * static_cast<int>(rank);
                 const int n0 = (FORM == WGRAD ? u.n0 : u.row0) + half * static_cast<int>(rank);
                 // rows: one box of 128 rows (a box costs more time than the rows it
                 // reads in vain), of 32 where those are enough.
                 const bool small = FORM != WGRAD && half <= 32;
-                const uint32_t bytes = g16::A_BYTES + (small ? 32 * 128 : g16::B_BYTES);
+                const int boxes = half > 64 ? 2 : 1;  // wgrad
+                const uint32_t bytes =
+                    g16::A_BYTES + (FORM == WGRAD ? boxes * g16::BOX : small ? 32 * 128 : g16::B_BYTES);
                 for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                     const int s = static_cast<int>(it % STAGES);
                     if (!mbar_wait<true>(bar(g16::EMPTY + s), ((it / STAGES) & 1) ^ 1, a, abort_flag, WD_PRODUCER)) {
@@ -231,7 +275,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                         return;
                     }
                     const uint32_t sa = base + static_cast<uint32_t>(s * g16::STAGE), sb = sa + g16::A_BYTES;
-                    const bool tail = FORM == WGRAD && (kb + 1) * g16::KB > u.k_rows;
+                    const bool tail = FORM == WGRAD && (kb + 1) * g16::KB > u.k_rows && u.k_rows % 16 != 0;
                     uint32_t to;
                     if (tail) {
                         // Each CTA's own barrier; its tail warp signals the even CTA's.
@@ -244,16 +288,15 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                     const int k = kb * g16::KB;
                     if (first) {
                         if (FORM == WGRAD)
-                            load_mn(sa, &tmA, m0, u.k0 + k, 0, to);
+                            load_mn(sa, &tmA, m0, u.k0 + k, 0, 2, to);
                         else if (FORM == ROWS_T)
                             tma_load_pair(sa, &tmA, k, m0, u.group, to);
                         else
-                            load_mn(sa, &tmA, m0, k, u.group, to);
+                            load_mn(sa, &tmA, m0, k, u.group, 2, to);
                     } else if (FORM == WGRAD) {
-                        load_mn(sb, &tmB, n0, u.k0 + k, 0, to);
+                        load_mn(sb, &tmB, n0, u.k0 + k, 0, boxes, to);
                     } else {
-                        if (!small) tma_load_pair(sb, &tmB, k, n0, 0, to);
-                        if (small) tma_load_pair(sb, &tmC, k, n0, 0, to);
+                        tma_load_pair(sb, small ? &tmC : &tmB, k, n0, 0, to);
                     }
                 }
             });
@@ -272,7 +315,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                 tc_fence_after();
                 const uint32_t dt = tmem_base + d * g16::PN;
                 const uint32_t idesc =
-                    a.idesc | (static_cast<uint32_t>((FORM == WGRAD ? g16::PN : width_of(u)) >> 3) << 17);
+                    a.idesc | (static_cast<uint32_t>(width_of<FORM>(a, u) >> 3) << 17);
                 for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                     const int s = static_cast<int>(it % STAGES);
                     ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(g16::FULL + s), (it / STAGES) & 1, a,
@@ -286,10 +329,12 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                     // rows of 128 bytes in an MN-major box.
                     constexpr uint64_t step_a = (FORM == ROWS_T ? 32 : 16 * 128) >> 4;
                     constexpr uint64_t step_b = (FORM == WGRAD ? 16 * 128 : 32) >> 4;
+                    // wgrad: of the last k-block only the 16s that hold rows of the group.
+                    const int left = FORM == WGRAD ? u.k_rows - kb * g16::KB : g16::KB;
                     if (leader) {
 #pragma unroll
                         for (int ks = 0; ks < g16::KB / 16; ++ks)
-                            mma16_pair(dt, da + ks * step_a, db + ks * step_b, idesc, kb > 0 || ks > 0);
+                            if (16 * ks < left) mma16_pair(dt, da + ks * step_a, db + ks * step_b, idesc, kb > 0 || ks > 0);
                         tc_commit2(bar(g16::EMPTY + s));
                     }
                     __syncwarp();
@@ -318,15 +363,16 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                 if (!ok || u.k_blocks == 0) return;
                 const int left = u.k_rows % g16::KB;
                 it += static_cast<uint32_t>(u.k_blocks);
-                if (left == 0) return;
+                if (left % 16 == 0) return;
                 const int s = static_cast<int>((it - 1) % STAGES);
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(bar(g16::TAIL + s), (uses >> s) & 1, a, abort_flag, WD_PRODUCER));
                 if (!ok) return;
                 uses ^= 1u << s;
                 const uint32_t st = base + static_cast<uint32_t>(s * g16::STAGE);
-                // Rows left .. 63 of each of the four boxes, 16 bytes a lane.
-                const int vecs = (g16::KB - left) * 8;
+                // Rows from `left` to the end of its 16 of each of the four boxes,
+                // 16 bytes a lane; the MMAs of later 16s are not issued.
+                const int vecs = (16 - left % 16) * 8;
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b)
                     for (int i = lane; i < vecs; i += 32)
@@ -381,27 +427,28 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) x[j] = 0.0f;
                     }
-                    if (a.c_pairs) {
-                        // Even lanes take row 2 j, odd lanes row 2 j + 1, of their own
-                        // and their neighbour's column.
-                        const bool odd = lane & 1;
-                        const int even_col = col & ~1;
-                        uint16_t *p = c0 + static_cast<int64_t>(r0 + (odd ? 1 : 0)) * a.ldc + even_col;
+                    if (a.c_vec) {
+                        uint32_t v[4][4];
+                        gather_rows<BF16>(x, lane, v);
+                        const int c8 = (col & ~31) + (lane >> 3) * 8;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j, p += 2 * a.ldc) {
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 1);
-                            const uint32_t v = odd ? pack16(got, x[2 * j + 1], a.bf16) : pack16(x[2 * j], got, a.bf16);
-                            if (r0 + 2 * j + (odd ? 1 : 0) >= rows || even_col >= a.N) continue;
-                            if (even_col + 1 < a.N)
-                                *reinterpret_cast<uint32_t *>(p) = v;
-                            else
-                                *p = static_cast<uint16_t>(v);
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = r0 + 8 * i + (lane & 7);
+                            uint16_t *p = c0 + static_cast<int64_t>(row) * a.ldc + c8;
+                            if (row >= rows) continue;
+                            if (c8 + 8 <= a.N) {
+                                *reinterpret_cast<uint4 *>(p) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (c8 + c < a.N) p[c] = static_cast<uint16_t>(v[i][c >> 1] >> (16 * (c & 1)));
+                            }
                         }
                     } else {
                         uint16_t *p = c0 + static_cast<int64_t>(r0) * a.ldc + col;
 #pragma unroll
                         for (int j = 0; j < 32; ++j, p += a.ldc)
-                            if (r0 + j < rows && col < a.N) *p = static_cast<uint16_t>(pack16(x[j], 0.0f, a.bf16));
+                            if (r0 + j < rows && col < a.N) *p = static_cast<uint16_t>(pack16<BF16>(x[j], 0.0f));
                     }
                 }
                 if (summed) release();
@@ -418,10 +465,10 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                     float x[32];
                     tmem_load32(dt + static_cast<uint32_t>(64 * ch), x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = pack16(x[2 * j], x[2 * j + 1], a.bf16);
+                    for (int j = 0; j < 16; ++j) v[j] = pack16<BF16>(x[2 * j], x[2 * j + 1]);
                     tmem_load32(dt + static_cast<uint32_t>(64 * ch + 32), x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[16 + j] = pack16(x[2 * j], x[2 * j + 1], a.bf16);
+                    for (int j = 0; j < 16; ++j) v[16 + j] = pack16<BF16>(x[2 * j], x[2 * j + 1]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0;
@@ -488,9 +535,9 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
 }
 
 constexpr int kMaxDevices = 64;
-std::once_flag g_once[kMaxDevices][3];
-cudaError_t g_err[kMaxDevices][3];
-int g_clusters[kMaxDevices][3];
+std::once_flag g_once[kMaxDevices][6];
+cudaError_t g_err[kMaxDevices][6];
+int g_clusters[kMaxDevices][6];
 
 // Whether a tensor map can describe `items` matrices of rows x ld 16-bit
 // values, `stride` apart.
@@ -499,9 +546,10 @@ bool mappable(const void *p, int64_t rows, int64_t ld, int64_t items, int64_t st
            (items == 1 || (stride % 8 == 0 && stride >= rows * ld));
 }
 
-template <Form FORM>
+template <Form FORM, bool BF16>
 int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    auto kernel = grouped16_kernel<FORM>;
+    auto kernel = grouped16_kernel<FORM, BF16>;
+    constexpr int idx = FORM + (BF16 ? 3 : 0);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -513,7 +561,7 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    std::call_once(g_once[dev.device][FORM], [&] {
+    std::call_once(g_once[dev.device][idx], [&] {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g16::smem_bytes(FORM == WGRAD));
         int n = 0;
         if (e == cudaSuccess) {
@@ -521,22 +569,21 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
             q.gridDim = dim3(2 * (dev.sm_count / 2));
             e = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
         }
-        g_err[dev.device][FORM] = e;
-        g_clusters[dev.device][FORM] = n;
+        g_err[dev.device][idx] = e;
+        g_clusters[dev.device][idx] = n;
     });
-    const int clusters = g_clusters[dev.device][FORM];
+    const int clusters = g_clusters[dev.device][idx];
     int *flag = watchdog_flag_device_ptr();
-    if (g_err[dev.device][FORM] != cudaSuccess || clusters < 1 || !flag) {
+    if (g_err[dev.device][idx] != cudaSuccess || clusters < 1 || !flag) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
     }
     const CUtensorMapDataType type =
-        p.type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     alignas(64) CUtensorMap mapA{}, mapB{}, mapC{};
     const int64_t strideB = p.experts > 1 ? p.strideB : 0, strideC = p.experts > 1 ? p.strideC : 0;
-    bool ok;
-    bool c_tma = false;
+    bool ok, c_tma = false;
     if (FORM == WGRAD) {
         ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.M, p.lda, 1, 0, 64, g16::KB, sw) &&
              encode_map_typed(&mapB, type, 2, p.B, p.rows, p.N, p.ldb, 1, 0, 64, g16::KB, sw);
@@ -568,12 +615,11 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
                          static_cast<int>(tiles_m),
                          static_cast<int>(tiles_n)};
     a.c_tma = c_tma ? 1 : 0;
-    a.c_pairs = reinterpret_cast<uintptr_t>(p.C) % 4 == 0 && p.ldc % 2 == 0;
-    a.bf16 = p.type == SGEMM_TYPE_BF16 ? 1 : 0;
+    a.c_vec = reinterpret_cast<uintptr_t>(p.C) % 16 == 0 && p.ldc % 8 == 0;
     // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B
     // fp16 (0) or bf16 (1) in bits 7-9 and 10-12, bit 15 / 16: A / B MN-major,
     // N >> 3 in bits 17-22 (the kernel's), M >> 4 in bits 24-28.
-    const uint32_t t = a.bf16 ? 1u : 0u;
+    const uint32_t t = BF16 ? 1u : 0u;
     a.idesc = (1u << 4) | (t << 7) | (t << 10) | (FORM == ROWS_T ? 0u : 1u << 15) | (FORM == WGRAD ? 1u << 16 : 0u) |
               (static_cast<uint32_t>(g16::PM >> 4) << 24);
     a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
@@ -665,10 +711,16 @@ int copy_operands(const GroupedProblem &p, uint16_t *scratch, const DeviceInfo &
     return SGEMM_OK;
 }
 
+template <bool BF16>
 int launch_form(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    if (p.wgrad) return launch16<WGRAD>(p, dev, stream, launches);
-    return p.transB == SGEMM_OP_T ? launch16<ROWS_T>(p, dev, stream, launches)
-                                  : launch16<ROWS_N>(p, dev, stream, launches);
+    if (p.wgrad) return launch16<WGRAD, BF16>(p, dev, stream, launches);
+    return p.transB == SGEMM_OP_T ? launch16<ROWS_T, BF16>(p, dev, stream, launches)
+                                  : launch16<ROWS_N, BF16>(p, dev, stream, launches);
+}
+
+int launch_any(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    return p.type == SGEMM_TYPE_BF16 ? launch_form<true>(p, dev, stream, launches)
+                                     : launch_form<false>(p, dev, stream, launches);
 }
 
 }  // namespace
@@ -693,12 +745,12 @@ bool grouped16_supports(const GroupedProblem &p) {
 
 int grouped16_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
-    if (a_mappable(p) && b_mappable(p)) return launch_form(p, dev, stream, launches);
+    if (a_mappable(p) && b_mappable(p)) return launch_any(p, dev, stream, launches);
     float *scratch = scratch_alloc(dev, copy_bytes(p), stream);
     if (!scratch) return SGEMM_ERR_UNSUPPORTED;
     GroupedProblem q;
     int rc = copy_operands(p, reinterpret_cast<uint16_t *>(scratch), dev, stream, &q, launches);
-    if (rc == SGEMM_OK) rc = launch_form(q, dev, stream, launches);
+    if (rc == SGEMM_OK) rc = launch_any(q, dev, stream, launches);
     scratch_free(scratch, stream);
     return rc;
 }
