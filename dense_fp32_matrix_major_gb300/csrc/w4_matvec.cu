@@ -22,7 +22,9 @@
 //     result keeps 8.
 //   * fp32 x: cut into three bf16 terms that add up to it (3 x 8 bits cover
 //     its 24), each multiplied exactly by q - zero, taken from 128 + q by
-//     subtracting 128 + zero before the product, so no bits are lost.
+//     subtracting 128 + zero before the product, so no bits are lost. A term
+//     is a column of the instruction: one or two rows of x fill one (6 of 8
+//     columns), three to five two, up to eight three.
 // The sums of x per group are made in fp32 when x is staged. One 32-bit word
 // holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j, j + 4), so x
 // is laid out in shared memory in the order 0 4 1 5 2 6 3 7. An infinity or
@@ -285,24 +287,28 @@ __device__ __forceinline__ int find_members(const W4Args &a, int pass, Members *
 // Steps of K values of k, in pairs: the last may hold zeros only.
 __host__ __device__ __forceinline__ int64_t steps_of(int64_t K) { return (K + PAIR * STEP - 1) / (PAIR * STEP) * PAIR; }
 
-// A step of x as the matrix instructions read it: term, unit u, row, lane t, 8
-// values, then, where zero points are taken from the sums, the sums of x
+// A step of x as the matrix instructions read it: set of columns, unit u,
+// column, lane t, 8 values, then, where zero points are taken from the sums, the sums of x
 // over every 32 k (width 32), 64 or 128: group, row.
-template <class T, int WIDTH, int NB>
+// With fp32 x, TILES sets of eight columns hold the terms: term m of row r is
+// column r of set m (three sets) or column 3 r + m of the sets in a row.
+template <class T, int WIDTH, int NB, int TILES>
 struct XStep {
-    static constexpr int UNIT_BYTES = NB * 64, TERM_BYTES = 4 * UNIT_BYTES;
+    static constexpr int UNIT_BYTES = NB * 64, TILE_BYTES = 4 * UNIT_BYTES;
     static constexpr int GROUPS = 128 / WIDTH;
-    static constexpr int SUMS = Operand<T>::TERMS * TERM_BYTES;  // where the sums start
+    static constexpr int SUMS = TILES * TILE_BYTES;  // where the sums start
+    static constexpr bool SPREAD = Operand<T>::TERMS > TILES;
+    static __device__ __forceinline__ int column(int r, int m) { return SPREAD ? 3 * r + m : 8 * m + r; }
     static constexpr int BYTES = SUMS + (Operand<T>::EXACT ? 0 : (GROUPS * NB * 4 + 15) / 16 * 16);
 };
 
 // Lays out values 8 piece .. 8 piece + 7 of step `st` of row `row` of x as row r
 // of `to` (the step); zeros past the end of k. The 16 pieces of a step are 16
 // consecutive lanes, all of which call this.
-template <class T, int WIDTH, int NB>
+template <class T, int WIDTH, int NB, int TILES>
 __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, int piece, int r, bool in, uint8_t *to) {
     using Op = Operand<T>;
-    using X = XStep<T, WIDTH, NB>;
+    using X = XStep<T, WIDTH, NB, TILES>;
     // Which unit of which lane holds them.
     const int u = WIDTH == 128 ? piece & 3 : WIDTH == 64 ? 2 * (piece >> 3) + (piece & 1) : piece >> 2;
     const int t = WIDTH == 128 ? piece >> 2 : WIDTH == 64 ? (piece >> 1) & 3 : ((piece >> 1) & 1) + 2 * (piece & 1);
@@ -331,9 +337,11 @@ __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, i
     }
     if (in) {
 #pragma unroll
-        for (int m = 0; m < Op::TERMS; ++m)
-            *reinterpret_cast<uint4 *>(to + m * X::TERM_BYTES + u * X::UNIT_BYTES + r * 64 + t * 16) =
+        for (int m = 0; m < Op::TERMS; ++m) {
+            const int c = X::column(r, m);
+            *reinterpret_cast<uint4 *>(to + (c >> 3) * X::TILE_BYTES + u * X::UNIT_BYTES + (c & 7) * 64 + t * 16) =
                 make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]);
+        }
     }
     if (!Op::EXACT) {
         float s = 0.0f;
@@ -348,7 +356,7 @@ __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, i
 
 // Lays out x of pass blockIdx.y for streaming: a thread per 8 values.
 constexpr int PREPARE_THREADS = 256;
-template <class T, int WIDTH>
+template <class T, int WIDTH, int TILES>
 __global__ void __launch_bounds__(PREPARE_THREADS) w4_prepare_kernel(const __grid_constant__ W4Args a, uint8_t *to) {
     __shared__ Members members;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -359,9 +367,9 @@ __global__ void __launch_bounds__(PREPARE_THREADS) w4_prepare_kernel(const __gri
     const int steps = static_cast<int>(steps_of(a.K));
     const int st = static_cast<int>(i / (16 * W4_ROWS)), r = static_cast<int>(i / 16) % W4_ROWS;
     const bool in = st < steps && r < nb;
-    lay_out_x<T, WIDTH, W4_ROWS>(
+    lay_out_x<T, WIDTH, W4_ROWS, TILES>(
         a, static_cast<const T *>(a.x) + (in ? members.row[r] * a.ldx : 0), in ? st : 0, static_cast<int>(i & 15), r, in,
-        to + (static_cast<int64_t>(blockIdx.y) * steps + (in ? st : 0)) * XStep<T, WIDTH, W4_ROWS>::BYTES);
+        to + (static_cast<int64_t>(blockIdx.y) * steps + (in ? st : 0)) * XStep<T, WIDTH, W4_ROWS, TILES>::BYTES);
 }
 
 // Untiled bulk copy global -> this block's shared memory (16-byte aligned).
@@ -393,11 +401,11 @@ __device__ __forceinline__ float lds32(uint32_t at) {
 // instruction are that row; with fewer than eight rows of x the rest of shared
 // memory is whatever it was. Columns do not mix, so only those of rows of x are
 // read out. STREAM: x comes with q from a.prepared.
-template <class T, int WIDTH, int NB, bool STREAM>
+template <class T, int WIDTH, int NB, int TILES, bool STREAM>
 __global__ void __launch_bounds__(W4_THREADS, 1)
     w4_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ W4Args a) {
     using Op = Operand<T>;
-    using X = XStep<T, WIDTH, NB>;
+    using X = XStep<T, WIDTH, NB, TILES>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Members members;
     __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES];
@@ -412,7 +420,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
     const uint32_t x_stage = STREAM ? static_cast<uint32_t>(KS * X::BYTES + 1023) / 1024 * 1024 : 0;
     const uint32_t stage_bytes = Q_STAGE + x_stage;
     // Behind the ring: the warps' sums of two units, x when it stays.
-    constexpr int PART = CONSUMERS * NB * 16;
+    constexpr int ACC = X::SPREAD ? TILES : 1;  // sets of sums
+    constexpr int PART = CONSUMERS * ACC * NB * 16;
     float *part = reinterpret_cast<float *>(smem_raw + (base - raw) + a.stages * stage_bytes);
     uint8_t *x_here = reinterpret_cast<uint8_t *>(part + 2 * PART);
     T *y = static_cast<T *>(a.y);
@@ -533,19 +542,19 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             const int i = i0 + static_cast<int>(threadIdx.x);
             const int r = (i >> 4) % NB, st = (i >> 4) / NB;
             const bool in = i < total && r < nb;
-            lay_out_x<T, WIDTH, NB>(a, static_cast<const T *>(a.x) + (in ? members.row[r] * a.ldx : 0), in ? st : 0, i & 15,
+            lay_out_x<T, WIDTH, NB, TILES>(a, static_cast<const T *>(a.x) + (in ? members.row[r] * a.ldx : 0), in ? st : 0, i & 15,
                                     r, in, x_here + (in ? st : 0) * X::BYTES);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
     }
     const uint32_t x_at0 = tc::smem_u32(x_here);
 
-    float sum[4] = {};
+    float sum[ACC][4] = {};
     // Two steps side by side: their chains of products do not depend on each
     // other.
     auto multiply = [&](const Weights (&w)[PAIR], const Scales (&sc)[PAIR], int j, uint32_t x_step) {
         // One accumulator per chain of dependent products.
-        constexpr int CHAINS = Op::TERMS == 1 ? 2 : Op::TERMS;
+        constexpr int CHAINS = TILES == 1 ? 2 : TILES;
         constexpr int PER_GROUP = WIDTH / 32;  // words of a group
         float c[PAIR][CHAINS][4];
         float s_lo[PAIR], s_hi[PAIR], z_lo[PAIR], z_hi[PAIR];
@@ -570,12 +579,12 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                     }
                 }
             }
-            uint4 xv[PAIR][Op::TERMS];
+            uint4 xv[PAIR][TILES];
 #pragma unroll
             for (int h = 0; h < PAIR; ++h)
 #pragma unroll
-                for (int m = 0; m < Op::TERMS; ++m)
-                    xv[h][m] = lds128(x_at + h * X::BYTES + m * X::TERM_BYTES + u * X::UNIT_BYTES);
+                for (int m = 0; m < TILES; ++m)
+                    xv[h][m] = lds128(x_at + h * X::BYTES + m * X::TILE_BYTES + u * X::UNIT_BYTES);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -592,10 +601,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                         f[3] = Op::minus(f[3], zz_hi[h]);
                     }
 #pragma unroll
-                    for (int m = 0; m < Op::TERMS; ++m) {
-                        float(&d)[4] = c[h][Op::TERMS == 1 ? half : m];
+                    for (int m = 0; m < TILES; ++m) {
+                        float(&d)[4] = c[h][TILES == 1 ? half : m];
                         const uint32_t b0 = half ? xv[h][m].z : xv[h][m].x, b1 = half ? xv[h][m].w : xv[h][m].y;
-                        if (u % PER_GROUP == 0 && (half == 0 || Op::TERMS == 1))  // the chain starts
+                        if (u % PER_GROUP == 0 && (half == 0 || TILES == 1))  // the chain starts
                             Op::mma(d, f, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
                         else
                             Op::mma(d, f, b0, b1, d[0], d[1], d[2], d[3]);
@@ -605,6 +614,16 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             if ((u + 1) % PER_GROUP == 0) {  // the group ends
 #pragma unroll
                 for (int h = 0; h < PAIR; ++h) {
+                    if (ACC > 1) {
+#pragma unroll
+                        for (int m = 0; m < ACC; ++m) {
+                            sum[m][0] = fmaf(s_lo[h], c[h][m][0], sum[m][0]);
+                            sum[m][1] = fmaf(s_lo[h], c[h][m][1], sum[m][1]);
+                            sum[m][2] = fmaf(s_hi[h], c[h][m][2], sum[m][2]);
+                            sum[m][3] = fmaf(s_hi[h], c[h][m][3], sum[m][3]);
+                        }
+                        continue;
+                    }
                     float d[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // small terms first
@@ -622,10 +641,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                         d[2] = fmaf(d[2], Op::UNIT, b_hi * xs0);
                         d[3] = fmaf(d[3], Op::UNIT, b_hi * xs1);
                     }
-                    sum[0] = fmaf(s_lo[h], d[0], sum[0]);
-                    sum[1] = fmaf(s_lo[h], d[1], sum[1]);
-                    sum[2] = fmaf(s_hi[h], d[2], sum[2]);
-                    sum[3] = fmaf(s_hi[h], d[3], sum[3]);
+                    sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
+                    sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
+                    sum[0][2] = fmaf(s_hi[h], d[2], sum[0][2]);
+                    sum[0][3] = fmaf(s_hi[h], d[3], sum[0][3]);
                 }
             }
         }
@@ -701,26 +720,30 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         }
         // Join the shares of the unit. Two buffers: a warp that writes the next
         // unit's sums may meet one that still reads this unit's.
-        float *mine = part + parity * PART + warp * NB * 16;
+        float *mine = part + parity * PART + warp * ACC * NB * 16;
         const int n_lo = row_of<WIDTH>(g);
-        if (NB == 1) {
-            if (t == 0) {
-                mine[n_lo] = sum[0];
-                mine[n_lo + 8] = sum[2];
+#pragma unroll
+        for (int m = 0; m < ACC; ++m) {
+            if (NB == 1) {
+                if (t == 0) {
+                    mine[n_lo] = sum[m][0];
+                    mine[n_lo + 8] = sum[m][2];
+                }
+            } else {
+                mine[(8 * m + 2 * t) * 16 + n_lo] = sum[m][0];
+                mine[(8 * m + 2 * t + 1) * 16 + n_lo] = sum[m][1];
+                mine[(8 * m + 2 * t) * 16 + n_lo + 8] = sum[m][2];
+                mine[(8 * m + 2 * t + 1) * 16 + n_lo + 8] = sum[m][3];
             }
-        } else {
-            mine[(2 * t) * 16 + n_lo] = sum[0];
-            mine[(2 * t + 1) * 16 + n_lo] = sum[1];
-            mine[(2 * t) * 16 + n_lo + 8] = sum[2];
-            mine[(2 * t + 1) * 16 + n_lo + 8] = sum[3];
+            sum[m][0] = sum[m][1] = sum[m][2] = sum[m][3] = 0.0f;
         }
-        sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
         asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
         for (int i = threadIdx.x; i < R * nb; i += CONSUMERS * 32) {
             const int r = i / R, n = i - r * R;
-            const float *from = part + parity * PART + ((n >> 4) * NB + r) * 16 + (n & 15);
+            const float *from = part + parity * PART + (n >> 4) * ACC * NB * 16 + (n & 15);
             float s = 0.0f;
-            for (int w = 0; w < CONSUMERS / RT; ++w) s += from[w * RT * NB * 16];
+            for (int w = 0; w < CONSUMERS / RT; ++w, from += RT * ACC * NB * 16)
+                s += X::SPREAD ? (from[(3 * r + 2) * 16] + from[(3 * r + 1) * 16]) + from[3 * r * 16] : from[r * 16];
             const int64_t row = static_cast<int64_t>(u) * R + n;
             if (row >= a.N) continue;
             if (!Op::EXACT && !(fabsf(s) <= 3.0e38f))
@@ -775,10 +798,10 @@ int launch_simple(const W4Args &a, cudaStream_t stream, int *launches) {
     return SGEMM_OK;
 }
 
-template <class T, int WIDTH, int NB, bool STREAM>
+template <class T, int WIDTH, int NB, int TILES, bool STREAM>
 int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    auto kernel = w4_kernel<T, WIDTH, NB, STREAM>;
-    using X = XStep<T, WIDTH, NB>;
+    auto kernel = w4_kernel<T, WIDTH, NB, TILES, STREAM>;
+    using X = XStep<T, WIDTH, NB, TILES>;
     const int passes = static_cast<int>(a.ids ? a.rows : (a.rows + W4_ROWS - 1) / W4_ROWS);
     const int64_t steps = steps_of(a.K);
     // Passes with work in them: with ids, the experts that rows with ids drawn
@@ -807,7 +830,7 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     a.units = static_cast<int>((a.N + a.unit_rows - 1) / a.unit_rows);
     const int64_t KS = PAIR * CONSUMERS / (a.unit_rows / 16);
     const int64_t stage = Q_STAGE + (STREAM ? (KS * X::BYTES + 1023) / 1024 * 1024 : 0);
-    const int64_t rest = 1024 + 2 * CONSUMERS * NB * 16 * 4 + (STREAM ? 0 : steps * X::BYTES);
+    const int64_t rest = 1024 + 2 * CONSUMERS * (X::SPREAD ? TILES : 1) * NB * 16 * 4 + (STREAM ? 0 : steps * X::BYTES);
     int64_t stages = (SMEM_BYTES - rest) / stage;
     if (stages > MAX_STAGES) stages = MAX_STAGES;
     a.stages = static_cast<int>(stages);
@@ -851,7 +874,7 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
         const int here = passes - a.first_pass < chunk ? passes - a.first_pass : chunk;
         if (STREAM) {
             const int64_t blocks = (steps * 16 * W4_ROWS + PREPARE_THREADS - 1) / PREPARE_THREADS;
-            w4_prepare_kernel<T, WIDTH><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(here)),
+            w4_prepare_kernel<T, WIDTH, TILES><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(here)),
                                           PREPARE_THREADS, 0, stream>>>(a, reinterpret_cast<uint8_t *>(scratch));
             if (cudaGetLastError() != cudaSuccess) {
                 rc = SGEMM_ERR_LAUNCH;
@@ -871,14 +894,24 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     return rc;
 }
 
+template <class T, int WIDTH, int TILES>
+int launch_tiles(const W4Args &a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (steps_of(a.K) * XStep<T, WIDTH, 8, TILES>::BYTES <= RESIDENT_EIGHT)
+        return launch<T, WIDTH, 8, TILES, false>(a, dev, stream, launches);
+    return launch<T, WIDTH, 8, TILES, true>(a, dev, stream, launches);
+}
+
 template <class T, int WIDTH>
 int launch_width(const W4Args &a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    const int64_t steps = steps_of(a.K);
-    if (a.rows == 1 && steps * XStep<T, WIDTH, 1>::BYTES <= RESIDENT_ONE)
-        return launch<T, WIDTH, 1, false>(a, dev, stream, launches);
-    if (steps * XStep<T, WIDTH, 8>::BYTES <= RESIDENT_EIGHT)
-        return launch<T, WIDTH, 8, false>(a, dev, stream, launches);
-    return launch<T, WIDTH, 8, true>(a, dev, stream, launches);
+    if constexpr (Operand<T>::TERMS == 3) {
+        if (a.rows <= 2) return launch_tiles<T, WIDTH, 1>(a, dev, stream, launches);
+        if (a.rows <= 5) return launch_tiles<T, WIDTH, 2>(a, dev, stream, launches);
+        return launch_tiles<T, WIDTH, 3>(a, dev, stream, launches);
+    } else {
+        if (a.rows == 1 && steps_of(a.K) * XStep<T, WIDTH, 1, 1>::BYTES <= RESIDENT_ONE)
+            return launch<T, WIDTH, 1, 1, false>(a, dev, stream, launches);
+        return launch_tiles<T, WIDTH, 1>(a, dev, stream, launches);
+    }
 }
 
 template <class T>
