@@ -25,10 +25,22 @@ int g_clusters[kMaxDevices][6];
 // below it the kernel loads them itself with 4-byte copies.
 constexpr double COPY_FROM = 1.25 * 1073741824.0;
 
+// Folds of the accumulators. The tensor core cuts its running sum at every MMA
+// (half a unit of the last place on average, towards zero), so the error grows
+// with the MMAs that add to a large running sum. The single product folds every
+// 8 k-blocks, 96 such MMAs: 2.0e-6 of the result's norm on normal inputs, where
+// fp32 sums give 0.57e-6 at K = 1024. Here a fold every 5 k-blocks, the small
+// products (lo hi, hi lo) of the first 4 before any large one, leaves 28: 0.7e-6.
+// A fold moves 128 KB through shared memory, which bounds the kernel: 8192 rows,
+// 8 experts, 1024 -> 2048 take 199 us (172 TFLOP/s), 160 with the single
+// product's folds; folds every 4 or 3 k-blocks in the usual order 208 and 242 us
+// for 1.0e-6 and 0.8e-6.
+constexpr int GROUP_FOLD = 5, GROUP_LEAD = 4;
+
 template <bool VEC_C, bool TA, bool TB, PairUnits UNITS>
 int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
            int *launches) {
-    auto kernel = tf32x3_pair_kernel<VEC_C, TA, TB, UNITS>;
+    auto kernel = tf32x3_pair_kernel<VEC_C, TA, TB, UNITS, GROUP_FOLD, GROUP_LEAD>;
     constexpr bool WG = UNITS == GROUP_WGRAD;
     constexpr int idx = (VEC_C ? 3 : 0) + (WG ? 2 : TB ? 1 : 0);
     cudaLaunchAttribute attr;

@@ -266,10 +266,13 @@ __global__ void __launch_bounds__(ROW_THREADS) gather_kernel(const RowArgs a, co
 // Choices whose rows a thread has in flight at once.
 constexpr int CHOICES = 8;
 
-// FITS: top_k is at most CH, and a thread reads its token's slots once.
+// FITS: top_k is at most CH, and a thread reads its token's slots once. AHEAD:
+// vectors of the row that a thread works on at once, so that CH * AHEAD = 8
+// loads are in flight whatever the choices.
 template <class T, int N, bool WEIGHTED, int CH, bool FITS>
 __global__ void __launch_bounds__(ROW_THREADS) combine_kernel(const RowArgs a, const T *h, int64_t ldh,
                                                               const float *weights, T *y, int64_t ldy) {
+    constexpr int AHEAD = CHOICES / CH;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.tokens) return;
     const int end = kept_end(a);
@@ -285,27 +288,36 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_kernel(const RowArgs a, c
         }
     };
     if (FITS) choices(0);
-    for (int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c < a.vecs;
-         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-        float sum[N] = {};
+    const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x;
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c0 < a.vecs; c0 += AHEAD * step) {
+        float sum[AHEAD][N] = {};
         for (int j0 = 0; j0 < (FITS ? 1 : a.top_k); j0 += CH) {
             if (!FITS) choices(j0);
-            Pack<T, N> rows[CH];
+            Pack<T, N> rows[AHEAD][CH];
 #pragma unroll
-            for (int j = 0; j < CH; ++j)
-                if (s[j] >= 0) rows[j] = load_pack<T, N>(h + s[j] * ldh + c * N);
+            for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                if (s[j] < 0) continue;
+                for (int j = 0; j < CH; ++j)
+                    if (s[j] >= 0 && c0 + u * step < a.vecs) rows[u][j] = load_pack<T, N>(h + s[j] * ldh + (c0 + u * step) * N);
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    sum[i] = WEIGHTED ? fmaf(w[j], to_f32(rows[j].v[i]), sum[i]) : sum[i] + to_f32(rows[j].v[i]);
-            }
+            for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    if (s[j] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        sum[u][i] = WEIGHTED ? fmaf(w[j], to_f32(rows[u][j].v[i]), sum[u][i])
+                                             : sum[u][i] + to_f32(rows[u][j].v[i]);
+                }
         }
-        Pack<T, N> out;
 #pragma unroll
-        for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(sum[i]);
-        store_pack(y + t * ldy + c * N, out);
+        for (int u = 0; u < AHEAD; ++u) {
+            if (c0 + u * step >= a.vecs) break;
+            Pack<T, N> out;
+#pragma unroll
+            for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(sum[u][i]);
+            store_pack(y + t * ldy + (c0 + u * step) * N, out);
+        }
     }
 }
 
@@ -336,11 +348,13 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[CHOICES]) {
 
 // blockDim.x (a multiple of 32) threads share a token and go over its whole
 // row, so the dot products end in the block: in the warp when it has the
-// token to itself.
-template <class T, int N>
+// token to itself. CH: choices at once, for as many vectors of the row that
+// CH * AHEAD = 8.
+template <class T, int N, int CH>
 __global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs a, const T *dy, int64_t lddy,
                                                                    const T *h, int64_t ldh, const float *weights,
                                                                    T *dh, int64_t lddh, float *dweights) {
+    constexpr int AHEAD = CHOICES / CH;
     __shared__ float part[ROW_THREADS / 32][CHOICES];
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool in = t < a.tokens;
@@ -348,12 +362,13 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs
     const int lane = threadIdx.x & 31;
     const int warp = static_cast<int>((threadIdx.y * blockDim.x + threadIdx.x) >> 5);
     const int warps = static_cast<int>(blockDim.x >> 5);  // of one token
-    for (int j0 = 0; j0 < a.top_k; j0 += CHOICES) {
+    const int64_t step = blockDim.x;
+    for (int j0 = 0; j0 < a.top_k; j0 += CH) {
         float dot[CHOICES] = {};
-        float w[CHOICES];
-        int s[CHOICES];  // -1: past top_k or not a slot; >= end: dropped
+        float w[CH];
+        int s[CH];  // -1: past top_k or not a slot; >= end: dropped
 #pragma unroll
-        for (int j = 0; j < CHOICES; ++j) {
+        for (int j = 0; j < CH; ++j) {
             s[j] = -1;
             w[j] = 0.0f;
             if (!in || j0 + j >= a.top_k) continue;
@@ -362,39 +377,49 @@ __global__ void __launch_bounds__(ROW_THREADS) combine_grad_kernel(const RowArgs
             w[j] = __ldg(weights + t * a.top_k + j0 + j);
         }
         if (in) {
-            for (int64_t c = threadIdx.x; c < a.vecs; c += blockDim.x) {
-                const Pack<T, N> g = load_pack<T, N>(dy + t * lddy + c * N);
-                Pack<T, N> rows[CHOICES];
+            for (int64_t c0 = threadIdx.x; c0 < a.vecs; c0 += AHEAD * step) {
+                Pack<T, N> g[AHEAD], rows[AHEAD][CH];
 #pragma unroll
-                for (int j = 0; j < CHOICES; ++j)
-                    if (s[j] >= 0 && s[j] < end) rows[j] = load_pack<T, N>(h + s[j] * ldh + c * N);
+                for (int u = 0; u < AHEAD; ++u) {
+                    const int64_t c = c0 + u * step;
+                    if (c >= a.vecs) break;
+                    g[u] = load_pack<T, N>(dy + t * lddy + c * N);
 #pragma unroll
-                for (int j = 0; j < CHOICES; ++j) {
-                    if (s[j] < 0) continue;
-                    Pack<T, N> out;
-                    if (s[j] < end) {
+                    for (int j = 0; j < CH; ++j)
+                        if (s[j] >= 0 && s[j] < end) rows[u][j] = load_pack<T, N>(h + s[j] * ldh + c * N);
+                }
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            dot[j] = fmaf(to_f32(g.v[i]), to_f32(rows[j].v[i]), dot[j]);
-                            out.v[i] = from_f32<T>(w[j] * to_f32(g.v[i]));
+                for (int u = 0; u < AHEAD; ++u) {
+                    const int64_t c = c0 + u * step;
+                    if (c >= a.vecs) break;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) {
+                        if (s[j] < 0) continue;
+                        Pack<T, N> out;
+                        if (s[j] < end) {
+#pragma unroll
+                            for (int i = 0; i < N; ++i) {
+                                dot[j] = fmaf(to_f32(g[u].v[i]), to_f32(rows[u][j].v[i]), dot[j]);
+                                out.v[i] = from_f32<T>(w[j] * to_f32(g[u].v[i]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(0.0f);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) out.v[i] = from_f32<T>(0.0f);
+                        store_pack(dh + s[j] * lddh + c * N, out);
                     }
-                    store_pack(dh + s[j] * lddh + c * N, out);
                 }
             }
         }
         const float d = warp_sum8(dot);
         const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
         if (warps == 1) {
-            if (in && (lane & 3) == 0 && j0 + j < a.top_k) dweights[t * a.top_k + j0 + j] = d;
+            if (in && (lane & 3) == 0 && j < CH && j0 + j < a.top_k) dweights[t * a.top_k + j0 + j] = d;
             continue;
         }
         if ((lane & 3) == 0) part[warp][j] = d;
         __syncthreads();
-        if (in && threadIdx.x < CHOICES && j0 + static_cast<int>(threadIdx.x) < a.top_k) {
+        if (in && threadIdx.x < CH && j0 + static_cast<int>(threadIdx.x) < a.top_k) {
             float sum = 0.0f;
             for (int i = 0; i < warps; ++i) sum += part[threadIdx.y * warps + i][threadIdx.x];
             dweights[t * a.top_k + j0 + threadIdx.x] = sum;
@@ -522,9 +547,16 @@ int combine_grad_typed(const Route &r, const void *dy, int64_t lddy, const void 
     const dim3 block = token_block(r, vecs, dev);
     dim3 grid;
     if (!row_grid(r, vecs, block, false, &grid)) return SGEMM_ERR_UNSUPPORTED;
-    combine_grad_kernel<T, N><<<grid, block, 0, stream>>>(row_args(r, vecs), static_cast<const T *>(dy), lddy,
-                                                          static_cast<const T *>(h), ldh, weights,
-                                                          static_cast<T *>(dh), lddh, dweights);
+    const RowArgs a = row_args(r, vecs);
+    const T *g = static_cast<const T *>(dy), *in = static_cast<const T *>(h);
+    T *out = static_cast<T *>(dh);
+    if (r.top_k <= 2)
+        combine_grad_kernel<T, N, 2><<<grid, block, 0, stream>>>(a, g, lddy, in, ldh, weights, out, lddh, dweights);
+    else if (r.top_k <= 4)
+        combine_grad_kernel<T, N, 4><<<grid, block, 0, stream>>>(a, g, lddy, in, ldh, weights, out, lddh, dweights);
+    else
+        combine_grad_kernel<T, N, CHOICES><<<grid, block, 0, stream>>>(a, g, lddy, in, ldh, weights, out, lddh,
+                                                                       dweights);
     return launched(launches);
 }
 

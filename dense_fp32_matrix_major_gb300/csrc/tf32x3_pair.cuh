@@ -262,11 +262,16 @@ __device__ __forceinline__ void for_each_pair_unit(const Args &a, const ex::Grou
 
 // TA: A stored K x M (op(A) = A^T); TB: B stored N x K (op(B) = B^T).
 // GROUP_WGRAD is op(A) = A^T, op(B) = B over a group's rows.
-template <bool VEC_C, bool TA, bool TB, PairUnits UNITS = TILES>
+// FOLD: the longest chain of k-blocks. LEAD > 0: in a chain's first LEAD
+// k-blocks (and within every other) the small products, lo hi and hi lo, come
+// before the large one, hi hi, while the accumulator is small and what the MMAs
+// cut off it is too. At most OP_STAGES, which hold the k-blocks meanwhile.
+template <bool VEC_C, bool TA, bool TB, PairUnits UNITS = TILES, int FOLD = pr::FOLD_KB, int LEAD = 0>
 __global__ void __launch_bounds__(pr::THREADS, 1)
     tf32x3_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Args a,
                        const __grid_constant__ ex::GroupTiles gt) {
+    static_assert(LEAD <= pr::OP_STAGES, "the leading k-blocks are staged together");
     static_assert(UNITS != GROUP_WGRAD || (TA && !TB), "groups are summed along the stored rows of both operands");
     constexpr bool SUMS_ROWS = UNITS == GROUP_WGRAD;
     extern __shared__ uint8_t smem_raw[];
@@ -485,8 +490,8 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             bool ready = false;  // the stage of k-block `it` was seen full (and fenced) early
             for_each_pair_unit<UNITS>(a, gt, abort_flag, pair, pairs, [&](const PairUnit &u) {
                 const int kb = u.kb, ke = u.ke;
-                for (int k0 = kb; k0 < ke; k0 += pr::FOLD_KB) {
-                    const int k1 = ke - k0 > pr::FOLD_KB ? k0 + pr::FOLD_KB : ke;
+                for (int k0 = kb; k0 < ke; k0 += FOLD) {
+                    const int k1 = ke - k0 > FOLD ? k0 + FOLD : ke;
                     const uint32_t d = iv & 1;
                     // Accumulator d is free once the epilogue has folded the
                     // interval that used it two intervals back.
@@ -495,7 +500,42 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                     if (!__all_sync(0xffffffffu, ok)) return;
                     tc_fence_after();
                     const uint32_t dt = tmem_base + d * pr::PN;
-                    for (int kblk = k0; kblk < k1; ++kblk, ++it) {
+                    if (LEAD > 0) {
+                        for (int kblk = k0; kblk < k1;) {
+                            const int lead = kblk == k0 && k1 - k0 > LEAD ? LEAD : 1;
+                            for (int i = 0; i < lead; ++i) {
+                                const uint32_t nx = it + static_cast<uint32_t>(i), s = nx % pr::OP_STAGES;
+                                const bool full = mbar_wait<true>(bar(pr::OP_FULL + s), (nx / pr::OP_STAGES) & 1, a,
+                                                                  abort_flag, WD_MMA_FULL);
+                                if (!__all_sync(0xffffffffu, full)) return;
+                                tc_fence_after();
+                                const uint64_t b_hi = desc0 + static_cast<uint64_t>(s * (pr::OP_STAGE >> 4));
+                                const uint64_t b_lo = b_hi + (pr::B_HALF >> 4);
+                                const uint32_t a_hi = a0 + 64 * s, a_lo = a_hi + 32;
+                                if (leader) {
+#pragma unroll
+                                    for (int ks = 0; ks < BK / 8; ++ks) {
+                                        tc_mma2_ts(dt, a_lo + ks * 8, b_hi + ks * 2, ks > 0 || i > 0 || kblk > k0);
+                                        tc_mma2_ts(dt, a_hi + ks * 8, b_lo + ks * 2, 1u);
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                            for (int i = 0; i < lead; ++i, ++it, ++kblk) {
+                                const uint32_t s = it % pr::OP_STAGES;
+                                const uint64_t b_hi = desc0 + static_cast<uint64_t>(s * (pr::OP_STAGE >> 4));
+                                const uint32_t a_hi = a0 + 64 * s;
+                                if (leader) {
+#pragma unroll
+                                    for (int ks = 0; ks < BK / 8; ++ks)
+                                        tc_mma2_ts(dt, a_hi + ks * 8, b_hi + ks * 2, 1u);
+                                    tc_commit2(bar(pr::OP_EMPTY + s));
+                                }
+                                __syncwarp();
+                            }
+                        }
+                    }
+                    for (int kblk = k0; LEAD == 0 && kblk < k1; ++kblk, ++it) {
                         const uint32_t s = it % pr::OP_STAGES;
                         if (!ready) {
                             const bool full = mbar_wait<true>(bar(pr::OP_FULL + s), (it / pr::OP_STAGES) & 1, a,
@@ -709,8 +749,8 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                 __syncwarp();
                 return;
             }
-            for (int k0 = kb; k0 < ke; k0 += pr::FOLD_KB) {
-                const bool first = k0 == kb, last = ke - k0 <= pr::FOLD_KB;
+            for (int k0 = kb; k0 < ke; k0 += FOLD) {
+                const bool first = k0 == kb, last = ke - k0 <= FOLD;
                 const uint32_t d = iv & 1;
                 if (!mbar_wait<true>(bar(pr::ACC_FULL + d), (iv >> 1) & 1, a, abort_flag, WD_EPILOGUE)) return;
                 tc_fence_after();

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             if ((u + 1) % PER_GROUP == 0) {  // the group ends
 #pragma unroll
                 for (int h = 0; h < PAIR; ++h) {
-                    if (ACC > 1) {
+                    if constexpr (ACC > 1) {
 #pragma unroll
                         for (int m = 0; m < ACC; ++m) {
                             sum[m][0] = fmaf(s_lo[h], c[h][m][0], sum[m][0]);
@@ -622,29 +622,29 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                             sum[m][2] = fmaf(s_hi[h], c[h][m][2], sum[m][2]);
                             sum[m][3] = fmaf(s_hi[h], c[h][m][3], sum[m][3]);
                         }
-                        continue;
-                    }
-                    float d[4];
+                    } else {
+                        float d[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // small terms first
-                        d[i] = c[h][CHAINS - 1][i];
+                        for (int i = 0; i < 4; ++i) {  // small terms first
+                            d[i] = c[h][CHAINS - 1][i];
 #pragma unroll
-                        for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                            for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                        }
+                        if (!Op::EXACT) {
+                            const uint32_t at = x_step + h * X::BYTES + X::SUMS + u / PER_GROUP * NB * 4;
+                            const float xs0 = lds32(NB == 1 ? at : at + 8 * t);
+                            const float xs1 = NB == 1 ? xs0 : lds32(at + 8 * t + 4);
+                            const float b_lo = -Op::BASE - z_lo[h], b_hi = -Op::BASE - z_hi[h];
+                            d[0] = fmaf(d[0], Op::UNIT, b_lo * xs0);
+                            d[1] = fmaf(d[1], Op::UNIT, b_lo * xs1);
+                            d[2] = fmaf(d[2], Op::UNIT, b_hi * xs0);
+                            d[3] = fmaf(d[3], Op::UNIT, b_hi * xs1);
+                        }
+                        sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
+                        sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
+                        sum[0][2] = fmaf(s_hi[h], d[2], sum[0][2]);
+                        sum[0][3] = fmaf(s_hi[h], d[3], sum[0][3]);
                     }
-                    if (!Op::EXACT) {
-                        const uint32_t at = x_step + h * X::BYTES + X::SUMS + u / PER_GROUP * NB * 4;
-                        const float xs0 = lds32(NB == 1 ? at : at + 8 * t);
-                        const float xs1 = NB == 1 ? xs0 : lds32(at + 8 * t + 4);
-                        const float b_lo = -Op::BASE - z_lo[h], b_hi = -Op::BASE - z_hi[h];
-                        d[0] = fmaf(d[0], Op::UNIT, b_lo * xs0);
-                        d[1] = fmaf(d[1], Op::UNIT, b_lo * xs1);
-                        d[2] = fmaf(d[2], Op::UNIT, b_hi * xs0);
-                        d[3] = fmaf(d[3], Op::UNIT, b_hi * xs1);
-                    }
-                    sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
-                    sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
-                    sum[0][2] = fmaf(s_hi[h], d[2], sum[0][2]);
-                    sum[0][3] = fmaf(s_hi[h], d[3], sum[0][3]);
                 }
             }
         }

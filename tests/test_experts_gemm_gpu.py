@@ -193,3 +193,64 @@ def test_refusals(ex):
     with pytest.raises(ex.SgemmError):
         ex.gemm(a, b[:, :, :16], off, out=a)  # overlaps its input
 
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_empty_sizes(ex, dtype):
+    """No rows, no columns, nothing to sum, no tokens: results of the right shape, zeros where a sum is empty."""
+    dt = DTYPES[dtype]
+
+    def zeros(*shape):
+        return torch.zeros(*shape, dtype=dt, device="cuda")
+
+    off = torch.tensor([0, 0, 0], dtype=torch.int32, device="cuda")
+    assert ex.gemm(zeros(0, 64), zeros(2, 64, 32), off).shape == (0, 32)
+    assert ex.gemm(zeros(8, 64), zeros(2, 64, 0), off).shape == (8, 0)
+    some = torch.tensor([0, 3, 8], dtype=torch.int32, device="cuda")
+    for trans in (False, True):
+        out = torch.ones(8, 32, dtype=dt, device="cuda")
+        ex.gemm(zeros(8, 0), zeros(2, 32, 0) if trans else zeros(2, 0, 32), some, out=out, transB=trans)
+        assert (out == 0).all()
+    out = torch.ones(2, 64, 32, dtype=dt, device="cuda")
+    ex.gemm_wgrad(zeros(0, 64), zeros(0, 32), off, out=out)
+    assert (out == 0).all()
+    assert ex.gemm_wgrad(zeros(8, 0), zeros(8, 32), some).shape == (2, 0, 32)
+    r = ex.sort(torch.zeros(0, 2, dtype=torch.int64, device="cuda"), 2)
+    assert r.offsets.tolist() == [0, 0, 0] and r.slot.shape == (0, 2) and r.order.shape == (0,)
+    w = torch.zeros(0, 2, device="cuda")
+    assert ex.gather(zeros(0, 16), r).shape == (0, 16) and ex.combine(zeros(0, 16), w, r).shape == (0, 16)
+    dh, dw = ex.combine_grad(zeros(0, 16), zeros(0, 16), w, r)
+    assert dh.shape == (0, 16) and dw.shape == (0, 2)
+    r = ex.sort(torch.zeros(4, 2, dtype=torch.int64, device="cuda"), 2)
+    w = torch.ones(4, 2, device="cuda")
+    assert ex.gather(zeros(4, 0), r).shape == (8, 0) and ex.combine(zeros(8, 0), w, r).shape == (4, 0)
+    dh, dw = ex.combine_grad(zeros(4, 0), zeros(8, 0), w, r)
+    assert dh.shape == (8, 0) and (dw == 0).all()
+    q, s = torch.zeros(32, 0, dtype=torch.uint8, device="cuda"), torch.zeros(32, 0, device="cuda")
+    assert (ex.w4_matvec(zeros(3, 0), q, s, group=64) == 0).all()
+    q, s = torch.zeros(0, 64, dtype=torch.uint8, device="cuda"), torch.zeros(0, 1, device="cuda")
+    assert ex.w4_matvec(zeros(3, 128), q, s, group=128).shape == (3, 0)
+
+
+def test_same_sign_sums(ex):
+    """Long sums of one sign, where cut sums drift in one direction: fp32 within the library's bound."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    a = torch.rand((300, 4096), generator=g, device="cuda")
+    b = torch.rand((2, 4096, 136), generator=g, device="cuda")
+    off = torch.tensor([0, 170, 300], dtype=torch.int32, device="cuda")
+    want = torch.cat([a[:170].double() @ b[0].double(), a[170:].double() @ b[1].double()])
+    assert float(((ex.gemm(a, b, off).double() - want).abs() / want).max()) <= 1e-5
+    d = torch.rand((300, 64), generator=g, device="cuda")
+    want = torch.stack([a[:170].double().t() @ d[:170].double(), a[170:].double().t() @ d[170:].double()])
+    assert float(((ex.gemm_wgrad(a, d, off).double() - want).abs() / want).max()) <= 1e-5
+
+
+def test_no_wait_gives_up(ex):
+    """The kernels' bounded waits report through sgemm_device_status, as the library's others do: none gave up."""
+    from dense_fp32_matrix_major_gb300 import sgemm
+
+    a, b = torch.randn(64, 128, device="cuda"), torch.randn(2, 128, 64, device="cuda")
+    off = torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+    ex.gemm(a, b, off)
+    ex.gemm(a.bfloat16(), b.bfloat16(), off)
+    assert sgemm.device_status() == 0
