@@ -244,21 +244,31 @@ __device__ __forceinline__ int kept_end(const RowArgs &a) {
     return static_cast<int>(max(int64_t(0), min(int64_t(o), a.pairs)));
 }
 
-// xs[slot[t][j]] = x[t]: a copy of V bytes a thread, so no types.
+// xs[slot[t][j]] = x[t]: a copy of sizeof(V) bytes a thread, so no types. Four
+// vectors of the row at once.
 template <class V>
 __global__ void __launch_bounds__(ROW_THREADS) gather_kernel(const RowArgs a, const char *x, int64_t ldx, char *xs,
                                                              int64_t ldxs) {
+    constexpr int AHEAD = 4;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.tokens) return;
     const int end = kept_end(a);
     const int32_t *slot = a.slot + t * a.top_k;
-    for (int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c < a.vecs;
-         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-        const V v = *reinterpret_cast<const V *>(x + t * ldx + c * static_cast<int64_t>(sizeof(V)));
+    const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.x;
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; c0 < a.vecs; c0 += AHEAD * step) {
+        V v[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (c0 + u * step < a.vecs) v[u] = *reinterpret_cast<const V *>(x + t * ldx + (c0 + u * step) * int64_t(sizeof(V)));
         for (int j = 0; j < a.top_k; ++j) {
             const int s = __ldg(slot + j);
             if (static_cast<unsigned>(s) >= a.pairs) continue;
-            *reinterpret_cast<V *>(xs + s * ldxs + c * static_cast<int64_t>(sizeof(V))) = s < end ? v : V{};
+            char *to = xs + s * ldxs;
+            const bool kept = s < end;
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (c0 + u * step < a.vecs)
+                    *reinterpret_cast<V *>(to + (c0 + u * step) * int64_t(sizeof(V))) = kept ? v[u] : V{};
         }
     }
 }
@@ -599,14 +609,14 @@ int sort_launch(const void *ids, int id_bits, int64_t pairs, int64_t experts, in
                       launches);
 }
 
-int gather_launch(int type, const Route &r, const void *x, int64_t ldx, void *xs, int64_t ldxs, const DeviceInfo &,
+int gather_launch(int type, const Route &r, const void *x, int64_t ldx, void *xs, int64_t ldxs, const DeviceInfo &dev,
                   cudaStream_t stream, int *launches) {
     const int64_t size = type_size(type);
     const int vb = vector_bytes(size, r.width, x, ldx, xs, ldxs);
     const int64_t vecs = r.width * size / vb;
-    const dim3 block = row_block(vecs);
+    const dim3 block = token_block(r, vecs, dev);
     dim3 grid;
-    if (!row_grid(r, vecs, block, true, &grid)) return SGEMM_ERR_UNSUPPORTED;
+    if (!row_grid(r, vecs, block, block.x > 32, &grid)) return SGEMM_ERR_UNSUPPORTED;
     const RowArgs a = row_args(r, vecs);
     const char *in = static_cast<const char *>(x);
     char *out = static_cast<char *>(xs);
