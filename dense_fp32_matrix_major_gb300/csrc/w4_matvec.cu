@@ -14,8 +14,9 @@
 // go from global memory to registers once and are used once.) Each group's
 // inner sum is scaled in fp32. How a 4-bit q becomes an operand:
 //   * fp16 x: q in the low bits of an fp16 number is q 2^-24 exactly (a
-//     subnormal), so masking is all; the group's sum is
-//     2^24 sum (q 2^-24) x - zero sum x.
+//     subnormal), four bits up it is 16 q 2^-24 (10 bits hold it), so masking
+//     is all; the group's sum is 2^24 (sum (q 2^-24) x) - zero sum x, the sums
+//     of the two positions kept apart until the 16 is taken out.
 //   * bf16 x: q in the low bits of 128.0 (last place 1) is 128 + q exactly;
 //     the group's sum is sum (128 + q) x - (128 + zero) sum x. The subtraction
 //     costs up to four of the 24 bits of the fp32 sums, of which a bf16
@@ -27,7 +28,8 @@
 //     columns), three to five two, up to eight three.
 // The sums of x per group are made in fp32 when x is staged. One 32-bit word
 // holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j, j + 4), so x
-// is laid out in shared memory in the order 0 4 1 5 2 6 3 7. An infinity or
+// is laid out in shared memory in the order 0 4 1 5 2 6 3 7 (fp16: 0 4 2 6 1 5
+// 3 7, the unshifted and four bits up apart). An infinity or
 // NaN in 16-bit x would turn the subtraction into NaN; rows of x that hold
 // one are recomputed with scalar arithmetic.
 //
@@ -44,6 +46,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -104,6 +107,7 @@ struct Operand;
 template <>
 struct Operand<__nv_bfloat16> {
     static constexpr int TERMS = 1;
+    static constexpr bool TWO_PLACES = false;  // q low and four bits up
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0x43004300u;  // 128, 128 in bf16
     static constexpr float BASE = 128.0f, UNIT = 1.0f;
@@ -126,6 +130,7 @@ struct Operand<__nv_bfloat16> {
 template <>
 struct Operand<__half> {
     static constexpr int TERMS = 1;
+    static constexpr bool TWO_PLACES = true;  // q low and four bits up
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0;
     static constexpr float BASE = 0.0f, UNIT = 16777216.0f;  // an operand's q is q 2^-24
@@ -144,6 +149,7 @@ struct Operand<__half> {
 template <>
 struct Operand<float> {
     static constexpr int TERMS = 3;
+    static constexpr bool TWO_PLACES = false;  // q low and four bits up
     static constexpr bool EXACT = true;
     static constexpr uint32_t ONE = Operand<__nv_bfloat16>::ONE;
     static constexpr float BASE = 0.0f, UNIT = 1.0f;
@@ -328,12 +334,13 @@ __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, i
     }
     uint32_t w[Op::TERMS][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < 4; ++i) {
+        const int j = Op::TWO_PLACES ? (i >> 1) | ((i & 1) << 1) : i;
         uint16_t x0[Op::TERMS], x1[Op::TERMS];
         Op::split(v.v[j], x0);
         Op::split(v.v[j + 4], x1);
 #pragma unroll
-        for (int m = 0; m < Op::TERMS; ++m) w[m][j] = x0[m] | (static_cast<uint32_t>(x1[m]) << 16);
+        for (int m = 0; m < Op::TERMS; ++m) w[m][i] = x0[m] | (static_cast<uint32_t>(x1[m]) << 16);
     }
     if (in) {
 #pragma unroll
@@ -590,10 +597,18 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < PAIR; ++h) {
                     uint32_t f[4];
-                    f[0] = ((w[h].lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                    f[1] = ((w[h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                    f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
-                    f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                    if (Op::TWO_PLACES) {
+                        const uint32_t mask = half ? 0x00F000F0u : 0x000F000Fu;
+                        f[0] = w[h].lo[u] & mask;
+                        f[1] = w[h].hi[u] & mask;
+                        f[2] = (w[h].lo[u] >> 8) & mask;
+                        f[3] = (w[h].hi[u] >> 8) & mask;
+                    } else {
+                        f[0] = ((w[h].lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                        f[1] = ((w[h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                        f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                        f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                    }
                     if (Op::EXACT) {
                         f[0] = Op::minus(f[0], zz_lo[h]);
                         f[1] = Op::minus(f[1], zz_hi[h]);
@@ -626,7 +641,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                         float d[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {  // small terms first
-                            d[i] = c[h][CHAINS - 1][i];
+                            d[i] = Op::TWO_PLACES ? c[h][CHAINS - 1][i] * 0.0625f : c[h][CHAINS - 1][i];
 #pragma unroll
                             for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
                         }
@@ -804,14 +819,19 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     using X = XStep<T, WIDTH, NB, TILES>;
     const int passes = static_cast<int>(a.ids ? a.rows : (a.rows + W4_ROWS - 1) / W4_ROWS);
     const int64_t steps = steps_of(a.K);
-    // Passes with work in them: with ids, the experts that rows with ids drawn
-    // evenly would use (blocks of other passes end at once).
+    // Passes with work in them. With ids, the experts that rows drawn evenly
+    // would use, and two standard deviations more: blocks of a pass too many
+    // would run after all others, blocks of other passes end at once.
     int64_t busy = passes;
     if (a.ids) {
-        double unused = 1.0;
-        for (int r = 0; r < a.rows && r < 64 * a.experts; ++r) unused *= 1.0 - 1.0 / a.experts;
-        const int64_t used = static_cast<int64_t>(a.experts * (1.0 - unused) + 0.5);
-        if (used < busy) busy = used < 1 ? 1 : used;
+        const double e = a.experts, one = pow(1.0 - 1.0 / e, a.rows), two = pow(1.0 - 2.0 / e, a.rows);
+        const double used = e * (1.0 - one), spread = e * one + e * (e - 1.0) * two - e * e * one * one;
+        const int64_t most = static_cast<int64_t>(used + 2.0 * sqrt(spread > 0.0 ? spread : 0.0) + 0.999);
+        const int64_t by_expert = (a.rows + W4_ROWS - 1) / W4_ROWS + a.experts;  // passes there can be
+        busy = a.rows > 8 * a.experts ? by_expert : most;
+        if (busy > passes) busy = passes;
+        if (busy > by_expert) busy = by_expert;
+        if (busy < 1) busy = 1;
     }
     // Rows of a unit: few give every SM its part, many need less of a streamed
     // x and end less often (about a stage's time). The choice makes the
@@ -820,8 +840,11 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     for (int R = 16; R <= 128; R *= 2) {
         const int64_t KS = PAIR * CONSUMERS / (R / 16), x = STREAM ? KS * X::BYTES : 0;
         if (x > X_STAGE) continue;
-        const int64_t units = (a.N + R - 1) / R * busy;
-        const int64_t cost = (units + dev.sm_count - 1) / dev.sm_count * ((steps + KS - 1) / KS + 1) * (Q_STAGE + x / 2);
+        const int64_t units = (a.N + R - 1) / R;
+        int64_t workers = dev.sm_count / busy;  // of a pass
+        workers = workers < 1 ? 1 : workers > units ? units : workers;
+        const int64_t rounds = (units + workers - 1) / workers * ((workers * busy + dev.sm_count - 1) / dev.sm_count);
+        const int64_t cost = rounds * ((steps + KS - 1) / KS + 1) * (Q_STAGE + x / 2);
         if (cost < least) {
             least = cost;
             a.unit_rows = R;
