@@ -17,10 +17,12 @@
 //     subnormal), four bits up it is 16 q 2^-24 (10 bits hold it), so masking
 //     is all; the group's sum is 2^24 (sum (q 2^-24) x) - zero sum x, the sums
 //     of the two positions kept apart until the 16 is taken out.
-//   * bf16 x: q in the low bits of 128.0 (last place 1) is 128 + q exactly;
-//     the group's sum is sum (128 + q) x - (128 + zero) sum x. The subtraction
-//     costs up to four of the 24 bits of the fp32 sums, of which a bf16
-//     result keeps 8.
+//   * bf16 x: q in the low bits of 128.0 (last place 1) is 128 + q exactly,
+//     and so is q - 8 after subtracting 136; the group's sum is
+//     sum (q - 8) x - (zero - 8) sum x. (Without the subtraction from every
+//     operand, sum (128 + q) x - (128 + zero) sum x, a large x whose q is the
+//     zero point would leave its rounding errors, 128 times enlarged, in the
+//     sum.)
 //   * fp32 x: cut into three bf16 terms that add up to it (3 x 8 bits cover
 //     its 24), each multiplied exactly by q - zero, taken from 128 + q by
 //     subtracting 128 + zero before the product, so no bits are lost. A term
@@ -37,10 +39,10 @@
 // all of k. A producer warp streams q into a ring in shared memory by TMA
 // (stages of 32 KB, boxes of 128 bytes x R rows in the 128-byte swizzle, some
 // 100 KB on their way per SM); 16 warps each take two steps of a stage, 16 rows
-// x 128 k each, side by side, and add up their shares of k at the end of a unit. x is laid out
-// either by every block for itself, once, and stays in shared memory, or,
-// where it is too large for that, by a small kernel before this one, and is
-// streamed with q. The swizzle lets a quad's lanes read 64 contiguous bytes of
+// x 128 k each, side by side, and add up their shares of k at the end of a unit.
+// x is laid out either by every block for itself, once, and stays in shared
+// memory, or, where it is too large for that, by a small kernel before this one,
+// and is streamed with q. The swizzle lets a quad's lanes read 64 contiguous bytes of
 // a row without bank conflicts if the rows of a quarter warp are four (groups
 // of 128) or two apart, so row g of a matrix instruction is row_of(g) of a tile.
 #include <cuda.h>
@@ -99,8 +101,9 @@ struct W4Args {
 
 // How a row type enters the matrix instruction: terms of x, the bits that q is
 // placed in, whether zero points are subtracted from the operand (EXACT) or
-// from the group's sum (BASE: what an operand holds on top of q, UNIT: what an
-// operand's 1 is worth), and the instruction itself.
+// from the group's sum (LESS: what is taken from every operand; BASE: what it
+// then holds on top of q, UNIT: what an operand's 1 is worth), and the
+// instruction itself.
 template <class T>
 struct Operand;
 
@@ -110,7 +113,8 @@ struct Operand<__nv_bfloat16> {
     static constexpr bool TWO_PLACES = false;  // q low and four bits up
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0x43004300u;  // 128, 128 in bf16
-    static constexpr float BASE = 128.0f, UNIT = 1.0f;
+    static constexpr uint32_t LESS = 0x43084308u;  // 136, 136: subtracted from every operand
+    static constexpr float BASE = -8.0f, UNIT = 1.0f;
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&d);
@@ -133,6 +137,7 @@ struct Operand<__half> {
     static constexpr bool TWO_PLACES = true;  // q low and four bits up
     static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0;
+    static constexpr uint32_t LESS = 0;
     static constexpr float BASE = 0.0f, UNIT = 16777216.0f;  // an operand's q is q 2^-24
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t) { return a; }
     static __device__ __forceinline__ uint32_t twice(float) { return 0; }
@@ -152,6 +157,7 @@ struct Operand<float> {
     static constexpr bool TWO_PLACES = false;  // q low and four bits up
     static constexpr bool EXACT = true;
     static constexpr uint32_t ONE = Operand<__nv_bfloat16>::ONE;
+    static constexpr uint32_t LESS = 0;
     static constexpr float BASE = 0.0f, UNIT = 1.0f;
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         return Operand<__nv_bfloat16>::minus(a, b);
@@ -608,6 +614,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                         f[1] = ((w[h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
                         f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
                         f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                    }
+                    if (Op::LESS != 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] = Op::minus(f[i], Op::LESS);
                     }
                     if (Op::EXACT) {
                         f[0] = Op::minus(f[0], zz_lo[h]);

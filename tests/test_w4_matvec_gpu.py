@@ -122,6 +122,31 @@ def test_large_and_small_fp32(ex):
         assert torch.equal(ex.w4_matvec(x, q, scales, group=128)[0], x[0, 77].expand(16))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_outliers(ex, dtype, zeros):
+    """Values of x a thousand times the others where q is the zero point: they must leave no trace in the sum."""
+    rng = np.random.default_rng(12)
+    dt, N, K, group = DTYPES[dtype], 64, 1024, 128
+    q, scales, z = _weights(rng, 1, N, K, group, zeros)
+    v = np.empty((N, K), dtype=np.uint8)
+    v[:, 0::2], v[:, 1::2] = q[0] & 15, q[0] >> 4
+    x = rng.standard_normal((3, K)).astype(np.float32)
+    for g in range(K // group):
+        x[:, g * group + 5] = 1000.0 * (g + 1)
+        v[:, g * group + 5] = 8 if z is None else z[0, :, g]
+    q[0] = v[:, 0::2] | (v[:, 1::2] << 4)
+    x = torch.from_numpy(x).to(dt)
+    w = _dense(q, scales.astype(np.float64), z, group)[0]
+    want, mag = x.double().numpy() @ w.T, np.abs(x.double().numpy()) @ np.abs(w).T
+    y = ex.w4_matvec(x.cuda(), torch.from_numpy(q[0]).cuda(), torch.from_numpy(scales[0]).cuda(), group=group,
+                     zeros=None if z is None else torch.from_numpy(z[0]).cuda())
+    # Zero points are taken from sums of q (fp16) or q - 8 (bf16): the outlier's share of those, at most 15 of it,
+    # is cut at each of a group's 8 matrix instructions and rounded twice when it is taken out (doubled, as in bound).
+    share = 0.0 if dtype == "f32" else 15.0 * scales.max() * sum(1000.0 * (g + 1) for g in range(K // group))
+    assert_within(y, want, bound(want, mag, 3 * K + K // group + 2, dt) + 20 * 2.0 ** -23 * share)
+
+
 def test_other_stream(ex):
     rng = np.random.default_rng(6)
     q, scales, _ = _weights(rng, 1, 512, 1024, 128, False)
