@@ -11,6 +11,8 @@ namespace {
 
 // Element offsets must fit in int64 bytes with room to spare.
 constexpr int64_t kLimit = INT64_C(1) << 58;
+// Rows of a product: a tile past the last one still fits 32 bits.
+constexpr int64_t kMostRows = INT32_MAX - 1024;
 
 bool type_ok(int type) { return type >= SGEMM_TYPE_F32 && type <= SGEMM_TYPE_F16; }
 
@@ -149,7 +151,7 @@ int sgemm_experts_combine_grad(int type, int64_t tokens, int64_t top_k, int64_t 
 int sgemm_experts_gemm(int type, int transB, int64_t rows, int64_t N, int64_t K, int64_t experts,
                        const int32_t *offsets, const void *A, int64_t lda, const void *B, int64_t ldb,
                        int64_t strideB, void *C, int64_t ldc, sgemm_stream_t stream) {
-    if (!type_ok(type) || (transB != SGEMM_OP_N && transB != SGEMM_OP_T) || rows < 0 || rows > INT32_MAX || N < 0 ||
+    if (!type_ok(type) || (transB != SGEMM_OP_N && transB != SGEMM_OP_T) || rows < 0 || rows > kMostRows || N < 0 ||
         K < 0 || experts < 1 || experts > SGEMM_EXPERTS_MAX)
         return SGEMM_ERR_INVALID_ARG;
     const int64_t size = type_size(type);
@@ -183,7 +185,7 @@ int sgemm_experts_gemm(int type, int transB, int64_t rows, int64_t N, int64_t K,
 int sgemm_experts_gemm_wgrad(int type, int64_t rows, int64_t M, int64_t N, int64_t experts, const int32_t *offsets,
                              const void *A, int64_t lda, const void *B, int64_t ldb, void *C, int64_t ldc,
                              int64_t strideC, sgemm_stream_t stream) {
-    if (!type_ok(type) || rows < 0 || rows > INT32_MAX || M < 0 || N < 0 || experts < 1 ||
+    if (!type_ok(type) || rows < 0 || rows > kMostRows || M < 0 || N < 0 || experts < 1 ||
         experts > SGEMM_EXPERTS_MAX)
         return SGEMM_ERR_INVALID_ARG;
     const int64_t size = type_size(type);

@@ -16,9 +16,9 @@ namespace ex {
 namespace {
 
 constexpr int kMaxDevices = 64;
-std::once_flag g_once[kMaxDevices][6];
-cudaError_t g_err[kMaxDevices][6];
-int g_clusters[kMaxDevices][6];
+std::once_flag g_once[kMaxDevices][9];
+cudaError_t g_err[kMaxDevices][9];
+int g_clusters[kMaxDevices][9];
 
 // The library's rule for one product: from here on operands that tensor maps
 // cannot describe are first copied into aligned rows (a pass over memory),
@@ -31,18 +31,18 @@ constexpr double COPY_FROM = 1.25 * 1073741824.0;
 // 8 k-blocks, 96 such MMAs: 2.0e-6 of the result's norm on normal inputs, where
 // fp32 sums give 0.57e-6 at K = 1024. Here a fold every 5 k-blocks, the small
 // products (lo hi, hi lo) of the first 4 before any large one, leaves 28: 0.7e-6.
-// A fold moves 128 KB through shared memory, which bounds the kernel: 8192 rows,
-// 8 experts, 1024 -> 2048 take 199 us (172 TFLOP/s), 160 with the single
-// product's folds; folds every 4 or 3 k-blocks in the usual order 208 and 242 us
-// for 1.0e-6 and 0.8e-6.
+// Folds move the tile through shared memory and held stages are not refilled:
+// 8192 rows, 8 experts, 1024 -> 2048 take 179 us (192 TFLOP/s); 4 k-blocks with 3
+// ahead 187 us (0.64e-6), 6 with 4 ahead 175 us (0.98e-6), 6 with 3 ahead 171 us
+// (1.15e-6).
 constexpr int GROUP_FOLD = 5, GROUP_LEAD = 4;
 
 template <bool VEC_C, bool TA, bool TB, PairUnits UNITS>
 int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
            int *launches) {
     auto kernel = tf32x3_pair_kernel<VEC_C, TA, TB, UNITS, GROUP_FOLD, GROUP_LEAD>;
-    constexpr bool WG = UNITS == GROUP_WGRAD;
-    constexpr int idx = (VEC_C ? 3 : 0) + (WG ? 2 : TB ? 1 : 0);
+    constexpr bool WG = sums_rows(UNITS), COLS = transposed(UNITS);
+    constexpr int idx = COLS ? 6 + (WG ? 2 : TA ? 1 : 0) : (VEC_C ? 3 : 0) + (WG ? 2 : TB ? 1 : 0);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -75,7 +75,12 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
     alignas(64) CUtensorMap mapA{}, mapB{}, mapC{};
     if (!cpa) {
         const bool ok =
-            WG ? encode_map(&mapA, q.A, p.rows, p.M, q.lda, 1, 0, 32, 32, sw) &&
+            WG && COLS ? encode_map(&mapA, q.B, p.rows, p.N, q.ldb, 1, 0, 32, 32, sw) &&
+                             encode_map(&mapB, q.A, p.rows, p.M, q.lda, 1, 0, pr::HN, BK, plain)
+            : COLS ? (TA ? encode_map(&mapA, q.B, p.K, p.N, q.ldb, p.experts, q.strideB, 32, 32, sw)
+                       : encode_map(&mapA, q.B, p.N, p.K, q.ldb, p.experts, q.strideB, BK, pr::HM, sw)) &&
+                       encode_map(&mapB, q.A, p.rows, p.K, q.lda, 1, 0, BK, pr::HN, sw)
+            : WG ? encode_map(&mapA, q.A, p.rows, p.M, q.lda, 1, 0, 32, 32, sw) &&
                      encode_map(&mapB, q.B, p.rows, p.N, q.ldb, 1, 0, pr::HN, BK, plain)
                : encode_map(&mapA, q.A, p.rows, p.K, q.lda, 1, 0, BK, pr::HM, sw) &&
                      (TB ? encode_map(&mapB, q.B, p.N, p.K, q.ldb, p.experts, q.strideB, BK, pr::HN, sw)
@@ -83,21 +88,23 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
         if (!ok) return SGEMM_ERR_LAUNCH;
     }
     const int64_t c_rows = WG ? p.M : p.rows, c_items = WG ? p.experts : 1, c_stride = c_items > 1 ? p.strideC : 0;
-    const bool c_tma = VEC_C && tma_operand_ok(q.C, p.ldc, c_stride, c_rows, c_items) &&
+    const bool c_tma = !COLS && VEC_C && tma_operand_ok(q.C, p.ldc, c_stride, c_rows, c_items) &&
                        encode_map(&mapC, q.C, c_rows, p.N, p.ldc, c_items, c_stride, 32, 32, sw);
     if (!c_tma) mapC = mapA;  // not read by the kernel
 
-    const int64_t tiles_n = (p.N + pr::PN - 1) / pr::PN, tiles_m = WG ? (p.M + pr::PM - 1) / pr::PM : 1;
+    const int64_t wide = COLS ? pr::PM : pr::PN, high = COLS ? pr::PN : pr::PM;  // of a tile of C
+    const int64_t tiles_n = (p.N + wide - 1) / wide, tiles_m = WG ? (p.M + high - 1) / high : 1;
     if (tiles_m * tiles_n > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     Args a{};
-    a.M = p.M;
-    a.N = p.N;
+    a.M = COLS ? p.N : p.M;
+    a.N = COLS ? p.M : p.N;
     a.K = p.K;
-    a.A = q.A;
-    a.lda = q.lda;
-    a.B = q.B;
-    a.ldb = q.ldb;
-    a.strideB = q.strideB;
+    a.A = COLS ? q.B : q.A;
+    a.lda = COLS ? q.ldb : q.lda;
+    a.strideA = COLS ? q.strideB : 0;
+    a.B = COLS ? q.A : q.B;
+    a.ldb = COLS ? q.lda : q.ldb;
+    a.strideB = COLS ? 0 : q.strideB;
     a.C = q.C;
     a.ldc = p.ldc;
     a.strideC = c_stride;
@@ -116,7 +123,7 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
                         static_cast<int>(tiles_n)};
     // Every group may end in a part of a tile, and so may the rest.
     const int64_t units =
-        WG ? tiles_m * tiles_n * p.experts : ((p.rows + pr::PM - 1) / pr::PM + p.experts) * tiles_n;
+        WG ? tiles_m * tiles_n * p.experts : ((p.rows + high - 1) / high + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a, gt) != cudaSuccess) {
         cudaGetLastError();
@@ -126,9 +133,30 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
     return SGEMM_OK;
 }
 
+// Whether the rows of C are the MMA's narrow side (C^T: 256 columns of C a
+// tile, rows by the 32) or its wide side (128 columns a tile, rows by the 256):
+// what a call is charged, with groups that end half a step short on average.
+// Narrow (C^T from registers) against wide (C through TMA): 168 and 179 us (8192
+// rows, 8 experts, 2048 -> 1024), 113 and 275 us (64 rows, 32 experts, 2048 ->
+// 2048; the matrices alone are 79 us of DRAM); for 8192 rows, 8 experts, 1024 ->
+// 128, where half of a narrow tile would be columns of nothing, wide takes 40 us.
+bool rows_narrow(const GroupedProblem &p) {
+    auto charged = [&](int64_t step) {
+        return p.wgrad ? (p.M + step - 1) / step * step : p.rows + p.experts * step / 2;
+    };
+    const int64_t narrow = (p.N + pr::PM - 1) / pr::PM * pr::PM * charged(pr::COL_STEP);
+    const int64_t wide = (p.N + pr::PN - 1) / pr::PN * pr::PN * charged(pr::PM);
+    return narrow <= wide;
+}
+
 template <bool VEC_C>
 int launch_form(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
                 int *launches) {
+    if (rows_narrow(p)) {
+        if (p.wgrad) return launch<true, true, false, GROUP_WGRAD_COLS>(p, q, cpa, dev, stream, launches);
+        return p.transB == SGEMM_OP_T ? launch<true, false, true, GROUP_COLS>(p, q, cpa, dev, stream, launches)
+                                      : launch<true, true, true, GROUP_COLS>(p, q, cpa, dev, stream, launches);
+    }
     if (p.wgrad) return launch<VEC_C, true, false, GROUP_WGRAD>(p, q, cpa, dev, stream, launches);
     return p.transB == SGEMM_OP_T ? launch<VEC_C, false, true, GROUP_ROWS>(p, q, cpa, dev, stream, launches)
                                   : launch<VEC_C, false, false, GROUP_ROWS>(p, q, cpa, dev, stream, launches);

@@ -60,7 +60,12 @@
 // tiles of row groups whose bounds are read on the device in place of the
 // tiles of one product (see GroupTiles), nothing else changed. Rows of A past
 // a group's end change only rows of C that are not written; where the rows
-// are the summed direction the converters put zeros in their place.
+// are the summed direction the converters put zeros in their place. The rows
+// of C may also be the MMA's narrow side (GROUP_COLS, GROUP_WGRAD_COLS): the
+// product is then C^T = op(B)^T A^T in tiles of 256 columns of C x 32 .. 128
+// rows, so a short group is charged for a multiple of 32 rows, and a lane of
+// the epilogue holds a column of C, so that warps write 128 bytes of its rows
+// from registers without another pass through shared memory.
 #pragma once
 
 #include <cuda.h>
@@ -114,9 +119,12 @@ constexpr int BAR_OFFSET = R0 + R_BYTES;
 constexpr int PBAR_BYTES = 256;
 constexpr int SMEM_BYTES = BAR_OFFSET + PBAR_BYTES + 1024;
 constexpr uint32_t TMEM_A = 2 * PN;  // A stages after the two 128-column accumulators
-// Instruction descriptor: D fp32, A and B tf32, both K-major, N = 128, M = 256.
-constexpr uint32_t kIdesc2 = (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(PN >> 3) << 17) |
-                             (static_cast<uint32_t>(PM >> 4) << 24);
+// Instruction descriptor: D fp32, A and B tf32, both K-major, N = n (128: a whole tile), M = 256.
+__host__ __device__ constexpr uint32_t idesc2(int n) {
+    return (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(PM >> 4) << 24);
+}
+constexpr int COL_STEP = 32;  // GROUP_COLS: a tile's width is a multiple of it
 // mbarrier indices
 constexpr int RAW_FULL = 0, RAW_FREE = RAW_FULL + RAW_SLOTS, OP_FULL = RAW_FREE + RAW_SLOTS,
               OP_EMPTY = OP_FULL + OP_STAGES, ACC_FULL = OP_EMPTY + OP_STAGES, ACC_EMPTY = ACC_FULL + 2,
@@ -136,16 +144,17 @@ static_assert(SLOT % 1024 == 0 && RAW0 % 1024 == 0 && R0 % 1024 == 0, "1024-byte
 
 }  // namespace pr
 
-// One 256 x 128 x 8 product of the pair: A (128 rows per CTA) from TMEM, B
-// (64 columns per CTA) from shared memory.
-__device__ __forceinline__ void tc_mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t accumulate) {
+// One 256 x n x 8 product of the pair: A (128 rows per CTA) from TMEM, B
+// (n / 2 columns per CTA) from shared memory.
+__device__ __forceinline__ void tc_mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t accumulate,
+                                           uint32_t idesc = pr::idesc2(pr::PN)) {
     asm volatile(
         "{\n"
         " .reg .pred p;\n"
         " setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::2.kind::tf32 [%0], [%1], %2, %3, p;\n"
         "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(pr::kIdesc2), "r"(accumulate)
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -188,6 +197,26 @@ __device__ __forceinline__ void stage32_fused(int act, uint32_t buf, int lane, f
     }
 }
 
+// NaN in a chunk of finished sums (chunk rc, swizzled, this lane holding row
+// `row`, columns from col0 on) recomputed over [k_begin, k_end), in shared
+// memory, one column at a time (few registers).
+__device__ __forceinline__ void repair_row(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row,
+                                           int64_t col0, int64_t n_end, int64_t k_begin, int64_t k_end) {
+    const int lane = static_cast<int>(threadIdx.x & 31);
+#pragma unroll 1
+    for (int j = 0; j < 32 && col0 + j < n_end; ++j) {
+        const uint32_t addr = rc + sw128_offset(lane, j >> 2) + static_cast<uint32_t>((j & 3) * 4);
+        const float x = ld_shared_f32(addr);
+        if (x != x) st_shared_f32(addr, dot_ieee(A, a.lda, a.ta, B, a.ldb, a.tb, row, col0 + j, k_begin, k_end));
+    }
+}
+
+// The same for a chunk of C^T: v is this lane's row of it (a column of C).
+__device__ __noinline__ void repair_column(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row,
+                                           int64_t col0, int64_t n_end, int64_t k_end) {
+    if (row < a.M) repair_row(a, rc, A, B, row, col0, n_end, 0, k_end);
+}
+
 // The last fold of a unit for a chunk written with per-thread stores: the
 // unit's finished sum for rows row0 .. row0 + 31, columns col0 .. col0 + 31
 // (chunk rc of shared memory, swizzled, lane l holding row row0 + l),
@@ -212,22 +241,17 @@ __device__ __noinline__ void edge_final_chunk(const Args &a, uint32_t rc, const 
         const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
         nan |= r.x != r.x || r.y != r.y || r.z != r.z || r.w != r.w;
     }
-    if (nan && row < m_end) {
-        // Repair in shared memory, one column at a time (few registers).
-#pragma unroll 1
-        for (int j = 0; j < 32 && col0 + j < a.N; ++j) {
-            const uint32_t addr = rc + sw128_offset(lane, j >> 2) + static_cast<uint32_t>((j & 3) * 4);
-            const float x = ld_shared_f32(addr);
-            if (x != x) st_shared_f32(addr, dot_ieee(A, a.lda, a.ta, B, a.ldb, a.tb, row, col0 + j, k_begin, k_end));
-        }
-    }
+    if (nan && row < m_end) repair_row(a, rc, A, B, row, col0, a.N, k_begin, k_end);
     __syncwarp();
     store_staged_rows(a, rc, citem, m_end, row0, col0, atomic);
 }
 
 // What the kernel's units are: k-block ranges of one product's tiles
-// (stream-K), or whole tiles of row groups.
-enum PairUnits { TILES, GROUP_ROWS, GROUP_WGRAD };
+// (stream-K), or whole tiles of row groups (_COLS: of C^T, with the operands'
+// places changed: M counts the columns of C and N its rows).
+enum PairUnits { TILES, GROUP_ROWS, GROUP_COLS, GROUP_WGRAD, GROUP_WGRAD_COLS };
+constexpr bool sums_rows(PairUnits u) { return u == GROUP_WGRAD || u == GROUP_WGRAD_COLS; }
+constexpr bool transposed(PairUnits u) { return u == GROUP_COLS || u == GROUP_WGRAD_COLS; }
 
 // A unit: k-blocks [kb, ke) of the tile at row m0, column n0 of C's item.
 // Rows of C from m_end on are not written.
@@ -235,8 +259,13 @@ struct PairUnit {
     int kb, ke;
     int item_a, item_b, item_c;
     int64_t m0, n0, m_end;
-    int64_t k0, k_end;  // first row of A and B that is summed and the values of k (GROUP_WGRAD: rows of the group)
+    int64_t k0, k_end;  // first row of A and B that is summed and the values of k (wgrad: rows of the group)
     bool atomic;        // a part of a tile: C += instead of C =
+    int64_t n_end;      // C^T: end of the tile's columns (rows of C)
+    // C^T: the MMA's width.
+    __device__ __forceinline__ int width() const {
+        return (static_cast<int>(n_end - n0) + pr::COL_STEP - 1) / pr::COL_STEP * pr::COL_STEP;
+    }
 };
 
 // Calls f(unit) for the units of worker `index` of `count`, in order.
@@ -247,21 +276,32 @@ __device__ __forceinline__ void for_each_pair_unit(const Args &a, const ex::Grou
         for_each_unit_of(a, abort_flag, index, count, [&](int tile, int kb, int ke) {
             const TileAt at = tile_at<pr::PM, pr::PN>(a, tile);
             f(PairUnit{kb, ke, a.a_shared ? 0 : at.item, a.b_shared ? 0 : at.item, at.item, at.m0, at.n0, a.M, 0, a.K,
-                       tile >= a.dp_tiles});
+                       tile >= a.dp_tiles, a.N});
         });
+    } else if (UNITS == GROUP_WGRAD_COLS) {
+        ex::for_each_group_tile<true, pr::PN, pr::PM, BK>(
+            gt, abort_flag, index, count, [&](const ex::GroupTile &t) {
+                f(PairUnit{0, t.k_blocks, 0, 0, t.group, t.n0, t.row0, a.M, t.k0, t.k_rows, false,
+                           min(t.row0 + pr::PN, t.row_end)});
+            });
+    } else if (UNITS == GROUP_COLS) {
+        ex::for_each_group_tile<false, pr::PN, pr::PM, BK, pr::COL_STEP>(
+            gt, abort_flag, index, count, [&](const ex::GroupTile &t) {
+                f(PairUnit{0, t.k_blocks, t.group, 0, 0, t.n0, t.row0, a.M, 0, a.K, false, t.row_end});
+            });
     } else {
         ex::for_each_group_tile<UNITS == GROUP_WGRAD, pr::PM, pr::PN, BK>(
             gt, abort_flag, index, count, [&](const ex::GroupTile &t) {
                 if (UNITS == GROUP_WGRAD)
-                    f(PairUnit{0, t.k_blocks, 0, 0, t.group, t.row0, t.n0, t.row_end, t.k0, t.k_rows, false});
+                    f(PairUnit{0, t.k_blocks, 0, 0, t.group, t.row0, t.n0, t.row_end, t.k0, t.k_rows, false, a.N});
                 else
-                    f(PairUnit{0, t.k_blocks, 0, t.group, 0, t.row0, t.n0, t.row_end, 0, a.K, false});
+                    f(PairUnit{0, t.k_blocks, 0, t.group, 0, t.row0, t.n0, t.row_end, 0, a.K, false, a.N});
             });
     }
 }
 
 // TA: A stored K x M (op(A) = A^T); TB: B stored N x K (op(B) = B^T).
-// GROUP_WGRAD is op(A) = A^T, op(B) = B over a group's rows.
+// Over a group's rows op(A) = A^T and op(B) = B.
 // FOLD: the longest chain of k-blocks. LEAD > 0: in a chain's first LEAD
 // k-blocks (and within every other) the small products, lo hi and hi lo, come
 // before the large one, hi hi, while the accumulator is small and what the MMAs
@@ -272,8 +312,10 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Args a,
                        const __grid_constant__ ex::GroupTiles gt) {
     static_assert(LEAD <= pr::OP_STAGES, "the leading k-blocks are staged together");
-    static_assert(UNITS != GROUP_WGRAD || (TA && !TB), "groups are summed along the stored rows of both operands");
-    constexpr bool SUMS_ROWS = UNITS == GROUP_WGRAD;
+    constexpr bool SUMS_ROWS = sums_rows(UNITS), COLS = transposed(UNITS);
+    static_assert(!SUMS_ROWS || (TA && !TB), "groups are summed along the stored rows of both operands");
+    static_assert(UNITS != GROUP_COLS || TB, "the rows of C are K-major");
+    static_assert(!COLS || LEAD > 0, "the width of tiles is the leading products' to set");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -305,7 +347,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                 return;
             }
             const int m0 = static_cast<int>(u.m0) + pr::HM * static_cast<int>(rank);
-            const int n0 = static_cast<int>(u.n0) + pr::HN * static_cast<int>(rank);
+            const int n0 = static_cast<int>(u.n0) + (COLS ? u.width() / 2 : pr::HN) * static_cast<int>(rank);
             const int za = u.item_a, zb = u.item_b;
             const int k0 = SUMS_ROWS ? static_cast<int>(u.k0) : 0;
             for (int kblk = kb; kblk < ke && it < to; ++kblk, ++it) {
@@ -356,7 +398,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                 return;
             }
             const int64_t m0 = u.m0 + pr::HM * static_cast<int64_t>(rank);
-            const int64_t n0 = u.n0 + pr::HN * static_cast<int64_t>(rank);
+            const int64_t n0 = u.n0 + (COLS ? u.width() / 2 : pr::HN) * static_cast<int64_t>(rank);
             const int64_t K = UNITS == TILES ? a.K : u.k_end;
             const float *Ai = a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0);
             const float *Bi = a.B + u.item_b * a.strideB + (SUMS_ROWS ? u.k0 * a.ldb : 0);
@@ -490,6 +532,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             bool ready = false;  // the stage of k-block `it` was seen full (and fenced) early
             for_each_pair_unit<UNITS>(a, gt, abort_flag, pair, pairs, [&](const PairUnit &u) {
                 const int kb = u.kb, ke = u.ke;
+                const uint32_t idesc = pr::idesc2(COLS ? u.width() : pr::PN);
                 for (int k0 = kb; k0 < ke; k0 += FOLD) {
                     const int k1 = ke - k0 > FOLD ? k0 + FOLD : ke;
                     const uint32_t d = iv & 1;
@@ -515,8 +558,12 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                                 if (leader) {
 #pragma unroll
                                     for (int ks = 0; ks < BK / 8; ++ks) {
-                                        tc_mma2_ts(dt, a_lo + ks * 8, b_hi + ks * 2, ks > 0 || i > 0 || kblk > k0);
-                                        tc_mma2_ts(dt, a_hi + ks * 8, b_lo + ks * 2, 1u);
+                                        // C^T: the factors' order the other way round, for the same sums.
+                                        const uint32_t more = ks > 0 || i > 0 || kblk > k0;
+                                        tc_mma2_ts(dt, (COLS ? a_hi : a_lo) + ks * 8, (COLS ? b_lo : b_hi) + ks * 2, more,
+                                                   idesc);
+                                        tc_mma2_ts(dt, (COLS ? a_lo : a_hi) + ks * 8, (COLS ? b_hi : b_lo) + ks * 2, 1u,
+                                                   idesc);
                                     }
                                 }
                                 __syncwarp();
@@ -528,7 +575,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                                 if (leader) {
 #pragma unroll
                                     for (int ks = 0; ks < BK / 8; ++ks)
-                                        tc_mma2_ts(dt, a_hi + ks * 8, b_hi + ks * 2, 1u);
+                                        tc_mma2_ts(dt, a_hi + ks * 8, b_hi + ks * 2, 1u, idesc);
                                     tc_commit2(bar(pr::OP_EMPTY + s));
                                 }
                                 __syncwarp();
@@ -604,6 +651,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
         for_each_pair_unit<UNITS>(a, gt, abort_flag, pair, pairs, [&](const PairUnit &u) {
             const int kb = u.kb, ke = u.ke;
             if (!ok) return;
+            const int quarters = COLS ? u.width() / 32 : 4;  // of 16 rows of B that the MMAs read
             for (int kblk = kb; kblk < ke; ++kblk, ++it) {
                 if (it % pr::CONV_GROUPS != group) continue;
                 const int slot = static_cast<int>(it % pr::RAW_SLOTS);
@@ -668,6 +716,8 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                     // Same swizzled K-major layout: chunk for chunk.
 #pragma unroll
                     for (int qq = 0; qq < 4; ++qq) {
+                        
+                        if (TB && COLS && qq >= quarters) break;
                         const uint32_t off = static_cast<uint32_t>((qq * pr::CONV_THREADS + ct) * 16);
                         split_store(st + off, st + pr::B_HALF + off, bq[qq].x, bq[qq].y, bq[qq].z, bq[qq].w);
                     }
@@ -730,6 +780,84 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             const bool fused = a.ep && !atomic;
             const bool col_bias = a.bias_kind == SGEMM_BIAS_PER_COL;
             const float rb = (a.bias_kind == SGEMM_BIAS_PER_ROW && row < u.m_end) ? __ldg(a.bias + row) : 0.0f;
+            if constexpr (COLS) {
+                // C^T: lanes are columns of C, accumulator columns its rows, written
+                // straight from registers, 128 bytes of a row at a time.
+                const int chunks = u.width() / 32;
+                const bool mine = row < u.m_end;
+                auto write = [&](int ch, const float (&v)[32]) {
+                    const int64_t r0 = u.n0 + ch * 32;
+                    float *p = a.C + u.item_c * a.strideC + r0 * a.ldc + row;
+                    const int rows = static_cast<int>(min(static_cast<int64_t>(32), u.n_end - r0));
+                    const int64_t ldc = a.ldc;
+                    if (!mine) return;
+                    if (rows == 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += ldc) *p = v[j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < rows) p[j * ldc] = v[j];
+                    }
+                };
+                if (ke == kb) {
+                    const float zeros[32] = {};
+#pragma unroll 1
+                    for (int ch = 0; ch < chunks; ++ch) write(ch, zeros);
+                    return;
+                }
+                for (int k0 = kb; k0 < ke; k0 += FOLD) {
+                    const bool first = k0 == kb, last = ke - k0 <= FOLD;
+                    const uint32_t d = iv & 1;
+                    if (!mbar_wait<true>(bar(pr::ACC_FULL + d), (iv >> 1) & 1, a, abort_flag, WD_EPILOGUE)) return;
+                    tc_fence_after();
+                    ++iv;
+                    const uint32_t dt = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + d * pr::PN;
+#pragma unroll 1
+                    for (int ch = 0; ch < chunks; ++ch) {
+                        const uint32_t rc = rq + static_cast<uint32_t>(ch * pr::C_CHUNK);
+                        float v[32];
+                        tmem_load32(dt + static_cast<uint32_t>(ch * 32), v);
+                        if (ch == chunks - 1) release(d);
+                        if (!first) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
+                                v[4 * j] += r.x;
+                                v[4 * j + 1] += r.y;
+                                v[4 * j + 2] += r.z;
+                                v[4 * j + 3] += r.w;
+                            }
+                        }
+                        bool nan = false;
+                        if (last) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) nan |= v[j] != v[j];
+                        }
+                        if (!last || nan) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                st_shared_v4(rc + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                                             v[4 * j + 3]);
+                        }
+                        if (nan) {
+                            repair_column(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
+                                          a.B + (SUMS_ROWS ? u.k0 * a.ldb : 0), row, u.n0 + ch * 32, u.n_end, u.k_end);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
+                                v[4 * j] = r.x;
+                                v[4 * j + 1] = r.y;
+                                v[4 * j + 2] = r.z;
+                                v[4 * j + 3] = r.w;
+                            }
+                        }
+                        if (last) write(ch, v);
+                        __syncwarp();
+                    }
+                }
+                return;
+            }
             // The previous unit's TMA stores read the running sum: wait until
             // they have, before this unit overwrites it.
             if (lane == 0) bulk_wait_read<0>();

@@ -104,13 +104,15 @@ int sgemm_experts_combine_grad(int type, int64_t tokens, int64_t top_k, int64_t 
  *   B, ldb     experts matrices strideB elements apart (strideB >= one
  *              matrix), each K x N (SGEMM_OP_N) or N x K (SGEMM_OP_T).
  *   C, ldc     out, rows x N.
- * rows must be below 2^31. fp32 inputs follow sgemm_f32's accuracy bound and
- * its rules for infinities and NaN (on normal inputs the error is that of
- * fp32 sums); bf16 and fp16 products are exact in fp32 and summed in fp32,
- * where the tensor core cuts a running sum at every 16 products: about 2e-8
- * of it each time, 2e-5 for sums of 16384, far below the rounding of the
- * result. A row's result depends on that row and its expert's matrix only. The gradient of A is the same call on C's gradient
- * with transB the other way round.
+ * rows must be below 2^31 - 1024. fp32 inputs follow sgemm_f32's accuracy
+ * bound and its rules for infinities and NaN (on normal inputs the error is
+ * that of fp32 sums); bf16 and fp16 products are exact in fp32 and summed in
+ * fp32, where the tensor core cuts a running sum at every 16 products: about
+ * 2e-8 of it each time, 2e-5 for sums of 16384, far below the rounding of the
+ * result. A row's result depends on that row and its expert's matrix only,
+ * whatever the other sizes (16-bit operands whose rows are not 16-byte aligned
+ * are summed in one of two orders, by the sizes). The gradient of A is the same
+ * call on C's gradient with transB the other way round.
  */
 int sgemm_experts_gemm(int type, int transB, int64_t rows, int64_t N, int64_t K, int64_t experts,
                        const int32_t *offsets, const void *A, int64_t lda, const void *B, int64_t ldb,
@@ -118,7 +120,7 @@ int sgemm_experts_gemm(int type, int transB, int64_t rows, int64_t N, int64_t K,
 
 /*
  * One product per group over its rows: C[e] = sum over s in group e of
- * A[s]^T * B[s] (an empty group gives zeros).
+ * A[s]^T * B[s] (an empty group gives zeros). rows must be below 2^31 - 1024.
  *   A, lda     rows x M.
  *   B, ldb     rows x N.
  *   C, ldc     out, experts matrices of M x N, strideC elements apart.

@@ -116,6 +116,13 @@ def test_gemm_wgrad_refuses(ex, change):
     assert ex.lib.sgemm_experts_gemm_wgrad(*a.values(), None) == 1
 
 
+def test_most_rows(ex):
+    """Rows near 2^31 are refused by their number alone: nothing else is wrong here, and nothing to do."""
+    for rows, refused in (((1 << 31) - 1025, False), ((1 << 31) - 1024, True)):
+        assert (ex.lib.sgemm_experts_gemm(0, 0, rows, 0, 0, 4, 4 * P, 0, 1, 0, 1, 0, 0, 1, None) == 1) == refused
+        assert (ex.lib.sgemm_experts_gemm_wgrad(0, rows, 0, 0, 4, 4 * P, 0, 1, 0, 1, 0, 1, 0, None) == 1) == refused
+
+
 @pytest.mark.parametrize("change", [
     {"type": 3}, {"rows": -1}, {"rows": 65536}, {"N": -1}, {"K": 63}, {"group": 48}, {"group": 0}, {"group": 512},
     {"experts": 0}, {"ids": 0}, {"x": 0}, {"q": 0}, {"scales": 0}, {"scale_type": 3}, {"y": 0}, {"ldx": 63},

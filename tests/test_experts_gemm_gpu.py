@@ -136,6 +136,27 @@ def test_gradients_against_differences(ex):
         assert abs(along_b - dot(db, v)) <= tol
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [104, 264])
+def test_a_rows_result_is_its_own(ex, dtype, N, trans):
+    """The same bits whatever rows a row is among, and however many: tiles are shaped by the sizes."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng(17)
+    counts, K = [700, 3, 650], 328
+    a, b = _inputs(rng, dt, counts, 0, K, N, trans)
+    a[10, 7], a[701, 5] = float("inf"), float("nan")
+    a, b, off = a.cuda(), b.cuda(), offsets_of(counts)
+    whole = ex.gemm(a, b, off.cuda(), transB=trans)
+    for e in range(3):
+        for first, few in ((0, 1), (1, 2), (counts[e] - 2, 2)):
+            at = int(off[e]) + first
+            part = ex.gemm(a[at:at + few], b[e:e + 1], offsets_of([few]).cuda(), transB=trans)
+            assert torch.equal(torch.nan_to_num(part, 7.0), torch.nan_to_num(whole[at:at + few], 7.0))
+            assert torch.equal(torch.isnan(part), torch.isnan(whole[at:at + few]))
+    assert torch.isinf(whole[10]).all() and torch.isnan(whole[701]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_integer_values_are_exact(ex, dtype):
     dt = DTYPES[dtype]
