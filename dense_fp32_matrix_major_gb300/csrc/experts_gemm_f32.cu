@@ -20,11 +20,6 @@ std::once_flag g_once[kMaxDevices][9];
 cudaError_t g_err[kMaxDevices][9];
 int g_clusters[kMaxDevices][9];
 
-// The library's rule for one product: from here on operands that tensor maps
-// cannot describe are first copied into aligned rows (a pass over memory),
-// below it the kernel loads them itself with 4-byte copies.
-constexpr double COPY_FROM = 1.25 * 1073741824.0;
-
 // Folds of the accumulators. The tensor core cuts its running sum at every MMA
 // (half a unit of the last place on average, towards zero), so the error grows
 // with the MMAs that add to a large running sum. The single product folds every
@@ -149,6 +144,24 @@ bool rows_narrow(const GroupedProblem &p) {
     return narrow <= wide;
 }
 
+// Operands that tensor maps cannot describe are either copied into aligned rows
+// first or loaded by the kernel with 4-byte copies, which take it 6 us a k-block.
+// What the busiest pair's k-blocks would cost that way against the copies' time.
+// Copied and loaded: 92 and 541 us (1745 rows, 64 experts, 2761 -> 35), 58 and
+// 218 us (2000 rows, 8 experts, 1001 -> 1001); 905 and 232 us (5 rows, 64
+// experts, 2047 -> 2047: the copy takes every expert's matrix).
+bool copy_first(const GroupedProblem &p, size_t bytes, const DeviceInfo &dev) {
+    const bool narrow = rows_narrow(p);
+    const int64_t wide = narrow ? pr::PM : pr::PN, high = narrow ? pr::PN : pr::PM;
+    const int64_t tiles_n = (p.N + wide - 1) / wide, workers = dev.sm_count / 2;
+    const int64_t tiles_m = p.wgrad ? (p.M + high - 1) / high * p.experts
+                                    : (p.rows + high - 1) / high + (p.rows < p.experts ? p.rows : p.experts) / 2;
+    const int64_t depth = p.wgrad ? (p.rows + p.experts - 1) / p.experts : p.K;
+    const double k_blocks = static_cast<double>((tiles_m * tiles_n + workers - 1) / workers) *
+                            static_cast<double>((depth + BK - 1) / BK);
+    return 2.0 * static_cast<double>(bytes) / 5e6 + 10.0 < 5.5 * k_blocks;
+}
+
 template <bool VEC_C>
 int launch_form(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo &dev, cudaStream_t stream,
                 int *launches) {
@@ -193,9 +206,8 @@ int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStrea
     const int64_t b_rows = q.transB == SGEMM_OP_T ? q.N : q.K;
     bool cpa = !tma_operand_ok(q.A, q.lda, 0, p.rows, 1) || !tma_operand_ok(q.B, q.ldb, q.strideB, b_rows, q.batch);
     float *scratch = nullptr;
-    if (cpa && static_cast<double>(p.rows) * static_cast<double>(p.wgrad ? p.M : p.K) * static_cast<double>(p.N) >=
-                   COPY_FROM) {
-        const size_t bytes = repack_bytes(q);
+    const size_t bytes = cpa ? repack_bytes(q) : 0;
+    if (cpa && copy_first(p, bytes, dev)) {
         scratch = scratch_alloc(dev, bytes, stream);
         if (scratch) {
             Problem copied;
