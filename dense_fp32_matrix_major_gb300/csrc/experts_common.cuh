@@ -98,12 +98,13 @@ struct GroupTiles {
     int rows, experts;
     int64_t M, K;          // wgrad: rows of a matrix; otherwise the summed length
     int tiles_m, tiles_n;  // tiles_m: wgrad only
+    int split;             // wgrad: slices of each group's rows, of whole k-blocks but the last
 };
 
 // One tile: rows [row0, row_end) of C (of the group's matrix in wgrad; at most
 // a tile of them) from column n0 on, summed over k_blocks k-blocks; in wgrad
-// those are the k_rows rows of A and B from k0 on. group = experts: rows of C
-// outside every group, nothing to sum.
+// those are the k_rows rows of A and B from k0 on, and group counts the slices of
+// all groups. group = experts: rows of C outside every group, nothing to sum.
 struct GroupTile {
     int group, row0, row_end, n0, k0, k_rows, k_blocks;
 };
@@ -118,13 +119,19 @@ __device__ __forceinline__ void for_each_group_tile(const GroupTiles &a, volatil
                                                     F &&f) {
     if (WGRAD) {
         const int per = a.tiles_m * a.tiles_n;
-        const int64_t total = static_cast<int64_t>(per) * a.experts;
+        const int64_t total = static_cast<int64_t>(per) * a.experts * a.split;
         for (int64_t u = index; u < total; u += count) {
             if (*abort_flag) return;
-            const int e = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<int64_t>(e) * per);
-            const int begin = group_start(a.offsets, e, a.rows);
-            const int end = max(begin, group_start(a.offsets, e + 1, a.rows));
-            f(GroupTile{e, r / a.tiles_n * TM, static_cast<int>(a.M), r % a.tiles_n * TN, begin, end - begin,
+            const int item = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<int64_t>(item) * per);
+            const int e = a.split > 1 ? item / a.split : item;
+            int begin = group_start(a.offsets, e, a.rows);
+            int end = max(begin, group_start(a.offsets, e + 1, a.rows));
+            if (a.split > 1) {
+                const int each = ((end - begin + TK - 1) / TK + a.split - 1) / a.split * TK;
+                begin = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(item - e * a.split) * each));
+                end = min(end - begin, each) + begin;
+            }
+            f(GroupTile{item, r / a.tiles_n * TM, static_cast<int>(a.M), r % a.tiles_n * TN, begin, end - begin,
                         (end - begin + TK - 1) / TK});
         }
     } else {

@@ -7,6 +7,8 @@
 // The group bounds are read on the device, so no call waits for the host. A
 // block makes one 64 x 64 tile of C with 16 x 16 threads, 4 x 4 sums each,
 // in fp32 from 64 x 16 tiles in shared memory; every product in fp32.
+//
+// Also the choice between the kernels, and the split of long sums of wgrad.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -137,13 +139,108 @@ int simple_launch(const GroupedProblem &p, cudaStream_t stream, int *launches) {
     return SGEMM_OK;
 }
 
+// wgrad in slices: few matrices whose tiles leave most SM pairs idle are summed
+// over slices of their groups' rows, each into fp32 sums of its own, which a
+// second kernel adds in the order of the slices.
+struct Join {
+    const float *part;
+    void *C;
+    int64_t rows;  // experts * M
+    int64_t M, N, ld, ldc, strideC;
+    int split, vector;
+};
+
+constexpr int JOIN_THREADS = 256;
+template <class T>
+__global__ void __launch_bounds__(JOIN_THREADS) join_slices_kernel(const Join j) {
+    const int64_t vecs = j.ld / 4, total = j.rows * vecs, item = j.M * j.ld;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * JOIN_THREADS + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * JOIN_THREADS) {
+        const int64_t row = i / vecs, n = (i - row * vecs) * 4, e = row / j.M, m = row - e * j.M;
+        const float *p = j.part + e * j.split * item + m * j.ld + n;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < j.split; ++k, p += item) {
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        T *c = static_cast<T *>(j.C) + e * j.strideC + m * j.ldc + n;
+        const Pack<T, 4> out{{from_f32<T>(s.x), from_f32<T>(s.y), from_f32<T>(s.z), from_f32<T>(s.w)}};
+        if (j.vector && n + 4 <= j.N) {
+            store_pack(c, out);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n + k < j.N) c[k] = out.v[k];
+        }
+    }
+}
+
+// Slices that pay: a k-block takes a pair 0.55 us (fp32, 32 rows) or 0.22 us (16
+// bits, 64 rows); the sums are written and read at 5 TB/s, the second launch
+// and its wait take 6 us. Groups are taken as even. In slices and whole, one
+// group of 30000 rows: 64 x 64 fp32 37 and 552 us, bf16 30 and 119 us; 512 x 512
+// fp32 91 and 593 us, bf16 35 and 138 us; 2000 rows, 64 x 64: fp32 24 and 49 us.
+int slices_of(const GroupedProblem &p, const DeviceInfo &dev) {
+    int64_t high = 256, wide = 256;
+    const bool f32 = p.type == SGEMM_TYPE_F32;
+    if (f32) grouped_f32_tile(p, &high, &wide);
+    const int64_t tiles = (p.M + high - 1) / high * ((p.N + wide - 1) / wide) * p.experts, pairs = dev.sm_count / 2;
+    if (2 * tiles > pairs) return 1;
+    const double k_blocks = static_cast<double>(p.rows) / static_cast<double>(p.experts * (f32 ? 32 : 64));
+    int64_t split = pairs / tiles;
+    if (split > k_blocks / 4) split = static_cast<int64_t>(k_blocks / 4);
+    if (split < 2) return 1;
+    const double sums = 8.0 * static_cast<double>(split * p.experts * p.M * p.N) / 5e6;
+    const double saved = k_blocks * (1.0 - 1.0 / static_cast<double>(split)) * (f32 ? 0.55 : 0.22);
+    return saved > 6.0 + sums ? static_cast<int>(split) : 1;
+}
+
+int tensor_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    return p.type == SGEMM_TYPE_F32 ? grouped_f32_launch(p, dev, stream, launches)
+                                    : grouped16_launch(p, dev, stream, launches);
+}
+
+int sliced_launch(const GroupedProblem &p, int split, float *sums, const DeviceInfo &dev, cudaStream_t stream,
+                  int *launches) {
+    GroupedProblem q = p;
+    q.split = split;
+    q.C = sums;
+    q.ldc = (p.N + 3) / 4 * 4;
+    q.strideC = p.M * q.ldc;
+    const int rc = tensor_launch(q, dev, stream, launches);
+    if (rc != SGEMM_OK) return rc;
+    const int64_t size = type_size(p.type);
+    Join j{sums, p.C, p.experts * p.M, p.M, p.N, q.ldc, p.ldc, p.experts > 1 ? p.strideC : 0, split, 0};
+    j.vector = (reinterpret_cast<uintptr_t>(p.C) % (4 * size) | (p.ldc % 4) | (j.strideC % 4)) == 0;
+    const int64_t blocks = (j.rows * (j.ld / 4) + JOIN_THREADS - 1) / JOIN_THREADS, most = 8LL * dev.sm_count;
+    const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+    if (p.type == SGEMM_TYPE_F32)
+        join_slices_kernel<float><<<grid, JOIN_THREADS, 0, stream>>>(j);
+    else if (p.type == SGEMM_TYPE_BF16)
+        join_slices_kernel<__nv_bfloat16><<<grid, JOIN_THREADS, 0, stream>>>(j);
+    else
+        join_slices_kernel<__half><<<grid, JOIN_THREADS, 0, stream>>>(j);
+    if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    ++*launches;
+    return SGEMM_OK;
+}
+
 }  // namespace
 
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    if (grouped_f32_supports(p)) return grouped_f32_launch(p, dev, stream, launches);
-    if (grouped16_supports(p)) {
-        const int rc = grouped16_launch(p, dev, stream, launches);
-        if (rc != SGEMM_ERR_UNSUPPORTED) return rc;  // no memory for copies: nothing was enqueued
+    if (grouped_f32_supports(p) || grouped16_supports(p)) {
+        int rc = SGEMM_ERR_UNSUPPORTED;
+        const int split = p.wgrad ? slices_of(p, dev) : 1;
+        if (split > 1) {
+            const int64_t bytes = split * p.experts * p.M * ((p.N + 3) / 4 * 4) * 4;
+            if (float *sums = scratch_alloc(dev, static_cast<size_t>(bytes), stream)) {
+                rc = sliced_launch(p, split, sums, dev, stream, launches);
+                scratch_free(sums, stream);
+            }
+        }
+        if (rc == SGEMM_ERR_UNSUPPORTED) rc = tensor_launch(p, dev, stream, launches);
+        if (rc != SGEMM_ERR_UNSUPPORTED) return rc;  // no memory for copies or slices: nothing was enqueued
     }
     return simple_launch(p, stream, launches);
 }

@@ -91,6 +91,7 @@ struct Args16 {
     int64_t ldc, strideC;
     int c_tma;  // wgrad: C through TMA
     int c_vec;  // rows: C in 16-byte stores
+    int slices; // wgrad: C is a slice's sums in fp32
     uint32_t idesc;  // without N
     uint64_t timeout_ns;
     int *watchdog;
@@ -460,6 +461,22 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
             for (int ch = 2 * second; ch < 2 * second + 2; ++ch) {
                 const int col0 = u.n0 + 64 * ch;
                 const bool wanted = rows > 0 && col0 < a.N;  // uniform over the warp
+                if (a.slices) {
+                    float *c = static_cast<float *>(a.C) + u.group * a.strideC +
+                               static_cast<int64_t>(row0 + lane) * a.ldc + col0;
+#pragma unroll 1
+                    for (int h = 0; h < 64 && wanted; h += 32) {
+                        float x[32] = {};
+                        if (summed) tmem_load32(dt + static_cast<uint32_t>(64 * ch + h), x);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            if (lane < rows && col0 + h + j < a.ldc)
+                                *reinterpret_cast<float4 *>(c + h + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                        __syncwarp();
+                    }
+                    if (summed && ch == 2 * second + 1) release();
+                    continue;
+                }
                 uint32_t v[32];
                 if (summed && wanted) {
                     float x[32];
@@ -587,7 +604,7 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     if (FORM == WGRAD) {
         ok = encode_map_typed(&mapA, type, 2, p.A, p.rows, p.M, p.lda, 1, 0, 64, g16::KB, sw) &&
              encode_map_typed(&mapB, type, 2, p.B, p.rows, p.N, p.ldb, 1, 0, 64, g16::KB, sw);
-        c_tma = mappable(p.C, p.M, p.ldc, p.experts, p.strideC) &&
+        c_tma = p.split == 1 && mappable(p.C, p.M, p.ldc, p.experts, p.strideC) &&
                 encode_map_typed(&mapC, type, 2, p.C, p.M, p.N, p.ldc, p.experts, strideC, 64, 32, sw);
         if (!c_tma) mapC = mapA;  // not read by the kernel
     } else {
@@ -613,7 +630,9 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
                          p.wgrad ? p.M : 0,
                          p.K,
                          static_cast<int>(tiles_m),
-                         static_cast<int>(tiles_n)};
+                         static_cast<int>(tiles_n),
+                         p.split};
+    a.slices = p.split > 1 ? 1 : 0;
     a.c_tma = c_tma ? 1 : 0;
     a.c_vec = reinterpret_cast<uintptr_t>(p.C) % 16 == 0 && p.ldc % 8 == 0;
     // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B
@@ -625,7 +644,7 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
     a.watchdog = flag;
     // Every group may end in a part of a tile, and so may the rest.
-    const int64_t units = FORM == WGRAD ? tiles_m * tiles_n * p.experts
+    const int64_t units = FORM == WGRAD ? tiles_m * tiles_n * p.experts * p.split
                                         : ((p.rows + g16::PN - 1) / g16::PN + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a) != cudaSuccess) {
@@ -672,7 +691,7 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const CopyRows j) {
     }
 }
 
-// Bytes of the copies that p needs (0: none).
+// Bytes of the copies that p needs.
 size_t copy_bytes(const GroupedProblem &p) {
     int64_t n = 0;
     if (!a_mappable(p)) n += p.rows * (((p.wgrad ? p.M : p.K) + 7) / 8 * 8);

@@ -82,7 +82,7 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
                          : encode_map(&mapB, q.B, p.K, p.N, q.ldb, p.experts, q.strideB, pr::HN, BK, plain));
         if (!ok) return SGEMM_ERR_LAUNCH;
     }
-    const int64_t c_rows = WG ? p.M : p.rows, c_items = WG ? p.experts : 1, c_stride = c_items > 1 ? p.strideC : 0;
+    const int64_t c_rows = WG ? p.M : p.rows, c_items = WG ? p.experts * p.split : 1, c_stride = c_items > 1 ? p.strideC : 0;
     const bool c_tma = !COLS && VEC_C && tma_operand_ok(q.C, p.ldc, c_stride, c_rows, c_items) &&
                        encode_map(&mapC, q.C, c_rows, p.N, p.ldc, c_items, c_stride, 32, 32, sw);
     if (!c_tma) mapC = mapA;  // not read by the kernel
@@ -115,10 +115,11 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
                         WG ? p.M : 0,
                         p.K,
                         static_cast<int>(tiles_m),
-                        static_cast<int>(tiles_n)};
+                        static_cast<int>(tiles_n),
+                        p.split};
     // Every group may end in a part of a tile, and so may the rest.
     const int64_t units =
-        WG ? tiles_m * tiles_n * p.experts : ((p.rows + high - 1) / high + p.experts) * tiles_n;
+        WG ? tiles_m * tiles_n * p.experts * p.split : ((p.rows + high - 1) / high + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a, gt) != cudaSuccess) {
         cudaGetLastError();
@@ -151,12 +152,12 @@ bool rows_narrow(const GroupedProblem &p) {
 // 218 us (2000 rows, 8 experts, 1001 -> 1001); 905 and 232 us (5 rows, 64
 // experts, 2047 -> 2047: the copy takes every expert's matrix).
 bool copy_first(const GroupedProblem &p, size_t bytes, const DeviceInfo &dev) {
-    const bool narrow = rows_narrow(p);
-    const int64_t wide = narrow ? pr::PM : pr::PN, high = narrow ? pr::PN : pr::PM;
+    int64_t high, wide;
+    grouped_f32_tile(p, &high, &wide);
     const int64_t tiles_n = (p.N + wide - 1) / wide, workers = dev.sm_count / 2;
-    const int64_t tiles_m = p.wgrad ? (p.M + high - 1) / high * p.experts
+    const int64_t tiles_m = p.wgrad ? (p.M + high - 1) / high * p.experts * p.split
                                     : (p.rows + high - 1) / high + (p.rows < p.experts ? p.rows : p.experts) / 2;
-    const int64_t depth = p.wgrad ? (p.rows + p.experts - 1) / p.experts : p.K;
+    const int64_t depth = p.wgrad ? p.rows / (p.experts * p.split) + 1 : p.K;
     const double k_blocks = static_cast<double>((tiles_m * tiles_n + workers - 1) / workers) *
                             static_cast<double>((depth + BK - 1) / BK);
     return 2.0 * static_cast<double>(bytes) / 5e6 + 10.0 < 5.5 * k_blocks;
@@ -182,6 +183,12 @@ bool grouped_f32_supports(const GroupedProblem &p) {
     const int64_t lim = INT32_MAX / 2;
     return p.type == SGEMM_TYPE_F32 && p.rows > 0 && p.rows < lim && p.M < lim && p.N < lim && p.K < lim &&
            (p.wgrad || p.K > 0);
+}
+
+void grouped_f32_tile(const GroupedProblem &p, int64_t *high, int64_t *wide) {
+    const bool narrow = rows_narrow(p);
+    *high = narrow ? pr::PN : pr::PM;
+    *wide = narrow ? pr::PM : pr::PN;
 }
 
 int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
@@ -221,7 +228,7 @@ int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStrea
         }
     }
     const bool vec_c = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0 &&
-                       (!p.wgrad || p.experts == 1 || p.strideC % 4 == 0);
+                       (!p.wgrad || p.experts * p.split == 1 || p.strideC % 4 == 0);
     const int rc = vec_c ? launch_form<true>(p, q, cpa, dev, stream, launches)
                          : launch_form<false>(p, q, cpa, dev, stream, launches);
     scratch_free(scratch, stream);

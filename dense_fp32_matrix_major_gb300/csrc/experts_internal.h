@@ -49,10 +49,12 @@ struct GroupedProblem {
     int64_t ldb, strideB;
     void *C;
     int64_t ldc, strideC;
+    int split = 1;  // wgrad: slices of a group's rows; C is then fp32, an item per slice, rows 16-byte aligned
 };
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 // fp32 on SM pairs (experts_gemm_f32.cu).
 bool grouped_f32_supports(const GroupedProblem &p);
+void grouped_f32_tile(const GroupedProblem &p, int64_t *high, int64_t *wide);  // of C
 int grouped_f32_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 // bf16 and fp16 on SM pairs (experts_gemm_16.cu).
 bool grouped16_supports(const GroupedProblem &p);

@@ -84,6 +84,41 @@ def test_wgrad(ex, dtype, counts, rest, M, N):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("counts,M,N", [
+    ([5003], 64, 100), ([2, 0, 9001, 70], 40, 33), ([4096, 4095], 264, 72), ([0], 64, 64), ([7000], 1, 1),
+])
+def test_wgrad_of_long_groups(ex, dtype, counts, M, N):
+    """Few small matrices summed over many rows: the sums are cut into slices of the rows."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng(M * 3 + N)
+    rest = 4000 if counts == [0] else 9
+    S, E = sum(counts) + rest, len(counts)
+    a = torch.from_numpy(rng.standard_normal((S, M)).astype(np.float32)).to(dt)
+    b = torch.from_numpy(rng.standard_normal((S, N)).astype(np.float32)).to(dt)
+    off = offsets_of(counts)
+    b[int(off[-1]):] = float("inf")  # rows of no group are not read into a sum
+    a64, b64 = a.double().numpy(), b.double().numpy()
+    want, mag = np.zeros((E, M, N)), np.zeros((E, M, N))
+    for e in range(E):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        want[e], mag[e] = a64[rows].T @ b64[rows], np.abs(a64[rows]).T @ np.abs(b64[rows])
+    for pad, offset in ((0, 0), (8, 0), (1, 3)):
+        out = strided(torch.full((E * M, N), 5.0, dtype=dt), pad, offset)
+        view = out.as_strided((E, M, N), (M * out.stride(0), out.stride(0), 1), offset)
+        ex.gemm_wgrad(strided(a, pad, offset), strided(b, pad, offset), off.cuda(), out=view)
+        assert_within(view, want, limit(want, mag, max(counts), dt), f"pad {pad}")
+        assert canaries_intact(out)
+        assert torch.equal(view, ex.gemm_wgrad(strided(a, pad, offset), strided(b, pad, offset), off.cuda()))
+    if counts[0] > 100:  # an infinity and a NaN of one row reach its column of C alone, whatever its slice
+        a[17, 3 % M], a[counts[0] - 1, 5 % M] = float("inf"), float("nan")
+        g = ex.gemm_wgrad(a.cuda(), b.cuda(), off.cuda()).cpu()[0]
+        touched = torch.zeros(M, dtype=torch.bool)
+        touched[3 % M] = touched[5 % M] = True
+        assert torch.isfinite(g[~touched]).all() and torch.isnan(g[5 % M]).all()
+        assert M == 1 or torch.isinf(g[3]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("trans", [False, True])
 def test_non_finite_values_stay_in_their_group(ex, dtype, trans):
     """NaN and infinities of one group's rows, of its neighbours' and of an empty group's matrix."""
