@@ -128,7 +128,8 @@ __device__ __forceinline__ void for_each_group_tile(const GroupTiles &a, volatil
             int end = max(begin, group_start(a.offsets, e + 1, a.rows));
             if (a.split > 1) {
                 const int each = ((end - begin + TK - 1) / TK + a.split - 1) / a.split * TK;
-                begin = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(item - e * a.split) * each));
+                const int64_t first = begin + static_cast<int64_t>(item - e * a.split) * each;
+                begin = static_cast<int>(min(static_cast<int64_t>(end), first));
                 end = min(end - begin, each) + begin;
             }
             f(GroupTile{item, r / a.tiles_n * TM, static_cast<int>(a.M), r % a.tiles_n * TN, begin, end - begin,

@@ -5,7 +5,10 @@
 //
 // Bound by the tensor pipe where groups are long, by reading B where they are
 // short. Products of two 16-bit values are exact in fp32 and are summed in
-// fp32 in tensor memory; a value is rounded once, when C is written.
+// fp32 in tensor memory; a value is rounded once, when C is written. Measured in
+// bf16 with 16384 rows, 32 experts, 2048 -> 4096: rows 188 us (1460 TFLOP/s, the
+// path from L2 to shared memory), wgrad 216 us (the stores of C on top of it); 64
+// rows, 32 experts, 2048 -> 2048: 43 us (6.2 TB/s, reading B).
 //
 // Two CTAs on two SMs of a cluster make one 256 x n tile (n <= 256): each
 // stages 128 rows of the first operand and n / 2 of the second per 64-deep
@@ -42,8 +45,9 @@
 // 150 instructions for 2048 values. rows: a lane holds a column of C; eight
 // lanes exchange values so that a lane stores 16 bytes of a row, about 200
 // instructions for 1024 values, hidden behind the longer sums, and rows past
-// the group's end cost nothing. (The same way for wgrad: 365 us in place of 224
-// for 16384 rows, 32 experts, 2048 x 4096.)
+// the group's end cost nothing. (The same way for wgrad: 365 us in place of 216
+// for 16384 rows, 32 experts, 2048 x 4096.) Slices of wgrad's sums, which are
+// small, are stored in fp32 row by row.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -335,7 +339,8 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
                     if (leader) {
 #pragma unroll
                         for (int ks = 0; ks < g16::KB / 16; ++ks)
-                            if (16 * ks < left) mma16_pair(dt, da + ks * step_a, db + ks * step_b, idesc, kb > 0 || ks > 0);
+                            if (16 * ks < left)
+                                mma16_pair(dt, da + ks * step_a, db + ks * step_b, idesc, kb > 0 || ks > 0);
                         tc_commit2(bar(g16::EMPTY + s));
                     }
                     __syncwarp();
@@ -471,7 +476,8 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             if (lane < rows && col0 + h + j < a.ldc)
-                                *reinterpret_cast<float4 *>(c + h + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                                *reinterpret_cast<float4 *>(c + h + j) =
+                                    make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                         __syncwarp();
                     }
                     if (summed && ch == 2 * second + 1) release();
@@ -579,7 +585,8 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     std::call_once(g_once[dev.device][idx], [&] {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g16::smem_bytes(FORM == WGRAD));
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             g16::smem_bytes(FORM == WGRAD));
         int n = 0;
         if (e == cudaSuccess) {
             cudaLaunchConfig_t q = cfg;

@@ -560,10 +560,10 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                                     for (int ks = 0; ks < BK / 8; ++ks) {
                                         // C^T: the factors' order the other way round, for the same sums.
                                         const uint32_t more = ks > 0 || i > 0 || kblk > k0;
-                                        tc_mma2_ts(dt, (COLS ? a_hi : a_lo) + ks * 8, (COLS ? b_lo : b_hi) + ks * 2, more,
-                                                   idesc);
-                                        tc_mma2_ts(dt, (COLS ? a_lo : a_hi) + ks * 8, (COLS ? b_hi : b_lo) + ks * 2, 1u,
-                                                   idesc);
+                                        const uint32_t a1 = COLS ? a_hi : a_lo, a2 = COLS ? a_lo : a_hi;
+                                        const uint64_t b1 = COLS ? b_lo : b_hi, b2 = COLS ? b_hi : b_lo;
+                                        tc_mma2_ts(dt, a1 + ks * 8, b1 + ks * 2, more, idesc);
+                                        tc_mma2_ts(dt, a2 + ks * 8, b2 + ks * 2, 1u, idesc);
                                     }
                                 }
                                 __syncwarp();
