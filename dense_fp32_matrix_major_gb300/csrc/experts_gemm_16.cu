@@ -245,6 +245,9 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
     }
     __syncthreads();
+    // Launched while the kernel before it in the stream ends: wait for its
+    // results (and its tensor memory).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(TMEM_COLS)
@@ -256,6 +259,7 @@ __global__ void __launch_bounds__(g16::THREADS, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0 || warp == g16::LOAD2_WARP) {
         // ------------------------------------------------------------------ loads
@@ -573,16 +577,18 @@ template <Form FORM, bool BF16>
 int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     auto kernel = grouped16_kernel<FORM, BF16>;
     constexpr int idx = FORM + (BF16 ? 3 : 0);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(g16::THREADS);
     cfg.dynamicSmemBytes = g16::smem_bytes(FORM == WGRAD);
     cfg.stream = stream;
-    cfg.attrs = &attr;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
     std::call_once(g_once[dev.device][idx], [&] {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -654,6 +660,7 @@ int launch16(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream
     const int64_t units = FORM == WGRAD ? tiles_m * tiles_n * p.experts * p.split
                                         : ((p.rows + g16::PN - 1) / g16::PN + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a) != cudaSuccess) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;

@@ -41,16 +41,18 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
     auto kernel = tf32x3_pair_kernel<VEC_C, TA, TB, UNITS, GROUP_FOLD, GROUP_LEAD>;
     constexpr bool WG = sums_rows(UNITS), COLS = transposed(UNITS);
     constexpr int idx = COLS ? 6 + (WG ? 2 : TA ? 1 : 0) : (VEC_C ? 3 : 0) + (WG ? 2 : TB ? 1 : 0);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(pr::THREADS);
     cfg.dynamicSmemBytes = pr::SMEM_BYTES;
     cfg.stream = stream;
-    cfg.attrs = &attr;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
     std::call_once(g_once[dev.device][idx], [&] {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pr::SMEM_BYTES);
@@ -125,6 +127,7 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
     const int64_t units =
         WG ? tiles_m * tiles_n * p.experts * p.split : ((p.rows + high - 1) / high + p.experts) * tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapC, a, gt) != cudaSuccess) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;

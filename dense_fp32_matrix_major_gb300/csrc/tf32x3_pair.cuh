@@ -488,6 +488,9 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(is_a ? &tmA : &tmB)) : "memory");
     }
     __syncthreads();  // this CTA's mbarriers are initialised
+    // Groups: launched while the kernel before it in the stream ends, whose
+    // results (the group bounds among them) and tensor memory are waited for.
+    if (UNITS != TILES) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
         // Both CTAs allocate: the pair's MMAs use the same columns in each.
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
     // A pass launched behind this kernel (the activation of split tiles) may
     // be scheduled now; it waits for this grid to finish before touching C.
+    if (UNITS != TILES) asm volatile("griddepcontrol.launch_dependents;");
     if (a.signal_dependents && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0) {

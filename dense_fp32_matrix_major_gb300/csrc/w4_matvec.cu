@@ -77,6 +77,7 @@ constexpr int RESIDENT_ONE = 144 * 1024;    // x in shared memory: one row, eigh
 constexpr int RESIDENT_EIGHT = 96 * 1024;
 constexpr int X_STAGE = 64 * 1024;          // x of a stage, at most, when it is streamed
 constexpr int PASSES = 256;                 // of one launch when x is streamed
+constexpr int64_t OVERLAP = INT64_C(48) << 20;  // weights of a call: about 12 us
 
 struct W4Args {
     int rows, experts;
@@ -375,6 +376,7 @@ constexpr int PREPARE_THREADS = 256;
 template <class T, int WIDTH, int TILES>
 __global__ void __launch_bounds__(PREPARE_THREADS) w4_prepare_kernel(const __grid_constant__ W4Args a, uint8_t *to) {
     __shared__ Members members;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before it ends
     asm volatile("griddepcontrol.launch_dependents;");
     int expert;
     const int nb = find_members(a, a.first_pass + static_cast<int>(blockIdx.y), &members, &expert);
@@ -452,6 +454,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
+    // Both forms may be launched while the kernel before them in the stream
+    // ends; behind the one that lays out x, which has waited for what was before
+    // it, only x is waited for.
+    if (!STREAM) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
     const int pass = a.first_pass + static_cast<int>(blockIdx.y);
     int expert;
@@ -905,16 +912,22 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     cfg.dynamicSmemBytes = static_cast<size_t>(rest + stages * stage);
     cfg.stream = stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = STREAM ? 1 : 0;
+    // A launch of that kind takes the host about 1 us more, so not for short
+    // calls, which the host bounds.
+    cfg.numAttrs = STREAM || busy * a.N * a.K >= OVERLAP ? 1 : 0;
     int rc = SGEMM_OK;
     const int chunk = STREAM ? PASSES : passes;
     for (a.first_pass = 0; a.first_pass < passes && rc == SGEMM_OK; a.first_pass += chunk) {
         const int here = passes - a.first_pass < chunk ? passes - a.first_pass : chunk;
         if (STREAM) {
             const int64_t blocks = (steps * 16 * W4_ROWS + PREPARE_THREADS - 1) / PREPARE_THREADS;
-            w4_prepare_kernel<T, WIDTH, TILES><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(here)),
-                                          PREPARE_THREADS, 0, stream>>>(a, reinterpret_cast<uint8_t *>(scratch));
-            if (cudaGetLastError() != cudaSuccess) {
+            cudaLaunchConfig_t before = cfg;
+            before.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(here));
+            before.blockDim = dim3(PREPARE_THREADS);
+            before.dynamicSmemBytes = 0;
+            if (cudaLaunchKernelEx(&before, w4_prepare_kernel<T, WIDTH, TILES>, a,
+                                   reinterpret_cast<uint8_t *>(scratch)) != cudaSuccess) {
+                cudaGetLastError();
                 rc = SGEMM_ERR_LAUNCH;
                 break;
             }
