@@ -102,7 +102,7 @@ int launch_pair(const Problem &p, const DeviceInfo &dev, int sk_mode, bool cpa, 
     a.dp_tiles = sch.dp_tiles;
     a.sk_ctas = sch.sk_ctas;
     a.sk_iters = sch.sk_iters;
-    a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
+    a.timeout_ns = wait_limit_ns(p.K);
     a.watchdog = flag;
     a.alpha = p.alpha;
     a.beta = p.beta;
