@@ -16,28 +16,26 @@
 // is their width, which is why eight rows share a pass. (tcgen05 wants its
 // operands in shared or tensor memory and 128 rows a tile; here the weights
 // go from global memory to registers once and are used once.) Each group's
-// inner sum is scaled in fp32. How a 4-bit q becomes an operand:
-//   * fp16 x: q in the low bits of an fp16 number is q 2^-24 exactly (a
-//     subnormal), four bits up it is 16 q 2^-24 (10 bits hold it), so masking
-//     is all; the group's sum is 2^24 (sum (q 2^-24) x) - zero sum x, the sums
-//     of the two positions kept apart until the 16 is taken out.
-//   * bf16 x: q in the low bits of 128.0 (last place 1) is 128 + q exactly,
-//     and so is q - 8 after subtracting 136; the group's sum is
-//     sum (q - 8) x - (zero - 8) sum x. (Without the subtraction from every
-//     operand, sum (128 + q) x - (128 + zero) sum x, a large x whose q is the
-//     zero point would leave its rounding errors, 128 times enlarged, in the
-//     sum.)
+// inner sum is scaled in fp32. An operand is q - zero, exact in every type, so a
+// value of x whose q is the zero point adds nothing, however large it is (taken
+// from the sums instead, sum q x - zero sum x, it would leave its rounding
+// errors there). How a 4-bit q becomes one:
+//   * bf16 x: q in the low bits of 128.0 (last place 1) is 128 + q; 128 + zero
+//     is subtracted.
+//   * fp16 x: q in the low bits of an fp16 number is q 2^-24 (a subnormal),
+//     four bits up it is 16 q 2^-24 (10 bits hold it), so masking is all; the
+//     zero point is subtracted in the same place, the sums of the two places
+//     are kept apart until the 16 is taken out, and the group's sum is scaled
+//     by 2^24.
 //   * fp32 x: cut into three bf16 terms that add up to it (3 x 8 bits cover
-//     its 24), each multiplied exactly by q - zero, taken from 128 + q by
-//     subtracting 128 + zero before the product, so no bits are lost. A term
-//     is a column of the instruction: one or two rows of x fill one (6 of 8
-//     columns), three to five two, up to eight three.
-// The sums of x per group are made in fp32 when x is staged. One 32-bit word
-// holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j, j + 4), so x
-// is laid out in shared memory in the order 0 4 1 5 2 6 3 7 (fp16: 0 4 2 6 1 5
-// 3 7, the unshifted and four bits up apart). An infinity or
-// NaN in 16-bit x would turn the subtraction into NaN; rows of x that hold
-// one are recomputed with scalar arithmetic.
+//     its 24), each multiplied as bf16 x is. A term is a column of the
+//     instruction: one or two rows of x fill one (6 of 8 columns), three to
+//     five two, up to eight three.
+// One 32-bit word holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j,
+// j + 4), so x is laid out in shared memory in the order 0 4 1 5 2 6 3 7 (fp16:
+// 0 4 2 6 1 5 3 7, the unshifted and four bits up apart). A 16-bit sum that is
+// not finite, or too large, is made again with scalar arithmetic: scaling only
+// the group's sum may overflow where scaled weights do not.
 //
 // Work. One block per SM goes through units of R = 16 .. 128 rows of q times
 // all of k. A producer warp streams q into a ring in shared memory by TMA
@@ -105,10 +103,8 @@ struct W4Args {
 };
 
 // How a row type enters the matrix instruction: terms of x, the bits that q is
-// placed in, whether zero points are subtracted from the operand (EXACT) or
-// from the group's sum (LESS: what is taken from every operand; BASE: what it
-// then holds on top of q, UNIT: what an operand's 1 is worth), and the
-// instruction itself.
+// placed in, the zero point as it is subtracted from both values of an operand,
+// what an operand's 1 stands for (UNIT), and the instruction itself.
 template <class T>
 struct Operand;
 
@@ -116,15 +112,13 @@ template <>
 struct Operand<__nv_bfloat16> {
     static constexpr int TERMS = 1;
     static constexpr bool TWO_PLACES = false;  // q low and four bits up
-    static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0x43004300u;  // 128, 128 in bf16
-    static constexpr uint32_t LESS = 0x43084308u;  // 136, 136: subtracted from every operand
-    static constexpr float BASE = -8.0f, UNIT = 1.0f;
+    static constexpr float UNIT = 1.0f;
+    static __device__ __forceinline__ uint32_t zero(uint32_t z) { return ONE + z * 0x00010001u; }
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&d);
     }
-    static __device__ __forceinline__ uint32_t twice(float) { return 0; }
     static __device__ __forceinline__ void split(__nv_bfloat16 x, uint16_t (&t)[1]) { t[0] = __bfloat16_as_ushort(x); }
     // d = a b + c
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -140,12 +134,14 @@ template <>
 struct Operand<__half> {
     static constexpr int TERMS = 1;
     static constexpr bool TWO_PLACES = true;  // q low and four bits up
-    static constexpr bool EXACT = false;
     static constexpr uint32_t ONE = 0;
-    static constexpr uint32_t LESS = 0;
-    static constexpr float BASE = 0.0f, UNIT = 16777216.0f;  // an operand's q is q 2^-24
-    static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t) { return a; }
-    static __device__ __forceinline__ uint32_t twice(float) { return 0; }
+    static constexpr float UNIT = 16777216.0f;  // an operand's q is q 2^-24
+    static __device__ __forceinline__ uint32_t zero(uint32_t z) { return z * 0x00010001u; }
+    // Differences of subnormals, exact.
+    static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
+        const __half2 d = __hsub2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&d);
+    }
     static __device__ __forceinline__ void split(__half x, uint16_t (&t)[1]) { t[0] = __half_as_ushort(x); }
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
                                                float c1, float c2, float c3) {
@@ -159,18 +155,12 @@ struct Operand<__half> {
 template <>
 struct Operand<float> {
     static constexpr int TERMS = 3;
-    static constexpr bool TWO_PLACES = false;  // q low and four bits up
-    static constexpr bool EXACT = true;
+    static constexpr bool TWO_PLACES = false;
     static constexpr uint32_t ONE = Operand<__nv_bfloat16>::ONE;
-    static constexpr uint32_t LESS = 0;
-    static constexpr float BASE = 0.0f, UNIT = 1.0f;
+    static constexpr float UNIT = 1.0f;
+    static __device__ __forceinline__ uint32_t zero(uint32_t z) { return Operand<__nv_bfloat16>::zero(z); }
     static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
         return Operand<__nv_bfloat16>::minus(a, b);
-    }
-    // x twice in bf16 (a whole number below 256, so exact).
-    static __device__ __forceinline__ uint32_t twice(float x) {
-        const uint32_t b = __float_as_uint(x);
-        return __byte_perm(b, b, 0x3232);
     }
     // The top 16 bits of x are a bf16 (truncated, so it cannot overflow); what
     // is left is exact in fp32 and is cut the same way. Infinities and NaN go
@@ -236,13 +226,15 @@ struct Raw {
     uint32_t lo, hi, z_lo, z_hi;
 };
 
+// Their values, zero points as the operands' type subtracts them.
 struct Scales {
-    float lo, hi, z_lo, z_hi;
+    float lo, hi;
+    uint32_t z_lo, z_hi;
 };
 
+template <class Op>
 __device__ __forceinline__ Scales values_of(const W4Args &a, const Raw &r) {
-    return Scales{scale_value(a, r.lo), scale_value(a, r.hi), static_cast<float>(r.z_lo & 15u),
-                  static_cast<float>(r.z_hi & 15u)};
+    return Scales{scale_value(a, r.lo), scale_value(a, r.hi), Op::zero(r.z_lo & 15u), Op::zero(r.z_hi & 15u)};
 }
 
 // y[r][n] with scalar arithmetic, for rows of x that hold infinities or NaN.
@@ -305,23 +297,19 @@ __device__ __forceinline__ int find_members(const W4Args &a, int pass, Members *
 __host__ __device__ __forceinline__ int64_t steps_of(int64_t K) { return (K + PAIR * STEP - 1) / (PAIR * STEP) * PAIR; }
 
 // A step of x as the matrix instructions read it: set of columns, unit u,
-// column, lane t, 8 values, then, where zero points are taken from the sums, the sums of x
-// over every 32 k (width 32), 64 or 128: group, row.
+// column, lane t, 8 values.
 // With fp32 x, TILES sets of eight columns hold the terms: term m of row r is
 // column r of set m (three sets) or column 3 r + m of the sets in a row.
 template <class T, int WIDTH, int NB, int TILES>
 struct XStep {
     static constexpr int UNIT_BYTES = NB * 64, TILE_BYTES = 4 * UNIT_BYTES;
-    static constexpr int GROUPS = 128 / WIDTH;
-    static constexpr int SUMS = TILES * TILE_BYTES;  // where the sums start
     static constexpr bool SPREAD = Operand<T>::TERMS > TILES;
     static __device__ __forceinline__ int column(int r, int m) { return SPREAD ? 3 * r + m : 8 * m + r; }
-    static constexpr int BYTES = SUMS + (Operand<T>::EXACT ? 0 : (GROUPS * NB * 4 + 15) / 16 * 16);
+    static constexpr int BYTES = TILES * TILE_BYTES;
 };
 
 // Lays out values 8 piece .. 8 piece + 7 of step `st` of row `row` of x as row r
-// of `to` (the step); zeros past the end of k. The 16 pieces of a step are 16
-// consecutive lanes, all of which call this.
+// of `to` (the step); zeros past the end of k.
 template <class T, int WIDTH, int NB, int TILES>
 __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, int piece, int r, bool in, uint8_t *to) {
     using Op = Operand<T>;
@@ -361,15 +349,6 @@ __device__ __forceinline__ void lay_out_x(const W4Args &a, const T *x, int st, i
                 make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]);
         }
     }
-    if (!Op::EXACT) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += to_f32(v.v[j]);
-#pragma unroll
-        for (int d = 1; d < WIDTH / 8; d *= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (in && piece % (WIDTH / 8) == 0)
-            reinterpret_cast<float *>(to + X::SUMS)[piece / (WIDTH / 8) * NB + r] = s;
-    }
 }
 
 // Lays out x of pass blockIdx.y for streaming: a thread per 8 values.
@@ -407,12 +386,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-    return v;
-}
-
-__device__ __forceinline__ float lds32(uint32_t at) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
     return v;
 }
 
@@ -583,8 +556,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         constexpr int CHAINS = TILES == 1 ? 2 : TILES;
         constexpr int PER_GROUP = WIDTH / 32;  // words of a group
         float c[PAIR][CHAINS][4];
-        float s_lo[PAIR], s_hi[PAIR], z_lo[PAIR], z_hi[PAIR];
-        uint32_t zz_lo[PAIR], zz_hi[PAIR];
+        float s_lo[PAIR], s_hi[PAIR];
+        uint32_t z_lo[PAIR], z_hi[PAIR];
         const uint32_t x_at = x_step + (NB == 1 ? t : lane) * 16;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -594,14 +567,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                     const int from = (lane & ~3) | (WIDTH == 128 ? PAIR * j + h : u);
                     s_lo[h] = __shfl_sync(0xffffffffu, sc[h].lo, from);
                     s_hi[h] = __shfl_sync(0xffffffffu, sc[h].hi, from);
-                    z_lo[h] = z_hi[h] = 8.0f;
+                    z_lo[h] = z_hi[h] = Op::zero(8);
                     if (a.zeros) {
                         z_lo[h] = __shfl_sync(0xffffffffu, sc[h].z_lo, from);
                         z_hi[h] = __shfl_sync(0xffffffffu, sc[h].z_hi, from);
-                    }
-                    if (Op::EXACT) {
-                        zz_lo[h] = Op::twice(128.0f + z_lo[h]);
-                        zz_hi[h] = Op::twice(128.0f + z_hi[h]);
                     }
                 }
             }
@@ -628,16 +597,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                         f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
                         f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
                     }
-                    if (Op::LESS != 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) f[i] = Op::minus(f[i], Op::LESS);
-                    }
-                    if (Op::EXACT) {
-                        f[0] = Op::minus(f[0], zz_lo[h]);
-                        f[1] = Op::minus(f[1], zz_hi[h]);
-                        f[2] = Op::minus(f[2], zz_lo[h]);
-                        f[3] = Op::minus(f[3], zz_hi[h]);
-                    }
+                    const int up = Op::TWO_PLACES ? 4 * half : 0;
+                    f[0] = Op::minus(f[0], z_lo[h] << up);
+                    f[1] = Op::minus(f[1], z_hi[h] << up);
+                    f[2] = Op::minus(f[2], z_lo[h] << up);
+                    f[3] = Op::minus(f[3], z_hi[h] << up);
 #pragma unroll
                     for (int m = 0; m < TILES; ++m) {
                         float(&d)[4] = c[h][TILES == 1 ? half : m];
@@ -663,20 +627,14 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                     } else {
                         float d[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {  // small terms first
-                            d[i] = Op::TWO_PLACES ? c[h][CHAINS - 1][i] * 0.0625f : c[h][CHAINS - 1][i];
+                        for (int i = 0; i < 4; ++i) {
+                            if (Op::TWO_PLACES) {
+                                d[i] = fmaf(c[h][1][i], Op::UNIT / 16, c[h][0][i] * Op::UNIT);
+                            } else {  // small terms first
+                                d[i] = c[h][CHAINS - 1][i];
 #pragma unroll
-                            for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
-                        }
-                        if (!Op::EXACT) {
-                            const uint32_t at = x_step + h * X::BYTES + X::SUMS + u / PER_GROUP * NB * 4;
-                            const float xs0 = lds32(NB == 1 ? at : at + 8 * t);
-                            const float xs1 = NB == 1 ? xs0 : lds32(at + 8 * t + 4);
-                            const float b_lo = -Op::BASE - z_lo[h], b_hi = -Op::BASE - z_hi[h];
-                            d[0] = fmaf(d[0], Op::UNIT, b_lo * xs0);
-                            d[1] = fmaf(d[1], Op::UNIT, b_lo * xs1);
-                            d[2] = fmaf(d[2], Op::UNIT, b_hi * xs0);
-                            d[3] = fmaf(d[3], Op::UNIT, b_hi * xs1);
+                                for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                            }
                         }
                         sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
                         sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
@@ -698,7 +656,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         for (int stage0 = 0; stage0 < per_unit; stage0 += TURN) {
             const bool last_turn = stage0 + TURN >= per_unit;
             if (WIDTH == 128) {
-                turn = values_of(a, next);
+                turn = values_of<Op>(a, next);
                 fetch_turn(last_turn ? u + du : u, last_turn ? 0 : stage0 + TURN);
             }
 #pragma unroll
@@ -742,7 +700,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                             const Scales both[PAIR] = {turn, turn};
                             multiply(w, both, j, x_step);
                         } else {
-                            const Scales both[PAIR] = {values_of(a, of_step[j][0]), values_of(a, of_step[j][1])};
+                            const Scales both[PAIR] = {values_of<Op>(a, of_step[j][0]), values_of<Op>(a, of_step[j][1])};
                             multiply(w, both, j, x_step);
                         }
                     }
@@ -784,7 +742,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                 s += X::SPREAD ? (from[(3 * r + 2) * 16] + from[(3 * r + 1) * 16]) + from[3 * r * 16] : from[r * 16];
             const int64_t row = static_cast<int64_t>(u) * R + n;
             if (row >= a.N) continue;
-            if (!Op::EXACT && !(fabsf(s) <= 3.0e38f))
+            if (Op::TERMS == 1 && !(fabsf(s) <= 3.0e38f))
                 s = scalar_row(a, static_cast<int64_t>(expert) * a.N + row,
                                static_cast<const T *>(a.x) + members.row[r] * a.ldx);
             y[members.row[r] * a.ldy + row] = from_f32<T>(s);

@@ -1,0 +1,64 @@
+"""4-bit products of values far apart: a large x whose q is the zero point adds nothing, and nothing overflows on the
+way to a result that fits."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.experts_harness import DTYPES, assert_within, bound
+
+N, K, GROUP = 64, 512, 128
+
+
+@pytest.fixture(scope="module")
+def ex():
+    from dense_fp32_matrix_major_gb300 import experts
+
+    return experts
+
+
+def outliers(dtype, zeros, seed):
+    """q (N x K), zero points (N x groups), x (3 x K) with a value of 60000 in each group where q is the zero point, and
+    a small one at every 16th k; the products in 64 bits, the sum of their magnitudes and their number."""
+    rng = np.random.default_rng(seed)
+    q = rng.integers(0, 16, (N, K))
+    z = rng.integers(0, 16, (N, K // GROUP)) if zeros else np.full((N, K // GROUP), 8)
+    x = np.zeros((3, K), np.float32)
+    x[:, ::16] = rng.standard_normal((3, K // 16)) * 2.0 ** -8
+    for g in range(K // GROUP):
+        x[:, g * GROUP + 5] = 60000.0 * (-1) ** g
+        q[:, g * GROUP + 5] = z[:, g]
+    x = torch.from_numpy(x).to(DTYPES[dtype])
+    x64, w = x.double().numpy(), (q - np.repeat(z, GROUP, 1)).astype(np.float64)
+    return q, z, x, x64 @ w.T, np.abs(x64) @ np.abs(w).T, K // 16
+
+
+def limit(want, mag, terms, dtype):
+    # Products of the outliers are 0 and add no error; an fp32 x has three terms, each group's sum is scaled once.
+    return bound(want, mag, 3 * terms + K // GROUP + 2, DTYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype,zeros,base", [("f16", False, 0), ("f16", True, 0), ("bf16", False, 0), ("bf16", True, 8)])
+def test_limit_notices_zero_points_taken_from_sums(dtype, zeros, base):
+    """sum (q - base) x - (zero - base) sum x in 32 bits, which the limit below must not let pass."""
+    q, z, x, want, mag, terms = outliers(dtype, zeros, 3)
+    x32, got = x.float().numpy(), np.zeros((3, N), np.float32)
+    for g in range(K // GROUP):
+        sums, total = np.zeros((3, N), np.float32), np.zeros((3, 1), np.float32)
+        for k in range(g * GROUP, (g + 1) * GROUP):
+            sums += x32[:, k:k + 1] * (q[:, k] - base).astype(np.float32)
+            total += x32[:, k:k + 1]
+        got += sums - (z[:, g] - base).astype(np.float32) * total
+    assert (np.abs(got - want) > 4 * limit(want, mag, terms, dtype)).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_outliers_at_the_zero_point_leave_no_trace(ex, dtype, zeros, rows):
+    q, z, x, want, mag, terms = outliers(dtype, zeros, 3)
+    packed = torch.from_numpy((q[:, ::2] | (q[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    y = ex.w4_matvec(x[:rows].cuda(), packed, torch.ones(N, K // GROUP, device="cuda"), group=GROUP,
+                     zeros=torch.from_numpy(z.astype(np.uint8)).cuda() if zeros else None)
+    assert_within(y, want[:rows], limit(want, mag, terms, dtype)[:rows])
