@@ -33,9 +33,9 @@
 //     five two, up to eight three.
 // One 32-bit word holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j,
 // j + 4), so x is laid out in shared memory in the order 0 4 1 5 2 6 3 7 (fp16:
-// 0 4 2 6 1 5 3 7, the unshifted and four bits up apart). A 16-bit sum that is
-// not finite, or too large, is made again with scalar arithmetic: scaling only
-// the group's sum may overflow where scaled weights do not.
+// 0 4 2 6 1 5 3 7, the unshifted and four bits up apart). A sum that is not
+// finite is made again with scalar arithmetic in 64 bits: a group's sum may
+// overflow before it is scaled where the result does not.
 //
 // Work. One block per SM goes through units of R = 16 .. 128 rows of q times
 // all of k. A producer warp streams q into a ring in shared memory by TMA
@@ -237,17 +237,25 @@ __device__ __forceinline__ Scales values_of(const W4Args &a, const Raw &r) {
     return Scales{scale_value(a, r.lo), scale_value(a, r.hi), Op::zero(r.z_lo & 15u), Op::zero(r.z_hi & 15u)};
 }
 
-// y[r][n] with scalar arithmetic, for rows of x that hold infinities or NaN.
+// y[r][n] with scalar arithmetic, 8 values at a time. 64 bits hold every product
+// exactly and no sum overflows in them; a NaN ends it.
 template <class T>
 __device__ __noinline__ float scalar_row(const W4Args &a, int64_t row, const T *x) {
-    float s = 0.0f;
-    for (int64_t k = 0; k < a.K; ++k) {
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row * (a.K / 2));
+    double s = 0.0;
+    for (int64_t k = 0; k < a.K && s == s; k += 8) {
         const int64_t gi = row * a.groups + (k >> a.group_shift);
-        const int v = (__ldg(a.q + row * (a.K / 2) + k / 2) >> (4 * (k & 1))) & 15;
+        const uint32_t word = __ldg(q + k / 8);
         const int z = a.zeros ? __ldg(a.zeros + gi) & 15 : 8;
-        s = fmaf(static_cast<float>(v - z) * scale_at(a, gi), to_f32(x[k]), s);
+        const double scale = scale_at(a, gi);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_f32(x[k + j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s = fma(static_cast<double>(static_cast<int>((word >> (4 * j)) & 15u) - z) * scale, v[j], s);
     }
-    return s;
+    return static_cast<float>(s);
 }
 
 // The rows of x of pass `pass`: eight consecutive ones, or, with ids, row
@@ -550,96 +558,101 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
 
     float sum[ACC][4] = {};
     // Two steps side by side: their chains of products do not depend on each
-    // other.
+    // other. One after the other where sets of columns give chains enough: the
+    // registers spilled otherwise (8 x 16384 x 8192 fp32, groups of 64: 40 and 61 us).
     auto multiply = [&](const Weights (&w)[PAIR], const Scales (&sc)[PAIR], int j, uint32_t x_step) {
         // One accumulator per chain of dependent products.
         constexpr int CHAINS = TILES == 1 ? 2 : TILES;
+        constexpr int SIDE = TILES > 1 ? 1 : PAIR;  // steps side by side
         constexpr int PER_GROUP = WIDTH / 32;  // words of a group
-        float c[PAIR][CHAINS][4];
-        float s_lo[PAIR], s_hi[PAIR];
-        uint32_t z_lo[PAIR], z_hi[PAIR];
-        const uint32_t x_at = x_step + (NB == 1 ? t : lane) * 16;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u % PER_GROUP == 0) {  // a group starts
+        for (int h0 = 0; h0 < PAIR; h0 += SIDE) {
+            float c[SIDE][CHAINS][4];
+            float s_lo[SIDE], s_hi[SIDE];
+            uint32_t z_lo[SIDE], z_hi[SIDE];
+            const uint32_t x_at = x_step + (NB == 1 ? t : lane) * 16;
 #pragma unroll
-                for (int h = 0; h < PAIR; ++h) {
-                    const int from = (lane & ~3) | (WIDTH == 128 ? PAIR * j + h : u);
-                    s_lo[h] = __shfl_sync(0xffffffffu, sc[h].lo, from);
-                    s_hi[h] = __shfl_sync(0xffffffffu, sc[h].hi, from);
-                    z_lo[h] = z_hi[h] = Op::zero(8);
-                    if (a.zeros) {
-                        z_lo[h] = __shfl_sync(0xffffffffu, sc[h].z_lo, from);
-                        z_hi[h] = __shfl_sync(0xffffffffu, sc[h].z_hi, from);
-                    }
-                }
-            }
-            uint4 xv[PAIR][TILES];
+            for (int u = 0; u < 4; ++u) {
+                if (u % PER_GROUP == 0) {  // a group starts
 #pragma unroll
-            for (int h = 0; h < PAIR; ++h)
-#pragma unroll
-                for (int m = 0; m < TILES; ++m)
-                    xv[h][m] = lds128(x_at + h * X::BYTES + m * X::TILE_BYTES + u * X::UNIT_BYTES);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int h = 0; h < PAIR; ++h) {
-                    uint32_t f[4];
-                    if (Op::TWO_PLACES) {
-                        const uint32_t mask = half ? 0x00F000F0u : 0x000F000Fu;
-                        f[0] = w[h].lo[u] & mask;
-                        f[1] = w[h].hi[u] & mask;
-                        f[2] = (w[h].lo[u] >> 8) & mask;
-                        f[3] = (w[h].hi[u] >> 8) & mask;
-                    } else {
-                        f[0] = ((w[h].lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                        f[1] = ((w[h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
-                        f[2] = ((w[h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
-                        f[3] = ((w[h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
-                    }
-                    const int up = Op::TWO_PLACES ? 4 * half : 0;
-                    f[0] = Op::minus(f[0], z_lo[h] << up);
-                    f[1] = Op::minus(f[1], z_hi[h] << up);
-                    f[2] = Op::minus(f[2], z_lo[h] << up);
-                    f[3] = Op::minus(f[3], z_hi[h] << up);
-#pragma unroll
-                    for (int m = 0; m < TILES; ++m) {
-                        float(&d)[4] = c[h][TILES == 1 ? half : m];
-                        const uint32_t b0 = half ? xv[h][m].z : xv[h][m].x, b1 = half ? xv[h][m].w : xv[h][m].y;
-                        if (u % PER_GROUP == 0 && (half == 0 || TILES == 1))  // the chain starts
-                            Op::mma(d, f, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
-                        else
-                            Op::mma(d, f, b0, b1, d[0], d[1], d[2], d[3]);
-                    }
-                }
-            }
-            if ((u + 1) % PER_GROUP == 0) {  // the group ends
-#pragma unroll
-                for (int h = 0; h < PAIR; ++h) {
-                    if constexpr (ACC > 1) {
-#pragma unroll
-                        for (int m = 0; m < ACC; ++m) {
-                            sum[m][0] = fmaf(s_lo[h], c[h][m][0], sum[m][0]);
-                            sum[m][1] = fmaf(s_lo[h], c[h][m][1], sum[m][1]);
-                            sum[m][2] = fmaf(s_hi[h], c[h][m][2], sum[m][2]);
-                            sum[m][3] = fmaf(s_hi[h], c[h][m][3], sum[m][3]);
+                    for (int h = 0; h < SIDE; ++h) {
+                        const int from = (lane & ~3) | (WIDTH == 128 ? PAIR * j + h0 + h : u);
+                        s_lo[h] = __shfl_sync(0xffffffffu, sc[h0 + h].lo, from);
+                        s_hi[h] = __shfl_sync(0xffffffffu, sc[h0 + h].hi, from);
+                        z_lo[h] = z_hi[h] = Op::zero(8);
+                        if (a.zeros) {
+                            z_lo[h] = __shfl_sync(0xffffffffu, sc[h0 + h].z_lo, from);
+                            z_hi[h] = __shfl_sync(0xffffffffu, sc[h0 + h].z_hi, from);
                         }
-                    } else {
-                        float d[4];
+                    }
+                }
+                uint4 xv[SIDE][TILES];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (Op::TWO_PLACES) {
-                                d[i] = fmaf(c[h][1][i], Op::UNIT / 16, c[h][0][i] * Op::UNIT);
-                            } else {  // small terms first
-                                d[i] = c[h][CHAINS - 1][i];
+                for (int h = 0; h < SIDE; ++h)
 #pragma unroll
-                                for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                    for (int m = 0; m < TILES; ++m)
+                        xv[h][m] = lds128(x_at + (h0 + h) * X::BYTES + m * X::TILE_BYTES + u * X::UNIT_BYTES);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int h = 0; h < SIDE; ++h) {
+                        uint32_t f[4];
+                        if (Op::TWO_PLACES) {
+                            const uint32_t mask = half ? 0x00F000F0u : 0x000F000Fu;
+                            f[0] = w[h0 + h].lo[u] & mask;
+                            f[1] = w[h0 + h].hi[u] & mask;
+                            f[2] = (w[h0 + h].lo[u] >> 8) & mask;
+                            f[3] = (w[h0 + h].hi[u] >> 8) & mask;
+                        } else {
+                            f[0] = ((w[h0 + h].lo[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                            f[1] = ((w[h0 + h].hi[u] >> (8 * half)) & 0x000F000Fu) | Op::ONE;
+                            f[2] = ((w[h0 + h].lo[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                            f[3] = ((w[h0 + h].hi[u] >> (8 * half + 4)) & 0x000F000Fu) | Op::ONE;
+                        }
+                        const int up = Op::TWO_PLACES ? 4 * half : 0;
+                        f[0] = Op::minus(f[0], z_lo[h] << up);
+                        f[1] = Op::minus(f[1], z_hi[h] << up);
+                        f[2] = Op::minus(f[2], z_lo[h] << up);
+                        f[3] = Op::minus(f[3], z_hi[h] << up);
+#pragma unroll
+                        for (int m = 0; m < TILES; ++m) {
+                            float(&d)[4] = c[h][TILES == 1 ? half : m];
+                            const uint32_t b0 = half ? xv[h][m].z : xv[h][m].x, b1 = half ? xv[h][m].w : xv[h][m].y;
+                            if (u % PER_GROUP == 0 && (half == 0 || TILES == 1))  // the chain starts
+                                Op::mma(d, f, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                            else
+                                Op::mma(d, f, b0, b1, d[0], d[1], d[2], d[3]);
+                        }
+                    }
+                }
+                if ((u + 1) % PER_GROUP == 0) {  // the group ends
+#pragma unroll
+                    for (int h = 0; h < SIDE; ++h) {
+                        if constexpr (ACC > 1) {
+#pragma unroll
+                            for (int m = 0; m < ACC; ++m) {
+                                sum[m][0] = fmaf(s_lo[h], c[h][m][0], sum[m][0]);
+                                sum[m][1] = fmaf(s_lo[h], c[h][m][1], sum[m][1]);
+                                sum[m][2] = fmaf(s_hi[h], c[h][m][2], sum[m][2]);
+                                sum[m][3] = fmaf(s_hi[h], c[h][m][3], sum[m][3]);
                             }
+                        } else {
+                            float d[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (Op::TWO_PLACES) {
+                                    d[i] = fmaf(c[h][1][i], Op::UNIT / 16, c[h][0][i] * Op::UNIT);
+                                } else {  // small terms first
+                                    d[i] = c[h][CHAINS - 1][i];
+#pragma unroll
+                                    for (int m = CHAINS - 2; m >= 0; --m) d[i] += c[h][m][i];
+                                }
+                            }
+                            sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
+                            sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
+                            sum[0][2] = fmaf(s_hi[h], d[2], sum[0][2]);
+                            sum[0][3] = fmaf(s_hi[h], d[3], sum[0][3]);
                         }
-                        sum[0][0] = fmaf(s_lo[h], d[0], sum[0][0]);
-                        sum[0][1] = fmaf(s_lo[h], d[1], sum[0][1]);
-                        sum[0][2] = fmaf(s_hi[h], d[2], sum[0][2]);
-                        sum[0][3] = fmaf(s_hi[h], d[3], sum[0][3]);
                     }
                 }
             }
@@ -742,7 +755,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                 s += X::SPREAD ? (from[(3 * r + 2) * 16] + from[(3 * r + 1) * 16]) + from[3 * r * 16] : from[r * 16];
             const int64_t row = static_cast<int64_t>(u) * R + n;
             if (row >= a.N) continue;
-            if (Op::TERMS == 1 && !(fabsf(s) <= 3.0e38f))
+            if (!isfinite(s))
                 s = scalar_row(a, static_cast<int64_t>(expert) * a.N + row,
                                static_cast<const T *>(a.x) + members.row[r] * a.ldx);
             y[members.row[r] * a.ldy + row] = from_f32<T>(s);

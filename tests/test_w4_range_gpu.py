@@ -62,3 +62,53 @@ def test_outliers_at_the_zero_point_leave_no_trace(ex, dtype, zeros, rows):
     y = ex.w4_matvec(x[:rows].cuda(), packed, torch.ones(N, K // GROUP, device="cuda"), group=GROUP,
                      zeros=torch.from_numpy(z.astype(np.uint8)).cuda() if zeros else None)
     assert_within(y, want[:rows], limit(want, mag, terms, dtype)[:rows])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 2, 4, 8])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_sums_that_overflow_before_their_scale(ex, dtype, zeros, rows):
+    """Values near the type's largest, weights up to 15, scales that bring the result back; pairs that cancel."""
+    rng = np.random.default_rng(rows)
+    q = rng.integers(0, 16, (N, K))
+    z = rng.integers(0, 16, (N, K // GROUP)) if zeros else np.full((N, K // GROUP), 8)
+    scales = (2.0 ** -rng.integers(7, 12, (N, K // GROUP))).astype(np.float32)
+    x = rng.standard_normal((rows, K)).astype(np.float32)
+    x[:, 3], x[:, 70], x[:, 200] = 1.0e38, -3.0e38, 2.5e38
+    x[:, 300], x[:, 301] = 3.0e38, -3.0e38
+    q[: N // 2, 301] = q[: N // 2, 300]  # these leave the small values' sum
+    q[: N // 4, [3, 70, 200]] = z[: N // 4, [0, 0, 1]]
+    x = torch.from_numpy(x).to(DTYPES[dtype])
+    w = (q - np.repeat(z, GROUP, 1)) * np.repeat(scales.astype(np.float64), GROUP, 1)
+    x64 = x.double().numpy()
+    want, mag = x64 @ w.T, np.abs(x64) @ np.abs(w).T
+    assert (np.abs(want) < 1e36).any() and (np.abs(want) > 1e36).any() and np.abs(want).max() < 3e38
+    packed = torch.from_numpy((q[:, ::2] | (q[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    y = ex.w4_matvec(x.cuda(), packed, torch.from_numpy(scales).cuda(), group=GROUP,
+                     zeros=torch.from_numpy(z.astype(np.uint8)).cuda() if zeros else None)
+    assert torch.isfinite(y).all()
+    assert_within(y, want, bound(want, mag, 3 * K + K // GROUP + 2, DTYPES[dtype]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 2, 4, 8])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_infinities_and_nan(ex, dtype, rows):
+    """The kinds of results are those of 64-bit sums, in every form of the kernel."""
+    rng = np.random.default_rng(9)
+    q = rng.integers(0, 16, (N, K))
+    x = rng.standard_normal((rows, K)).astype(np.float32)
+    x[0, 17] = np.inf
+    if rows > 1:
+        x[1, 9], x[1, 400] = np.inf, -np.inf
+    if rows > 2:
+        x[2, 500] = np.nan
+    with np.errstate(invalid="ignore"):
+        w = (q - 8).astype(np.float64)
+        want = np.stack([(r[None] * w).sum(1) for r in x.astype(np.float64)])
+    packed = torch.from_numpy((q[:, ::2] | (q[:, 1::2] << 4)).astype(np.uint8)).cuda()
+    y = ex.w4_matvec(torch.from_numpy(x).to(DTYPES[dtype]).cuda(), packed, torch.ones(N, K // GROUP, device="cuda"),
+                     group=GROUP).double().cpu().numpy()
+    assert np.array_equal(np.isnan(y), np.isnan(want))
+    assert np.array_equal(np.isposinf(y), np.isposinf(want)) and np.array_equal(np.isneginf(y), np.isneginf(want))
