@@ -205,15 +205,18 @@ __device__ __forceinline__ void stage32_fused(int act, uint32_t buf, int lane, f
 // A NaN of one row of a gradient makes every output of its matrix NaN, so the
 // dot products are not simply made again (a serial sum per output: 193 ms for
 // 4096 rows, 2048 x 2048, in place of 0.19, and past the limit of the other
-// roles' waits for 49152 rows). First each lane looks for a NaN in its column of
-// op(B) and, if outputs are left, in its row of op(A), 8 loads at a time; that
-// explains all outputs but those that infinities made. For these the warp makes
-// one dot product at a time, its lanes along k (partial sums added in a fixed
-// order), until it is NaN. Called by all 32 lanes; the chunk is complete in
-// shared memory before and after.
-__device__ __noinline__ void repair_chunk(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row0,
-                                          int64_t m_end, int64_t col0, int64_t n_end, int64_t k_begin, int64_t k_end) {
-    constexpr int AHEAD = 8;
+// roles' waits for 49152 rows). First each lane looks for a NaN in its row of
+// op(A), once for all chunks of a unit (`row_nan`: what the last call returned;
+// UNKNOWN at first), and, if outputs are left, in its column of op(B), 16 loads at
+// a time; that explains all outputs but those that infinities made. For these
+// the warp makes one dot product at a time, its lanes along k (partial sums added
+// in a fixed order), until it is NaN. Called by all 32 lanes; the chunk is
+// complete in shared memory before and after.
+enum RowNan { UNKNOWN, NONE, SOME };
+__device__ __noinline__ RowNan repair_chunk(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row0,
+                                            int64_t m_end, int64_t col0, int64_t n_end, int64_t k_begin, int64_t k_end,
+                                            RowNan row_nan) {
+    constexpr int AHEAD = 16, LANES_AHEAD = 4;
     const int lane = static_cast<int>(threadIdx.x & 31);
     const int rows = static_cast<int>(min(static_cast<int64_t>(32), m_end - row0));
     const int cols = static_cast<int>(min(static_cast<int64_t>(32), n_end - col0));
@@ -239,9 +242,12 @@ __device__ __noinline__ void repair_chunk(const Args &a, uint32_t rc, const floa
         }
         return found;
     };
+    const bool asks = left != 0 && row_nan == UNKNOWN;
+    const bool found = holds_nan(asks, A + lane * am, ak);
+    if (asks) row_nan = found ? SOME : NONE;
+    if (row_nan == SOME) left = 0;
     const unsigned some = __reduce_or_sync(0xffffffffu, left);  // columns with such a NaN
     left &= ~__ballot_sync(0xffffffffu, holds_nan((some >> lane) & 1, B + lane * bn, bk));
-    if (holds_nan(left != 0, A + lane * am, ak)) left = 0;
 #pragma unroll 1
     for (unsigned at; (at = __ballot_sync(0xffffffffu, left != 0)) != 0;) {
         const int r = __ffs(at) - 1;
@@ -249,16 +255,16 @@ __device__ __noinline__ void repair_chunk(const Args &a, uint32_t rc, const floa
         const float *x = A + r * am, *y = B + j * bn;
         float sum = 0.0f;
 #pragma unroll 1
-        for (int64_t k0 = k_begin; k0 < k_end && !__any_sync(0xffffffffu, sum != sum); k0 += 32 * AHEAD / 2) {
-            float p[AHEAD / 2], q[AHEAD / 2];
+        for (int64_t k0 = k_begin; k0 < k_end && !__any_sync(0xffffffffu, sum != sum); k0 += 32 * LANES_AHEAD) {
+            float p[LANES_AHEAD], q[LANES_AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD / 2; ++i) {
+            for (int i = 0; i < LANES_AHEAD; ++i) {
                 const int64_t k = k0 + 32 * i + lane;
                 p[i] = k < k_end ? x[k * ak] : 0.0f;
                 q[i] = k < k_end ? y[k * bk] : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < AHEAD / 2; ++i) sum = fmaf(p[i], q[i], sum);
+            for (int i = 0; i < LANES_AHEAD; ++i) sum = fmaf(p[i], q[i], sum);
         }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -268,6 +274,7 @@ __device__ __noinline__ void repair_chunk(const Args &a, uint32_t rc, const floa
         }
     }
     __syncwarp();
+    return row_nan;
 }
 
 // The last fold of a unit for a chunk written with per-thread stores: the
@@ -282,11 +289,11 @@ __device__ __noinline__ void repair_chunk(const Args &a, uint32_t rc, const floa
 // it is rare, and inlined it would compete for registers with the interior
 // path.
 template <bool VEC_C>
-__device__ __noinline__ void edge_final_chunk(const Args &a, uint32_t rc, const float *A, const float *B, float *citem,
-                                              int64_t m_end, int64_t row0, int64_t col0, bool atomic, int64_t k_begin,
-                                              int64_t k_end) {
+__device__ __noinline__ RowNan edge_final_chunk(const Args &a, uint32_t rc, const float *A, const float *B,
+                                                float *citem, int64_t m_end, int64_t row0, int64_t col0, bool atomic,
+                                                int64_t k_begin, int64_t k_end, RowNan row_nan) {
     const int lane = static_cast<int>(threadIdx.x & 31);
-    if (col0 >= a.N) return;  // uniform over the warp
+    if (col0 >= a.N) return row_nan;  // uniform over the warp
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -294,8 +301,10 @@ __device__ __noinline__ void edge_final_chunk(const Args &a, uint32_t rc, const 
         nan |= r.x != r.x || r.y != r.y || r.z != r.z || r.w != r.w;
     }
     __syncwarp();
-    if (__any_sync(0xffffffffu, nan)) repair_chunk(a, rc, A, B, row0, m_end, col0, a.N, k_begin, k_end);
+    if (__any_sync(0xffffffffu, nan))
+        row_nan = repair_chunk(a, rc, A, B, row0, m_end, col0, a.N, k_begin, k_end, row_nan);
     store_staged_rows(a, rc, citem, m_end, row0, col0, atomic);
+    return row_nan;
 }
 
 // What the kernel's units are: k-block ranges of one product's tiles
@@ -836,6 +845,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             const bool fused = a.ep && !atomic;
             const bool col_bias = a.bias_kind == SGEMM_BIAS_PER_COL;
             const float rb = (a.bias_kind == SGEMM_BIAS_PER_ROW && row < u.m_end) ? __ldg(a.bias + row) : 0.0f;
+            RowNan row_nan = UNKNOWN;
             if constexpr (COLS) {
                 // C^T: lanes are columns of C, accumulator columns its rows, written
                 // straight from registers, 128 bytes of a row at a time.
@@ -899,9 +909,9 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                         }
                         if (nan) {
                             __syncwarp();
-                            repair_chunk(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
-                                         a.B + (SUMS_ROWS ? u.k0 * a.ldb : 0), row0, u.m_end, u.n0 + ch * 32, u.n_end, 0,
-                                         u.k_end);
+                            row_nan = repair_chunk(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
+                                                   a.B + (SUMS_ROWS ? u.k0 * a.ldb : 0), row0, u.m_end,
+                                                   u.n0 + ch * 32, u.n_end, 0, u.k_end, row_nan);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
@@ -977,10 +987,10 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                             st_shared_v4(rc + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2],
                                          v[4 * j + 3]);
                         const int64_t k_end = min(static_cast<int64_t>(ke) * BK, u.k_end);
-                        edge_final_chunk<VEC_C>(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
-                                                a.B + u.item_b * a.strideB + (SUMS_ROWS ? u.k0 * a.ldb : 0),
-                                                a.C + u.item_c * a.strideC, u.m_end, row0, col0, atomic,
-                                                static_cast<int64_t>(kb) * BK, k_end);
+                        row_nan = edge_final_chunk<VEC_C>(
+                            a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
+                            a.B + u.item_b * a.strideB + (SUMS_ROWS ? u.k0 * a.ldb : 0), a.C + u.item_c * a.strideC,
+                            u.m_end, row0, col0, atomic, static_cast<int64_t>(kb) * BK, k_end, row_nan);
                         continue;
                     }
                     if (fused) {
