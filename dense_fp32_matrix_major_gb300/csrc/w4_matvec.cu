@@ -39,8 +39,8 @@
 //
 // Work. One block per SM goes through units of R = 16 .. 128 rows of q times
 // all of k. A producer warp streams q into a ring in shared memory by TMA
-// (stages of 32 KB, boxes of 128 bytes x R rows in the 128-byte swizzle, some
-// 100 KB on their way per SM); 16 warps each take two steps of a stage, 16 rows
+// (two to four stages of 32 KB, boxes of 128 bytes x R rows in the 128-byte
+// swizzle); 16 warps each take two steps of a stage, 16 rows
 // x 128 k each, side by side, and add up their shares of k at the end of a unit.
 // x is laid out either by every block for itself, once, and stays in shared
 // memory, or, where it is too large for that, by a small kernel before this one,
@@ -70,8 +70,12 @@ constexpr int STEP = 128;          // values of k per warp step
 constexpr int PAIR = 2;            // steps of a warp in a stage
 constexpr int TURN = 2;            // stages between fetches of scales
 constexpr int Q_STAGE = 32 * 1024;
-constexpr int MAX_STAGES = 6;
-constexpr int SMEM_BYTES = 224 * 1024;      // of a block, at most
+// Stages of the ring. More only take shared memory from the L1 cache, which
+// holds scales and spilled registers: 1 x 28672 x 4096 bf16 19.5 us with four,
+// 21.3 with six; x streamed, 4 x 16384 x 8192 fp32, groups of 64, 34.5 us with
+// two, 40.2 with three.
+constexpr int MAX_STAGES = 4, STREAM_STAGES = 2;
+constexpr int SMEM_BYTES = 225 * 1024;      // of a block, at most (and 144 bytes of static shared memory)
 constexpr int RESIDENT_ONE = 144 * 1024;    // x in shared memory: one row, eight rows
 constexpr int RESIDENT_EIGHT = 96 * 1024;
 constexpr int X_STAGE = 64 * 1024;          // x of a stage, at most, when it is streamed
@@ -829,11 +833,14 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
     }
     // Rows of a unit: few give every SM its part, many need less of a streamed
     // x and end less often (about a stage's time). The choice makes the
-    // busiest SM's bytes least.
+    // busiest SM's bytes least. The ring has two stages at least: with one, loads
+    // and products would take turns.
+    const int64_t rest = 1024 + 2 * CONSUMERS * (X::SPREAD ? TILES : 1) * NB * 16 * 4 + (STREAM ? 0 : steps * X::BYTES);
+    auto stage_of = [](int64_t KS) { return Q_STAGE + (STREAM ? (KS * X::BYTES + 1023) / 1024 * 1024 : 0); };
     int64_t least = INT64_MAX;
     for (int R = 16; R <= 128; R *= 2) {
         const int64_t KS = PAIR * CONSUMERS / (R / 16), x = STREAM ? KS * X::BYTES : 0;
-        if (x > X_STAGE) continue;
+        if (x > X_STAGE || 2 * stage_of(KS) > SMEM_BYTES - rest) continue;
         const int64_t units = (a.N + R - 1) / R;
         int64_t workers = dev.sm_count / busy;  // of a pass
         workers = workers < 1 ? 1 : workers > units ? units : workers;
@@ -845,11 +852,9 @@ int launch(W4Args a, const DeviceInfo &dev, cudaStream_t stream, int *launches) 
         }
     }
     a.units = static_cast<int>((a.N + a.unit_rows - 1) / a.unit_rows);
-    const int64_t KS = PAIR * CONSUMERS / (a.unit_rows / 16);
-    const int64_t stage = Q_STAGE + (STREAM ? (KS * X::BYTES + 1023) / 1024 * 1024 : 0);
-    const int64_t rest = 1024 + 2 * CONSUMERS * (X::SPREAD ? TILES : 1) * NB * 16 * 4 + (STREAM ? 0 : steps * X::BYTES);
+    const int64_t stage = stage_of(PAIR * CONSUMERS / (a.unit_rows / 16));
     int64_t stages = (SMEM_BYTES - rest) / stage;
-    if (stages > MAX_STAGES) stages = MAX_STAGES;
+    if (stages > (STREAM ? STREAM_STAGES : MAX_STAGES)) stages = STREAM ? STREAM_STAGES : MAX_STAGES;
     a.stages = static_cast<int>(stages);
     a.x_vector = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * static_cast<int64_t>(sizeof(T)) % 16 == 0;
     a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
