@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_rank_kernel(const Id *ids, 
     for (int i = threadIdx.x; i < warps * keys; i += SORT_THREADS) smem[i] = 0;
     for (int i = threadIdx.x; i < keys; i += SORT_THREADS) start[i] = 0;
     __syncthreads();
-    // The one-kernel form follows any kernel; the other its count, which has
-    // waited for what was before it: the pairs' ids can be read now.
-    if (blocks == 1) after_previous();
+    // Before the first read of ids, in both forms: the count kernel has waited
+    // for what wrote them, but that makes them visible to its grid, not to this.
+    after_previous();
 
     int64_t begin, end;
     block_range(pairs, block, blocks, &begin, &end);
@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_rank_kernel(const Id *ids, 
             start[e] = sum;
         }
     } else {
-        after_previous();
         const int parts = max(1, SORT_THREADS / keys);
         // Warp 0's row takes the pairs of earlier blocks on top of the counts
         // before warp 0, which are none: fold it in by adding after the loop.

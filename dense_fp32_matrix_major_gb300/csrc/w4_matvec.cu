@@ -440,10 +440,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    // Both forms may be launched while the kernel before them in the stream
-    // ends; behind the one that lays out x, which has waited for what was before
-    // it, only x is waited for.
-    if (!STREAM) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // May be launched while the kernel before it in the stream ends. Nothing is
+    // read before that one's end, whichever it is: what kernels before it wrote
+    // (ids, weights) is visible to the grid that waited for them, and to this one
+    // by its own wait only.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
     const int pass = a.first_pass + static_cast<int>(blockIdx.y);
@@ -454,8 +455,6 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             for (int64_t n = static_cast<int64_t>(blockIdx.x) * W4_THREADS + threadIdx.x; n < a.N;
                  n += static_cast<int64_t>(gridDim.x) * W4_THREADS)
                 y[pass * a.ldy + n] = from_f32<T>(0.0f);
-        // Where no pass has rows, this grid still ends after the one before it.
-        if (STREAM && blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
 
@@ -465,24 +464,9 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             const uint8_t *x_from = STREAM ? a.prepared + static_cast<int64_t>(blockIdx.y) * steps * X::BYTES : nullptr;
             int slot = 0;
             uint32_t phase = 0;
-            bool waited = !STREAM;
-            auto copy_x = [&](int to, int stage) {  // of stage `stage` of a unit
-                const int first = stage * KS, here = min(KS, steps - first);
-                bulk_load(base + to * stage_bytes + Q_STAGE, x_from + static_cast<int64_t>(first) * X::BYTES,
-                          static_cast<uint32_t>(here * X::BYTES), full(to));
-            };
-            // Stages of the first turn of the ring whose q is on its way while
-            // the kernel that lays out x runs.
-            int without_x = 0;
-            auto catch_up = [&] {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                waited = true;
-                for (int i = 0; i < without_x; ++i) copy_x(i, i % per_unit);
-            };
             for (int u = static_cast<int>(blockIdx.x); u < a.units; u += static_cast<int>(gridDim.x)) {
                 const int row = expert * static_cast<int>(a.N) + u * R;
                 for (int stage = 0; stage < per_unit; ++stage) {
-                    if (!waited && without_x == a.stages) catch_up();
                     if (!tc::mbar_wait(empty(slot), phase ^ 1, a, abort_flag, tc::WD_PRODUCER)) return;
                     const int boxes = min(KS / 2, (K / 2 - stage * KS * 64 + 127) / 128);
                     const int here = min(KS, steps - stage * KS);
@@ -491,19 +475,16 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
                     for (int b = 0; b < boxes; ++b)
                         tc::tma_load_3d(base + slot * stage_bytes + b * R * 128, &tmQ, stage * KS * 64 + b * 128, row, 0,
                                         full(slot));
-                    if (STREAM) {
-                        if (waited)
-                            copy_x(slot, stage);
-                        else
-                            ++without_x;
-                    }
+                    if (STREAM)
+                        bulk_load(base + slot * stage_bytes + Q_STAGE,
+                                  x_from + static_cast<int64_t>(stage) * KS * X::BYTES,
+                                  static_cast<uint32_t>(here * X::BYTES), full(slot));
                     if (++slot == a.stages) {
                         slot = 0;
                         phase ^= 1;
                     }
                 }
             }
-            if (!waited) catch_up();
         }
         return;
     }
