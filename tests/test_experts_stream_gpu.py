@@ -1,4 +1,5 @@
-"""The mixture-of-experts operators between other work on a stream: inputs written by the kernel right before."""
+"""The mixture-of-experts operators between other work on a stream: inputs written by the kernel right before, and
+calls captured in a CUDA graph."""
 
 import pytest
 import torch
@@ -51,3 +52,54 @@ def test_w4_matvec_of_inputs_that_are_just_written(ex, dtype, K):
         got.append(ex.w4_matvec(x, q, s, group=group, ids=at))
     for n, y in enumerate(got):
         assert torch.equal(y, want[n % sets]), n
+
+
+def step(ex, ids, x, w, b, q, scales):
+    """A layer's calls, forward and backward, and a decoding step; with copies of unaligned operands, slices of a long
+    sum and streamed x, which take memory from the library's pool."""
+    r = ex.sort(ids, b.shape[0])
+    xs = ex.gather(x, r)
+    h = ex.gemm(xs, b, r.offsets)
+    y = ex.combine(h, w, r)
+    dh, dw = ex.combine_grad(y, h, w, r)
+    dxs = ex.gemm(dh, b, r.offsets, transB=True)
+    db = ex.gemm_wgrad(xs, dh, r.offsets)
+    dx = ex.gather_grad(dxs, r)
+    few = ex.w4_matvec(x[:5], q, scales, group=128)
+    odd = ex.gemm(xs[:, 1:], b[:, 1:], r.offsets)
+    return r.order, xs, h, y, dh, dw, db, dx, few, odd
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens", [6, 6000])
+def test_captured_in_a_graph(ex, dtype, tokens):
+    from dense_fp32_matrix_major_gb300 import sgemm
+
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    width, N, E = 6400, 96, 2
+
+    def inputs():
+        return (torch.randint(-1, E, (tokens, 2), generator=g, device="cuda"),
+                torch.randn((tokens, width), generator=g, device="cuda").to(dtype),
+                torch.rand((tokens, 2), generator=g, device="cuda"))
+
+    b = (torch.randn((E, width, N), generator=g, device="cuda") * 0.01).to(dtype)
+    q = torch.randint(0, 256, (300, width // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.rand((300, width // 128), generator=g, device="cuda") * 0.01
+    fixed = inputs()
+    step(ex, *fixed, b, q, scales)  # the first calls set kernels up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(ex, *fixed, b, q, scales)
+    for _ in range(4):
+        new = inputs()
+        for to, source in zip(fixed, new):
+            to.copy_(source)
+        graph.replay()
+        replayed = [t.clone() for t in out]
+        want = step(ex, *new, b, q, scales)
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(replayed, want)):
+            assert torch.equal(x, y), i
+    assert sgemm.device_status() == 0

@@ -61,3 +61,41 @@ def test_limits_of_x_in_shared_memory(ex, dtype, rows, K, past):
     group = 128 if dtype != "f16" else 64
     x, q, s, z, w = case(dtype, rows, 70, K, group)
     check(ex.w4_matvec(x, q, s, group=group, zeros=z), x, w, None, K, group, dtype)
+
+
+@pytest.mark.parametrize("dtype,rows,K", [("bf16", 600, 8192), ("f32", 700, 4096)])
+def test_streamed_x_with_ids_in_several_launches(ex, dtype, rows, K):
+    """More passes than one launch takes, x streamed, some rows without an expert, twice in a row."""
+    x, q, s, z, w = case(dtype, rows, 40, K, 128, experts=5)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    ids = torch.randint(-1, 6, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    first = ex.w4_matvec(x, q, s, group=128, zeros=z, ids=ids)
+    second = ex.w4_matvec(x, q, s, group=128, zeros=z, ids=ids)
+    check(first, x, w, ids, K, 128, dtype)
+    assert torch.equal(first, second)
+    assert (first[(ids < 0) | (ids > 4)] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_streamed_x_of_many_rows(ex, dtype):
+    """256 passes of eight rows a launch, and a part of a pass after two of them."""
+    rows, K = 2 * 256 * 8 + 3, 6272
+    x, q, s, z, w = case(dtype, rows, 24, K, 128)
+    y = ex.w4_matvec(x, q, s, group=128, zeros=z)
+    check(y, x, w, None, K, 128, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_streamed_x_of_rows_without_an_expert(ex, dtype):
+    """No pass has work: zeros, and what follows on the stream is not disturbed."""
+    K, rows = 8192, 9
+    x, q, s, z, w = case(dtype, rows, 200, K, 64, experts=3)
+    none = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    some = torch.tensor([2, 0, 1, 1, -1, 2, 0, 7, 1], dtype=torch.int32, device="cuda")
+    x[4] = x[7] = float("nan")  # rows without an expert
+    for _ in range(5):
+        y = torch.ones((rows, 200), dtype=x.dtype, device="cuda")
+        ex.w4_matvec(x, q, s, group=64, zeros=z, ids=none, out=y)
+        again = ex.w4_matvec(x, q, s, group=64, zeros=z, ids=some)
+        assert (y == 0).all()
+        check(again, torch.nan_to_num(x), w, some, K, 64, dtype)
