@@ -69,12 +69,17 @@ class Routing(NamedTuple):
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream_handle(stream, t):
-    """The stream's handle; the tensors' device must be the current one, which the library launches on."""
-    device = t.device.index
-    if device != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _current_stream(device) if stream is None else stream.cuda_stream
+def _stream_handle(stream, *tensors):
+    """The stream's handle; every tensor (or None) must be on the current device, which the library launches on."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{device}")
+    if stream is None:
+        return _current_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{device}")
+    return stream.cuda_stream
 
 
 def _check(rc, what):
@@ -174,7 +179,8 @@ def gather(x, routing, out=None, stream=None):
     if tuple(out.shape) != (tokens * top_k, width):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gather(code, tokens, top_k, experts, width, x.data_ptr(), ldx, slot, offsets,
-                                    out.data_ptr(), ldo, _stream_handle(stream, x)), "sgemm_experts_gather")
+                                    out.data_ptr(), ldo, _stream_handle(stream, x, out, routing.slot, routing.offsets)),
+           "sgemm_experts_gather")
     return out
 
 
@@ -193,7 +199,8 @@ def _combine(h, weights, routing, out, stream):
     if tuple(out.shape) != (tokens, width):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_combine(code, tokens, top_k, experts, width, h.data_ptr(), ldh, w, slot, offsets,
-                                     out.data_ptr(), ldo, _stream_handle(stream, h)), "sgemm_experts_combine")
+                                     out.data_ptr(), ldo, _stream_handle(stream, h, weights, out, routing.slot, routing.offsets)),
+           "sgemm_experts_combine")
     return out
 
 
@@ -225,7 +232,8 @@ def combine_grad(dy, h, weights, routing, stream=None):
     dw = _empty((tokens, top_k), torch.float32, h.device, stream)
     _check(lib.sgemm_experts_combine_grad(code, tokens, top_k, experts, width, dy.data_ptr(), lddy, h.data_ptr(), ldh,
                                           w, slot, offsets, dh.data_ptr(), max(width, 1), dw.data_ptr(),
-                                          _stream_handle(stream, h)), "sgemm_experts_combine_grad")
+                                          _stream_handle(stream, dy, h, weights, routing.slot, routing.offsets)),
+           "sgemm_experts_combine_grad")
     return dh, dw
 
 
@@ -248,7 +256,8 @@ def gemm(a, b, offsets, out=None, *, transB=False, stream=None):
     if tuple(out.shape) != (rows, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gemm(code, int(transB), rows, N, K, E, off, a.data_ptr(), lda, b.data_ptr(), ldb, stride,
-                                  out.data_ptr(), ldo, _stream_handle(stream, a)), "sgemm_experts_gemm")
+                                  out.data_ptr(), ldo, _stream_handle(stream, a, b, offsets, out)),
+           "sgemm_experts_gemm")
     return out
 
 
@@ -274,7 +283,7 @@ def gemm_wgrad(a, b, offsets, out=None, *, stream=None):
     if tuple(out.shape) != (E, M, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_gemm_wgrad(code, rows, M, N, E, off, a.data_ptr(), lda, b.data_ptr(), ldb,
-                                        out.data_ptr(), ldo, stride, _stream_handle(stream, a)),
+                                        out.data_ptr(), ldo, stride, _stream_handle(stream, a, b, offsets, out)),
            "sgemm_experts_gemm_wgrad")
     return out
 
@@ -309,5 +318,6 @@ def w4_matvec(x, q, scales, *, group, zeros=None, ids=None, out=None, stream=Non
     if tuple(out.shape) != (rows, N):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_w4_matvec(code, rows, N, K, group, E, ip, x.data_ptr(), ldx, qp, sp, TYPES[scales.dtype], zp,
-                               out.data_ptr(), ldo, _stream_handle(stream, x)), "sgemm_w4_matvec")
+                               out.data_ptr(), ldo, _stream_handle(stream, x, q, scales, zeros, ids, out)),
+           "sgemm_w4_matvec")
     return out
