@@ -14,12 +14,14 @@ A layer's forward pass::
 
 and its gradients: :func:`combine_grad`, :func:`gemm` with ``transB`` the other way round for the rows,
 :func:`gemm_wgrad` for the experts' matrices, :func:`gather_grad`. :func:`w4_matvec` serves single tokens from
-4-bit matrices.
+4-bit matrices. The calls record no gradients of their own: in a model they stand inside a torch.autograd.Function
+(an input that requires a gradient elsewhere draws a warning).
 """
 
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -70,8 +72,13 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream_handle(stream, *tensors):
-    """The stream's handle; every tensor (or None) must be on the current device, which the library launches on."""
+    """The stream's handle; every tensor (or None) must be on the current device, which the library launches on.
+
+    Warns where PyTorch would expect a gradient to flow through the call."""
     device = torch.cuda.current_device()
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        warnings.warn("an input requires a gradient, but these calls record none: the result is cut from the graph "
+                      "(call them inside torch.autograd.Function or torch.no_grad())", stacklevel=3)
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{device}")
@@ -199,7 +206,8 @@ def _combine(h, weights, routing, out, stream):
     if tuple(out.shape) != (tokens, width):
         raise ValueError("out has the wrong shape")
     _check(lib.sgemm_experts_combine(code, tokens, top_k, experts, width, h.data_ptr(), ldh, w, slot, offsets,
-                                     out.data_ptr(), ldo, _stream_handle(stream, h, weights, out, routing.slot, routing.offsets)),
+                                     out.data_ptr(), ldo,
+                                     _stream_handle(stream, h, weights, out, routing.slot, routing.offsets)),
            "sgemm_experts_combine")
     return out
 

@@ -5,8 +5,8 @@ import torch
 
 
 class On:
-    def __init__(self, device):
-        self.device_index, self.cuda_stream = device, 77
+    def __init__(self, device, requires_grad=False):
+        self.device_index, self.cuda_stream, self.requires_grad = device, 77, requires_grad
 
     def get_device(self):
         return self.device_index
@@ -50,8 +50,8 @@ def test_calls_check_every_tensor(ex, monkeypatch):
     i32 = {"dtype": torch.int32}
     r = ex.Routing(torch.zeros(3, **i32), torch.zeros(8, **i32), torch.zeros(4, 2, **i32))
     x, h, w, y = torch.zeros(4, 8), torch.zeros(8, 8), torch.zeros(4, 2), torch.zeros(4, 8)
-    b, q, s, z, ids = torch.zeros(2, 8, 6), torch.zeros(2, 5, 4), torch.zeros(2, 5, 1), torch.zeros(2, 5, 1), torch.zeros(4)
-    c, y5 = torch.zeros(8, 6), torch.zeros(4, 5)
+    b, q, s, z = torch.zeros(2, 8, 6), torch.zeros(2, 5, 4), torch.zeros(2, 5, 1), torch.zeros(2, 5, 1)
+    ids, c, y5 = torch.zeros(4), torch.zeros(8, 6), torch.zeros(4, 5)
     for call, tensors in (
         (lambda: ex.gather(x, r, out=h), (x, h, r.slot, r.offsets)),
         (lambda: ex.combine(h, w, r, out=y), (h, w, y, r.slot, r.offsets)),
@@ -65,3 +65,15 @@ def test_calls_check_every_tensor(ex, monkeypatch):
             call()
         got = seen.pop()
         assert all(any(t is g for g in got) for t in tensors)
+
+
+def test_a_lost_gradient_draws_a_warning(ex):
+    import warnings
+
+    with pytest.warns(UserWarning, match="cut from the graph"):
+        ex._stream_handle(On(0), On(0), None, On(0, requires_grad=True))
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        ex._stream_handle(On(0), On(0), None, On(0))
+        with torch.no_grad():
+            ex._stream_handle(On(0), On(0, requires_grad=True))
