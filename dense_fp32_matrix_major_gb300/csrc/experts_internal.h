@@ -77,7 +77,11 @@ int w4_launch(const W4Problem &p, const DeviceInfo &dev, cudaStream_t stream, in
 
 }  // namespace ex
 
-// Records the launches of the last successful call (sgemm_last_launch_count).
+// Records the launches of the last successful call (sgemm_last_launch_count)
+// and the variant of the last fp32 product (sgemm_last_variant_used).
 void note_launches(int launches);
+void note_variant(int variant);
+// The caller's choice (sgemm_set_variant).
+int chosen_variant();
 
 }  // namespace sgemm

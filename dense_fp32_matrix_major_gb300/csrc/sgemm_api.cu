@@ -275,6 +275,13 @@ int current_device(DeviceInfo *info) {
 
 void note_launches(int launches) { g_last_launches.store(launches); }
 
+void note_variant(int variant) { g_last_variant.store(variant); }
+
+int chosen_variant() {
+    read_env();
+    return g_variant.load();
+}
+
 }  // namespace sgemm
 
 using sgemm::Problem;

@@ -105,10 +105,14 @@ int sgemm_experts_combine_grad(int type, int64_t tokens, int64_t top_k, int64_t 
  *              matrix), each K x N (SGEMM_OP_N) or N x K (SGEMM_OP_T).
  *   C, ldc     out, rows x N.
  * rows must be below 2^31 - 1024. fp32 inputs follow sgemm_f32's accuracy
- * bound and its rules for infinities and NaN (on normal inputs the error is
- * that of fp32 sums); bf16 and fp16 products are exact in fp32 and summed in
- * fp32, where the tensor core cuts a running sum at every 16 products: about
- * 2e-8 of it each time, 2e-5 for sums of 16384, far below the rounding of the
+ * bound and its rules for infinities and NaN, and the variant that
+ * sgemm_set_variant chose: SGEMM_AUTO and SGEMM_TF32X3 the three-term TF32
+ * split (two 11-bit parts of each factor, the product of the low parts left
+ * out), whose error on normal inputs is 0.7e-6 of the result's norm where that of
+ * fp32 sums is 0.3e-6 to 0.6e-6; SGEMM_FFMA fp32 multiply-adds, one after the
+ * other, about eight times slower. bf16 and fp16 products are exact in fp32 and
+ * summed in fp32, where the tensor core cuts a running sum at every 16 products:
+ * about 2e-8 of it each time, 2e-5 for sums of 16384, far below the rounding of the
  * result. A row's result depends on that row and its expert's matrix only,
  * whatever the other sizes (16-bit operands whose rows are not 16-byte aligned
  * are summed in one of two orders, by the sizes). The gradient of A is the same

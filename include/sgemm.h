@@ -254,11 +254,13 @@ int sgemm_set_variant(int variant);
 int sgemm_get_variant(void);
 /* Name of a variant ("auto", "ffma", "tf32x3"), or "unknown". Static storage. */
 const char *sgemm_variant_name(int variant);
-/* Variant that the most recent successful product call (any entry point) in
- * this process enqueued (SGEMM_AUTO before any call). For reporting only. */
+/* Variant that the most recent successful fp32 product call (any entry point,
+ * sgemm_experts_gemm and sgemm_experts_gemm_wgrad among them) in this process
+ * enqueued (SGEMM_AUTO before any call). For reporting only. */
 int sgemm_last_variant_used(void);
 /* Number of kernel launches that the most recent successful product call
- * (any entry point) enqueued (0 for an empty product). For reporting only. */
+ * (any entry point, those of experts.h among them) enqueued (0 for an empty product).
+ * For reporting only. */
 int sgemm_last_launch_count(void);
 
 /* Human-readable text of a status code. Static storage. */
