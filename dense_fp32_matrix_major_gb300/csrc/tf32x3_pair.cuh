@@ -1021,9 +1021,15 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
     }
 
     // The odd CTA's TMEM is written by the even CTA's MMAs: wait for them to
-    // drain before the pair releases it.
+    // drain before the pair releases it. After a wait that gave up, loads may
+    // still be on their way: leave them time to land.
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        const uint64_t t0 = global_timer();
+        while (global_timer() - t0 < 10000000ull) {
+        }
+    }
     if (rank != 0 && threadIdx.x == 0) {
         if (!mbar_wait<true>(bar(pr::DRAIN), 0, a, abort_flag, WD_DRAIN)) {
             const uint64_t t0 = global_timer();
