@@ -113,7 +113,7 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
     a.ta = TA ? 1 : 0;
     a.tb = TB ? 1 : 0;
     a.c_tma = c_tma ? 1 : 0;
-    a.timeout_ns = wait_limit_ns(p.K);
+    a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
     a.watchdog = flag;
     const GroupTiles gt{p.offsets,
                         static_cast<int>(p.rows),

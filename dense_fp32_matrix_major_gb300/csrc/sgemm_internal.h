@@ -160,13 +160,13 @@ void scratch_free(float *ptr, cudaStream_t stream);
 // tf32x3 translation unit). Read-and-clear; returns 0 or the first recorded code.
 int watchdog_read_and_clear(int *code);
 int64_t watchdog_ms();
-// The same for a kernel that sums `terms` products and makes outputs that
-// infinities turned into NaN again, while its other roles wait: at most 128 x
-// 32 dot products a warp, 25 us a term at 0.2 us a step of 32 terms, doubled.
-// At most a minute.
+// The same for the SM-pair kernel of sgemm_f32, which sums `terms` products and
+// makes outputs that infinities turned into NaN again while its other roles wait:
+// at most 128 dot products a lane, 0.44 us a term each (measured), doubled. At
+// most a minute.
 inline uint64_t wait_limit_ns(int64_t terms) {
     const uint64_t most = 60000000000ull, own = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
-    const uint64_t more = terms < 1200000 ? static_cast<uint64_t>(terms) * 50000ull : most;
+    const uint64_t more = terms < 600000 ? static_cast<uint64_t>(terms) * 100000ull : most;
     return own + more < most ? own + more : (own > most ? own : most);
 }
 int watchdog_set_ms(int64_t ms);

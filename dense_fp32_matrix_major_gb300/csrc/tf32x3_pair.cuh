@@ -135,7 +135,7 @@ constexpr int RAW_FULL = 0, RAW_FREE = RAW_FULL + RAW_SLOTS, OP_FULL = RAW_FREE 
 // scope, without stalling the warp (a remote mbarrier.arrive.release.cluster
 // held the arriving thread ~0.8 us per k-block on GB300, measured).
 constexpr uint32_t SIGNAL_BYTES = 4 * GROUP_WARPS;
-static_assert(NBARS * 8 + 24 <= PBAR_BYTES, "barrier block");
+static_assert(NBARS * 8 + 32 <= PBAR_BYTES, "barrier block");
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 static_assert(TMEM_A + OP_STAGES * 64 <= TMEM_COLS, "TMEM columns");
 static_assert((HN / 4) * (BK / 4) == CONV_THREADS, "one 4 x 4 B block per converter thread");
@@ -197,84 +197,18 @@ __device__ __forceinline__ void stage32_fused(int act, uint32_t buf, int lane, f
     }
 }
 
-// NaN in a chunk of finished sums (chunk rc, swizzled, lane l holding row
-// row0 + l, columns from col0 on; rows from m_end and columns from n_end on are
-// not looked at) made what IEEE arithmetic gives over [k_begin, k_end): a NaN
-// among the inputs gives NaN, an infinity the dot product's own result.
-//
-// A NaN of one row of a gradient makes every output of its matrix NaN, so the
-// dot products are not simply made again (a serial sum per output: 193 ms for
-// 4096 rows, 2048 x 2048, in place of 0.19, and past the limit of the other
-// roles' waits for 49152 rows). First each lane looks for a NaN in its row of
-// op(A), once for all chunks of a unit (`row_nan`: what the last call returned;
-// UNKNOWN at first), and, if outputs are left, in its column of op(B), 16 loads at
-// a time; that explains all outputs but those that infinities made. For these
-// the warp makes one dot product at a time, its lanes along k (partial sums added
-// in a fixed order), until it is NaN. Called by all 32 lanes; the chunk is
-// complete in shared memory before and after.
-enum RowNan { UNKNOWN, NONE, SOME };
-__device__ __noinline__ RowNan repair_chunk(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row0,
-                                            int64_t m_end, int64_t col0, int64_t n_end, int64_t k_begin, int64_t k_end,
-                                            RowNan row_nan) {
-    constexpr int AHEAD = 16, LANES_AHEAD = 4;
+// NaN in a chunk of finished sums (chunk rc, swizzled, this lane holding row
+// `row`, columns from col0 on) recomputed over [k_begin, k_end), in shared
+// memory, one column at a time (few registers).
+__device__ __forceinline__ void repair_row(const Args &a, uint32_t rc, const float *A, const float *B, int64_t row,
+                                           int64_t col0, int64_t n_end, int64_t k_begin, int64_t k_end) {
     const int lane = static_cast<int>(threadIdx.x & 31);
-    const int rows = static_cast<int>(min(static_cast<int64_t>(32), m_end - row0));
-    const int cols = static_cast<int>(min(static_cast<int64_t>(32), n_end - col0));
-    const int64_t am = a.ta ? 1 : a.lda, ak = a.ta ? a.lda : 1, bn = a.tb ? a.ldb : 1, bk = a.tb ? 1 : a.ldb;
-    A += row0 * am;
-    B += col0 * bn;
-    unsigned left = 0;  // of this lane's row: columns that hold an unexplained NaN
 #pragma unroll 1
-    for (int j = 0; j < cols; ++j) {
-        const float x = ld_shared_f32(rc + sw128_offset(lane, j >> 2) + static_cast<uint32_t>((j & 3) * 4));
-        if (lane < rows && x != x) left |= 1u << j;
+    for (int j = 0; j < 32 && col0 + j < n_end; ++j) {
+        const uint32_t addr = rc + sw128_offset(lane, j >> 2) + static_cast<uint32_t>((j & 3) * 4);
+        const float x = ld_shared_f32(addr);
+        if (x != x) st_shared_f32(addr, dot_ieee(A, a.lda, a.ta, B, a.ldb, a.tb, row, col0 + j, k_begin, k_end));
     }
-    // Whether x[k_begin * step], x[(k_begin + 1) * step], ... hold a NaN, for the lanes that ask.
-    auto holds_nan = [&](bool asks, const float *x, int64_t step) {
-        bool found = false;
-#pragma unroll 1
-        for (int64_t k = k_begin; k < k_end && __any_sync(0xffffffffu, asks && !found); k += AHEAD) {
-            float v[AHEAD];
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) v[i] = asks && k + i < k_end ? x[(k + i) * step] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) found |= v[i] != v[i];
-        }
-        return found;
-    };
-    const bool asks = left != 0 && row_nan == UNKNOWN;
-    const bool found = holds_nan(asks, A + lane * am, ak);
-    if (asks) row_nan = found ? SOME : NONE;
-    if (row_nan == SOME) left = 0;
-    const unsigned some = __reduce_or_sync(0xffffffffu, left);  // columns with such a NaN
-    left &= ~__ballot_sync(0xffffffffu, holds_nan((some >> lane) & 1, B + lane * bn, bk));
-#pragma unroll 1
-    for (unsigned at; (at = __ballot_sync(0xffffffffu, left != 0)) != 0;) {
-        const int r = __ffs(at) - 1;
-        const int j = __ffs(__shfl_sync(0xffffffffu, left, r)) - 1;
-        const float *x = A + r * am, *y = B + j * bn;
-        float sum = 0.0f;
-#pragma unroll 1
-        for (int64_t k0 = k_begin; k0 < k_end && !__any_sync(0xffffffffu, sum != sum); k0 += 32 * LANES_AHEAD) {
-            float p[LANES_AHEAD], q[LANES_AHEAD];
-#pragma unroll
-            for (int i = 0; i < LANES_AHEAD; ++i) {
-                const int64_t k = k0 + 32 * i + lane;
-                p[i] = k < k_end ? x[k * ak] : 0.0f;
-                q[i] = k < k_end ? y[k * bk] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < LANES_AHEAD; ++i) sum = fmaf(p[i], q[i], sum);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == r) {
-            st_shared_f32(rc + sw128_offset(lane, j >> 2) + static_cast<uint32_t>((j & 3) * 4), sum);
-            left &= ~(1u << j);
-        }
-    }
-    __syncwarp();
-    return row_nan;
 }
 
 // The last fold of a unit for a chunk written with per-thread stores: the
@@ -287,24 +221,26 @@ __device__ __noinline__ RowNan repair_chunk(const Args &a, uint32_t rc, const fl
 // chunks that cross the last row or column of C, for C that TMA cannot
 // address and for chunks holding a NaN; called by all 32 lanes. Out of line:
 // it is rare, and inlined it would compete for registers with the interior
-// path.
-template <bool VEC_C>
-__device__ __noinline__ RowNan edge_final_chunk(const Args &a, uint32_t rc, const float *A, const float *B,
-                                                float *citem, int64_t m_end, int64_t row0, int64_t col0, bool atomic,
-                                                int64_t k_begin, int64_t k_end, RowNan row_nan) {
+// path. REPAIR: not for row groups, whose NaN are seen to at the end
+// (repair_units).
+template <bool VEC_C, bool REPAIR>
+__device__ __noinline__ void edge_final_chunk(const Args &a, uint32_t rc, const float *A, const float *B, float *citem,
+                                              int64_t m_end, int64_t row0, int64_t col0, bool atomic, int64_t k_begin,
+                                              int64_t k_end) {
     const int lane = static_cast<int>(threadIdx.x & 31);
-    if (col0 >= a.N) return row_nan;  // uniform over the warp
-    bool nan = false;
+    if (col0 >= a.N) return;  // uniform over the warp
+    const int64_t row = row0 + lane;
+    if (REPAIR) {
+        bool nan = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
-        nan |= r.x != r.x || r.y != r.y || r.z != r.z || r.w != r.w;
+        for (int j = 0; j < 8; ++j) {
+            const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
+            nan |= r.x != r.x || r.y != r.y || r.z != r.z || r.w != r.w;
+        }
+        if (nan && row < m_end) repair_row(a, rc, A, B, row, col0, a.N, k_begin, k_end);
     }
     __syncwarp();
-    if (__any_sync(0xffffffffu, nan))
-        row_nan = repair_chunk(a, rc, A, B, row0, m_end, col0, a.N, k_begin, k_end, row_nan);
     store_staged_rows(a, rc, citem, m_end, row0, col0, atomic);
-    return row_nan;
 }
 
 // What the kernel's units are: k-block ranges of one product's tiles
@@ -361,6 +297,91 @@ __device__ __forceinline__ void for_each_pair_unit(const Args &a, const ex::Grou
     }
 }
 
+// Outputs of row groups that came out NaN made what IEEE arithmetic gives: a NaN
+// among the inputs gives NaN, an infinity the dot product's own result. Run by
+// the whole block for its units when all is written, so that nothing waits for
+// it: the sums may be a whole group's rows long.
+//
+// A NaN in one row of a gradient makes every output of its matrix NaN, so dot
+// products are not simply made again (a serial sum per output took 193 ms for
+// 4096 rows, 2048 x 2048, and past the limit of the other roles' waits for 49152).
+// A warp takes 32 x 32 outputs. Each lane looks for a NaN in its row of op(A)
+// and, if outputs are left, in its column of op(B), 16 loads at a time; that
+// explains all outputs but those that infinities made. For these the warp makes
+// one dot product at a time, its lanes along k (partial sums added in a fixed
+// order), until it is NaN. One NaN row in 4096: 0.72 ms in all (0.17 without), in
+// 49152 9.7 ms (1.8).
+template <PairUnits UNITS>
+__device__ __noinline__ void repair_units(const Args &a, const ex::GroupTiles &gt, volatile int *abort_flag, int pair,
+                                          int pairs, int rank) {
+    constexpr int AHEAD = 16, LANES_AHEAD = 4;
+    constexpr bool COLS = transposed(UNITS);
+    const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+    const int64_t am = a.ta ? 1 : a.lda, ak = a.ta ? a.lda : 1, bn = a.tb ? a.ldb : 1, bk = a.tb ? 1 : a.ldb;
+    const int64_t cm = COLS ? 1 : a.ldc, cn = COLS ? a.ldc : 1;
+    for_each_pair_unit<UNITS>(a, gt, abort_flag, pair, pairs, [&](const PairUnit &u) {
+        if (u.ke == u.kb) return;
+#pragma unroll 1
+        for (int chunk = warp; chunk < 4 * pr::CHUNKS; chunk += pr::THREADS / 32) {
+            const int64_t row0 = u.m0 + pr::HM * rank + 32 * (chunk / pr::CHUNKS), col0 = u.n0 + 32 * (chunk % pr::CHUNKS);
+            const int rows = static_cast<int>(min(static_cast<int64_t>(32), u.m_end - row0));
+            const int cols = static_cast<int>(min(static_cast<int64_t>(32), u.n_end - col0));
+            if (rows <= 0 || cols <= 0) continue;
+            const float *A = a.A + u.item_a * a.strideA + u.k0 * a.lda + row0 * am;
+            const float *B = a.B + u.item_b * a.strideB + u.k0 * a.ldb + col0 * bn;
+            float *C = a.C + u.item_c * a.strideC + row0 * cm + col0 * cn;
+            const int64_t k_end = u.k_end;
+            unsigned left = 0;  // of this lane's row: columns that hold an unexplained NaN
+#pragma unroll 4
+            for (int j = 0; j < cols; ++j) {
+                const float x = lane < rows ? C[lane * cm + j * cn] : 0.0f;
+                if (x != x) left |= 1u << j;
+            }
+            // Whether x[0], x[step], ... hold a NaN, for the lanes that ask.
+            auto holds_nan = [&](bool asks, const float *x, int64_t step) {
+                bool found = false;
+#pragma unroll 1
+                for (int64_t k = 0; k < k_end && __any_sync(0xffffffffu, asks && !found); k += AHEAD) {
+                    float v[AHEAD];
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) v[i] = asks && k + i < k_end ? x[(k + i) * step] : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) found |= v[i] != v[i];
+                }
+                return found;
+            };
+            if (holds_nan(left != 0, A + lane * am, ak)) left = 0;
+            const unsigned some = __reduce_or_sync(0xffffffffu, left);  // columns with such a NaN
+            left &= ~__ballot_sync(0xffffffffu, holds_nan((some >> lane) & 1, B + lane * bn, bk));
+#pragma unroll 1
+            for (unsigned open; (open = __ballot_sync(0xffffffffu, left != 0)) != 0;) {
+                const int r = __ffs(open) - 1;
+                const int j = __ffs(__shfl_sync(0xffffffffu, left, r)) - 1;
+                const float *x = A + r * am, *y = B + j * bn;
+                float sum = 0.0f;
+#pragma unroll 1
+                for (int64_t k0 = 0; k0 < k_end && !__any_sync(0xffffffffu, sum != sum); k0 += 32 * LANES_AHEAD) {
+                    float p[LANES_AHEAD], q[LANES_AHEAD];
+#pragma unroll
+                    for (int i = 0; i < LANES_AHEAD; ++i) {
+                        const int64_t k = k0 + 32 * i + lane;
+                        p[i] = k < k_end ? x[k * ak] : 0.0f;
+                        q[i] = k < k_end ? y[k * bk] : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < LANES_AHEAD; ++i) sum = fmaf(p[i], q[i], sum);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == r) {
+                    C[r * cm + j * cn] = sum;
+                    left &= ~(1u << j);
+                }
+            }
+        }
+    });
+}
+
 // TA: A stored K x M (op(A) = A^T); TB: B stored N x K (op(B) = B^T).
 // Over a group's rows op(A) = A^T and op(B) = B.
 // FOLD: the longest chain of k-blocks. LEAD > 0: in a chain's first LEAD
@@ -386,6 +407,8 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + pr::NBARS + 1);
     // Target word of the odd CTA's st.async signals (its value is not used).
     const uint32_t signal_word = smem_u32(bars + pr::NBARS + 2);
+    // Groups: this CTA wrote a NaN.
+    volatile int *nan_flag = reinterpret_cast<volatile int *>(bars + pr::NBARS + 3);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             mbar_init(bar(pr::ACC_EMPTY + d), 2 * pr::EPI_WARPS);
         }
         mbar_init(bar(pr::DRAIN), 1);
-        *abort_flag = 0;
+        *abort_flag = *nan_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tma_warp && lane == 0 && !a.cpa) {
@@ -845,7 +868,6 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
             const bool fused = a.ep && !atomic;
             const bool col_bias = a.bias_kind == SGEMM_BIAS_PER_COL;
             const float rb = (a.bias_kind == SGEMM_BIAS_PER_ROW && row < u.m_end) ? __ldg(a.bias + row) : 0.0f;
-            RowNan row_nan = UNKNOWN;
             if constexpr (COLS) {
                 // C^T: lanes are columns of C, accumulator columns its rows, written
                 // straight from registers, 128 bytes of a row at a time.
@@ -895,31 +917,16 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                                 v[4 * j + 3] += r.w;
                             }
                         }
-                        bool nan = false;
-                        if (last) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) nan |= v[j] != v[j];
-                            nan = __any_sync(0xffffffffu, nan);
-                        }
-                        if (!last || nan) {
+                        if (!last) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 st_shared_v4(rc + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2],
                                              v[4 * j + 3]);
-                        }
-                        if (nan) {
-                            __syncwarp();
-                            row_nan = repair_chunk(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
-                                                   a.B + (SUMS_ROWS ? u.k0 * a.ldb : 0), row0, u.m_end,
-                                                   u.n0 + ch * 32, u.n_end, 0, u.k_end, row_nan);
+                        } else {
+                            bool nan = false;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 r = ld_shared_v4(rc + sw128_offset(lane, j));
-                                v[4 * j] = r.x;
-                                v[4 * j + 1] = r.y;
-                                v[4 * j + 2] = r.z;
-                                v[4 * j + 3] = r.w;
-                            }
+                            for (int j = 0; j < 32; ++j) nan |= v[j] != v[j];
+                            if (nan) *nan_flag = 1;
                         }
                         if (last) write(ch, v);
                         __syncwarp();
@@ -981,16 +988,18 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
                     bool nan = false;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) nan |= v[j] != v[j];
-                    if (__any_sync(0xffffffffu, nan) || !a.c_tma || col0 + 32 > a.N || row0 + 32 > u.m_end) {
+                    if (UNITS != TILES && nan) *nan_flag = 1;
+                    if ((UNITS == TILES && __any_sync(0xffffffffu, nan)) || !a.c_tma || col0 + 32 > a.N ||
+                        row0 + 32 > u.m_end) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             st_shared_v4(rc + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2],
                                          v[4 * j + 3]);
                         const int64_t k_end = min(static_cast<int64_t>(ke) * BK, u.k_end);
-                        row_nan = edge_final_chunk<VEC_C>(
-                            a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
-                            a.B + u.item_b * a.strideB + (SUMS_ROWS ? u.k0 * a.ldb : 0), a.C + u.item_c * a.strideC,
-                            u.m_end, row0, col0, atomic, static_cast<int64_t>(kb) * BK, k_end, row_nan);
+                        edge_final_chunk<VEC_C, UNITS == TILES>(a, rc, a.A + u.item_a * a.strideA + (SUMS_ROWS ? u.k0 * a.lda : 0),
+                                                a.B + u.item_b * a.strideB + (SUMS_ROWS ? u.k0 * a.ldb : 0),
+                                                a.C + u.item_c * a.strideC, u.m_end, row0, col0, atomic,
+                                                static_cast<int64_t>(kb) * BK, k_end);
                         continue;
                     }
                     if (fused) {
@@ -1043,6 +1052,9 @@ __global__ void __launch_bounds__(pr::THREADS, 1)
     if (warp == 0) {
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
                      : "memory");
+    }
+    if constexpr (UNITS != TILES) {
+        if (*nan_flag) repair_units<UNITS>(a, gt, abort_flag, pair, pairs, static_cast<int>(rank));
     }
 }
 

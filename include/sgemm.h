@@ -296,10 +296,10 @@ int sgemm_watchdog_selftest(int64_t wait_ms, sgemm_stream_t stream);
  *                            2 = data-parallel waves plus a stream-K remainder;
  *                            3 = stream-K over all tiles
  *   SGEMM_TUNE_WATCHDOG_MS   milliseconds a bounded wait polls before it gives
- *                            up (1 .. 60000; default 2000). The SM-pair kernels
- *                            add 50 us per term of an output's sum, up to a
- *                            minute: outputs that infinities turned into NaN are
- *                            made again meanwhile.
+ *                            up (1 .. 60000; default 2000). The SM-pair kernel
+ *                            of sgemm_f32 and its forms adds 100 us per term of
+ *                            an output's sum, up to a minute: outputs that came
+ *                            out NaN are made again meanwhile.
  *   SGEMM_TUNE_TF32X3_KERNEL  tensor-core kernel: 0 = automatic (default):
  *                            where A and B have 16-byte aligned bases and
  *                            row strides, the SM-pair kernel from 2^20
