@@ -34,8 +34,10 @@
 // One 32-bit word holds k = 0 .. 7; masking it shifted by 4 j gives the pair (j,
 // j + 4), so x is laid out in shared memory in the order 0 4 1 5 2 6 3 7 (fp16:
 // 0 4 2 6 1 5 3 7, the unshifted and four bits up apart). A sum that is not
-// finite is made again with scalar arithmetic in 64 bits: a group's sum may
-// overflow before it is scaled where the result does not.
+// finite, though its row of x is, is made again with scalar arithmetic in 64
+// bits: a group's sum may overflow before it is scaled where the result does not.
+// (Infinities and NaN of x need none of this: operands are exact, so the products
+// and sums are IEEE's already.)
 //
 // Work. One block per SM goes through units of R = 16 .. 128 rows of q times
 // all of k. A producer warp streams q into a ring in shared memory by TMA
@@ -241,13 +243,34 @@ __device__ __forceinline__ Scales values_of(const W4Args &a, const Raw &r) {
     return Scales{scale_value(a, r.lo), scale_value(a, r.hi), Op::zero(r.z_lo & 15u), Op::zero(r.z_hi & 15u)};
 }
 
-// y[r][n] with scalar arithmetic, 8 values at a time. 64 bits hold every product
-// exactly and no sum overflows in them; a NaN ends it.
+// What a sum s = y[r][n] that is not finite should be: itself where x holds an
+// infinity or a NaN (a look at 32 values at a time, which the lanes share: 8 x
+// 16384 x 8192 bf16 0.47 ms, 9.8 ms where such rows were summed again), otherwise
+// the sum in 64 bits, which hold every product exactly and do not overflow.
 template <class T>
-__device__ __noinline__ float scalar_row(const W4Args &a, int64_t row, const T *x) {
+__device__ __noinline__ float scalar_row(const W4Args &a, int64_t row, const T *x, float s32) {
+    constexpr int PER = 16 / sizeof(T);
+    bool finite = true;
+#pragma unroll 1
+    for (int64_t k = 0; k < a.K && finite; k += 32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += PER) {
+            Pack<T, PER> p;
+            if (a.x_vector) {
+                p = load_pack<T, PER>(x + k + j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) p.v[i] = x[k + j + i];
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) finite = finite && isfinite(to_f32(p.v[i]));
+        }
+    }
+    if (!finite) return s32;
     const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row * (a.K / 2));
     double s = 0.0;
-    for (int64_t k = 0; k < a.K && s == s; k += 8) {
+#pragma unroll 1
+    for (int64_t k = 0; k < a.K; k += 8) {
         const int64_t gi = row * a.groups + (k >> a.group_shift);
         const uint32_t word = __ldg(q + k / 8);
         const int z = a.zeros ? __ldg(a.zeros + gi) & 15 : 8;
@@ -742,7 +765,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
             if (row >= a.N) continue;
             if (!isfinite(s))
                 s = scalar_row(a, static_cast<int64_t>(expert) * a.N + row,
-                               static_cast<const T *>(a.x) + members.row[r] * a.ldx);
+                               static_cast<const T *>(a.x) + members.row[r] * a.ldx, s);
             y[members.row[r] * a.ldy + row] = from_f32<T>(s);
         }
     }

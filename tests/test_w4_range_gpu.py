@@ -112,3 +112,32 @@ def test_infinities_and_nan(ex, dtype, rows):
                      group=GROUP).double().cpu().numpy()
     assert np.array_equal(np.isnan(y), np.isnan(want))
     assert np.array_equal(np.isposinf(y), np.isposinf(want)) and np.array_equal(np.isneginf(y), np.isneginf(want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_time_of_rows_that_are_not_finite(ex, dtype, value):
+    """Such rows are not summed again (9.8 ms here, 0.04 ms otherwise): the products are IEEE's as they are."""
+    rows, n, k = 8, 16384, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.rand((n, k // 128), generator=g, device="cuda")
+    x = torch.randn((rows, k), generator=g, device="cuda").to(DTYPES[dtype])
+    x[:, k - 1] = value
+    y = torch.empty((rows, n), dtype=x.dtype, device="cuda")
+    times = []
+    for _ in range(4):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        ex.w4_matvec(x, q, scales, group=128, out=y)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    assert min(times) < 2.0
+    last = (q[:, -1] >> 4).float() - 8
+    if value != value:
+        assert torch.isnan(y).all()
+    else:
+        assert torch.equal(torch.isnan(y), (last == 0).expand(rows, n))
+        assert torch.equal(torch.sign(y.float()[:, last != 0]), torch.sign(last[last != 0]).expand(rows, -1))
