@@ -103,3 +103,30 @@ def test_captured_in_a_graph(ex, dtype, tokens):
         for i, (x, y) in enumerate(zip(replayed, want)):
             assert torch.equal(x, y), i
     assert sgemm.device_status() == 0
+
+
+def test_two_streams_at_once(ex):
+    """Calls on two streams that nothing orders: each has its own scratch and gives its own results."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    width, N, E = 6400, 96, 2
+    jobs = []
+    for tokens, dtype in ((700, torch.float32), (500, torch.bfloat16)):
+        jobs.append((torch.randint(-1, E, (tokens, 2), generator=g, device="cuda"),
+                     torch.randn((tokens, width), generator=g, device="cuda").to(dtype),
+                     torch.rand((tokens, 2), generator=g, device="cuda"),
+                     (torch.randn((E, width, N), generator=g, device="cuda") * 0.01).to(dtype),
+                     torch.randint(0, 256, (300, width // 2), generator=g, device="cuda", dtype=torch.uint8),
+                     torch.rand((300, width // 128), generator=g, device="cuda") * 0.01))
+    want = [step(ex, *j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for s, j, out in zip(streams, jobs, got):
+            with torch.cuda.stream(s):
+                out.append(step(ex, *j))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        for o in outs:
+            for i, (x, y) in enumerate(zip(o, w)):
+                assert torch.equal(x, y), i
