@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_slices_kernel(const Join j)
 // Slices that pay: a k-block takes a pair 0.55 us (fp32, 32 rows) or 0.22 us (16
 // bits, 64 rows); the sums are written and read at 5 TB/s, the second launch
 // and its wait take 6 us. Groups are taken as even. In slices and whole, one
-// group of 30000 rows: 64 x 64 fp32 37 and 552 us, bf16 30 and 119 us; 512 x 512
+// group of 30000 rows, cold: 64 x 64 fp32 37 and 552 us, bf16 33 and 119 us; 512 x 512
 // fp32 91 and 593 us, bf16 35 and 138 us; 2000 rows, 64 x 64: fp32 24 and 49 us.
 int slices_of(const GroupedProblem &p, const DeviceInfo &dev) {
     int64_t high = 256, wide = 256;

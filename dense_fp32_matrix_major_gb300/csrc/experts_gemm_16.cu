@@ -7,8 +7,9 @@
 // short. Products of two 16-bit values are exact in fp32 and are summed in
 // fp32 in tensor memory; a value is rounded once, when C is written. Measured in
 // bf16 with 16384 rows, 32 experts, 2048 -> 4096: rows 188 us (1460 TFLOP/s, the
-// path from L2 to shared memory), wgrad 216 us (the stores of C on top of it); 64
-// rows, 32 experts, 2048 -> 2048: 43 us (6.2 TB/s, reading B).
+// path from L2 to shared memory; 170 us where groups are even), wgrad 216 us (the
+// stores of C on top of it; 198); 64 rows, two for each of 32 experts, 2048 -> 2048:
+// 52 us (5.2 TB/s, reading B).
 //
 // Two CTAs on two SMs of a cluster make one 256 x n tile (n <= 256): each
 // stages 128 rows of the first operand and n / 2 of the second per 64-deep

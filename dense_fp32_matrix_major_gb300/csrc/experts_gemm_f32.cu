@@ -2,8 +2,10 @@
 // pairs (tf32x3_pair.cuh) over row groups. Accuracy and the treatment of
 // infinities and NaN are that kernel's. Bound by shared memory (operand tiles,
 // their split, folds) where groups are long: 8192 rows, 8 experts, 1024 -> 2048
-// 176 us (195 TFLOP/s, of 320 with three TF32 products for one); by reading B
-// where they are short: 64 rows, 32 experts, 2048 -> 2048 111 us (4.8 TB/s).
+// 170 us (202 TFLOP/s, of 320 with three TF32 products for one; 154 us where groups
+// are even, their gradient of the matrices 149 us); by reading and splitting B,
+// which goes through registers value by value however few rows there are, where
+// they are short: 64 rows, two for each of 32 experts, 2048 -> 2048 137 us (3.9 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -30,7 +32,7 @@ int g_clusters[kMaxDevices][9];
 // fp32 sums give 0.57e-6 at K = 1024. Here a fold every 5 k-blocks, the small
 // products (lo hi, hi lo) of the first 4 before any large one, leaves 28: 0.7e-6.
 // Folds move the tile through shared memory and held stages are not refilled:
-// 8192 rows, 8 experts, 1024 -> 2048 take 179 us (192 TFLOP/s); 4 k-blocks with 3
+// 8192 rows, 8 experts, 1024 -> 2048 took 179 us (now 170); 4 k-blocks with 3
 // ahead 187 us (0.64e-6), 6 with 4 ahead 175 us (0.98e-6), 6 with 3 ahead 171 us
 // (1.15e-6).
 constexpr int GROUP_FOLD = 5, GROUP_LEAD = 4;
@@ -143,7 +145,8 @@ int launch(const GroupedProblem &p, const Problem &q, bool cpa, const DeviceInfo
 // rows, 8 experts, 2048 -> 1024), 113 and 275 us (64 rows, 32 experts, 2048 ->
 // 2048; the matrices alone are 79 us of DRAM); for 8192 rows, 8 experts, 1024 ->
 // 128, where half of a narrow tile would be columns of nothing, wide takes 40 us.
-// wgrad: 158 and 183 us for groups of two rows, 179 and 175 us for groups of 1024.
+// wgrad: 158 and 183 us for groups of two rows, 179 and 175 us for groups of 1024
+// (narrow 149 us since no sums are repaired among the folds).
 bool rows_narrow(const GroupedProblem &p) {
     auto charged = [&](int64_t step) {
         return p.wgrad ? (p.M + step - 1) / step * step : p.rows + p.experts * step / 2;
@@ -156,7 +159,8 @@ bool rows_narrow(const GroupedProblem &p) {
 // Operands that tensor maps cannot describe are either copied into aligned rows
 // first or loaded by the kernel with 4-byte copies, which take it 6 us a k-block.
 // What the busiest pair's k-blocks would cost that way against the copies' time.
-// Copied and loaded: 92 and 541 us (1745 rows, 64 experts, 2761 -> 35), 58 and
+// Copied and loaded: 92 and 541 us (1745 rows, 64 experts, 2761 -> 35, B stored 35 x
+// 2761; 257 us stored 2761 x 35, whose short rows a block copies one by one), 58 and
 // 218 us (2000 rows, 8 experts, 1001 -> 1001); 905 and 232 us (5 rows, 64
 // experts, 2047 -> 2047: the copy takes every expert's matrix).
 bool copy_first(const GroupedProblem &p, size_t bytes, const DeviceInfo &dev) {

@@ -23,7 +23,7 @@
 // tokens x 8 choices of 64 experts, width 2048, bf16 (a plain copy makes 6.8
 // TB/s): gather 95 us (6.4 TB/s), combine 103 us (5.9), its gradient 197 us
 // (5.8); the sort of the 131072 pairs 17 us, two launches of which the second
-// is resident before the first ends.
+// is resident before the first ends and reads nothing until then.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -501,8 +501,8 @@ bool many(dim3 grid, const DeviceInfo &dev) { return int64_t(grid.x) * grid.y >=
 // A launch that may begin while the kernel before it in the stream ends: its
 // blocks are resident by then. It takes the host about 1 us more than a plain
 // launch, so small grids, whose calls the host bounds, are launched plainly. Sort
-// and gather of 16384 tokens x 8: 106.5 us, 112.6 plainly; of 4 tokens x 2: 28.9
-// and 26.7 us.
+// and gather of 16384 tokens x 8: 108 us, 113 plainly; of 4 tokens x 2: 28.9 and
+// 26.7 us.
 template <class... P, class... A>
 int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool overlap,
                  int *launches, A... args) {

@@ -5,11 +5,14 @@
 // for up to eight rows r at a time that share a matrix. Bound by reading q:
 // half a byte per weight, so the instructions spent on a weight have to be
 // few: at 6.8 TB/s an SM has about 170 issue slots for the 1 KB of q that a
-// warp takes in a step. Measured cold: 1 x 4096 x 4096 bf16 13 us, 1 x 28672 x
-// 4096 27 us (2.2 TB/s, the operand instructions), 8 x 16384 x 8192 with zero
-// points 32 us in bf16 and 41 us in fp32 (35 us in a row of calls:
-// there the 24 matrix instructions a step bound it). 16 rows of 16 experts, 2048
-// -> 4096, fp16: 26 us.
+// warp takes in a step. In a row of calls: 1 x 4096 x 4096 bf16 8 us, 1 x 28672 x
+// 4096 bf16 19.5 us (3.1 TB/s), fp16 16 us; 8 x 16384 x 8192 with zero points bf16
+// 26.5 us, fp32 33 us; 16 rows of 16 experts, 2048 -> 4096, fp16 25 us. (Cold, alone:
+// 13, 25, 23, 35, 41 and 31 us.) No unit is full where q is large: one bf16 row takes
+// 57% of the issue slots and 61% of the ALU pipe, eight fp32 rows 53% and 41% of the
+// tensor pipe, so it is the wait in each warp's chain of loads, masks and products
+// that bounds it, with four warps a scheduler; where many experts share the
+// SMs, also the start and the end of each pass.
 //
 // Arithmetic. The inner sums run on warp matrix instructions (16 rows of q x
 // 16 k x 8 rows of x, fp32 sums) with the rows of x as the narrow side; eight
@@ -42,11 +45,11 @@
 // Work. One block per SM goes through units of R = 16 .. 128 rows of q times
 // all of k. A producer warp streams q into a ring in shared memory by TMA
 // (two to four stages of 32 KB, boxes of 128 bytes x R rows in the 128-byte
-// swizzle); 16 warps each take two steps of a stage, 16 rows
-// x 128 k each, side by side, and add up their shares of k at the end of a unit.
-// x is laid out either by every block for itself, once, and stays in shared
-// memory, or, where it is too large for that, by a small kernel before this one,
-// and is streamed with q. The swizzle lets a quad's lanes read 64 contiguous bytes of
+// swizzle); 16 warps each take two steps of a stage, 16 rows x 128 k each, side by
+// side (one after the other where x has several sets of columns), and add up
+// their shares of k at the end of a unit. x is laid out either by every block for
+// itself, once, and stays in shared memory, or, where it is too large for that, by
+// a small kernel before this one, and is streamed with q. The swizzle lets a quad's lanes read 64 contiguous bytes of
 // a row without bank conflicts if the rows of a quarter warp are four (groups
 // of 128) or two apart, so row g of a matrix instruction is row_of(g) of a tile.
 #include <cuda.h>

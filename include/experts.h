@@ -24,6 +24,11 @@
  * Numbers. Rows are fp32, bf16 or fp16. Sums are held in fp32 and rounded
  * once to the row type; the order of every sum is fixed by the sizes, so the
  * same call gives the same bits. No atomics touch results.
+ *
+ * Streams and graphs. Calls may be captured in a CUDA graph once a call of the
+ * same kind has run on the device (the first sets kernels and the scratch pool
+ * up). A kernel may become resident while the one before it in the stream ends;
+ * it reads nothing before that one's end.
  */
 #ifndef SGEMM_GB300_EXPERTS_H
 #define SGEMM_GB300_EXPERTS_H
@@ -150,7 +155,10 @@ int sgemm_experts_gemm_wgrad(int type, int64_t rows, int64_t M, int64_t N, int64
  *              1). A row whose id is below 0 or not below experts is zero.
  *   y, ldy     out, rows x N, of x's type.
  * Meant for few rows: the matrices are read once per eight rows that share
- * one.
+ * one. q - zero is exact, so an x whose q is the zero point adds nothing, however
+ * large it is. The inner sums are scaled group by group; where one overflows
+ * and x is finite the output is summed again in 64 bits (K a multiple of 32 and q
+ * 16-byte aligned; otherwise every term is scaled first, and sums are fp32).
  */
 int sgemm_w4_matvec(int type, int64_t rows, int64_t N, int64_t K, int64_t group, int64_t experts,
                     const int32_t *ids, const void *x, int64_t ldx, const uint8_t *q, const void *scales,
