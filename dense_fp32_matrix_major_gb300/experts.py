@@ -76,12 +76,15 @@ def _stream_handle(stream, *tensors):
 
     Warns where PyTorch would expect a gradient to flow through the call."""
     device = torch.cuda.current_device()
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    lost = False
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != device:
+                raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{device}")
+            lost |= t.requires_grad
+    if lost and torch.is_grad_enabled():
         warnings.warn("an input requires a gradient, but these calls record none: the result is cut from the graph "
                       "(call them inside torch.autograd.Function or torch.no_grad())", stacklevel=3)
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{device}")
     if stream is None:
         return _current_stream(device)
     if stream.device_index != device:

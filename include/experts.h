@@ -113,9 +113,9 @@ int sgemm_experts_combine_grad(int type, int64_t tokens, int64_t top_k, int64_t 
  * bound and its rules for infinities and NaN, and the variant that
  * sgemm_set_variant chose: SGEMM_AUTO and SGEMM_TF32X3 the three-term TF32
  * split (two 11-bit parts of each factor, the product of the low parts left
- * out), whose error on normal inputs is 0.7e-6 of the result's norm where that of
- * fp32 sums is 0.3e-6 to 0.6e-6; SGEMM_FFMA fp32 multiply-adds, one after the
- * other, about eight times slower. bf16 and fp16 products are exact in fp32 and
+ * out), whose error on normal inputs is up to 0.7e-6 of the result's norm where
+ * that of fp32 sums is 0.1e-6 (of a few dozen terms) to 0.6e-6 (of a thousand);
+ * SGEMM_FFMA fp32 multiply-adds, one after the other, about eight times slower. bf16 and fp16 products are exact in fp32 and
  * summed in fp32, where the tensor core cuts a running sum at every 16 products:
  * about 2e-8 of it each time, 2e-5 for sums of 16384, far below the rounding of the
  * result. A row's result depends on that row and its expert's matrix only,

@@ -67,7 +67,8 @@ def step(ex, ids, x, w, b, q, scales):
     dx = ex.gather_grad(dxs, r)
     few = ex.w4_matvec(x[:5], q, scales, group=128)
     odd = ex.gemm(xs[:, 1:], b[:, 1:], r.offsets)
-    return r.order, xs, h, y, dh, dw, db, dx, few, odd
+    sliced = ex.gemm_wgrad(xs[:, :64], dh, r.offsets)
+    return r.order, xs, h, y, dh, dw, db, dx, few, odd, sliced
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
