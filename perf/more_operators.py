@@ -283,11 +283,14 @@ def _quantized(x, block, to, pow2):
     R, C = x.shape[-2:]
     b = _cut(x.float(), high, wide)
     finite = torch.isfinite(b)
-    scale = (torch.where(finite, b.abs(), 0.0).amax((-3, -1)) / LARGEST[to]).clamp(min=TINY)
+    # A divisor on the device: PyTorch multiplies by the reciprocal of a plain number.
+    largest = torch.full((1,), LARGEST[to], device=x.device)
+    scale = (torch.where(finite, b.abs(), 0.0).amax((-3, -1)) / largest).clamp(min=TINY)
     if pow2:
         mantissa, e = torch.frexp(scale)
         scale = torch.ldexp(torch.ones_like(scale), torch.where(mantissa == 0.5, e - 1, e))
-    y = torch.where(finite, b, float("nan")).double() / scale.double()[..., :, None, :, None]
+    # As defined: the product with the scale's reciprocal, both in fp32, then the nearest 8-bit value.
+    y = (torch.where(finite, b, float("nan")) * torch.reciprocal(scale)[..., :, None, :, None]).double()
     y = y.reshape(*x.shape[:-2], -(-R // high) * high, -(-C // wide) * wide)[..., :R, :C]
     q = torch.where(torch.isnan(y), float("nan"), _nearest(torch.nan_to_num(y), to).float()).to(FP8[to])
     return q, (scale.transpose(-1, -2) if block == "rows" else scale).contiguous()
@@ -394,11 +397,11 @@ def work(case):
 
 
 def _exact_codes(x, scale, to):
-    """The nearest 8-bit values by a search among all of them, ties to the even code."""
+    """The 8-bit values nearest to fp32(x * fp32(1 / scale)) by a search among all of them, ties to the even code."""
     codes = torch.arange(127 if to == "e4m3" else 124, dtype=torch.uint8, device=x.device)
     values = codes.view(FP8[to]).double()
     borders = (values[1:] + values[:-1]) / 2
-    y = (x.double() / scale.double()).abs()
+    y = (x.double() * (1 / scale.double()).float().double()).float().double().abs()
     at = torch.bucketize(y, borders)
     tie = (at < borders.numel()) & (y == borders[at.clamp(max=borders.numel() - 1)]) & (at % 2 == 1)
     return torch.copysign(values[at + tie], x.double())
