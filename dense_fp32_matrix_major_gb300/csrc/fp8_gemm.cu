@@ -9,20 +9,22 @@
 // takes it out, scales it and adds it, in fp32 and in the blocks' order, to a
 // running sum in registers, which is rounded once, when C is written.
 //
-// Two CTAs on two SMs of a cluster make a tile of 256 columns of C by up to 256
-// rows. The MMA's first operand gives C's columns (op(B), 128 of them staged by
-// each CTA) and its second C's rows (A), whose number, the MMA's width, costs
-// time in steps of 32: a group of 40 rows is charged 64. A group's rows are
-// spread evenly over its tiles. Two buffers of 256 columns fill tensor memory:
-// the epilogue empties one while the tensor core fills the other.
+// Two CTAs on two SMs of a cluster make a tile of 256 rows by up to 256 columns
+// of C. The MMA's first operand gives C's rows (A, 128 of them staged by each
+// CTA: the lanes of tensor memory), its second C's columns (B, half of them
+// staged by each CTA). Two buffers of 256 columns fill tensor memory: the
+// epilogue empties one while the tensor core fills the other.
 //
-// Scales. The lanes of tensor memory are C's columns, so in rows a CTA's 128
-// lanes share B's scale and the product of the two scales depends on C's row
-// only, an accumulator column. Loads of 16 lanes x 8 columns (16x256b) leave
-// each thread four lanes and a quarter of the columns, so it needs a quarter of
-// the scales. Warp 2 multiplies them ahead of time and lays them out in a ring in
-// the order the threads read them. wgrad's second factor, C's column, is a factor
-// for each of the thread's four lanes.
+// What bounds it. A k-block's MMAs take 512 cycles, in which shared memory takes
+// in 32 KB from TMA and gives 32 KB to the MMA, all it can. So nothing else may
+// go through shared memory while blocks are summed: in rows a lane needs one
+// factor a block, its row's scale times the scale of the 128 columns that the warp
+// sums, and gets it from global memory two blocks ahead. (With C's columns as
+// the lanes, which charges short groups less, every thread needs a factor for
+// each of its 32 columns: 319 us for 16384 x 4096 x 4096.) In wgrad both factors
+// vary; the columns' come through a ring in shared memory that warp 2 fills, in
+// the order in which the threads read them, and loads of 16 lanes x 4 columns
+// (16x128b) leave a thread a quarter of the columns.
 //
 // Layouts. An operand whose summed direction is contiguous in memory is staged
 // K-major, otherwise MN-major, both in 128-byte swizzled rows as TMA writes
@@ -31,14 +33,16 @@
 // Groups. The bounds are read on the device. Tiles never cross groups; the
 // workers (one CTA pair each) take the tiles of the groups in order, round
 // robin, each role of a worker walking the bounds for itself. Rows staged past a
-// tile's end belong to the next and change only sums that are not written. In
-// wgrad every group's rows start in a block of their own and end in zeros.
+// tile's end belong to the next and change only sums that are not written; a CTA
+// whose rows all lie past it stages none. In wgrad every group's rows start in a
+// block of their own and end in zeros.
 //
 // Roles in each CTA (12 warps): warp 0 loads the first operand and warp 3 the
-// second (TMA), warp 1 of the even CTA issues the MMAs, warp 2 prepares scales,
-// warps 4 to 11 sum and write C (two per quarter of tensor memory's lanes). They
-// hold 128 sums a thread and take registers that the first four give up. The
-// loads of both CTAs complete on the even CTA's barriers. Every wait is bounded.
+// second (TMA), warp 1 of the even CTA issues the MMAs, warp 2 prepares wgrad's
+// scales, warps 4 to 11 sum and write C (two per quarter of tensor memory's
+// lanes, half of the columns each). They hold 128 sums a thread and take
+// registers that the first four give up. The loads of both CTAs complete on the
+// even CTA's barriers. Every wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -58,14 +62,16 @@ using namespace tc;
 
 constexpr int PN = 256, PM = 256, HALF = 128;  // C's columns and rows of a pair, a CTA's share
 constexpr int KB = BLOCK;                      // k-block: 128 values = 128 bytes
-constexpr int ROW_STEP = 32;                   // a tile's rows are charged in multiples of it
+constexpr int COL_STEP = 32;                   // the MMA's width is a multiple of it
+constexpr int FEW = 32;                        // rows of the small box of A
 constexpr int BOX = 128 * 128;                 // bytes of a staged operand
 constexpr int STAGE = 2 * BOX, STAGES = 6;
 constexpr int EPI_WARPS = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI_WARPS) * 32;
-constexpr int RING = 8;                        // k-blocks of prepared scales
-constexpr int RING_BYTES = (PM + HALF) * 4;    // of C's rows, and of the CTA's columns (wgrad)
-constexpr int OUT_ROW = 144;                   // bytes between rows of a warp's 8 x 32 values of C on their way out
-constexpr int OUT_BYTES = 8 * OUT_ROW;
+constexpr int RING = 8;                        // k-blocks of wgrad's prepared scales
+constexpr int RING_BYTES = PN * 4;
+// A warp's part of C on its way out: rows of 64 bytes (rows), 8 rows of 32 fp32
+// values (wgrad), both padded so that every phase of the accesses meets all banks.
+constexpr int OUT_ROW = 80, OUT_WGRAD = 144, OUT_BYTES = 32 * OUT_ROW;
 constexpr int RING0 = STAGES * STAGE, OUT0 = RING0 + RING * RING_BYTES, BAR0 = OUT0 + EPI_WARPS * OUT_BYTES;
 // mbarriers
 constexpr int FULL = 0, EMPTY = FULL + STAGES, SUM_FULL = EMPTY + STAGES, SUM_EMPTY = SUM_FULL + 2,
@@ -73,9 +79,10 @@ constexpr int FULL = 0, EMPTY = FULL + STAGES, SUM_FULL = EMPTY + STAGES, SUM_EM
 constexpr int SMEM_BYTES = BAR0 + 512 + 1024;
 static_assert(NBARS * 8 + 16 <= 512, "barrier block");
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(8 * OUT_WGRAD <= OUT_BYTES, "staging of C");
 static_assert(RING0 % 1024 == 0 && RING_BYTES % 16 == 0 && OUT0 % 16 == 0 && BAR0 % 8 == 0, "alignment");
 // Registers a thread of the four and of the eight warps, out of 168 each.
-constexpr int FEW_REGS = 80, MANY_REGS = 208;
+constexpr int FEW_REGS = 88, MANY_REGS = 208;
 static_assert(4 * FEW_REGS + 8 * MANY_REGS <= 12 * 168, "registers of the launch");
 
 enum Form { ROWS_N, ROWS_T, WGRAD };
@@ -135,16 +142,22 @@ __device__ __forceinline__ void for_each_tile(const Args &a, volatile int *abort
             const int b0 = min(first, a.blocks), b1 = min(first + (end - begin + KB - 1) / KB, a.blocks);
             f(Tile{e, row0, static_cast<int>(min(static_cast<int64_t>(row0 + PM), a.M)), n0, b0, b1 - b0});
         } else {
-            const int each = ((end - begin + tiles - 1) / tiles + ROW_STEP - 1) / ROW_STEP * ROW_STEP;
-            const int row0 = min(begin + (rt - base) * each, end);
-            f(Tile{e, row0, min(row0 + each, end), n0, 0, e < a.experts && row0 < end ? a.k_blocks : 0});
+            const int row0 = begin + (rt - base) * PM;
+            f(Tile{e, row0, min(row0 + PM, end), n0, 0, e < a.experts ? a.k_blocks : 0});
         }
     }
 }
 
-// The MMA's width: the tile's rows, rounded up.
-__device__ __forceinline__ int width_of(const Tile &u) {
-    return (u.row_end - u.row0 + ROW_STEP - 1) / ROW_STEP * ROW_STEP;
+// The MMA's width: the tile's columns, rounded up.
+__device__ __forceinline__ int width_of(const Args &a, const Tile &u) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(PN), a.N - u.n0));
+    return (n + COL_STEP - 1) / COL_STEP * COL_STEP;
+}
+
+// Rows of A that CTA `rank` stages in a k-block: as many as a box has, or none.
+__device__ __forceinline__ int box_rows(const Tile &u, uint32_t rank) {
+    const int n = u.row_end - u.row0 - HALF * static_cast<int>(rank);
+    return n <= 0 ? 0 : (n <= FEW ? FEW : HALF);
 }
 
 // TMA load into this CTA's shared memory that completes its bytes on the
@@ -175,19 +188,38 @@ __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// 16 lanes x 16 columns of 32 bits from tensor memory: r[4 g + 2 h + i] is lane
-// (thread / 4) + 8 h, column 8 g + 2 (thread % 4) + i. Not waited for.
-__device__ __forceinline__ void tmem_load_16x16(uint32_t taddr, uint32_t *r) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
+// 16 lanes x 32 columns of 32 bits from tensor memory: r[2 i + h] is lane
+// (thread / 4) + 8 h, column 4 i + thread % 4. Not waited for.
+__device__ __forceinline__ void tmem_load_16x32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// 32 lanes x 32 columns: r[i] is this lane's column i. Not waited for.
+__device__ __forceinline__ void tmem_load_32x32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 }
 
 // Waits for the thread's loads from tensor memory; ties the registers to it.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
 }
@@ -213,8 +245,14 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
     return r;
 }
 
-__device__ __forceinline__ void lds_2x64(uint32_t at, uint64_t &x, uint64_t &y) {
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at) : "memory");
+// Arrives on the mbarrier at this offset in the even CTA. Relaxed: what went
+// before is reads of tensor memory, complete when their wait returned. (With
+// release semantics at cluster scope 578 us in place of 354 for 16384 x 4096 x
+// 4096: the arrival waits out the thread's memory operations.)
+__device__ __forceinline__ void arrive_even(uint32_t bar) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(0));
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds_128(uint32_t at) {
@@ -223,17 +261,7 @@ __device__ __forceinline__ uint4 lds_128(uint32_t at) {
     return v;
 }
 
-// Four 8 x 8 blocks of 16-bit values stored transposed; lane 8 i + r gives the
-// address of row r of block i.
-__device__ __forceinline__ void stmatrix4_trans(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b),
-                 "r"(c), "r"(d)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t round2(uint64_t v, bool bf16) {
-    float lo, hi;
-    unpack2(v, lo, hi);
+__device__ __forceinline__ uint32_t round2(float lo, float hi, bool bf16) {
     if (bf16) {
         const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&r);
@@ -242,64 +270,48 @@ __device__ __forceinline__ uint32_t round2(uint64_t v, bool bf16) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Eight rows of C by a warp's 32 columns, v[h] the sums of lanes (columns) 8 h ..
-// 8 h + 7, through shared memory: rows of 64 or 128 bytes, 16 bytes a store.
-__device__ __forceinline__ void write_rows(const Args &a, uint32_t out, int lane, const uint64_t (&v)[4], void *c_item,
-                                           int64_t row, int rows, int64_t col) {
-    const int t = lane & 3, g = lane >> 2;
-    __syncwarp();  // what the buffer held is read
-    if (a.out_type == SGEMM_TYPE_F32) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            float lo, hi;
-            unpack2(v[h], lo, hi);
-            const uint32_t at = out + static_cast<uint32_t>(2 * t * OUT_ROW + (8 * h + g) * 4);
-            st_shared_f32(at, lo);
-            st_shared_f32(at + OUT_ROW, hi);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7);
-            const uint4 x = lds_128(out + static_cast<uint32_t>(r * OUT_ROW + c * 4));
-            float *p = static_cast<float *>(c_item) + (row + r) * a.ldc + col + c;
-            if (r >= rows) continue;
-            if (a.vector && col + c + 4 <= a.N) {
-                *reinterpret_cast<uint4 *>(p) = x;
-            } else {
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (col + c + j < a.N) p[j] = __uint_as_float(w[j]);
-            }
-        }
+__device__ __forceinline__ void sts_128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 16 bytes of a row of C at p, the first of its PER values being column col.
+template <class T, int PER>
+__device__ __forceinline__ void store16(const Args &a, T *p, int64_t col, const uint4 &x) {
+    if (a.vector && col + PER <= a.N) {
+        *reinterpret_cast<uint4 *>(p) = x;
     } else {
-        const bool bf16 = a.out_type == SGEMM_TYPE_BF16;
-        constexpr int ROW16 = 80;  // bytes: every phase of the stores and loads meets all banks
-        stmatrix4_trans(out + static_cast<uint32_t>((lane & 7) * ROW16 + (lane >> 3) * 16), round2(v[0], bf16),
-                        round2(v[1], bf16), round2(v[2], bf16), round2(v[3], bf16));
-        __syncwarp();
-        const int c = 8 * t;
-        const uint4 x = lds_128(out + static_cast<uint32_t>(g * ROW16 + c * 2));
-        uint16_t *p = static_cast<uint16_t *>(c_item) + (row + g) * a.ldc + col + c;
-        if (g < rows) {
-            if (a.vector && col + c + 8 <= a.N) {
-                *reinterpret_cast<uint4 *>(p) = x;
-            } else {
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + c + j < a.N) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-            }
-        }
+        for (int j = 0; j < PER; ++j)
+            if (col + j < a.N) p[j] = static_cast<T>(PER == 4 ? w[j] : w[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// Rows of 64 bytes of C, this lane's first: staged in shared memory and written
+// eight rows at a time.
+template <class T>
+__device__ __forceinline__ void write_lanes(const Args &a, uint32_t out, int lane, const uint32_t (&v)[16], T *c,
+                                            int64_t row, int rows, int64_t col) {
+    constexpr int PER = 16 / sizeof(T);
+    __syncwarp();  // what the buffer held is read
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts_128(out + static_cast<uint32_t>(lane * OUT_ROW + 16 * j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const int64_t at = col + PER * (lane & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + (lane >> 2);
+        const uint4 x = lds_128(out + static_cast<uint32_t>(r * OUT_ROW + 16 * (lane & 3)));
+        if (r < rows) store16<T, PER>(a, c + (row + r) * a.ldc + at, at, x);
     }
 }
 
 template <Form FORM>
 __global__ void __launch_bounds__(THREADS, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
-                    const __grid_constant__ CUtensorMap tm2_small, const __grid_constant__ Args a) {
-    // tm1, tm2: the operands of C's columns and rows; tm2_small: the second in boxes of 32 rows (rows).
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm1_few,
+                    const __grid_constant__ CUtensorMap tm2, const __grid_constant__ Args a) {
+    // tm1, tm2: A and B; tm1_few: A in boxes of 32 rows (rows).
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -358,15 +370,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t it = 0;
                 bool ok = true;
                 for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
-                    const int half = width_of(u) / 2;
-                    const int n0 = u.n0 + HALF * static_cast<int>(rank);
-                    const int r0 = u.row0 + half * static_cast<int>(rank);
-                    // One box of 128 rows, or of 32 where those are enough.
-                    const bool small = FORM != WGRAD && half <= 32;
-                    const uint32_t bytes = BOX + (small ? 32 * 128 : BOX);
+                    const int n0 = u.n0 + width_of(a, u) / 2 * static_cast<int>(rank);
+                    const int r0 = u.row0 + HALF * static_cast<int>(rank);
+                    const int own = FORM == WGRAD ? HALF : box_rows(u, rank);
+                    const uint32_t bytes =
+                        2 * BOX + (FORM == WGRAD ? 2 * BOX : 128 * (box_rows(u, 0) + box_rows(u, 1)));
                     for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                         const int s = static_cast<int>(it % STAGES);
-                        if (!mbar_wait<true>(bar(EMPTY + s), ((it / STAGES) & 1) ^ 1, a, abort_flag, WD_PRODUCER)) {
+                        if (!mbar_wait(bar(EMPTY + s), ((it / STAGES) & 1) ^ 1, a, abort_flag, WD_PRODUCER)) {
                             ok = false;
                             return;
                         }
@@ -374,17 +385,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint32_t to = map_to_cta(bar(FULL + s), 0);
                         const int k = (u.k0 + kb) * KB;
                         if (first) {
-                            if (rank == 0) mbar_arrive_expect_tx(bar(FULL + s), 2 * bytes);
+                            if (rank == 0) mbar_arrive_expect_tx(bar(FULL + s), bytes);
                             if (FORM == WGRAD)
-                                tma_load_pair(s1, &tm1, n0, k, 0, to);
-                            else if (FORM == ROWS_T)
-                                tma_load_pair(s1, &tm1, k, n0, u.group, to);
-                            else
-                                tma_load_pair(s1, &tm1, n0, k, u.group, to);
+                                tma_load_pair(s1, &tm1, r0, k, 0, to);
+                            else if (own > 0)
+                                tma_load_pair(s1, own == FEW ? &tm1_few : &tm1, k, r0, 0, to);
                         } else if (FORM == WGRAD) {
-                            tma_load_pair(s2, &tm2, r0, k, 0, to);
+                            tma_load_pair(s2, &tm2, n0, k, 0, to);
+                        } else if (FORM == ROWS_T) {
+                            tma_load_pair(s2, &tm2, k, n0, u.group, to);
                         } else {
-                            tma_load_pair(s2, small ? &tm2_small : &tm2, k, r0, 0, to);
+                            tma_load_pair(s2, &tm2, n0, k, u.group, to);
                         }
                     }
                 });
@@ -396,31 +407,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t it = 0;
                 bool ok = true;
                 for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
-                    const uint32_t idesc = a.idesc | (static_cast<uint32_t>(width_of(u) >> 3) << 17);
+                    const uint32_t idesc = a.idesc | (static_cast<uint32_t>(width_of(a, u) >> 3) << 17);
+                    // 32 values of k further: 32 bytes along a K-major row, 32 rows of 128
+                    // bytes in an MN-major box.
+                    constexpr uint32_t step1 = (FORM == WGRAD ? 32 * 128 : 32) >> 4;
+                    constexpr uint32_t step2 = (FORM == ROWS_T ? 32 : 32 * 128) >> 4;
                     for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                         const int s = static_cast<int>(it % STAGES);
                         const uint32_t d = it & 1;
-                        ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(SUM_EMPTY + d), ((it >> 1) & 1) ^ 1, a,
-                                                                     abort_flag, WD_MMA_ACC));
-                        if (!ok) return;
-                        ok = __all_sync(0xffffffffu, mbar_wait<true>(bar(FULL + s), (it / STAGES) & 1, a, abort_flag,
-                                                                     WD_MMA_FULL));
-                        if (!ok) return;
-                        tc_fence_after();
                         const uint32_t s1 = base + static_cast<uint32_t>(s * STAGE), s2 = s1 + BOX;
                         // The descriptors of both layouts are alike: 8 rows (K-major) or 8
                         // k (MN-major, 128 values each) to the next 8 are 1024 bytes.
                         const uint64_t d1 = sw128_desc(s1), d2 = sw128_desc(s2);
-                        // 32 values of k further: 32 bytes along a K-major row, 32 rows of
-                        // 128 bytes in an MN-major box.
-                        constexpr uint64_t step1 = (FORM == ROWS_T ? 32 : 32 * 128) >> 4;
-                        constexpr uint64_t step2 = (FORM == WGRAD ? 32 * 128 : 32) >> 4;
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait(bar(FULL + s), (it / STAGES) & 1, a, abort_flag, WD_MMA_FULL));
+                        if (!ok) return;
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(SUM_EMPTY + d), ((it >> 1) & 1) ^ 1, a, abort_flag,
+                                                               WD_MMA_ACC));
+                        if (!ok) return;
+                        tc_fence_after();
                         if (leader) {
 #pragma unroll
                             for (int ks = 0; ks < KB / 32; ++ks)
-                                mma8_pair(tmem_base + d * PM, d1 + ks * step1, d2 + ks * step2, idesc, ks > 0);
-                            tc_commit2(bar(EMPTY + s));
+                                mma8_pair(tmem_base + d * PN, d1 + ks * step1, d2 + ks * step2, idesc, ks > 0);
                             tc_commit2(bar(SUM_FULL + d));
+                            tc_commit2(bar(EMPTY + s));
                         }
                         __syncwarp();
                     }
@@ -429,44 +440,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     const bool was_aborted = *abort_flag != 0;
-                    if (!mbar_wait<true>(bar(DRAIN), 0, a, abort_flag, WD_DRAIN) && was_aborted) {
+                    if (!mbar_wait(bar(DRAIN), 0, a, abort_flag, WD_DRAIN) && was_aborted) {
                         const uint64_t t0 = global_timer();
-                        while (!mbar_try_wait<true>(bar(DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
+                        while (!mbar_try_wait(bar(DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
                         }
                     }
                 }
             }
-        } else {
-            // ------------------------------------------------------------- scales
+        } else if (FORM == WGRAD) {
+            // ------------------------------------------------- scales of C's columns
             // Of several k-blocks at once, so that their latency is met once.
-            constexpr int AHEAD = FORM == WGRAD ? 2 : 4;
+            constexpr int AHEAD = 4;
             uint32_t it = 0;
             bool ok = true;
             for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
-                const int rows = u.row_end - u.row0;
-                const int64_t n0 = u.n0 + HALF * static_cast<int64_t>(rank);
-                const float *sr = a.scale_rows + static_cast<int64_t>(u.k0) * a.ld_rows + u.row0;
-                const float *sc = a.scale_cols + (FORM == WGRAD ? static_cast<int64_t>(u.k0) * a.b_cols + n0
-                                                                : u.group * a.item_cols + n0 / BLOCK * a.n_cols);
-                const bool in_cols = n0 < a.N;
+                const float *from = a.scale_cols + static_cast<int64_t>(u.k0) * a.b_cols + u.n0 + lane;
+                const int cols = static_cast<int>(min(static_cast<int64_t>(PN), a.N - u.n0)) - lane;
+                // Column 16 c + 4 i + t goes where thread t of a quad reads its four of c.
+                const int at = (lane & ~15) + ((lane & 3) << 2) + ((lane >> 2) & 3);
                 for (int kb = 0; kb < u.k_blocks && ok; kb += AHEAD) {
-                    float r[AHEAD][PM / 32], c[AHEAD][FORM == WGRAD ? HALF / 32 : 1];
+                    float v[AHEAD][PN / 32];
 #pragma unroll
-                    for (int i = 0; i < AHEAD; ++i) {
-                        const bool in = kb + i < u.k_blocks;
+                    for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-                        for (int j = 0; j < PM / 32; ++j)
-                            r[i][j] = in && lane + 32 * j < rows ? __ldg(sr + (kb + i) * a.ld_rows + lane + 32 * j) : 0.0f;
-                        if (FORM == WGRAD) {
-#pragma unroll
-                            for (int j = 0; j < HALF / 32; ++j)
-                                c[i][j] = in && n0 + lane + 32 * j < a.N
-                                              ? __ldg(sc + (kb + i) * a.b_cols + lane + 32 * j)
-                                              : 0.0f;
-                        } else {
-                            c[i][0] = in && in_cols ? __ldg(sc + (kb + i) * a.b_cols) : 0.0f;
-                        }
-                    }
+                        for (int j = 0; j < PN / 32; ++j)
+                            v[i][j] = kb + i < u.k_blocks && 32 * j < cols ? __ldg(from + (kb + i) * a.b_cols + 32 * j) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
                         if (kb + i >= u.k_blocks || !ok) break;
@@ -474,21 +472,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(RING_EMPTY + s), ((it / RING) & 1) ^ 1, a,
                                                                abort_flag, WD_PRODUCER));
                         if (!ok) break;
-                        const uint32_t to = base + RING0 + static_cast<uint32_t>(s * RING_BYTES);
-                        // Row 16 c + 8 g + 2 t + i goes where thread t of a quad reads the
-                        // four of c that it needs at once.
+                        const uint32_t to = base + RING0 + static_cast<uint32_t>(s * RING_BYTES + at * 4);
 #pragma unroll
-                        for (int j = 0; j < PM / 32; ++j) {
-                            const int row = lane + 32 * j;
-                            const int at = (row & ~15) + ((row & 6) << 1) + ((row & 8) >> 2) + (row & 1);
-                            st_shared_f32(to + static_cast<uint32_t>(at * 4),
-                                          FORM == WGRAD ? r[i][j] : r[i][j] * c[i][0]);
-                        }
-                        if (FORM == WGRAD) {
-#pragma unroll
-                            for (int j = 0; j < HALF / 32; ++j)
-                                st_shared_f32(to + static_cast<uint32_t>((PM + lane + 32 * j) * 4), c[i][j]);
-                        }
+                        for (int j = 0; j < PN / 32; ++j) st_shared_f32(to + 128 * j, v[i][j]);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(RING_FULL + s));
                         ++it;
@@ -503,79 +489,173 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = w & 3, second = w >> 2;  // quarter of tensor memory's lanes, half of the columns
         const int t = lane & 3, g = lane >> 2;
         const uint32_t out = base + OUT0 + static_cast<uint32_t>(w * OUT_BYTES);
-        const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+        const uint32_t sums = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(HALF * second);
         uint32_t it = 0;
         bool ok = true;
+        // The accumulator is out of tensor memory (this warp's part).
+        auto release = [&](uint32_t d) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_even(bar(SUM_EMPTY + d));
+        };
         for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
             if (!ok) return;
-            const int chunks = width_of(u) / 32, col0 = chunks * 16 * second;  // 16 columns each, of this half
-            // acc[c][4 i + 2 g + h]: columns 16 c + 8 g + 2 t and the next, lane 16 i + 8 h + (thread / 4).
-            uint64_t acc[8][8];
+            const int row0 = u.row0 + HALF * static_cast<int>(rank) + 32 * q;
+            const int64_t col0 = u.n0 + HALF * static_cast<int64_t>(second);
+            const int rows = u.row_end - row0;                                                      // may be negative
+            const int cols = static_cast<int>(min(static_cast<int64_t>(HALF), a.N - col0));         // likewise
+            const int chunks = cols > 0 ? (cols + 31) / 32 : 0;
+            if constexpr (FORM != WGRAD) {
+                // acc[c][i]: column 32 c + i of this lane's row.
+                float acc[4][32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[c][i] = 0;
-            for (int kb = 0; kb < u.k_blocks; ++kb, ++it) {
-                const uint32_t d = it & 1;
-                const int s = static_cast<int>(it % RING);
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(RING_FULL + s), (it / RING) & 1, a, abort_flag, WD_EPILOGUE));
-                if (!ok) return;
-                const uint32_t ring = base + RING0 + static_cast<uint32_t>(s * RING_BYTES);
-                uint64_t of_lane[4];
-                if (FORM == WGRAD) {
+                    for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+                // Factors two blocks ahead.
+                const float *sr = a.scale_rows + row0 + lane;
+                const float *sc = a.scale_cols + u.group * a.item_cols + col0 / BLOCK * a.n_cols;
+                const bool in = lane < rows && cols > 0;
+                auto factors = [&](int kb, float &x, float &y) {
+                    const bool there = in && kb < u.k_blocks;
+                    x = there ? __ldg(sr + kb * a.ld_rows) : 0.0f;
+                    y = there ? __ldg(sc + kb * a.b_cols) : 0.0f;
+                };
+                float x0, y0, x1, y1;
+                factors(0, x0, y0);
+                factors(1, x1, y1);
+                for (int kb = 0; kb < u.k_blocks; ++kb, ++it) {
+                    const uint32_t d = it & 1;
+                    const float factor = x0 * y0;
+                    x0 = x1;
+                    y0 = y1;
+                    factors(kb + 2, x1, y1);
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(bar(SUM_FULL + d), (it >> 1) & 1, a, abort_flag, WD_EPILOGUE));
+                    if (!ok) return;
+                    tc_fence_after();
+                    // A warp without rows or columns only lets go.
+                    if (rows <= 0 || chunks == 0) release(d);
+                    else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t v = __float_as_uint(
-                            ld_shared_f32(ring + static_cast<uint32_t>((PM + 32 * q + 8 * i + g) * 4)));
-                        of_lane[i] = pack2(v, v);
-                    }
-                }
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait<true>(bar(SUM_FULL + d), (it >> 1) & 1, a, abort_flag, WD_EPILOGUE));
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t from = lanes + d * PM + static_cast<uint32_t>(col0);
+                        for (int c = 0; c < 4; ++c) {
+                            if (c >= chunks) break;
+                            uint32_t p[32];
+                            tmem_load_32x32(sums + d * PN + 32 * c, p);
+                            tmem_wait(p);
+                            if (c == chunks - 1) release(d);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if (c >= chunks) break;
-                    uint32_t p[16];
-                    tmem_load_16x16(from + 16 * c, p);
-                    tmem_load_16x16(from + 16 * c + (16u << 16), p + 8);
-                    uint64_t x0, x1;
-                    lds_2x64(ring + static_cast<uint32_t>((col0 + 16 * c + 4 * t) * 4), x0, x1);
-                    tmem_wait(p);
-                    if (c == chunks - 1) {
-                        // The accumulator is out of tensor memory, the scales are read.
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive_at(bar(SUM_EMPTY + d), 0);
-                            mbar_arrive(bar(RING_EMPTY + s));
+                            for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(p[i]), factor, acc[c][i]);
                         }
                     }
+                }
+                if (rows <= 0) return;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint64_t v = pack2(p[2 * i], p[2 * i + 1]);
-                        if (FORM == WGRAD) v = mul2(v, of_lane[2 * (i >> 2) + (i & 1)]);
-                        fma2(acc[c][i], v, (i & 2) ? x1 : x0);
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= chunks) break;
+                    const int64_t col = col0 + 32 * c;
+                    uint32_t v[16];
+                    if (a.out_type == SGEMM_TYPE_F32) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[c][16 * h + i]);
+                            write_lanes(a, out, lane, v, static_cast<uint32_t *>(a.C), row0, rows, col + 16 * h);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] = round2(acc[c][2 * i], acc[c][2 * i + 1], a.out_type == SGEMM_TYPE_BF16);
+                        write_lanes(a, out, lane, v, static_cast<uint16_t *>(a.C), row0, rows, col);
                     }
                 }
-            }
-            const int64_t col = u.n0 + HALF * static_cast<int64_t>(rank) + 32 * q;
-            const int rows = u.row_end - u.row0 - col0;
-            const int64_t item = FORM == WGRAD ? u.group * a.strideC : 0;
-            void *c_item = a.out_type == SGEMM_TYPE_F32 ? static_cast<void *>(static_cast<float *>(a.C) + item)
-                                                        : static_cast<void *>(static_cast<uint16_t *>(a.C) + item);
-            if (col >= a.N) return;
+            } else {
+                // wgrad. acc[c][i][h]: column 32 c + 4 i + (thread % 4), lanes 16 h + (thread / 4) and 8 further.
+                uint64_t acc[4][8][2];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (c >= chunks) break;
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint64_t v[4] = {acc[c][2 * h], acc[c][2 * h + 1], acc[c][4 + 2 * h], acc[c][4 + 2 * h + 1]};
-                    const int r = 16 * c + 8 * h;
-                    write_rows(a, out, lane, v, c_item, u.row0 + col0 + r, rows - r, col);
+                    for (int i = 0; i < 8; ++i) acc[c][i][0] = acc[c][i][1] = 0;
+                const float *sr = a.scale_rows + static_cast<int64_t>(u.k0) * a.ld_rows + row0 + g;
+                auto factors = [&](int kb, float (&x)[4]) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        x[h] = kb < u.k_blocks && 8 * h + g < rows ? __ldg(sr + kb * a.ld_rows + 8 * h) : 0.0f;
+                };
+                float next[4];
+                factors(0, next);
+                for (int kb = 0; kb < u.k_blocks; ++kb, ++it) {
+                    const uint32_t d = it & 1;
+                    const int s = static_cast<int>(it % RING);
+                    const uint64_t of_lane[2] = {pack2(__float_as_uint(next[0]), __float_as_uint(next[1])),
+                                                 pack2(__float_as_uint(next[2]), __float_as_uint(next[3]))};
+                    factors(kb + 1, next);
+                    const uint32_t scales =
+                        base + RING0 + static_cast<uint32_t>(s * RING_BYTES + (HALF * second + 4 * t) * 4);
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(bar(RING_FULL + s), (it / RING) & 1, a, abort_flag, WD_EPILOGUE)) &&
+                         __all_sync(0xffffffffu,
+                                    mbar_wait(bar(SUM_FULL + d), (it >> 1) & 1, a, abort_flag, WD_EPILOGUE));
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (rows <= 0 || chunks == 0) release(d);
+                    else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c >= chunks) break;
+                            uint32_t p[32];
+                            tmem_load_16x32(sums + d * PN + 32 * c, p);
+                            tmem_load_16x32(sums + d * PN + 32 * c + (16u << 16), p + 16);
+                            const uint4 s0 = lds_128(scales + 128 * c), s1 = lds_128(scales + 128 * c + 64);
+                            tmem_wait(p);
+                            if (c == chunks - 1) release(d);
+                            const uint32_t x[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint64_t xx = pack2(x[i], x[i]);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    fma2(acc[c][i][h], mul2(pack2(p[16 * h + 2 * i], p[16 * h + 2 * i + 1]), of_lane[h]), xx);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(RING_EMPTY + s));
+                }
+                // Eight rows by 32 columns at a time, as fp32 through shared memory.
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= chunks) break;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float x, y;
+                            unpack2(acc[c][i][h >> 1], x, y);
+                            st_shared_f32(out + static_cast<uint32_t>(g * OUT_WGRAD + (4 * i + t) * 4), h & 1 ? y : x);
+                        }
+                        __syncwarp();
+                        const int64_t item = u.group * a.strideC + static_cast<int64_t>(row0 + 8 * h) * a.ldc;
+                        const int left = rows - 8 * h;
+                        if (a.out_type == SGEMM_TYPE_F32) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int r = 4 * j + (lane >> 3);
+                                const int64_t col = col0 + 32 * c + 4 * (lane & 7);
+                                const uint4 x = lds_128(out + static_cast<uint32_t>(r * OUT_WGRAD + 16 * (lane & 7)));
+                                if (r < left) store16<uint32_t, 4>(a, static_cast<uint32_t *>(a.C) + item + r * a.ldc + col, col, x);
+                            }
+                        } else {
+                            const bool bf16 = a.out_type == SGEMM_TYPE_BF16;
+                            const int64_t col = col0 + 32 * c + 8 * t;
+                            const float4 x = ld_shared_v4(out + static_cast<uint32_t>(g * OUT_WGRAD + 32 * t)),
+                                         y = ld_shared_v4(out + static_cast<uint32_t>(g * OUT_WGRAD + 32 * t + 16));
+                            const uint4 v = make_uint4(round2(x.x, x.y, bf16), round2(x.z, x.w, bf16),
+                                                       round2(y.x, y.y, bf16), round2(y.z, y.w, bf16));
+                            if (g < left) store16<uint16_t, 8>(a, static_cast<uint16_t *>(a.C) + item + g * a.ldc + col, col, v);
+                        }
+                    }
                 }
             }
         });
@@ -592,9 +672,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     if (rank != 0 && threadIdx.x == 0) {
-        if (!mbar_wait<true>(bar(DRAIN), 0, a, abort_flag, WD_DRAIN)) {
+        if (!mbar_wait(bar(DRAIN), 0, a, abort_flag, WD_DRAIN)) {
             const uint64_t t0 = global_timer();
-            while (!mbar_try_wait<true>(bar(DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
+            while (!mbar_try_wait(bar(DRAIN), 0) && global_timer() - t0 < a.timeout_ns) {
             }
         }
     }
@@ -647,7 +727,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     }
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    alignas(64) CUtensorMap map1{}, map2{}, map3{};
+    alignas(64) CUtensorMap map1{}, map2{}, few{};
     Args a{};
     a.offsets = p.offsets;
     a.rows = static_cast<int>(p.rows);
@@ -670,9 +750,9 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
         a.ld_rows = p.M;
         a.b_cols = p.N;
         row_tiles = (p.M + PM - 1) / PM * p.experts;
-        ok = encode_map_typed(&map1, type, 1, p.B, p.rows, p.N, p.ldb, 1, 0, HALF, KB, sw) &&
-             encode_map_typed(&map2, type, 1, p.A, p.rows, p.M, p.lda, 1, 0, HALF, KB, sw);
-        map3 = map2;  // not read by the kernel
+        ok = encode_map_typed(&map1, type, 1, p.A, p.rows, p.M, p.lda, 1, 0, HALF, KB, sw) &&
+             encode_map_typed(&map2, type, 1, p.B, p.rows, p.N, p.ldb, 1, 0, HALF, KB, sw);
+        few = map1;  // not read by the kernel
     } else {
         const int64_t strideB = p.experts > 1 ? p.strideB : 0, kb = blocks_of(p.K), nb = blocks_of(p.N);
         a.k_blocks = static_cast<int>(kb);
@@ -682,10 +762,10 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
         a.b_cols = FORM == ROWS_T ? 1 : nb;
         // Every group may end in a part of a tile, and so may the rest.
         row_tiles = (p.rows + PM - 1) / PM + (p.offsets ? p.experts : 0);
-        ok = (FORM == ROWS_T ? encode_map_typed(&map1, type, 1, p.B, p.N, p.K, p.ldb, p.experts, strideB, KB, HALF, sw)
-                             : encode_map_typed(&map1, type, 1, p.B, p.K, p.N, p.ldb, p.experts, strideB, HALF, KB, sw)) &&
-             encode_map_typed(&map2, type, 1, p.A, p.rows, p.K, p.lda, 1, 0, KB, HALF, sw) &&
-             encode_map_typed(&map3, type, 1, p.A, p.rows, p.K, p.lda, 1, 0, KB, 32, sw);
+        ok = encode_map_typed(&map1, type, 1, p.A, p.rows, p.K, p.lda, 1, 0, KB, HALF, sw) &&
+             encode_map_typed(&few, type, 1, p.A, p.rows, p.K, p.lda, 1, 0, KB, FEW, sw) &&
+             (FORM == ROWS_T ? encode_map_typed(&map2, type, 1, p.B, p.N, p.K, p.ldb, p.experts, strideB, KB, HALF, sw)
+                             : encode_map_typed(&map2, type, 1, p.B, p.K, p.N, p.ldb, p.experts, strideB, HALF, KB, sw));
     }
     if (!ok) return SGEMM_ERR_LAUNCH;
     if (row_tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
@@ -694,15 +774,15 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     // second operand E4M3 (0) or E5M2 (1) in bits 7-9 and 10-12, bit 15 / 16:
     // first / second MN-major, N >> 3 in bits 17-22 (the kernel's), M >> 4 in
     // bits 24-28.
-    const uint32_t t1 = p.type_b == SGEMM_FP8_E5M2, t2 = p.type_a == SGEMM_FP8_E5M2;
-    a.idesc = (1u << 4) | (t1 << 7) | (t2 << 10) | (FORM == ROWS_T ? 0u : 1u << 15) | (FORM == WGRAD ? 1u << 16 : 0u) |
-              (static_cast<uint32_t>(PN >> 4) << 24);
+    const uint32_t t1 = p.type_a == SGEMM_FP8_E5M2, t2 = p.type_b == SGEMM_FP8_E5M2;
+    a.idesc = (1u << 4) | (t1 << 7) | (t2 << 10) | (FORM == WGRAD ? 1u << 15 : 0u) | (FORM == ROWS_T ? 0u : 1u << 16) |
+              (static_cast<uint32_t>(PM >> 4) << 24);
     a.timeout_ns = static_cast<uint64_t>(watchdog_ms()) * 1000000ull;
     a.watchdog = flag;
     const int64_t units = row_tiles * a.tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, map1, map2, map3, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, map1, few, map2, a) != cudaSuccess) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
     }
