@@ -6,6 +6,48 @@
 #include "api_checks.h"
 #include "layer_internal.h"
 
+namespace sgemm {
+namespace fl {
+
+int layer_launch(const LayerProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const int64_t per_x = 16 / ex::type_size(p.type);
+    LArgs a{};
+    a.pairs = static_cast<int>(p.tokens * p.top_k);
+    a.top_k = static_cast<int>(p.top_k);
+    a.experts = static_cast<int>(p.experts);
+    a.tokens = static_cast<int>(p.tokens);
+    a.activation = p.activation;
+    a.gated = p.gated;
+    a.width = static_cast<int>(p.width);
+    a.hidden = static_cast<int>(p.hidden);
+    a.x = p.x;
+    a.ldx = p.ldx;
+    a.x_size = static_cast<int>(ex::type_size(p.type));
+    a.x_type = p.type;
+    a.x_vector = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && (p.tokens == 1 || p.ldx % per_x == 0);
+    a.ids = p.ids;
+    a.id_bits = p.id_bits;
+    a.weights = p.weights;
+    a.w1 = p.w1;
+    a.ld1 = p.ld1;
+    a.stride1 = p.experts > 1 ? p.stride1 : 0;
+    a.s1 = p.s1;
+    a.w2 = p.w2;
+    a.ld2 = p.ld2;
+    a.stride2 = p.experts > 1 ? p.stride2 : 0;
+    a.s2 = p.s2;
+    a.y = p.y;
+    a.ldy = p.ldy;
+    a.h = p.h;
+    a.ldh = h_stride(p.hidden);
+    if (p.type == SGEMM_TYPE_F32) return layer_launch_f32(p, a, dev, stream, launches);
+    if (p.held == SGEMM_LAYER_SAME) return layer_launch_16(p, a, dev, stream, launches);
+    return layer_launch_fp8(p, a, dev, stream, launches);
+}
+
+}  // namespace fl
+}  // namespace sgemm
+
 using namespace sgemm;
 using namespace sgemm::api;
 using namespace sgemm::fl;
@@ -14,7 +56,7 @@ extern "C" {
 
 size_t sgemm_experts_layer_workspace(int64_t tokens, int64_t top_k, int64_t hidden) {
     if (tokens < 0 || top_k < 1 || top_k > SGEMM_TOP_K_MAX || tokens > MAX_PAIRS / top_k || hidden < 0 ||
-        hidden > kMostRows / 2)
+        hidden > kMostHidden)
         return 0;
     return static_cast<size_t>(tokens * top_k * h_stride(hidden)) * sizeof(float);
 }
@@ -27,7 +69,7 @@ int sgemm_experts_layer(int type, int held, int activation, int gated, int64_t t
     if (!type_ok(type) || held < SGEMM_LAYER_SAME || held > SGEMM_LAYER_E5M2 || activation < SGEMM_ACT_NONE ||
         activation > SGEMM_ACT_SILU || tokens < 0 || top_k < 1 || top_k > SGEMM_TOP_K_MAX ||
         tokens > MAX_PAIRS / top_k || experts < 1 || experts > SGEMM_EXPERTS_MAX || width < 0 || width > kMostRows ||
-        hidden < 0 || hidden > kMostRows / 2 || (id_bits != 32 && id_bits != 64))
+        hidden < 0 || hidden > kMostHidden || (id_bits != 32 && id_bits != 64))
         return SGEMM_ERR_INVALID_ARG;
     const int64_t pairs = tokens * top_k, rows1 = gated ? 2 * hidden : hidden;
     const bool fp8 = held != SGEMM_LAYER_SAME;
@@ -42,6 +84,10 @@ int sgemm_experts_layer(int type, int held, int activation, int gated, int64_t t
     if (!in.ok() || !id.ok() || !w.ok() || !m1.ok() || !m2.ok() || !c1.ok() || !c2.ok() || !out.ok() || !ws.ok() ||
         workspace_bytes < need)
         return SGEMM_ERR_INVALID_ARG;
+    // Rows of 8-bit matrices start on 16-byte boundaries, as sgemm_fp8_gemm wants them.
+    for (const Span *s : {&m1, &m2})
+        if (fp8 && !s->empty() && (s->begin() % 16 != 0 || s->ld % 16 != 0 || (experts > 1 && s->stride % 16 != 0)))
+            return SGEMM_ERR_INVALID_ARG;
     for (const Span *s : {&in, &id, &w, &m1, &m2, &c1, &c2})
         if (out.overlaps(*s) || ws.overlaps(*s)) return SGEMM_ERR_INVALID_ARG;
     if (out.overlaps(ws)) return SGEMM_ERR_INVALID_ARG;

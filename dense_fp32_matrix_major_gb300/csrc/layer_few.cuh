@@ -1,0 +1,888 @@
+// A mixture-of-experts layer for a few tokens, in two kernels:
+//
+//     h[p] = act(W1[e(p)] x[t(p)])              (or act(first half) * second half)
+//     y[t] = sum over j of weights[t][j] W2[e] h[t, j]
+//
+// for at most 512 (token, choice) pairs p. Bound by reading the matrices of the
+// experts that are used, once per 8 pairs that share one.
+//
+// Work. Every block sorts the pairs by expert for itself (a comparison of each
+// pair with each, 512 at most) into entries of up to 8 pairs of an expert. First
+// kernel: the entries' hidden features in tiles of 16 rows of W1 (8 features and
+// their gates), each block a run of tiles. Second kernel: each block some of y's
+// columns, in tiles of 16 rows of W2 for every entry, so a token's experts meet in
+// one block and are added up in the order of its choices. In a block the tiles
+// times their slices of 256 bytes a row are cut evenly among 16 warps, which
+// stream them without a pause; a tile that a warp has whole it finishes itself,
+// one that is cut is joined, in order, when all are done.
+//
+// Loads. A lane copies the 16 bytes that it will use itself into its place in a
+// ring in shared memory (cp.async), two slices ahead: 128 KB on their way to an SM
+// at no cost in registers, and no lane waits for another's copies. (Slices of 128
+// bytes, four ahead: 203 us in place of 185 for 32 tokens through 8 of 128 experts
+// of 2048 x 768.) (Bulk copies
+// of 256 bytes a row take 38 cycles each: 274 us for the 8-bit layer of 16 experts
+// of 4096 x 4096.) x and h come by plain loads two to four chunks ahead, mostly from
+// the caches.
+//
+// Arithmetic. Where x is 16-bit and the matrices' rows are 16-byte aligned, warp
+// matrix instructions (16 rows of the matrix x k x 8 pairs, fp32 sums) on the
+// values as they are: bf16 and fp16 with x of the same type; 8-bit ones as fp16
+// with fp16 x, as tf32 with bf16 x. h enters as two bf16 terms, 16 of its 24 bits (y
+// is rounded to 11 at most), which the first kernel stores apart: as they are with
+// bf16 matrices, as tf32 with fp16 and 8-bit ones. With fp32 x fp32 multiply-adds, because the
+// instruction cuts its running sums (1.3e-6 of the result's norm where
+// multiply-adds leave 0.2e-6). (tcgen05 wants its operands in shared memory and
+// 128 rows a tile for at most 16 columns of x here.) Which k a lane holds does not
+// matter to a matrix instruction as long as matrix and x agree, so a lane takes 16
+// bytes of a row that lie together. Rows that are not 16-byte aligned, or end in a
+// part of 16 bytes, are read value by value, and summed by multiply-adds.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "epilogue.cuh"
+#include "experts_common.cuh"
+#include "layer_internal.h"
+
+namespace sgemm {
+namespace fl {
+namespace {
+
+using ex::from_f32;
+using ex::to_f32;
+
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int MEMBERS = 8;   // pairs of an entry, the columns of the matrix instructions
+constexpr int COLUMNS = 32;  // of y that a block of the second kernel makes at once
+static_assert(MAX_PAIRS <= THREADS, "a thread a pair");
+// A warp's ring: slices of 256 bytes of 16 rows, in 16-byte pieces by lane.
+constexpr int SLICE = 256, CHUNKS = SLICE / 64, STAGE = 2 * CHUNKS * 512, STAGES = 2;
+constexpr int RING_BYTES = STAGES * STAGE;
+// Shared memory: the rings, a tile's sums of each warp, and in the second kernel
+// the pairs' sums.
+constexpr int SMEM = WARPS * (RING_BYTES + 512);
+constexpr int smem_out(int pairs) { return SMEM + pairs * COLUMNS * 4; }
+
+// The pairs sorted by expert, and the entries: runs of up to MEMBERS pairs of an
+// expert.
+struct Lists {
+    alignas(16) int key[MAX_PAIRS];
+    int order[MAX_PAIRS];     // pair at a sorted place
+    int place[MAX_PAIRS];     // of a pair; -1: left out
+    int entry_at[MAX_PAIRS];  // entry of a sorted place
+    int expert[MAX_PAIRS], begin[MAX_PAIRS], count[MAX_PAIRS];  // of an entry
+    int total[WARPS];
+    int entries;
+};
+
+__device__ __forceinline__ int id_of(const LArgs &a, int p) {
+    if (a.id_bits == 64) {
+        const int64_t e = __ldg(static_cast<const long long *>(a.ids) + p);
+        return e < 0 || e >= a.experts ? a.experts : static_cast<int>(e);
+    }
+    const int e = __ldg(static_cast<const int *>(a.ids) + p);
+    return e < 0 || e >= a.experts ? a.experts : e;
+}
+
+// Called by the whole block.
+__device__ __forceinline__ void build_lists(const LArgs &a, Lists &l) {
+    const int p = static_cast<int>(threadIdx.x), lane = p & 31, warp = p >> 5;
+    const int padded = (a.pairs + 3) & ~3;
+    if (p < padded) l.key[p] = p < a.pairs ? id_of(a, p) : a.experts;
+    l.entry_at[p] = 0;
+    __syncthreads();
+    int place = 0, rank = 0, same = 0;
+    const int key = p < a.pairs ? l.key[p] : a.experts;
+    if (p < a.pairs) {
+        for (int q = 0; q < padded; q += 4) {
+            const int4 k = *reinterpret_cast<const int4 *>(l.key + q);
+            const int v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int eq = v[i] == key, before = eq && q + i < p;
+                same += eq;
+                rank += before;
+                place += before || v[i] < key;
+            }
+        }
+    }
+    const bool used = key < a.experts;
+    if (p < a.pairs) l.place[p] = used ? place : -1;
+    if (used) {
+        l.order[place] = p;
+        l.entry_at[place] = rank % MEMBERS == 0;  // an entry starts
+    }
+    __syncthreads();
+    // Numbers the entries in sorted order.
+    const int starts = l.entry_at[p];
+    const unsigned ballot = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0) l.total[warp] = __popc(ballot);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        before += w < warp ? l.total[w] : 0;
+        all += l.total[w];
+    }
+    l.entry_at[p] = before + __popc(ballot & (0xffffffffu >> (31 - lane))) - 1;
+    if (p == 0) l.entries = all;
+    __syncthreads();
+    if (used && rank % MEMBERS == 0) {
+        const int e = l.entry_at[place];
+        l.expert[e] = key;
+        l.begin[e] = place;
+        l.count[e] = min(MEMBERS, same - rank);
+    }
+    __syncthreads();
+}
+
+// How a matrix is held. PER: values in 16 bytes, which a lane takes of a row in a
+// chunk of 64 bytes; four chunks make a slice.
+enum Held { F32, BF16, F16, E4M3, E5M2 };
+template <int H>
+struct Matrix {
+    static constexpr int SIZE = H == F32 ? 4 : (H >= E4M3 ? 1 : 2), PER = 16 / SIZE, CHUNK = 4 * PER, SLICE_K = SLICE / SIZE;
+    static constexpr bool FP8 = H >= E4M3;
+};
+
+// How sums are made: fp32 multiply-adds; matrix instructions on 16-bit values,
+// with x, or with h in two planes; on fp16 made of 8-bit values; on tf32 with x of
+// bf16, or with h in two planes.
+enum Math { FMA, NATIVE, PLANES, HALF8, TF32_X, TF32_H };
+
+// 16 bytes of a row of K values from value k on, zeros past its end. whole: they
+// may be loaded at once where the row has them all (they are 16-byte aligned).
+template <int SIZE>
+__device__ __forceinline__ void load_piece(const uint8_t *row, int k, int K, bool whole, uint32_t (&v)[4]) {
+    constexpr int PER = 16 / SIZE;
+    v[0] = v[1] = v[2] = v[3] = 0;
+    if (k >= K) return;
+    const uint8_t *p = row + static_cast<int64_t>(k) * SIZE;
+    if (whole && k + PER <= K) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < PER && k + i < K; ++i) {
+        uint32_t x;
+        if (SIZE == 4) x = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        if (SIZE == 2) x = __ldg(reinterpret_cast<const uint16_t *>(p) + i);
+        x <<= 8 * (i * SIZE % 4);
+        v[0] |= i * SIZE / 4 == 0 ? x : 0;
+        v[1] |= i * SIZE / 4 == 1 ? x : 0;
+        v[2] |= i * SIZE / 4 == 2 ? x : 0;
+        v[3] |= i * SIZE / 4 == 3 ? x : 0;
+    }
+}
+
+__device__ __forceinline__ float half_of(uint32_t w, int i, bool bf16) {
+    if (bf16) return __uint_as_float(i ? w & 0xFFFF0000u : w << 16);
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(i ? w >> 16 : w)));
+}
+
+// Two 8-bit values (the low 16 bits of w) as fp16, exactly.
+template <int H>
+__device__ __forceinline__ uint32_t fp8_halves(uint32_t w) {
+    if (H == E5M2) return __byte_perm(w, 0, 0x1404);  // the upper half of an fp16
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w)));
+    return h2;
+}
+
+// Value i of 16 bytes as fp32.
+template <int H>
+__device__ __forceinline__ float value_of(const uint32_t (&w)[4], int i) {
+    if (H == F32) return __uint_as_float(w[i]);
+    if (H == BF16 || H == F16) return half_of(w[i / 2], i & 1, H == BF16);
+    return half_of(fp8_halves<H>(w[i / 4] >> (16 * ((i >> 1) & 1))), i & 1, false);
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    if (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A block's warps sum `items` tiles of 16 rows over k, cut with their slices of k
+// into equal shares: this warp has `mine` slices from slice `from` on.
+struct Share {
+    int slices, from, mine;
+};
+
+__device__ __forceinline__ Share share_of(int items, int K, int slice) {
+    const int warp = threadIdx.x >> 5, slices = (K + slice - 1) / slice;
+    const int64_t all = static_cast<int64_t>(items) * slices;
+    const int64_t from = all * warp / WARPS;
+    return Share{slices, static_cast<int>(from), static_cast<int>(all * (warp + 1) / WARPS - from)};
+}
+
+// A place in a share: a tile's number among the block's, its entry, which of the
+// entry's (first kernel) or block's (second) tiles it is, and the slice.
+struct Cursor {
+    int item, entry, tile, slice;
+};
+
+// 16-byte asynchronous copy to shared memory, past the L1 cache; valid == false
+// writes zeros and reads nothing.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void lds_128(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+// The jobs of the two kernels say which rows and pairs a tile has:
+//   cursor(item)       the block's item-th tile; next(c): the one after c
+//   base(c, g)         address of row g (0 .. 7) of the tile
+//   delta()            from there to row 8 + g, in bytes
+//   there(c, i, g)     whether the tile has row 8 i + g
+//   scales(c)          scales of the entry's 8-bit matrix
+//   scale_row(c, i, g) where those of row 8 i + g begin
+//   members(c)         pairs
+//   x(c, m)            pair m's row of x or h
+//   whole()            whether those rows are 16-byte aligned
+//   finish(c, sum)     takes a tile's sums: sum[2 i + j] of lane 4 g + t is row 8 i + g, pair 2 t + j
+
+// The next slice; true where a tile starts.
+template <class Job>
+__device__ __forceinline__ bool step(const Job &job, const Share &s, Cursor &c) {
+    if (++c.slice < s.slices) return false;
+    c.slice = 0;
+    ++c.item;
+    job.next(c);
+    return true;
+}
+
+template <class Job>
+__device__ __forceinline__ Cursor first_of(const Job &job, const Share &s) {
+    Cursor c = job.cursor(s.from / s.slices);
+    c.slice = s.from % s.slices;
+    return c;
+}
+
+// What is left when a warp's share is done: parts of tiles that other warps have
+// too. The part of a tile that started in an earlier warp's share lies in `parts`;
+// a tile that started in this one and goes on is in `sum`.
+struct Rest {
+    bool open;
+    Cursor at;
+    float sum[4];
+};
+
+// Joins the tiles that are cut. Called by the whole block; parts_of: the tile that
+// each warp's part belongs to, -1: none.
+template <class Job>
+__device__ __forceinline__ void join(const Job &job, Rest &rest, const float4 *parts, const int *part_of) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (!rest.open) return;
+    for (int w = warp + 1; w < WARPS; ++w) {
+        if (part_of[w] != rest.at.item) continue;  // another tile, or no share at all
+        const float4 p = parts[w * 32 + lane];
+        rest.sum[0] += p.x;
+        rest.sum[1] += p.y;
+        rest.sum[2] += p.z;
+        rest.sum[3] += p.w;
+    }
+    job.finish(rest.at, rest.sum);
+}
+
+// Sums of multiply-adds: f[m]: rows g and g + 8, pair m, this lane's k only.
+__device__ __forceinline__ void gather_lanes(float (&f)[MEMBERS][2], int t, float (&sum)[4]) {
+#pragma unroll
+    for (int m = 0; m < MEMBERS; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v = f[m][i];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (m / 2 == t) sum[2 * i + (m & 1)] = v;
+        }
+}
+
+// Tiles whose rows are 16-byte aligned and a multiple of 16 bytes long. ring: this
+// lane's place in its warp's ring.
+template <int H, int MATH, class X, class Job>
+__device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint32_t ring, float4 *parts, int *part_of,
+                                         Rest &rest) {
+    using M = Matrix<H>;
+    // 16-byte pieces of x in a lane's part of a chunk, and chunks of them on their way.
+    constexpr int PX = M::PER * static_cast<int>(sizeof(X)) / 16, PIECES = MATH == PLANES || MATH == TF32_H ? 2 * M::PER / 8 : PX, XP = PIECES > 2 ? 2 : 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const Share s = share_of(items, K, M::SLICE_K);
+    rest.open = false;
+    if (lane == 0) part_of[warp] = -1;
+    if (s.mine == 0) return;
+    Cursor load = first_of(job, s), use = load;
+    const int64_t delta = job.delta();
+    const uint8_t *row;
+    bool there0, there1;
+    auto enter = [&] {
+        row = job.base(load, g) + M::PER * t * M::SIZE;
+        there0 = job.there(load, 0, g);
+        there1 = job.there(load, 1, g);
+    };
+    enter();
+    // Copies the next slice; one group of copies each, empty or not.
+    auto fetch = [&](int stage, bool in) {
+        if (in) {
+            const uint32_t to = ring + static_cast<uint32_t>(stage * STAGE);
+#pragma unroll
+            for (int q = 0; q < CHUNKS; ++q) {
+                const uint8_t *p = row + (load.slice * SLICE + q * 64);
+                const bool inside = load.slice * M::SLICE_K + q * M::CHUNK + M::PER * t < K;
+                copy_16(to + 1024 * q, p, there0 && inside);
+                copy_16(to + 1024 * q + 512, p + delta, there1 && inside);
+            }
+            if (step(job, s, load)) enter();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Scales of rows g and g + 8 of the next slice.
+    constexpr int BLOCKS = M::FP8 ? M::SLICE_K / SGEMM_FP8_BLOCK_SIZE : 1;
+    Cursor ahead = use;
+    const float *scale_at[2];
+    auto enter_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) scale_at[i] = job.scales(ahead) + job.scale_row(ahead, i, g);
+    };
+    float next_scale[2][BLOCKS] = {};
+    auto fetch_scales = [&](bool in) {
+        if (!M::FP8 || !in) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int block = ahead.slice * BLOCKS + b;
+                next_scale[i][b] = block * SGEMM_FP8_BLOCK_SIZE < K ? __ldg(scale_at[i] + block) : 0.0f;
+            }
+        if (step(job, s, ahead)) enter_scales();
+    };
+    // x of member g, XP chunks ahead of the sums.
+    Cursor pre = use;
+    const uint8_t *x_row = nullptr;
+    auto enter_x = [&] {
+        const int n = job.members(pre);
+        x_row = static_cast<const uint8_t *>(job.x(pre, g < n ? g : 0));
+    };
+    const bool whole = job.whole();
+    uint32_t xw[XP][PIECES][4];
+    auto load_x = [&](int q, bool in) {  // chunk q of slice `pre`
+        if (!in) return;
+        const int k = pre.slice * M::SLICE_K + q * M::CHUNK + M::PER * t;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            if (MATH == PLANES || MATH == TF32_H)  // plane i % 2
+                load_piece<2>(x_row + (i & 1) * job.plane(), k + i / 2 * 8, K, true, xw[q % XP][i]);
+            else
+                load_piece<sizeof(X)>(x_row, k + i * (16 / static_cast<int>(sizeof(X))), K, whole, xw[q % XP][i]);
+        }
+        if (q == CHUNKS - 1 && step(job, s, pre)) enter_x();
+    };
+    float sum[4], fma[MATH == FMA ? MEMBERS : 1][2];
+    int count = 0;
+    bool started = false;  // the tile started in this share
+    auto start = [&] {
+        count = job.members(use);
+        started = use.slice == 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
+#pragma unroll
+        for (int m = 0; m < (MATH == FMA ? MEMBERS : 1); ++m) fma[m][0] = fma[m][1] = 0.0f;
+    };
+    // Adds a chunk's products with the members' x in v to d.
+    auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&v)[PIECES][4], float (&d)[4]) {
+        if (MATH == NATIVE || MATH == PLANES) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                mma_16<H == BF16>(d, lo[0], hi[0], lo[1], hi[1], v[i][0], v[i][1]);
+                mma_16<H == BF16>(d, lo[2], hi[2], lo[3], hi[3], v[i][2], v[i][3]);
+            }
+        } else if (MATH == HALF8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mma_16<false>(d, fp8_halves<H>(lo[j]), fp8_halves<H>(hi[j]), fp8_halves<H>(lo[j] >> 16),
+                              fp8_halves<H>(hi[j] >> 16), v[j / 2][2 * (j & 1)], v[j / 2][2 * (j & 1) + 1]);
+        } else if (MATH == TF32_X || MATH == TF32_H) {
+#pragma unroll
+            for (int j = 0; j < M::PER; j += 2) {
+                const float a0 = value_of<H>(lo, j), a1 = value_of<H>(hi, j), a2 = value_of<H>(lo, j + 1),
+                            a3 = value_of<H>(hi, j + 1);
+                if (MATH == TF32_X) {
+                    const uint32_t two = v[j / 8][(j / 2) % 4];
+                    mma_tf32(d, a0, a1, a2, a3, half_of(two, 0, true), half_of(two, 1, true));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t two = v[j / 8 * 2 + i][(j / 2) % 4];
+                        mma_tf32(d, a0, a1, a2, a3, half_of(two, 0, true), half_of(two, 1, true));
+                    }
+                }
+            }
+        }
+    };
+#pragma unroll
+    for (int n = 0; n < STAGES; ++n) fetch(n, n < s.mine);
+    if (M::FP8) enter_scales();
+    fetch_scales(true);
+    if (MATH != FMA) {
+        enter_x();
+#pragma unroll
+        for (int q = 0; q < XP; ++q) load_x(q, true);
+    }
+    start();
+    for (int n = 0; n < s.mine; ++n) {
+        const int stage = n % STAGES;
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        const uint32_t at = ring + static_cast<uint32_t>(stage * STAGE);
+        const bool last = n + 1 == s.mine;
+        float scale[2][BLOCKS];
+#pragma unroll
+        for (int i = 0; i < 2 * BLOCKS; ++i) scale[i / BLOCKS][i % BLOCKS] = next_scale[i / BLOCKS][i % BLOCKS];
+        fetch_scales(!last);
+        float part[4];  // of a block of an 8-bit matrix
+#pragma unroll
+        for (int q = 0; q < CHUNKS; ++q) {
+            constexpr int PER_BLOCK = CHUNKS / BLOCKS;
+            if (M::FP8 && q % PER_BLOCK == 0) part[0] = part[1] = part[2] = part[3] = 0.0f;
+            uint32_t lo[4], hi[4];
+            lds_128(at + 1024 * q, lo);
+            lds_128(at + 1024 * q + 512, hi);
+            if (MATH == FMA) {
+                const int k0 = use.slice * M::SLICE_K + q * M::CHUNK + M::PER * t;
+#pragma unroll
+                for (int j0 = 0; j0 < M::PER; j0 += 4) {
+                    float a0[4], a1[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a0[j] = value_of<H>(lo, j0 + j) * (M::FP8 ? scale[0][q / PER_BLOCK] : 1.0f);
+                        a1[j] = value_of<H>(hi, j0 + j) * (M::FP8 ? scale[1][q / PER_BLOCK] : 1.0f);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MEMBERS; ++m) {
+                        if (m >= count) break;
+                        uint32_t b[4];
+                        load_piece<4>(static_cast<const uint8_t *>(job.x(use, m)), k0 + j0, K, whole, b);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float(&f)[2] = fma[MATH == FMA ? m : 0];
+                            f[0] = fmaf(a0[j], __uint_as_float(b[j]), f[0]);
+                            f[1] = fmaf(a1[j], __uint_as_float(b[j]), f[1]);
+                        }
+                    }
+                }
+            } else {
+                multiply(lo, hi, xw[q % XP], M::FP8 ? part : sum);
+                load_x((q + XP) % CHUNKS, !last || q + XP < CHUNKS);
+            }
+            if (M::FP8 && MATH != FMA && q % PER_BLOCK == PER_BLOCK - 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = fmaf(part[i], scale[i >> 1][q / PER_BLOCK], sum[i]);
+            }
+        }
+        fetch(stage, n + STAGES < s.mine);
+        const bool done = use.slice + 1 == s.slices;
+        if (last || done) {
+            if constexpr (MATH == FMA) gather_lanes(fma, t, sum);
+            if (done && started) {
+                job.finish(use, sum);
+            } else if (started) {
+                rest.open = true;
+                rest.at = use;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rest.sum[i] = sum[i];
+            } else {
+                parts[warp * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                if (lane == 0) part_of[warp] = use.item;
+            }
+        }
+        if (step(job, s, use) && !last) start();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Tiles whose rows are anywhere: value by value, multiply-adds. A lane takes
+// every fourth k of a slice of 32.
+template <int H, class X, class Job>
+__device__ __forceinline__ void sum_values(const Job &job, int items, int K, float4 *parts, int *part_of, Rest &rest) {
+    using M = Matrix<H>;
+    constexpr int N = 8, D = 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const Share s = share_of(items, K, 4 * N);
+    rest.open = false;
+    if (lane == 0) part_of[warp] = -1;
+    if (s.mine == 0) return;
+    Cursor load = first_of(job, s), use = load;
+    const int64_t delta = job.delta();
+    const uint8_t *row;
+    const float *scale_at[2];
+    bool there[2];
+    auto enter = [&] {
+        row = job.base(load, g);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            there[r] = job.there(load, r, g);
+            if (M::FP8) scale_at[r] = job.scales(load) + job.scale_row(load, r, g);
+        }
+    };
+    enter();
+    uint32_t w[D][2][N];
+    float sw[D][2];
+    auto load_w = [&](int d, bool in) {
+        const int k0 = load.slice * 4 * N + t;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int k = k0 + 4 * j;
+                w[d][r][j] = 0;
+                if (!in || !there[r] || k >= K) continue;
+                const uint8_t *p = row + r * delta + static_cast<int64_t>(k) * M::SIZE;
+                if (M::SIZE == 4) w[d][r][j] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                if (M::SIZE == 2) w[d][r][j] = __ldg(reinterpret_cast<const uint16_t *>(p));
+                if (M::SIZE == 1) w[d][r][j] = __ldg(p);
+            }
+            if (M::FP8) sw[d][r] = in ? __ldg(scale_at[r] + load.slice * 4 * N / SGEMM_FP8_BLOCK_SIZE) : 0.0f;
+        }
+        if (in && step(job, s, load)) enter();
+    };
+    float fma[MEMBERS][2];
+    int count = 0;
+    bool started = false;
+    auto start = [&] {
+        count = job.members(use);
+        started = use.slice == 0;
+#pragma unroll
+        for (int m = 0; m < MEMBERS; ++m) fma[m][0] = fma[m][1] = 0.0f;
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d < s.mine);
+    start();
+    for (int i0 = 0; i0 < s.mine; i0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (i0 + d >= s.mine) break;
+            const int k0 = use.slice * 4 * N + t;
+            float a[2][N];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const uint32_t one[4] = {w[d][r][j], 0, 0, 0};
+                    a[r][j] = value_of<H>(one, 0) * (M::FP8 ? sw[d][r] : 1.0f);
+                }
+#pragma unroll
+            for (int m = 0; m < MEMBERS; ++m) {
+                if (m >= count) break;
+                const X *x = static_cast<const X *>(job.x(use, m));
+                float b[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) b[j] = k0 + 4 * j < K ? to_f32(x[k0 + 4 * j]) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    fma[m][0] = fmaf(a[0][j], b[j], fma[m][0]);
+                    fma[m][1] = fmaf(a[1][j], b[j], fma[m][1]);
+                }
+            }
+            load_w(d, i0 + d + D < s.mine);
+            const bool last = i0 + d + 1 == s.mine, done = use.slice + 1 == s.slices;
+            if (last || done) {
+                float sum[4];
+                gather_lanes(fma, t, sum);
+                if (done && started) {
+                    job.finish(use, sum);
+                } else if (started) {
+                    rest.open = true;
+                    rest.at = use;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rest.sum[i] = sum[i];
+                } else {
+                    parts[warp * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                    if (lane == 0) part_of[warp] = use.item;
+                }
+            }
+            if (step(job, s, use) && !last) start();
+        }
+    }
+}
+
+extern __shared__ __align__(16) uint8_t dynamic_smem[];
+
+// Sums and finishes a block's tiles. VALUES: rows that the ring cannot take.
+template <int H, int MATH, bool VALUES, class X, class Job>
+__device__ __forceinline__ void sum_tiles(const Job &job, int items, int K, int *part_of) {
+    float4 *parts = reinterpret_cast<float4 *>(dynamic_smem + WARPS * RING_BYTES);
+    Rest rest;
+    if constexpr (VALUES)
+        sum_values<H, X>(job, items, K, parts, part_of, rest);
+    else
+        sum_ring<H, MATH, X>(job, items, K,
+                             static_cast<uint32_t>(__cvta_generic_to_shared(dynamic_smem)) +
+                                 (threadIdx.x >> 5) * RING_BYTES + (threadIdx.x & 31) * 16,
+                             parts, part_of, rest);
+    join(job, rest, parts, part_of);
+}
+
+// h of the entries' tiles of features: 16 rows of W1, 8 features with their gates
+// or 16 without.
+template <int H>
+struct HiddenJob {
+    using M = Matrix<H>;
+    const LArgs &a;
+    const Lists &l;
+    int first, per_tile, per_entry, kblocks;
+    int64_t item_scales;
+    __device__ __forceinline__ Cursor cursor(int item) const {
+        const int i = first + item, entry = i / per_entry;
+        return Cursor{item, entry, i - entry * per_entry, 0};
+    }
+    __device__ __forceinline__ void next(Cursor &c) const {
+        if (++c.tile < per_entry) return;
+        c.tile = 0;
+        c.entry = min(c.entry + 1, l.entries - 1);  // past the last: never used
+    }
+    __device__ __forceinline__ int feature(const Cursor &c) const { return c.tile * per_tile; }
+    // Row 8 i + g of a tile is, in W1, row feature + offset(i) + g.
+    __device__ __forceinline__ int offset(int i) const { return i == 0 ? 0 : (a.gated ? a.hidden : 8); }
+    __device__ __forceinline__ const uint8_t *base(const Cursor &c, int g) const {
+        return static_cast<const uint8_t *>(a.w1) + (l.expert[c.entry] * a.stride1 + (feature(c) + g) * a.ld1) * M::SIZE;
+    }
+    __device__ __forceinline__ int64_t delta() const { return offset(1) * a.ld1 * M::SIZE; }
+    __device__ __forceinline__ bool there(const Cursor &c, int i, int g) const {
+        return feature(c) + (a.gated ? 0 : 8 * i) + g < a.hidden;
+    }
+    __device__ __forceinline__ const float *scales(const Cursor &c) const { return a.s1 + l.expert[c.entry] * item_scales; }
+    __device__ __forceinline__ int scale_row(const Cursor &c, int i, int g) const {
+        return there(c, i, g) ? (feature(c) + offset(i) + g) / SGEMM_FP8_BLOCK_SIZE * kblocks : 0;
+    }
+    __device__ __forceinline__ int members(const Cursor &c) const { return l.count[c.entry]; }
+    __device__ __forceinline__ int pair(const Cursor &c, int m) const { return l.order[l.begin[c.entry] + m]; }
+    __device__ __forceinline__ const void *x(const Cursor &c, int m) const {
+        return static_cast<const uint8_t *>(a.x) + pair(c, m) / a.top_k * a.ldx * a.x_size;
+    }
+    __device__ __forceinline__ int64_t plane() const { return 0; }
+    __device__ __forceinline__ bool whole() const { return a.x_vector; }
+    __device__ __forceinline__ void write(const Cursor &c, int m, int feature, float v) const {
+        float *to = a.h + pair(c, m) * a.ldh;
+        if (a.planes) {
+            // Two bf16 terms, 16 bits of v: what a 16-bit y rounds away is 2^7 times as large.
+            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+            __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(to) + feature;
+            p[0] = hi;
+            p[a.ldh] = __float2bfloat16_rn(isfinite(v) ? v - __bfloat162float(hi) : 0.0f);
+        } else {
+            to[feature] = v;
+        }
+    }
+    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const {
+        const int lane = threadIdx.x & 31, f = feature(c) + (lane >> 2), count = members(c);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int m = 2 * (lane & 3) + j;
+            if (m >= count) continue;
+            const float v = activate(sum[j], a.activation);
+            if (a.gated) {
+                if (f < a.hidden) write(c, m, f, v * sum[2 + j]);
+            } else {
+                if (f < a.hidden) write(c, m, f, v);
+                if (f + 8 < a.hidden) write(c, m, f + 8, activate(sum[2 + j], a.activation));
+            }
+        }
+    }
+};
+
+template <int H, int MATH, bool VALUES, class X>
+__global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_constant__ LArgs a) {
+    __shared__ Lists l;
+    __shared__ int part_of[WARPS];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    build_lists(a, l);
+    const int per_tile = a.gated ? 8 : 16;  // features
+    const int rows1 = a.gated ? 2 * a.hidden : a.hidden;
+    HiddenJob<H> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
+                     (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
+    job.item_scales = static_cast<int64_t>((rows1 + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
+    const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
+    job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
+    const int items = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) - job.first;
+    sum_tiles<H, MATH, VALUES, X>(job, items, a.width, part_of);
+}
+
+// y from h: block b has columns width * b / grid .. width * (b + 1) / grid - 1,
+// `cols` of them, from `at` on, at once.
+template <int H>
+struct OutJob {
+    using M = Matrix<H>;
+    const LArgs &a;
+    const Lists &l;
+    float *sums;  // of a pair's place, COLUMNS each
+    int at, cols, kblocks;
+    int64_t item_scales;
+    __device__ __forceinline__ Cursor cursor(int item) const {
+        const int tile = item / l.entries;
+        return Cursor{item, item - tile * l.entries, tile, 0};
+    }
+    __device__ __forceinline__ void next(Cursor &c) const {
+        if (++c.entry < l.entries) return;
+        c.entry = 0;
+        ++c.tile;
+    }
+    __device__ __forceinline__ const uint8_t *base(const Cursor &c, int g) const {
+        return static_cast<const uint8_t *>(a.w2) +
+               (l.expert[c.entry] * a.stride2 + static_cast<int64_t>(at + 16 * c.tile + g) * a.ld2) * M::SIZE;
+    }
+    __device__ __forceinline__ int64_t delta() const { return 8 * a.ld2 * M::SIZE; }
+    __device__ __forceinline__ bool there(const Cursor &c, int i, int g) const { return 16 * c.tile + 8 * i + g < cols; }
+    __device__ __forceinline__ const float *scales(const Cursor &c) const { return a.s2 + l.expert[c.entry] * item_scales; }
+    __device__ __forceinline__ int scale_row(const Cursor &c, int i, int g) const {
+        return there(c, i, g) ? (at + 16 * c.tile + 8 * i + g) / SGEMM_FP8_BLOCK_SIZE * kblocks : 0;
+    }
+    __device__ __forceinline__ int members(const Cursor &c) const { return l.count[c.entry]; }
+    __device__ __forceinline__ const void *x(const Cursor &c, int m) const {
+        return a.h + l.order[l.begin[c.entry] + m] * a.ldh;
+    }
+    __device__ __forceinline__ int64_t plane() const { return a.ldh * 2; }
+    __device__ __forceinline__ bool whole() const { return true; }
+    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const {
+        const int lane = threadIdx.x & 31, count = members(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 2 * (lane & 3) + (i & 1), n = 16 * c.tile + 8 * (i >> 1) + (lane >> 2);
+            if (m < count) sums[(l.begin[c.entry] + m) * COLUMNS + n] = sum[i];
+        }
+    }
+};
+
+template <int H, int MATH, bool VALUES>
+__global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_constant__ LArgs a) {
+    __shared__ Lists l;
+    __shared__ int part_of[WARPS];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    build_lists(a, l);
+    const int n0 = static_cast<int>(static_cast<int64_t>(a.width) * blockIdx.x / gridDim.x),
+              n1 = static_cast<int>(static_cast<int64_t>(a.width) * (blockIdx.x + 1) / gridDim.x);
+    OutJob<H> job{a, l, reinterpret_cast<float *>(dynamic_smem + SMEM), n0, 0,
+                  (a.hidden + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
+    job.item_scales = static_cast<int64_t>((a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
+    for (; job.at < n1; job.at += COLUMNS) {
+        job.cols = min(COLUMNS, n1 - job.at);
+        sum_tiles<H, MATH, VALUES, float>(job, a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0, a.hidden, part_of);
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.tokens * COLUMNS; i += THREADS) {
+            const int n = i % COLUMNS, token = i / COLUMNS;
+            if (n >= job.cols) continue;
+            float y = 0.0f;
+            for (int j = 0; j < a.top_k && a.hidden > 0; ++j) {
+                const int p = token * a.top_k + j, place = l.place[p];
+                if (place >= 0) y = fmaf(__ldg(a.weights + p), job.sums[place * COLUMNS + n], y);
+            }
+            const int64_t to = token * a.ldy + job.at + n;
+            if (a.x_type == SGEMM_TYPE_F32)
+                static_cast<float *>(a.y)[to] = y;
+            else if (a.x_type == SGEMM_TYPE_BF16)
+                static_cast<__nv_bfloat16 *>(a.y)[to] = __float2bfloat16_rn(y);
+            else
+                static_cast<__half *>(a.y)[to] = __float2half_rn(y);
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <auto KERNEL>
+int enqueue_kernel(const LArgs &a, int grid, int smem, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    std::call_once(once[dev.device],
+                   [&] { err[dev.device] = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                            smem_out(MAX_PAIRS)); });
+    if (err[dev.device] != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, KERNEL, a) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    ++*launches;
+    return SGEMM_OK;
+}
+
+// Rows of K values that the ring can take: they start on 16-byte boundaries and
+// are a multiple of 16 bytes long.
+template <int H>
+bool ring_takes(const void *w, int64_t ld, int64_t stride, int64_t K) {
+    constexpr int64_t per = Matrix<H>::PER;
+    return reinterpret_cast<uintptr_t>(w) % 16 == 0 && ld % per == 0 && stride % per == 0 && K % per == 0;
+}
+
+// Blocks of the second kernel: four columns of y a block at least.
+inline int out_grid(const LArgs &a, const DeviceInfo &dev) {
+    const int most = (a.width + 3) / 4;
+    return most < dev.sm_count ? most : dev.sm_count;
+}
+
+// Both kernels. HIDDEN, OUT: how their sums are made where the ring takes the rows.
+template <int H, int HIDDEN, int OUT, class X>
+int launch_layer(const LayerProblem &p, LArgs a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const bool out_ring = ring_takes<H>(p.w2, p.ld2, a.stride2, p.hidden);
+    a.planes = (OUT == PLANES || OUT == TF32_H) && out_ring;
+    int rc = SGEMM_OK;
+    if (p.hidden > 0)
+        rc = ring_takes<H>(p.w1, p.ld1, a.stride1, p.width)
+                 ? enqueue_kernel<layer_hidden_kernel<H, HIDDEN, false, X>>(a, dev.sm_count, SMEM, dev, stream, launches)
+                 : enqueue_kernel<layer_hidden_kernel<H, FMA, true, X>>(a, dev.sm_count, SMEM, dev, stream, launches);
+    if (rc != SGEMM_OK) return rc;
+    return out_ring ? enqueue_kernel<layer_out_kernel<H, OUT, false>>(a, out_grid(a, dev), smem_out(a.pairs), dev, stream, launches)
+                    : enqueue_kernel<layer_out_kernel<H, FMA, true>>(a, out_grid(a, dev), smem_out(a.pairs), dev, stream, launches);
+}
+
+}  // namespace
+
+}  // namespace fl
+}  // namespace sgemm

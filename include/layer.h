@@ -51,7 +51,7 @@ enum sgemm_layer_weights {
  *               sgemm_experts_layer_workspace(tokens, top_k, hidden). Contents
  *               need not be set. Not to be shared by calls that may run at once.
  * tokens * top_k is SGEMM_LAYER_PAIRS_MAX at most. Sums are fp32; h is held in
- * fp32 (with x of 16 bits its products see 22 bits of it), y is rounded once. Each expert's matrices are read
+ * fp32 (with x of 16 bits as two bf16 terms, 16 bits of it), y is rounded once. Each expert's matrices are read
  * once per 16 pairs that share it, so every width, alignment and stride is
  * served, fastest where rows are 16-byte aligned. Infinities and NaN follow IEEE
  * arithmetic, except that an infinite matrix element gives NaN.
