@@ -197,12 +197,20 @@ __device__ __forceinline__ uint32_t fp8_halves(uint32_t w) {
     return h2;
 }
 
+// Values 2 i and 2 i + 1 of 16 bytes of 16- or 8-bit values as fp32.
+template <int H>
+__device__ __forceinline__ float2 two_of(const uint32_t (&w)[4], int i) {
+    if (H == BF16) return make_float2(half_of(w[i], 0, true), half_of(w[i], 1, true));
+    const uint32_t h = H == F16 ? w[i] : fp8_halves<H>(w[i / 2] >> (16 * (i & 1)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
 // Value i of 16 bytes as fp32.
 template <int H>
 __device__ __forceinline__ float value_of(const uint32_t (&w)[4], int i) {
     if (H == F32) return __uint_as_float(w[i]);
-    if (H == BF16 || H == F16) return half_of(w[i / 2], i & 1, H == BF16);
-    return half_of(fp8_halves<H>(w[i / 4] >> (16 * ((i >> 1) & 1))), i & 1, false);
+    const float2 v = two_of<H>(w, i / 2);
+    return i & 1 ? v.y : v.x;
 }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
@@ -410,44 +418,41 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
         }
         if (q == CHUNKS - 1 && step(job, s, pre)) enter_x();
     };
-    float sum[4], fma[MATH == FMA ? MEMBERS : 1][2];
+    float sum[4], side[2][4], fma[MATH == FMA ? MEMBERS : 1][2];
     int count = 0;
     bool started = false;  // the tile started in this share
     auto start = [&] {
         count = job.members(use);
         started = use.slice == 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) sum[i] = side[0][i] = side[1][i] = 0.0f;
 #pragma unroll
         for (int m = 0; m < (MATH == FMA ? MEMBERS : 1); ++m) fma[m][0] = fma[m][1] = 0.0f;
     };
-    // Adds a chunk's products with the members' x in v to d.
-    auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&v)[PIECES][4], float (&d)[4]) {
+    // Adds a chunk's products with the members' x in v to d[0] and d[1]: two chains
+    // of instructions that wait for their own sums only.
+    auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&v)[PIECES][4],
+                        float (&d)[2][4]) {
         if (MATH == NATIVE || MATH == PLANES) {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                mma_16<H == BF16>(d, lo[0], hi[0], lo[1], hi[1], v[i][0], v[i][1]);
-                mma_16<H == BF16>(d, lo[2], hi[2], lo[3], hi[3], v[i][2], v[i][3]);
+                mma_16<H == BF16>(d[0], lo[0], hi[0], lo[1], hi[1], v[i][0], v[i][1]);
+                mma_16<H == BF16>(d[1], lo[2], hi[2], lo[3], hi[3], v[i][2], v[i][3]);
             }
         } else if (MATH == HALF8) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                mma_16<false>(d, fp8_halves<H>(lo[j]), fp8_halves<H>(hi[j]), fp8_halves<H>(lo[j] >> 16),
+                mma_16<false>(d[j & 1], fp8_halves<H>(lo[j]), fp8_halves<H>(hi[j]), fp8_halves<H>(lo[j] >> 16),
                               fp8_halves<H>(hi[j] >> 16), v[j / 2][2 * (j & 1)], v[j / 2][2 * (j & 1) + 1]);
         } else if (MATH == TF32_X || MATH == TF32_H) {
 #pragma unroll
-            for (int j = 0; j < M::PER; j += 2) {
-                const float a0 = value_of<H>(lo, j), a1 = value_of<H>(hi, j), a2 = value_of<H>(lo, j + 1),
-                            a3 = value_of<H>(hi, j + 1);
-                if (MATH == TF32_X) {
-                    const uint32_t two = v[j / 8][(j / 2) % 4];
-                    mma_tf32(d, a0, a1, a2, a3, half_of(two, 0, true), half_of(two, 1, true));
-                } else {
+            for (int j = 0; j < M::PER / 2; ++j) {
+                const float2 a0 = two_of<H>(lo, j), a1 = two_of<H>(hi, j);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t two = v[j / 8 * 2 + i][(j / 2) % 4];
-                        mma_tf32(d, a0, a1, a2, a3, half_of(two, 0, true), half_of(two, 1, true));
-                    }
+                for (int i = 0; i < (MATH == TF32_H ? 2 : 1); ++i) {
+                    const uint32_t two = v[MATH == TF32_H ? j / 4 * 2 + i : j / 4][j % 4];
+                    mma_tf32(d[MATH == TF32_H ? i : j & 1], a0.x, a1.x, a0.y, a1.y, half_of(two, 0, true),
+                             half_of(two, 1, true));
                 }
             }
         }
@@ -471,11 +476,9 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
 #pragma unroll
         for (int i = 0; i < 2 * BLOCKS; ++i) scale[i / BLOCKS][i % BLOCKS] = next_scale[i / BLOCKS][i % BLOCKS];
         fetch_scales(!last);
-        float part[4];  // of a block of an 8-bit matrix
 #pragma unroll
         for (int q = 0; q < CHUNKS; ++q) {
             constexpr int PER_BLOCK = CHUNKS / BLOCKS;
-            if (M::FP8 && q % PER_BLOCK == 0) part[0] = part[1] = part[2] = part[3] = 0.0f;
             uint32_t lo[4], hi[4];
             lds_128(at + 1024 * q, lo);
             lds_128(at + 1024 * q + 512, hi);
@@ -503,18 +506,27 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
                     }
                 }
             } else {
-                multiply(lo, hi, xw[q % XP], M::FP8 ? part : sum);
+                multiply(lo, hi, xw[q % XP], side);
                 load_x((q + XP) % CHUNKS, !last || q + XP < CHUNKS);
             }
             if (M::FP8 && MATH != FMA && q % PER_BLOCK == PER_BLOCK - 1) {
+                // A block of an 8-bit matrix ends.
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = fmaf(part[i], scale[i >> 1][q / PER_BLOCK], sum[i]);
+                for (int i = 0; i < 4; ++i) {
+                    sum[i] = fmaf(side[0][i] + side[1][i], scale[i >> 1][q / PER_BLOCK], sum[i]);
+                    side[0][i] = side[1][i] = 0.0f;
+                }
             }
         }
         fetch(stage, n + STAGES < s.mine);
         const bool done = use.slice + 1 == s.slices;
         if (last || done) {
-            if constexpr (MATH == FMA) gather_lanes(fma, t, sum);
+            if constexpr (MATH == FMA) {
+                gather_lanes(fma, t, sum);
+            } else if constexpr (!M::FP8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = side[0][i] + side[1][i];
+            }
             if (done && started) {
                 job.finish(use, sum);
             } else if (started) {
@@ -722,24 +734,6 @@ struct HiddenJob {
     }
 };
 
-template <int H, int MATH, bool VALUES, class X>
-__global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_constant__ LArgs a) {
-    __shared__ Lists l;
-    __shared__ int part_of[WARPS];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    build_lists(a, l);
-    const int per_tile = a.gated ? 8 : 16;  // features
-    const int rows1 = a.gated ? 2 * a.hidden : a.hidden;
-    HiddenJob<H> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
-                     (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
-    job.item_scales = static_cast<int64_t>((rows1 + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
-    const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
-    job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
-    const int items = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) - job.first;
-    sum_tiles<H, MATH, VALUES, X>(job, items, a.width, part_of);
-}
-
 // y from h: block b has columns width * b / grid .. width * (b + 1) / grid - 1,
 // `cols` of them, from `at` on, at once.
 template <int H>
@@ -785,6 +779,35 @@ struct OutJob {
     }
 };
 
+// The columns of y that block b of the second kernel makes.
+template <int H>
+__device__ __forceinline__ OutJob<H> out_job(const LArgs &a, const Lists &l, int b, int blocks, int *end) {
+    const int n0 = static_cast<int>(static_cast<int64_t>(a.width) * b / blocks);
+    *end = static_cast<int>(static_cast<int64_t>(a.width) * (b + 1) / blocks);
+    const int kblocks = (a.hidden + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE,
+              nblocks = (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE;
+    return OutJob<H>{a, l, reinterpret_cast<float *>(dynamic_smem + SMEM), n0, min(COLUMNS, *end - n0), kblocks,
+                     static_cast<int64_t>(nblocks) * kblocks};
+}
+
+template <int H, int MATH, bool VALUES, class X>
+__global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_constant__ LArgs a) {
+    __shared__ Lists l;
+    __shared__ int part_of[WARPS];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    build_lists(a, l);
+    const int per_tile = a.gated ? 8 : 16;  // features
+    const int rows1 = a.gated ? 2 * a.hidden : a.hidden;
+    HiddenJob<H> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
+                     (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
+    job.item_scales = static_cast<int64_t>((rows1 + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
+    const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
+    job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
+    const int items = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) - job.first;
+    sum_tiles<H, MATH, VALUES, X>(job, items, a.width, part_of);
+}
+
 template <int H, int MATH, bool VALUES>
 __global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_constant__ LArgs a) {
     __shared__ Lists l;
@@ -792,11 +815,8 @@ __global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     build_lists(a, l);
-    const int n0 = static_cast<int>(static_cast<int64_t>(a.width) * blockIdx.x / gridDim.x),
-              n1 = static_cast<int>(static_cast<int64_t>(a.width) * (blockIdx.x + 1) / gridDim.x);
-    OutJob<H> job{a, l, reinterpret_cast<float *>(dynamic_smem + SMEM), n0, 0,
-                  (a.hidden + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
-    job.item_scales = static_cast<int64_t>((a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
+    int n1;
+    OutJob<H> job = out_job<H>(a, l, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), &n1);
     for (; job.at < n1; job.at += COLUMNS) {
         job.cols = min(COLUMNS, n1 - job.at);
         sum_tiles<H, MATH, VALUES, float>(job, a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0, a.hidden, part_of);

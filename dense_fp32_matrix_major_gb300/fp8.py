@@ -73,6 +73,8 @@ def _strides(t, name, dtypes, dims):
     rows, cols = t.shape[-2:]
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
+    if rows == 0 or cols == 0:
+        return max(-(-cols // 16) * 16, 16), 0
     return (t.stride(-2) if rows > 1 else max(-(-cols // 16) * 16, 16)), (t.stride(0) if t.dim() == 3 else 0)
 
 

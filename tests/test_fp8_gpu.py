@@ -1,0 +1,359 @@
+"""Quantisation to 8-bit floating point and products of 8-bit matrices, against definitions in 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.experts_harness import DTYPES, canaries_intact, offsets_of, strided
+from tests.fp8_harness import E4M3, E5M2, LARGEST, check_product, meaning, quantize64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    from dense_fp32_matrix_major_gb300 import fp8
+
+    return fp8
+
+
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    yield
+    from dense_fp32_matrix_major_gb300 import sgemm
+
+    torch.cuda.synchronize()
+    assert sgemm.device_status() == 0
+
+
+def same(got, want):
+    got = got.double().cpu().numpy()
+    assert got.shape == want.shape
+    assert np.array_equal(got, want, equal_nan=True), f"{(got != want).sum()} of {got.size} differ"
+
+
+def rows_of(rows, cols, dtype, seed=0, spread=2.0):
+    g = torch.Generator().manual_seed(seed + 1000 * rows + cols)
+    x = torch.randn((rows, cols), generator=g) * torch.exp(spread * torch.randn((rows, 1), generator=g))
+    return x.to(dtype)
+
+
+# ------------------------------------------------------------------ quantisation
+
+
+@pytest.mark.parametrize("block", ["rows", "columns", "blocks"])
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 127), (5, 128), (130, 129), (257, 515), (128, 512), (2, 1040)])
+def test_quantize(fp8, block, name, rows, cols):
+    x = rows_of(rows, cols, DTYPES[name])
+    for to in (E4M3, E5M2):
+        for pow2 in (False, True):
+            q = fp8.quantize(x.cuda(), block, dtype=to, pow2=pow2)
+            values, scales = quantize64(x, block, to, pow2)
+            same(q.values, values)
+            same(q.scales, scales.astype(np.float64))
+            assert q.values.stride(0) % 16 == 0 or rows == 1
+
+
+@pytest.mark.parametrize("block", ["rows", "columns", "blocks"])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (0, 1), (7, 3), (8, 8)])
+def test_quantize_strides(fp8, block, pad, offset):
+    for name, dtype in DTYPES.items():
+        x = strided(rows_of(70, 260, dtype), pad, offset)
+        store = torch.full((70 * 300 + 40,), 0x5A, dtype=torch.uint8, device="cuda")
+        out = store.view(E4M3).as_strided((70, 260), (260 + pad, 1), offset)
+        want = fp8.quantize(x.contiguous(), block)
+        got = fp8.quantize(x, block, out=fp8.Quantized(out, torch.empty_like(want.scales)))
+        assert torch.equal(got.values.view(torch.uint8), want.values.view(torch.uint8)), name
+        assert torch.equal(got.scales, want.scales)
+        out.view(torch.uint8).fill_(0x5A)
+        assert bool((store == 0x5A).all()) and canaries_intact(x.copy_(x))
+
+
+def test_quantize_a_stack(fp8):
+    x = torch.stack([rows_of(130, 200, torch.float32, s) for s in range(3)])
+    q = fp8.quantize(x.cuda(), "blocks")
+    assert q.values.shape == (3, 130, 200) and q.scales.shape == (3, 2, 2)
+    for i in range(3):
+        values, scales = quantize64(x[i], "blocks", E4M3)
+        same(q.values[i], values)
+        same(q.scales[i], scales.astype(np.float64))
+    part = fp8.quantize(x.cuda()[:, 5:100], "blocks")  # items further apart than they are long
+    assert torch.equal(part.scales[1], fp8.quantize(x[1, 5:100].contiguous().cuda(), "blocks").scales)
+
+
+@pytest.mark.parametrize("block", ["rows", "columns", "blocks"])
+def test_quantize_special_values(fp8, block):
+    """Zeros, the smallest and largest numbers, infinities and NaN."""
+    x = rows_of(140, 260, torch.float32, 5)
+    x[0:128, 0:128] = 0.0
+    x[3, 200] = float("inf")
+    x[4, 201] = float("-inf")
+    x[5, 202] = float("nan")
+    x[130, :] = torch.linspace(-1e-38, 1e-38, 260)
+    x[131, 0:128] = 3e38
+    x[132, :] = float("nan")
+    x[133, 5] = -0.0
+    x[134, :] = float("inf")
+    x[135, :] = 1e-45
+    for to in (E4M3, E5M2):
+        for pow2 in (False, True):
+            q = fp8.quantize(x.cuda(), block, dtype=to, pow2=pow2)
+            values, scales = quantize64(x, block, to, pow2)
+            same(q.values, values)
+            same(q.scales, scales.astype(np.float64))
+            assert bool(torch.isfinite(q.scales).all()) and bool((q.scales >= 2.0 ** -126).all())
+
+
+def test_quantize_every_border(fp8):
+    """All 8-bit values, the borders between them and their neighbours in fp32, at a scale of 1."""
+    for to in (E4M3, E5M2):
+        v = torch.arange(127 if to == E4M3 else 124, dtype=torch.uint8).view(to).float()
+        mid = (v[1:] + v[:-1]) / 2
+        near = torch.cat([v, mid, torch.nextafter(mid, mid + 1), torch.nextafter(mid, mid - 1)])
+        near = torch.cat([near, -near])
+        x = torch.zeros((near.numel(), 128))
+        x[:, 0], x[:, 1] = LARGEST[to], near
+        q = fp8.quantize(x.cuda(), "rows", dtype=to)
+        same(q.values, quantize64(x, "rows", to)[0])
+        assert bool((q.scales == 1).all())
+
+
+@pytest.mark.parametrize("counts,tail", [([5, 0, 128, 129, 0], 0), ([300], 7), ([0, 0, 0], 3), ([1] * 40, 0),
+                                         ([128, 128], 0), ([0] * 100 + [1, 200], 50)])
+def test_quantize_groups(fp8, counts, tail):
+    rows, cols = sum(counts) + tail, 200
+    x = rows_of(rows, cols, torch.bfloat16)
+    q = fp8.quantize(x.cuda(), "columns", dtype=E5M2, offsets=offsets_of(counts).cuda())
+    at, values, scales = 0, [], []
+    for c in counts:
+        v, s = quantize64(x[at:at + c], "columns", E5M2)
+        at += c
+        values += [v, np.zeros((-c % 128, cols))]
+        scales.append(s)
+    values, scales = np.concatenate(values), np.concatenate(scales)
+    blocks = (rows + 127 * min(rows, len(counts))) // 128
+    assert q.values.shape == (128 * blocks, cols) and q.scales.shape == (blocks, cols)
+    n = scales.shape[0]
+    same(q.values[:128 * n], values)
+    same(q.scales[:n], scales.astype(np.float64))
+    assert not q.values[128 * n:].view(torch.uint8).any() and bool((q.scales[n:] == 2.0 ** -126).all())
+
+
+def test_quantize_groups_of_bad_offsets(fp8):
+    """Offsets past the rows or that decrease are limited: no row is read from outside."""
+    x = rows_of(300, 130, torch.float32).cuda()
+    for off in ([0, 1000, 2000], [0, -5, 300], [0, 200, 100], [7, 8, 9]):
+        q = fp8.quantize(x, "columns", offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+        assert bool(torch.isfinite(q.scales).all())
+
+
+def test_quantize_nothing(fp8):
+    for shape in ((0, 64), (64, 0), (0, 0)):
+        for block in ("rows", "columns", "blocks"):
+            q = fp8.quantize(torch.empty(shape, device="cuda"), block)
+            assert q.values.shape == shape
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    assert fp8.quantize(torch.empty((0, 64), device="cuda"), "columns", offsets=off).values.shape == (0, 64)
+
+
+# ---------------------------------------------------------------------- products
+
+
+def operands(fp8, rows, N, K, trans, ta=E4M3, tb=E4M3, experts=0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + rows + 7 * N + 31 * K)
+    x = torch.randn((rows, K), generator=g, device="cuda") * torch.exp(torch.randn((rows, 1), generator=g, device="cuda"))
+    shape = (N, K) if trans else (K, N)
+    w = torch.randn((experts, *shape) if experts else shape, generator=g, device="cuda")
+    return fp8.quantize(x, "rows", dtype=ta), fp8.quantize(w, "blocks", dtype=tb)
+
+
+def op(w, trans):
+    return w.transpose(-1, -2) if trans else w
+
+
+SIZES = [(1, 1, 1), (1, 256, 128), (3, 5, 16), (31, 33, 129), (128, 128, 128), (129, 257, 127), (255, 256, 384),
+         (256, 512, 640), (257, 300, 1000), (600, 40, 260), (33, 700, 2049)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("rows,N,K", SIZES)
+def test_gemm(fp8, rows, N, K, trans):
+    a, b = operands(fp8, rows, N, K, trans)
+    A, B = meaning(a, "rows"), op(meaning(b, "blocks"), trans)
+    for dtype in DTYPES.values():
+        check_product(fp8.gemm(a, b, transB=trans, dtype=dtype), A, B, K, f"{dtype}")
+
+
+@pytest.mark.parametrize("ta", [E4M3, E5M2])
+@pytest.mark.parametrize("tb", [E4M3, E5M2])
+def test_gemm_types(fp8, ta, tb):
+    for trans in (False, True):
+        a, b = operands(fp8, 200, 300, 400, trans, ta, tb)
+        check_product(fp8.gemm(a, b, transB=trans, dtype=torch.float32), meaning(a, "rows"),
+                      op(meaning(b, "blocks"), trans), 400)
+    x, y = (fp8.quantize(torch.randn((300, n), device="cuda"), "columns", dtype=t) for n, t in ((200, ta), (150, tb)))
+    check_product(fp8.gemm_wgrad(x, y), meaning(x, "columns").t(), meaning(y, "columns"), 300)
+
+
+GROUPS = [([40, 0, 256, 1, 300], 0), ([0, 0, 5], 9), ([128], 0), ([1] * 12, 3), ([257, 255], 1), ([0, 0], 4)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts,tail", GROUPS)
+def test_gemm_of_groups(fp8, counts, tail, trans):
+    rows, N, K, E = sum(counts) + tail, 270, 200, len(counts)
+    a, b = operands(fp8, rows, N, K, trans, experts=E)
+    off = offsets_of(counts).cuda()
+    out = torch.full((rows, N), float("nan"), device="cuda")
+    c = fp8.gemm(a, b, off, out, transB=trans)
+    A, B, at = meaning(a, "rows"), op(meaning(b, "blocks"), trans), 0
+    for e, n in enumerate(counts):
+        if n:
+            check_product(c[at:at + n], A[at:at + n], B[e], K, f"group {e}")
+        at += n
+    assert not c[at:].any() and bool(torch.isfinite(c).all())
+
+
+@pytest.mark.parametrize("counts,tail", GROUPS)
+@pytest.mark.parametrize("M,N", [(1, 1), (130, 270), (256, 96), (300, 33)])
+def test_wgrad_of_groups(fp8, counts, tail, M, N):
+    rows, E = sum(counts) + tail, len(counts)
+    g = torch.Generator(device="cuda").manual_seed(rows + M)
+    x, y = (torch.randn((rows, n), generator=g, device="cuda") for n in (M, N))
+    off = offsets_of(counts).cuda()
+    a, b = fp8.quantize(x, "columns", offsets=off), fp8.quantize(y, "columns", dtype=E5M2, offsets=off)
+    out = torch.full((E, M, N), float("nan"), device="cuda")
+    c = fp8.gemm_wgrad(a, b, off, out)
+    A, B, at = meaning(a, "columns"), meaning(b, "columns"), 0
+    for e, n in enumerate(counts):
+        blocks = -(-n // 128)
+        r = slice(128 * at, 128 * (at + blocks))
+        check_product(c[e], A[r].t(), B[r], n, f"group {e}")
+        at += blocks
+    for dtype in (torch.bfloat16, torch.float16):
+        half = fp8.gemm_wgrad(a, b, off, dtype=dtype)
+        assert torch.equal(half, c.to(dtype))
+
+
+@pytest.mark.parametrize("rows,M,N", [(1, 1, 1), (127, 64, 40), (128, 128, 128), (300, 257, 260), (1025, 33, 300)])
+def test_wgrad(fp8, rows, M, N):
+    g = torch.Generator(device="cuda").manual_seed(rows + M)
+    a, b = (fp8.quantize(torch.randn((rows, n), generator=g, device="cuda"), "columns") for n in (M, N))
+    check_product(fp8.gemm_wgrad(a, b), meaning(a, "columns").t(), meaning(b, "columns"), rows)
+
+
+def test_a_row_depends_on_itself(fp8):
+    """The same row gives the same bits alone, among others and in a group."""
+    a, b = operands(fp8, 700, 520, 384, True)
+    all_rows = fp8.gemm(a, b, transB=True, dtype=torch.float32)
+    for r in (slice(0, 1), slice(3, 50), slice(255, 600)):
+        some = fp8.Quantized(a.values[r], a.scales[:, r].contiguous())
+        assert torch.equal(fp8.gemm(some, b, transB=True, dtype=torch.float32), all_rows[r])
+    stack = fp8.Quantized(b.values[None].repeat(3, 1, 1), b.scales[None].repeat(3, 1, 1))
+    off = torch.tensor([0, 37, 37, 700], dtype=torch.int32, device="cuda")
+    assert torch.equal(fp8.gemm(a, stack, off, transB=True, dtype=torch.float32), all_rows)
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (3, 1), (8, 8)])
+def test_strides_and_what_lies_around(fp8, pad, offset):
+    a, b = operands(fp8, 300, 260, 300, True)
+    for dtype in DTYPES.values():
+        want = fp8.gemm(a, b, transB=True, dtype=dtype)
+        out = strided(torch.zeros((300, 260), dtype=dtype), pad, offset)
+        assert torch.equal(fp8.gemm(a, b, out=out, transB=True), want)
+        assert canaries_intact(out)
+    x, y = (fp8.quantize(torch.randn((300, n), device="cuda"), "columns") for n in (140, 150))
+    want = fp8.gemm_wgrad(x, y)
+    out = strided(torch.zeros((140, 150)), pad, offset)
+    assert torch.equal(fp8.gemm_wgrad(x, y, out=out), want) and canaries_intact(out)
+    # Operands with rows further apart, and matrices of a stack further apart than they are long.
+    wide = torch.zeros((300, 512), dtype=torch.uint8, device="cuda").view(E4M3)
+    wide.view(torch.uint8)[:, 16:316] = a.values.view(torch.uint8)
+    stack = torch.zeros((2, 400, 320), dtype=torch.uint8, device="cuda").view(E4M3)
+    stack.view(torch.uint8)[:, :260, :300] = b.values.view(torch.uint8)
+    b2 = fp8.Quantized(stack[:, :260, :300], b.scales[None].repeat(2, 1, 1))
+    off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    got = fp8.gemm(fp8.Quantized(wide[:, 16:316], a.scales), b2, off, transB=True)
+    assert torch.equal(got, fp8.gemm(a, b, transB=True))
+
+
+def test_nan_stays_in_its_row(fp8):
+    x = torch.randn((300, 260), device="cuda")
+    x[7, 200], x[290, 0] = float("nan"), float("inf")
+    w = torch.randn((300, 260), device="cuda")
+    clean = x.clone()
+    clean[7, 200] = clean[290, 0] = 0
+    b = fp8.quantize(w, "blocks")
+    bad = fp8.gemm(fp8.quantize(x, "rows"), b, transB=True)
+    assert bool(torch.isnan(bad[[7, 290]]).all())
+    rest = [r for r in range(300) if r not in (7, 290)]
+    assert torch.equal(bad[rest], fp8.gemm(fp8.quantize(clean, "rows"), b, transB=True)[rest])
+    # A group's NaN does not reach the next group, whose rows share its tiles' loads.
+    off = torch.tensor([0, 8, 300], dtype=torch.int32, device="cuda")
+    stack = fp8.quantize(torch.stack([w, w]), "blocks")
+    assert bool(torch.isfinite(fp8.gemm(fp8.quantize(x, "rows"), stack, off, transB=True)[rest]).all())
+    g = fp8.gemm_wgrad(fp8.quantize(x, "columns", offsets=off), fp8.quantize(x, "columns", offsets=off), off)
+    assert bool(torch.isnan(g[0, 200]).all()) and bool(torch.isnan(g[1, 0]).all())
+    assert bool(torch.isfinite(g[0, :200, :200]).all()) and bool(torch.isfinite(g[1, 1:, 1:]).all())
+
+
+def test_products_of_nothing(fp8):
+    q = lambda r, c, block: fp8.quantize(torch.zeros((r, c), device="cuda"), block)  # noqa: E731
+    assert fp8.gemm(q(0, 64, "rows"), q(32, 64, "blocks"), transB=True).shape == (0, 32)
+    assert fp8.gemm(q(4, 64, "rows"), q(0, 64, "blocks"), transB=True).shape == (4, 0)
+    out = torch.full((4, 32), 5.0, device="cuda")
+    fp8.gemm(q(4, 0, "rows"), q(32, 0, "blocks"), out=out, transB=True)
+    assert not out.any()
+    out = torch.full((2, 16, 32), 5.0, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    fp8.gemm_wgrad(q(0, 16, "columns"), q(0, 32, "columns"), off, out)
+    assert not out.any()
+
+
+def test_offsets_are_limited(fp8):
+    a, b = operands(fp8, 200, 64, 128, True, experts=2)
+    for off in ([0, 1000, 2000], [0, 150, 100], [0, -3, 200]):
+        t = torch.tensor(off, dtype=torch.int32, device="cuda")
+        assert bool(torch.isfinite(fp8.gemm(a, b, t, transB=True)).all())
+        x = fp8.quantize(torch.randn((200, 64), device="cuda"), "columns", offsets=t)
+        assert bool(torch.isfinite(fp8.gemm_wgrad(x, x, t)).all())
+
+
+def test_gradients_against_differences(fp8):
+    """The products are bilinear: with changes E and G of the values (8-bit ones, at the same scales), <D, (A + E) B -
+    A B> = <D B^T, E> and <D, A (B + G) - A B> = <A^T D, G>."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    S, N, K = 256, 128, 256
+
+    def pick(*shape):  # whole numbers: sums below 2^24 are exact
+        return torch.randint(-4, 5, shape, generator=g, device="cuda").float()
+
+    def quantized(v, block):
+        high, wide = {"rows": (1, 128), "columns": (128, 1), "blocks": (128, 128)}[block]
+        s = torch.ones((-(-v.shape[0] // high), -(-v.shape[1] // wide)), device="cuda")
+        return fp8.Quantized(v.to(E4M3), s.t().contiguous() if block == "rows" else s)
+
+    A, B, D, E, G = pick(S, K), pick(K, N), pick(S, N), pick(S, K), pick(K, N)
+    f = lambda a, b: fp8.gemm(quantized(a, "rows"), quantized(b, "blocks"), dtype=torch.float32).double()  # noqa: E731
+    dA = fp8.gemm(quantized(D, "rows"), quantized(B, "blocks"), transB=True, dtype=torch.float32).double()
+    dB = fp8.gemm_wgrad(quantized(A, "columns"), quantized(D, "columns")).double()
+    assert float((D * (f(A + E, B) - f(A, B))).sum()) == float((dA * E).sum())
+    assert float((D * (f(A, B + G) - f(A, B))).sum()) == float((dB * G).sum())
+
+
+def test_refusals(fp8):
+    a, b = operands(fp8, 32, 64, 128, True)
+    with pytest.raises(ValueError, match="16-byte"):
+        fp8.gemm(fp8.Quantized(a.values[:, 1:], a.scales), fp8.Quantized(b.values[:, 1:], b.scales), transB=True)
+    with pytest.raises(ValueError, match="inner"):
+        fp8.gemm(a, b)
+    with pytest.raises(ValueError, match="shape"):
+        fp8.gemm(fp8.Quantized(a.values, a.scales.t().contiguous()), b, transB=True)
+    with pytest.raises(ValueError, match="whole blocks"):
+        x = fp8.quantize(torch.zeros((130, 64), device="cuda"), "columns")
+        fp8.gemm_wgrad(x, x, torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        fp8.quantize(torch.zeros((4, 4), device="cuda"), "rows", offsets=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(TypeError):
+        fp8.gemm(a, b, transB=True, dtype=torch.float64)

@@ -1,0 +1,219 @@
+"""The mixture-of-experts layer for a few tokens against its definition in 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.experts_harness import DTYPES, canaries_intact, random_ids, strided
+from tests.fp8_harness import E4M3, E5M2, check_layer, meaning
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from dense_fp32_matrix_major_gb300 import layer
+
+    return layer
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    from dense_fp32_matrix_major_gb300 import fp8
+
+    return fp8
+
+
+def case(tokens, top_k, experts, width, hidden, dtype, gated, drop=0.0, skew=0.0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + tokens + 3 * width + 5 * hidden)
+
+    def randn(*shape, scale=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+    ids = random_ids(np.random.default_rng(seed + tokens), tokens, top_k, experts, drop, skew).cuda()
+    return {"x": randn(tokens, width), "ids": ids, "weights": torch.rand((tokens, top_k), generator=g, device="cuda"),
+            "w1": randn(experts, hidden * (2 if gated else 1), width, scale=max(width, 1) ** -0.5),
+            "w2": randn(experts, width, hidden, scale=max(hidden, 1) ** -0.5)}
+
+
+def check(layer, c, gated, act, fp8=None, to=None, what=""):
+    w1, w2 = c["w1"], c["w2"]
+    if fp8 is not None:
+        w1, w2 = fp8.quantize(w1, "blocks", dtype=to), fp8.quantize(w2, "blocks", dtype=to)
+        d1, d2 = meaning(w1, "blocks"), meaning(w2, "blocks")
+    else:
+        d1, d2 = w1.double(), w2.double()
+    y = layer.forward(c["x"], c["ids"], c["weights"], w1, w2, gated=gated, activation=act)
+    check_layer(y, c["x"], c["ids"], c["weights"], d1, d2, gated, act, what)
+    return y
+
+
+# tokens, top_k, experts, width, hidden
+SIZES = [(1, 1, 1, 1, 1), (1, 8, 64, 256, 64), (2, 2, 4, 64, 1), (3, 4, 9, 301, 133), (1, 1, 3, 8, 2000),
+         (5, 2, 3, 1000, 72), (17, 1, 1, 130, 96), (9, 6, 5, 520, 248), (40, 4, 6, 328, 160), (64, 8, 8, 256, 512),
+         (512, 1, 40, 64, 40), (8, 64, 100, 72, 24), (4, 2, 4096, 32, 16), (2, 2, 2, 5000, 24)]
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("size", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
+def test_layer(layer, name, size):
+    for gated, act in ((True, "silu"), (False, "gelu")):
+        check(layer, case(*size, DTYPES[name], gated, drop=0.1), gated, act, what=f"{gated}")
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("to", [E4M3, E5M2])
+@pytest.mark.parametrize("size", SIZES[:12], ids=["x".join(map(str, s)) for s in SIZES[:12]])
+def test_layer_of_8_bit_matrices(layer, fp8, name, to, size):
+    for gated, act in ((True, "silu"), (False, "relu")):
+        check(layer, case(*size, DTYPES[name], gated, drop=0.1), gated, act, fp8, to, f"{gated}")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu", None])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations(layer, act, gated):
+    for dtype in DTYPES.values():
+        check(layer, case(6, 2, 4, 128, 96, dtype, gated), gated, act)
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_all_pairs_of_one_expert(layer, name):
+    """Entries of eight pairs each, the last of any number; the same expert twice for a token."""
+    for tokens in (1, 7, 8, 9, 16, 33, 64):
+        c = case(tokens, 2, 3, 136, 72, DTYPES[name], True)
+        c["ids"][:] = 1
+        check(layer, c, True, "silu", what=str(tokens))
+
+
+def test_dropped_pairs(layer):
+    for dtype in DTYPES.values():
+        c = case(6, 3, 4, 96, 80, dtype, True)
+        c["ids"][0] = torch.tensor([-1, 4, 1 << 40])
+        c["ids"][1, 1] = -7
+        c["weights"][0] = float("nan")
+        c["weights"][1, 1] = float("inf")
+        y = check(layer, c, True, "silu")
+        assert not y[0].any()
+        c["ids"][:] = -1
+        assert not layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True).any()
+        c["ids"] = torch.randint(-1, 4, (6, 3), device="cuda", dtype=torch.int32)
+        c["weights"] = torch.rand((6, 3), device="cuda")
+        check(layer, c, True, "silu")
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (0, 1), (8, 8), (3, 5)])
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_strides(layer, name, pad, offset):
+    dtype = DTYPES[name]
+    c = case(5, 2, 3, 136, 72, dtype, True)
+    want = layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True)
+    flat = {k: strided(c[k].flatten(0, -2), pad, offset) for k in ("x", "w1", "w2")}
+    out = strided(torch.zeros((5, 136), dtype=dtype), pad, offset)
+    args = {k: (v if k == "x" else v.as_strided(c[k].shape, (v.stride(0) * c[k].shape[1], v.stride(0), 1),
+                                                v.storage_offset())) for k, v in flat.items()}
+    y = layer.forward(args["x"], c["ids"], c["weights"], args["w1"], args["w2"], gated=True, out=out)
+    check_layer(y, c["x"], c["ids"], c["weights"], c["w1"].double(), c["w2"].double(), True, "silu")
+    assert canaries_intact(out)
+    if pad == offset == 0:
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_infinities_and_nan(layer, fp8, name):
+    """What is not finite stays with its token, and infinities are what IEEE arithmetic makes of them."""
+    c = case(6, 2, 4, 128, 64, DTYPES[name], False)
+    bad = dict(c, x=c["x"].clone())
+    bad["x"][1, 5] = float("nan")
+    bad["x"][4, 100] = float("inf")
+    for w1, w2 in ((c["w1"], c["w2"]), tuple(fp8.quantize(c[w], "blocks") for w in ("w1", "w2"))):
+        fine = layer.forward(c["x"], c["ids"], c["weights"], w1, w2, activation="relu")
+        y = layer.forward(bad["x"], c["ids"], c["weights"], w1, w2, activation="relu")
+        assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[4]).any())
+        rest = [0, 2, 3, 5]
+        assert torch.equal(y[rest], fine[rest])
+    # Positive weights: an infinity in x is one in h and in y, not a NaN.
+    y = layer.forward(bad["x"], c["ids"], c["weights"], torch.ones_like(c["w1"]), torch.ones_like(c["w2"]),
+                      activation="relu")
+    assert bool((y[4] == float("inf")).all()) and bool(torch.isfinite(y[rest]).all())
+
+
+def test_outliers_at_zero_weights(layer, fp8):
+    """A value of x far above the rest, at weights that are zero, costs the rest no digits."""
+    for dtype in DTYPES.values():
+        c = case(4, 2, 3, 256, 64, dtype, True)
+        big = 6e4 if dtype == torch.float16 else 1e30
+        c["w1"][:, :, 17] = 0
+        want = layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True)
+        q1, q2 = fp8.quantize(c["w1"], "blocks"), fp8.quantize(c["w2"], "blocks")
+        want8 = layer.forward(c["x"], c["ids"], c["weights"], q1, q2, gated=True)
+        c["x"][:, 17] = big
+        assert torch.equal(layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True), want)
+        assert torch.equal(layer.forward(c["x"], c["ids"], c["weights"], q1, q2, gated=True), want8)
+
+
+def test_hidden_values_past_fp16(layer):
+    """h above fp16's largest number, where y is within its range."""
+    c = case(3, 2, 3, 64, 40, torch.float16, True)
+    c["w1"] *= 300
+    c["w2"] *= 1e-3
+    check(layer, c, True, None)
+
+
+def test_nothing(layer):
+    f = lambda t, k, w, h: layer.forward(  # noqa: E731
+        torch.zeros((t, w), device="cuda"), torch.zeros((t, k), dtype=torch.int64, device="cuda"),
+        torch.ones((t, k), device="cuda"), torch.zeros((2, h, w), device="cuda"), torch.zeros((2, w, h), device="cuda"))
+    assert f(0, 2, 16, 8).shape == (0, 16)
+    assert f(3, 2, 0, 8).shape == (3, 0)
+    out = torch.full((3, 16), 7.0, device="cuda")
+    layer.forward(torch.zeros((3, 16), device="cuda"), torch.zeros((3, 2), dtype=torch.int64, device="cuda"),
+                  torch.ones((3, 2), device="cuda"), torch.zeros((2, 0, 16), device="cuda"),
+                  torch.zeros((2, 16, 0), device="cuda"), out=out)
+    assert not out.any()
+
+
+def test_same_bits_again(layer):
+    for dtype in DTYPES.values():
+        c = case(30, 4, 7, 520, 264, dtype, True)
+        one = layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True)
+        for _ in range(5):
+            assert torch.equal(layer.forward(c["x"], c["ids"], c["weights"], c["w1"], c["w2"], gated=True), one)
+
+
+def test_offsets_past_32_bits(layer):
+    """Matrices whose elements lie more than 2^31 elements into the stack."""
+    E, D, F = 1100, 1024, 2048
+    w1 = torch.empty((E, F, D), dtype=torch.bfloat16, device="cuda").fill_(float("nan"))
+    w2 = torch.empty((E, D, F), dtype=torch.bfloat16, device="cuda").fill_(float("nan"))
+    assert w1.numel() > 2 ** 31
+    used = [0, 1099, 1050]
+    for e in used:
+        w1[e] = torch.randn((F, D), device="cuda") * D ** -0.5
+        w2[e] = torch.randn((D, F), device="cuda") * F ** -0.5
+    x = torch.randn((2, D), device="cuda").bfloat16()
+    ids = torch.tensor([[1099, 0], [1050, 1099]], device="cuda")
+    w = torch.rand((2, 2), device="cuda")
+    y = layer.forward(x, ids, w, w1, w2, activation="relu")
+    small = torch.tensor([[1, 0], [2, 1]], device="cuda")
+    check_layer(y, x, small, w, w1[used].double(), w2[used].double(), False, "relu")
+
+
+def test_refusals(layer, fp8):
+    c = case(4, 2, 3, 64, 32, torch.bfloat16, True)
+    args = [c["x"], c["ids"], c["weights"], c["w1"], c["w2"]]
+
+    def call(i, value, **kw):
+        return layer.forward(*[value if j == i else a for j, a in enumerate(args)], **{"gated": True, **kw})
+
+    for i, value, error in ((0, c["x"].float(), TypeError), (1, c["ids"].float(), TypeError),
+                            (1, c["ids"][:2], ValueError), (2, c["weights"].double(), TypeError),
+                            (2, c["weights"][:, :1].contiguous(), ValueError), (3, c["w1"][:, :, :32], ValueError),
+                            (4, c["w2"].transpose(1, 2), ValueError), (4, c["w2"][:2], ValueError),
+                            (4, fp8.quantize(c["w2"], "blocks"), TypeError), (3, c["w1"][:, :63], ValueError)):
+        with pytest.raises(error):
+            call(i, value)
+    with pytest.raises(ValueError, match="activation"):
+        call(0, c["x"], activation="tanh")
+    with pytest.raises(ValueError, match="pairs"):
+        layer.forward(torch.zeros((300, 64), device="cuda"), torch.zeros((300, 2), dtype=torch.int64, device="cuda"),
+                      torch.zeros((300, 2), device="cuda"), c["w1"].float(), c["w2"].float(), gated=True)
