@@ -62,25 +62,25 @@ using namespace tc;
 
 constexpr int PN = 256, PM = 256, HALF = 128;  // C's columns and rows of a pair, a CTA's share
 constexpr int KB = BLOCK;                      // k-block: 128 values = 128 bytes
-constexpr int COL_STEP = 32;                   // the MMA's width is a multiple of it
 constexpr int FEW = 32;                        // rows of the small box of A
 constexpr int BOX = 128 * 128;                 // bytes of a staged operand
-constexpr int STAGE = 2 * BOX, STAGES = 6;
+constexpr int STAGE = 2 * BOX, STAGES = 4;
 constexpr int EPI_WARPS = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI_WARPS) * 32;
 constexpr int RING = 8;                        // k-blocks of wgrad's prepared scales
 constexpr int RING_BYTES = PN * 4;
-// A warp's part of C on its way out: rows of 64 bytes (rows), 8 rows of 32 fp32
-// values (wgrad), both padded so that every phase of the accesses meets all banks.
-constexpr int OUT_ROW = 80, OUT_WGRAD = 144, OUT_BYTES = 32 * OUT_ROW;
-constexpr int RING0 = STAGES * STAGE, OUT0 = RING0 + RING * RING_BYTES, BAR0 = OUT0 + EPI_WARPS * OUT_BYTES;
+// C on its way out: two chunks a warp of 32 rows by 128 bytes, as TMA takes them; or,
+// where it cannot, rows of 64 bytes (rows) or 8 rows of 32 fp32 values (wgrad),
+// padded so that every phase of the accesses meets all banks.
+constexpr int OUT_CHUNK = 32 * 128, OUT_ROW = 80, OUT_WGRAD = 144, OUT_BYTES = 2 * OUT_CHUNK;
+constexpr int OUT0 = STAGES * STAGE, RING0 = OUT0 + EPI_WARPS * OUT_BYTES, BAR0 = RING0 + RING * RING_BYTES;
 // mbarriers
-constexpr int FULL = 0, EMPTY = FULL + STAGES, SUM_FULL = EMPTY + STAGES, SUM_EMPTY = SUM_FULL + 2,
-              RING_FULL = SUM_EMPTY + 2, RING_EMPTY = RING_FULL + RING, DRAIN = RING_EMPTY + RING, NBARS = DRAIN + 1;
+constexpr int FULL = 0, EMPTY = FULL + STAGES, SUM_FULL = EMPTY + STAGES, SUM_EMPTY = SUM_FULL + 4,
+              RING_FULL = SUM_EMPTY + 4, RING_EMPTY = RING_FULL + RING, DRAIN = RING_EMPTY + RING, NBARS = DRAIN + 1;
 constexpr int SMEM_BYTES = BAR0 + 512 + 1024;
 static_assert(NBARS * 8 + 16 <= 512, "barrier block");
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert(8 * OUT_WGRAD <= OUT_BYTES, "staging of C");
-static_assert(RING0 % 1024 == 0 && RING_BYTES % 16 == 0 && OUT0 % 16 == 0 && BAR0 % 8 == 0, "alignment");
+static_assert(8 * OUT_WGRAD <= OUT_CHUNK && 32 * OUT_ROW <= OUT_CHUNK, "staging of C");
+static_assert(OUT0 % 1024 == 0 && RING_BYTES % 16 == 0 && BAR0 % 8 == 0, "alignment");
 // Registers a thread of the four and of the eight warps, out of 168 each.
 constexpr int FEW_REGS = 88, MANY_REGS = 208;
 static_assert(4 * FEW_REGS + 8 * MANY_REGS <= 12 * 168, "registers of the launch");
@@ -100,7 +100,7 @@ struct Args {
     int64_t item_cols, n_cols, b_cols;
     void *C;
     int64_t ldc, strideC;
-    int out_type, vector;  // C in 16-byte stores
+    int out_type, vector, tma;  // C in 16-byte stores; through TMA
     uint32_t idesc;        // without N
     uint64_t timeout_ns;
     int *watchdog;
@@ -148,11 +148,12 @@ __device__ __forceinline__ void for_each_tile(const Args &a, volatile int *abort
     }
 }
 
-// The MMA's width: the tile's columns, rounded up.
-__device__ __forceinline__ int width_of(const Args &a, const Tile &u) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(PN), a.N - u.n0));
-    return (n + COL_STEP - 1) / COL_STEP * COL_STEP;
-}
+// Columns of B that a CTA stages for each half of the tile: a quarter of 256 or of
+// 128. Half h of the tile is columns [h * quarter, (h + 1) * quarter) of what the
+// even CTA stages, then of what the odd one does: accumulator column j < quarter
+// is column h * quarter + j of the tile, column quarter + j column (2 + h) *
+// quarter + j.
+__device__ __forceinline__ int quarter_of(const Args &a, const Tile &u) { return a.N - u.n0 > PN / 2 ? PN / 4 : PN / 8; }
 
 // Rows of A that CTA `rank` stages in a k-block: as many as a box has, or none.
 __device__ __forceinline__ int box_rows(const Tile &u, uint32_t rank) {
@@ -188,40 +189,36 @@ __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// 16 lanes x 32 columns of 32 bits from tensor memory: r[2 i + h] is lane
-// (thread / 4) + 8 h, column 4 i + thread % 4. Not waited for.
-__device__ __forceinline__ void tmem_load_16x32(uint32_t taddr, uint32_t *r) {
+// 32 lanes x 32 columns of 32 bits from tensor memory, waited for: r[i] is this
+// lane's column i. (The wait in a statement of its own, with the registers tied to
+// it, cost a hundred moves a k-block and warp.)
+__device__ __forceinline__ void tmem_load_32x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-// 32 lanes x 32 columns: r[i] is this lane's column i. Not waited for.
-__device__ __forceinline__ void tmem_load_32x32(uint32_t taddr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
+        : "r"(taddr)
+        : "memory");
 }
 
-// Waits for the thread's loads from tensor memory; ties the registers to it.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
+// The same 32 x 32 values by four lanes and a quarter of the columns a thread:
+// r[16 l + 2 i + h] is lane 16 l + 8 h + (thread / 4), column 4 i + thread % 4.
+__device__ __forceinline__ void tmem_load_2x16x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n"
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "[%33];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
 }
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -310,8 +307,9 @@ __device__ __forceinline__ void write_lanes(const Args &a, uint32_t out, int lan
 template <Form FORM>
 __global__ void __launch_bounds__(THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm1_few,
-                    const __grid_constant__ CUtensorMap tm2, const __grid_constant__ Args a) {
-    // tm1, tm2: A and B; tm1_few: A in boxes of 32 rows (rows).
+                    const __grid_constant__ CUtensorMap tm2, const __grid_constant__ CUtensorMap tm_out,
+                    const __grid_constant__ Args a) {
+    // tm1, tm2: A and B; tm1_few: A in boxes of 32 rows (rows); tm_out: C in boxes of 32 rows by 128 bytes.
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -328,9 +326,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(bar(FULL + s), 1);
             mbar_init(bar(EMPTY + s), 1);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < 4; ++d) {
             mbar_init(bar(SUM_FULL + d), 1);
-            mbar_init(bar(SUM_EMPTY + d), 2 * EPI_WARPS);
+            mbar_init(bar(SUM_EMPTY + d), EPI_WARPS);
         }
         for (int r = 0; r < RING; ++r) {
             mbar_init(bar(RING_FULL + r), 1);
@@ -370,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t it = 0;
                 bool ok = true;
                 for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
-                    const int n0 = u.n0 + width_of(a, u) / 2 * static_cast<int>(rank);
+                    const int n0 = u.n0 + 2 * quarter_of(a, u) * static_cast<int>(rank);
                     const int r0 = u.row0 + HALF * static_cast<int>(rank);
                     const int own = FORM == WGRAD ? HALF : box_rows(u, rank);
                     const uint32_t bytes =
@@ -407,14 +405,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t it = 0;
                 bool ok = true;
                 for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
-                    const uint32_t idesc = a.idesc | (static_cast<uint32_t>(width_of(a, u) >> 3) << 17);
+                    const int quarter = quarter_of(a, u);
+                    const uint32_t idesc = a.idesc | (static_cast<uint32_t>(2 * quarter >> 3) << 17);
+                    // The second half's columns: rows of 128 bytes each, or one byte.
+                    const uint32_t next_half = static_cast<uint32_t>(quarter * (FORM == ROWS_T ? 128 : 1)) >> 4;
                     // 32 values of k further: 32 bytes along a K-major row, 32 rows of 128
                     // bytes in an MN-major box.
                     constexpr uint32_t step1 = (FORM == WGRAD ? 32 * 128 : 32) >> 4;
                     constexpr uint32_t step2 = (FORM == ROWS_T ? 32 : 32 * 128) >> 4;
                     for (int kb = 0; kb < u.k_blocks && ok; ++kb, ++it) {
                         const int s = static_cast<int>(it % STAGES);
-                        const uint32_t d = it & 1;
                         const uint32_t s1 = base + static_cast<uint32_t>(s * STAGE), s2 = s1 + BOX;
                         // The descriptors of both layouts are alike: 8 rows (K-major) or 8
                         // k (MN-major, 128 values each) to the next 8 are 1024 bytes.
@@ -422,18 +422,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(bar(FULL + s), (it / STAGES) & 1, a, abort_flag, WD_MMA_FULL));
                         if (!ok) return;
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(SUM_EMPTY + d), ((it >> 1) & 1) ^ 1, a, abort_flag,
-                                                               WD_MMA_ACC));
-                        if (!ok) return;
-                        tc_fence_after();
-                        if (leader) {
 #pragma unroll
-                            for (int ks = 0; ks < KB / 32; ++ks)
-                                mma8_pair(tmem_base + d * PN, d1 + ks * step1, d2 + ks * step2, idesc, ks > 0);
-                            tc_commit2(bar(SUM_FULL + d));
-                            tc_commit2(bar(EMPTY + s));
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t d = 2 * (it & 1) + h;
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar(SUM_EMPTY + d), ((it >> 1) & 1) ^ 1, a,
+                                                                   abort_flag, WD_MMA_ACC));
+                            if (!ok) return;
+                            tc_fence_after();
+                            if (leader) {
+#pragma unroll
+                                for (int ks = 0; ks < KB / 32; ++ks)
+                                    mma8_pair(tmem_base + d * (PN / 2), d1 + ks * step1,
+                                              d2 + h * next_half + ks * step2, idesc, ks > 0);
+                                tc_commit2(bar(SUM_FULL + d));
+                                if (h == 1) tc_commit2(bar(EMPTY + s));
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 });
                 if (leader) tc_commit2(bar(DRAIN));
@@ -456,7 +461,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
                 const float *from = a.scale_cols + static_cast<int64_t>(u.k0) * a.b_cols + u.n0 + lane;
                 const int cols = static_cast<int>(min(static_cast<int64_t>(PN), a.N - u.n0)) - lane;
-                // Column 16 c + 4 i + t goes where thread t of a quad reads its four of c.
+                const int quarter = quarter_of(a, u);
+                // In each half, accumulator column 16 c + 4 i + t goes where thread t of a
+                // quad reads its four of c. Quarters are multiples of 32 columns.
                 const int at = (lane & ~15) + ((lane & 3) << 2) + ((lane >> 2) & 3);
                 for (int kb = 0; kb < u.k_blocks && ok; kb += AHEAD) {
                     float v[AHEAD][PN / 32];
@@ -474,7 +481,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!ok) break;
                         const uint32_t to = base + RING0 + static_cast<uint32_t>(s * RING_BYTES + at * 4);
 #pragma unroll
-                        for (int j = 0; j < PN / 32; ++j) st_shared_f32(to + 128 * j, v[i][j]);
+                        for (int j = 0; j < PN / 32; ++j) {
+                            const int part = 32 * j / quarter;
+                            if (part < 4)
+                                st_shared_f32(to + static_cast<uint32_t>((part & 1) * (PN / 2) + (part >> 1) * quarter +
+                                                                         32 * j - part * quarter) * 4, v[i][j]);
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(RING_FULL + s));
                         ++it;
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = w & 3, second = w >> 2;  // quarter of tensor memory's lanes, half of the columns
         const int t = lane & 3, g = lane >> 2;
         const uint32_t out = base + OUT0 + static_cast<uint32_t>(w * OUT_BYTES);
-        const uint32_t sums = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(HALF * second);
+        const uint32_t sums = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(PN / 2 * second);
         uint32_t it = 0;
         bool ok = true;
         // The accumulator is out of tensor memory (this warp's part).
@@ -498,13 +510,35 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) arrive_even(bar(SUM_EMPTY + d));
         };
+        // Sends a chunk to C once fill(address) has written it; two are on their way at most.
+        uint32_t sent = 0;
+        auto send = [&](int64_t col, int row, int item, auto &&fill) {
+            const uint32_t to = out + (sent & 1) * OUT_CHUNK;
+            ++sent;
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            fill(to);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&tm_out, static_cast<int>(col), row, item, to);
+                bulk_commit();
+            }
+        };
+        // Before a chunk's memory is used for other staging.
+        auto settle = [&] {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+        };
         for_each_tile<FORM>(a, abort_flag, pair, pairs, [&](const Tile &u) {
             if (!ok) return;
             const int row0 = u.row0 + HALF * static_cast<int>(rank) + 32 * q;
-            const int64_t col0 = u.n0 + HALF * static_cast<int64_t>(second);
-            const int rows = u.row_end - row0;                                                      // may be negative
-            const int cols = static_cast<int>(min(static_cast<int64_t>(HALF), a.N - col0));         // likewise
-            const int chunks = cols > 0 ? (cols + 31) / 32 : 0;
+            const int rows = u.row_end - row0;  // may be negative
+            const int quarter = quarter_of(a, u), chunks = quarter / 16;
+            // Column of C that chunk c, 32 accumulator columns of this warp's half, starts at.
+            auto column = [&](int c) {
+                return u.n0 + (32 * c < quarter ? second * quarter : (1 + second) * quarter) + 32 * static_cast<int64_t>(c);
+            };
             if constexpr (FORM != WGRAD) {
                 // acc[c][i]: column 32 c + i of this lane's row.
                 float acc[4][32];
@@ -512,50 +546,78 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-                // Factors two blocks ahead.
+                // Factors two blocks ahead: of the lane's row, and of B's blocks of the
+                // half's two parts, which lie in the tile's first and second 128 columns.
                 const float *sr = a.scale_rows + row0 + lane;
-                const float *sc = a.scale_cols + u.group * a.item_cols + col0 / BLOCK * a.n_cols;
-                const bool in = lane < rows && cols > 0;
-                auto factors = [&](int kb, float &x, float &y) {
+                const float *sc = a.scale_cols + u.group * a.item_cols + u.n0 / BLOCK * a.n_cols;
+                const bool in = lane < rows, wide = quarter == PN / 4;
+                auto factors = [&](int kb, float (&f)[3]) {
                     const bool there = in && kb < u.k_blocks;
-                    x = there ? __ldg(sr + kb * a.ld_rows) : 0.0f;
-                    y = there ? __ldg(sc + kb * a.b_cols) : 0.0f;
+                    f[0] = there ? __ldg(sr + kb * a.ld_rows) : 0.0f;
+                    f[1] = there ? __ldg(sc + kb * a.b_cols) : 0.0f;
+                    f[2] = there ? __ldg(sc + kb * a.b_cols + (wide ? a.n_cols : 0)) : 0.0f;
                 };
-                float x0, y0, x1, y1;
-                factors(0, x0, y0);
-                factors(1, x1, y1);
+                float next[2][3];
+                factors(0, next[0]);
+                factors(1, next[1]);
                 for (int kb = 0; kb < u.k_blocks; ++kb, ++it) {
-                    const uint32_t d = it & 1;
-                    const float factor = x0 * y0;
-                    x0 = x1;
-                    y0 = y1;
-                    factors(kb + 2, x1, y1);
+                    const uint32_t d = 2 * (it & 1) + second;
+                    const float factor[2] = {next[0][0] * next[0][1], next[0][0] * next[0][2]};
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) next[0][i] = next[1][i];
+                    factors(kb + 2, next[1]);
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(bar(SUM_FULL + d), (it >> 1) & 1, a, abort_flag, WD_EPILOGUE));
                     if (!ok) return;
                     tc_fence_after();
-                    // A warp without rows or columns only lets go.
-                    if (rows <= 0 || chunks == 0) release(d);
+                    // A warp without rows only lets go.
+                    if (rows <= 0) release(d);
                     else {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             if (c >= chunks) break;
                             uint32_t p[32];
-                            tmem_load_32x32(sums + d * PN + 32 * c, p);
-                            tmem_wait(p);
+                            tmem_load_32x32(sums + (it & 1) * PN + 32 * c, p);
                             if (c == chunks - 1) release(d);
+                            const float f = 2 * c < chunks ? factor[0] : factor[1];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(p[i]), factor, acc[c][i]);
+                            for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(p[i]), f, acc[c][i]);
                         }
                     }
                 }
                 if (rows <= 0) return;
+                const bool f32 = a.out_type == SGEMM_TYPE_F32, bf16 = a.out_type == SGEMM_TYPE_BF16;
+                if (a.tma && rows >= 32 && wide) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (column(c) >= a.N) break;
+                        if (f32) {
+                            send(column(c), row0, 0, [&](uint32_t to) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    st_shared_v4(to + sw128_offset(lane, j), acc[c][4 * j], acc[c][4 * j + 1],
+                                                 acc[c][4 * j + 2], acc[c][4 * j + 3]);
+                            });
+                        } else if (c % 2 == 0) {  // two of them are 64 columns of C
+                            send(column(c), row0, 0, [&](uint32_t to) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float *v = &acc[c + j / 4][8 * (j % 4)];
+                                    sts_128(to + sw128_offset(lane, j), round2(v[0], v[1], bf16), round2(v[2], v[3], bf16),
+                                            round2(v[4], v[5], bf16), round2(v[6], v[7], bf16));
+                                }
+                            });
+                        }
+                    }
+                    return;
+                }
+                settle();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c >= chunks) break;
-                    const int64_t col = col0 + 32 * c;
+                    const int64_t col = column(c);
                     uint32_t v[16];
-                    if (a.out_type == SGEMM_TYPE_F32) {
+                    if (f32) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -565,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            v[i] = round2(acc[c][2 * i], acc[c][2 * i + 1], a.out_type == SGEMM_TYPE_BF16);
+                            v[i] = round2(acc[c][2 * i], acc[c][2 * i + 1], bf16);
                         write_lanes(a, out, lane, v, static_cast<uint16_t *>(a.C), row0, rows, col);
                     }
                 }
@@ -585,29 +647,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float next[4];
                 factors(0, next);
                 for (int kb = 0; kb < u.k_blocks; ++kb, ++it) {
-                    const uint32_t d = it & 1;
+                    const uint32_t d = 2 * (it & 1) + second;
                     const int s = static_cast<int>(it % RING);
                     const uint64_t of_lane[2] = {pack2(__float_as_uint(next[0]), __float_as_uint(next[1])),
                                                  pack2(__float_as_uint(next[2]), __float_as_uint(next[3]))};
                     factors(kb + 1, next);
                     const uint32_t scales =
-                        base + RING0 + static_cast<uint32_t>(s * RING_BYTES + (HALF * second + 4 * t) * 4);
+                        base + RING0 + static_cast<uint32_t>(s * RING_BYTES + (PN / 2 * second + 4 * t) * 4);
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(bar(RING_FULL + s), (it / RING) & 1, a, abort_flag, WD_EPILOGUE)) &&
                          __all_sync(0xffffffffu,
                                     mbar_wait(bar(SUM_FULL + d), (it >> 1) & 1, a, abort_flag, WD_EPILOGUE));
                     if (!ok) return;
                     tc_fence_after();
-                    if (rows <= 0 || chunks == 0) release(d);
+                    if (rows <= 0) release(d);
                     else {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             if (c >= chunks) break;
                             uint32_t p[32];
-                            tmem_load_16x32(sums + d * PN + 32 * c, p);
-                            tmem_load_16x32(sums + d * PN + 32 * c + (16u << 16), p + 16);
                             const uint4 s0 = lds_128(scales + 128 * c), s1 = lds_128(scales + 128 * c + 64);
-                            tmem_wait(p);
+                            tmem_load_2x16x32(sums + (it & 1) * PN + 32 * c, p);
                             if (c == chunks - 1) release(d);
                             const uint32_t x[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
@@ -622,6 +682,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(RING_EMPTY + s));
                 }
+                if (a.tma && rows >= 32 && a.out_type == SGEMM_TYPE_F32) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c >= chunks) break;
+                        if (column(c) >= a.N) continue;
+                        send(column(c), row0, u.group, [&](uint32_t to) {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float x, y;
+                                    unpack2(acc[c][i][h >> 1], x, y);
+                                    st_shared_f32(to + sw128_offset(8 * h + g, i) + 4 * t, h & 1 ? y : x);
+                                }
+                        });
+                    }
+                    return;
+                }
+                settle();
                 // Eight rows by 32 columns at a time, as fp32 through shared memory.
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -642,13 +721,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int r = 4 * j + (lane >> 3);
-                                const int64_t col = col0 + 32 * c + 4 * (lane & 7);
+                                const int64_t col = column(c) + 4 * (lane & 7);
                                 const uint4 x = lds_128(out + static_cast<uint32_t>(r * OUT_WGRAD + 16 * (lane & 7)));
                                 if (r < left) store16<uint32_t, 4>(a, static_cast<uint32_t *>(a.C) + item + r * a.ldc + col, col, x);
                             }
                         } else {
                             const bool bf16 = a.out_type == SGEMM_TYPE_BF16;
-                            const int64_t col = col0 + 32 * c + 8 * t;
+                            const int64_t col = column(c) + 8 * t;
                             const float4 x = ld_shared_v4(out + static_cast<uint32_t>(g * OUT_WGRAD + 32 * t)),
                                          y = ld_shared_v4(out + static_cast<uint32_t>(g * OUT_WGRAD + 32 * t + 16));
                             const uint4 v = make_uint4(round2(x.x, x.y, bf16), round2(x.z, x.w, bf16),
@@ -661,6 +740,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         });
     }
 
+    bulk_wait<0>();  // C is written
     // The odd CTA's tensor memory is written by the even CTA's MMAs: wait for
     // them to drain before the pair releases it. After a wait that gave up,
     // loads may still be on their way: leave them time to land.
@@ -727,7 +807,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     }
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    alignas(64) CUtensorMap map1{}, map2{}, few{};
+    alignas(64) CUtensorMap map1{}, map2{}, few{}, out{};
     Args a{};
     a.offsets = p.offsets;
     a.rows = static_cast<int>(p.rows);
@@ -768,6 +848,13 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
                              : encode_map_typed(&map2, type, 1, p.B, p.K, p.N, p.ldb, p.experts, strideB, HALF, KB, sw));
     }
     if (!ok) return SGEMM_ERR_LAUNCH;
+    const int64_t size = ex::type_size(p.out_type), items = p.wgrad ? p.experts : 1;
+    const CUtensorMapDataType out_type = p.out_type == SGEMM_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : p.out_type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    a.tma = a.vector && encode_map_typed(&out, out_type, size, p.C, p.wgrad ? p.M : p.rows, p.N, p.ldc, items,
+                                         items > 1 ? p.strideC : 0, static_cast<uint32_t>(128 / size), 32, sw);
+    if (!a.tma) out = map1;  // not used by the kernel
     if (row_tiles > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     a.tiles_n = static_cast<int>((p.N + PN - 1) / PN);
     // Instruction descriptor of kind::f8f6f4: D fp32 (bits 4-5 = 1), first and
@@ -782,7 +869,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     const int64_t units = row_tiles * a.tiles_n;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < clusters ? units : clusters)));
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, map1, few, map2, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, map1, few, map2, out, a) != cudaSuccess) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
     }
