@@ -880,6 +880,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
 }  // namespace
 
 int gemm_launch(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    if (gemm_few(p, dev)) return gemm_few_launch(p, stream, launches);
     if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
     if (p.wgrad) return launch_form<WGRAD>(p, dev, stream, launches);
     return p.transB == SGEMM_OP_T ? launch_form<ROWS_T>(p, dev, stream, launches)

@@ -48,5 +48,9 @@ struct GemmProblem {
 };
 int gemm_launch(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 
+// The same for a few rows (fp8_few.cu): whether it takes the problem, and the launch.
+bool gemm_few(const GemmProblem &p, const DeviceInfo &dev);
+int gemm_few_launch(const GemmProblem &p, cudaStream_t stream, int *launches);
+
 }  // namespace f8
 }  // namespace sgemm

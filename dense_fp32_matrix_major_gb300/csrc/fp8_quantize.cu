@@ -35,6 +35,8 @@ constexpr float SMALLEST_SCALE = 1.17549435e-38f;  // 2^-126
 
 struct QArgs {
     int64_t rows, cols;
+    unsigned high, wide;  // blocks of rows and of columns of an item
+    int64_t tiles;        // 128 x 128 tiles of all
     const void *x;
     int64_t ldx, strideX;
     const int32_t *offsets;
@@ -170,128 +172,230 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const __grid_con
 
 // ----------------------------------------------- 128 x 1 and 128 x 128 blocks
 
-// Columns of a thread: VECTOR: eight next to one another; otherwise sixteen
-// apart, so that a warp's scalar loads are next to one another, and q goes
-// through shared memory on its way out.
-template <class T, bool E5M2, bool COLUMNS, bool VECTOR>
-__global__ void __launch_bounds__(THREADS) quantize_tiles_kernel(const __grid_constant__ QArgs a) {
+// How a thread gets its 8 x 8 values, rows 16 apart:
+//   ASYNC   16-bit values in rows that are 16-byte aligned: eight columns next to one
+//           another, copied to shared memory while the CTA is at the tile before;
+//   VECTOR  32-bit values in such rows: the same columns, straight to registers;
+//   SCALAR  columns 16 apart, so that a warp's loads are next to one another; q goes
+//           through shared memory on its way out.
+enum Load { ASYNC, VECTOR, SCALAR };
+
+constexpr int TILE_STAGES = 2, TILE_CTAS = 3;  // ASYNC: tiles in shared memory, CTAs of an SM
+constexpr int TILE_STAGE = 8 * THREADS * 16;
+
+// 16 bytes of which the first `bytes` are read, the others zero.
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
+// Tiles [first, last) of 128 x 128 values, in the order items, row blocks, columns.
+template <class T, bool E5M2, bool COLUMNS, Load LOAD>
+__global__ void __launch_bounds__(THREADS, LOAD == ASYNC || !COLUMNS ? TILE_CTAS : 2)
+    quantize_tiles_kernel(const __grid_constant__ QArgs a) {
+    constexpr int MAXIMA = COLUMNS ? 8 : 1;
     __shared__ float most_of[COLUMNS ? 8 * BLOCK : 8];
-    __shared__ float scale_s[COLUMNS ? BLOCK : 1], inverse_s[COLUMNS ? BLOCK : 1];
-    __shared__ int infinite_s;
-    __shared__ alignas(16) uint8_t tile[VECTOR ? 16 : BLOCK * (BLOCK + 16)];
+    __shared__ float inverse_s[COLUMNS ? BLOCK : 1];
+    __shared__ alignas(16) uint8_t tile[LOAD == SCALAR ? BLOCK * (BLOCK + 16) : 16];
+    extern __shared__ __align__(16) uint8_t staged[];
     const int tid = static_cast<int>(threadIdx.x), part = tid & 15, r0 = tid >> 4, warp = tid >> 5, lane = tid & 31;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.y) * BLOCK;
-    if (tid == 0) infinite_s = 0;
-    // Rows of x, and the row of q they start at.
-    int64_t begin = static_cast<int64_t>(blockIdx.x) * BLOCK;
-    const int64_t at = begin;
-    int rows = static_cast<int>(min(static_cast<int64_t>(BLOCK), a.rows - begin)), kept = rows;
-    if (COLUMNS && a.offsets) {
-        const RowTile t = row_tile_of(a.offsets, a.experts, static_cast<int>(a.rows), BLOCK, static_cast<int>(blockIdx.x));
-        const bool used = t.group >= 0 && t.group < a.experts;
-        begin = used ? t.begin : 0;
-        rows = used ? t.end - t.begin : 0;
-        kept = BLOCK;
-    }
-    const T *x = static_cast<const T *>(a.x) + blockIdx.z * a.strideX + begin * a.ldx + c0;
-    const int64_t cols = a.cols - c0;
-    auto col = [&](int j) { return VECTOR ? 8 * part + j : part + 16 * j; };
-    float v[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        const T *p = x + r * a.ldx;
-        if (VECTOR && r < rows && 8 * part + 8 <= cols) {
-            load_vector<T, 8>(p + 8 * part, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = r < rows && col(j) < cols ? to_f32(p[col(j)]) : 0.0f;
-        }
-    }
-    float most[COLUMNS ? 8 : 1], inverse[COLUMNS ? 8 : 1];
-    // Joins the maxima of the block's threads, or of a column's.
-    auto join = [&](auto &&larger_of) {
-#pragma unroll
-        for (int j = 0; j < (COLUMNS ? 8 : 1); ++j) most[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) most[COLUMNS ? j : 0] = larger_of(most[COLUMNS ? j : 0], v[i][j]);
-        if (COLUMNS) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                most[j] = fmaxf(most[j], __shfl_xor_sync(0xffffffffu, most[j], 16));
-                if (lane < 16) most_of[warp * BLOCK + col(j)] = most[j];
-            }
-        } else {
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], d));
-            if (lane == 0) most_of[warp] = most[0];
-        }
-        __syncthreads();
-        if (COLUMNS ? tid < BLOCK : tid == 0) {
-            float m = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, most_of[COLUMNS ? w * BLOCK + tid : w]);
-            if (m == __int_as_float(0x7F800000)) infinite_s = 1;
-            const float s = scale_of<E5M2>(m, a.pow2);
-            scale_s[COLUMNS ? tid : 0] = s;
-            inverse_s[COLUMNS ? tid : 0] = 1.0f / s;
-        }
-        __syncthreads();
+    const unsigned high = a.high, wide = a.wide;
+    const unsigned first = static_cast<unsigned>(static_cast<uint64_t>(a.tiles) * blockIdx.x / gridDim.x),
+                   last = static_cast<unsigned>(static_cast<uint64_t>(a.tiles) * (blockIdx.x + 1) / gridDim.x);
+
+    struct Place {
+        int item, row_block, col_block;
+        int64_t begin;   // first row of x
+        int rows, kept;  // rows of x in the tile, rows of q
     };
-    join(larger);
-    const bool infinite = infinite_s != 0;
-    if (infinite) {
-        __syncthreads();
-        join(larger_finite);
-    }
+    // The place of tile u, after that of the tile before it.
+    auto place = [&](unsigned u, Place &p) {
+        const int before = p.row_block;
+        const unsigned row_blocks = u / wide;
+        p.item = static_cast<int>(row_blocks / high);
+        p.row_block = static_cast<int>(row_blocks % high);
+        p.col_block = static_cast<int>(u % wide);
+        if (COLUMNS && a.offsets) {
+            if (p.row_block == before) return;
+            const RowTile t =
+                row_tile_of(a.offsets, a.experts, static_cast<int>(a.rows), BLOCK, p.row_block);
+            const bool used = t.group >= 0 && t.group < a.experts;
+            p.begin = used ? t.begin : 0;
+            p.rows = used ? t.end - t.begin : 0;
+            p.kept = BLOCK;
+        } else {
+            p.begin = static_cast<int64_t>(p.row_block) * BLOCK;
+            p.rows = p.kept = static_cast<int>(min(static_cast<int64_t>(BLOCK), a.rows - p.begin));
+        }
+    };
+    auto col = [&](int j) { return LOAD == SCALAR ? part + 16 * j : 8 * part + j; };
+    const uint32_t slot = LOAD == ASYNC ? static_cast<uint32_t>(__cvta_generic_to_shared(staged)) + 16u * tid : 0u;
+    auto fetch = [&](const Place &p, unsigned n) {
+        const T *x = static_cast<const T *>(a.x) + p.item * a.strideX + p.begin * a.ldx + static_cast<int64_t>(p.col_block) * BLOCK;
+        const int64_t left = a.cols - static_cast<int64_t>(p.col_block) * BLOCK - 8 * part;
+        const int bytes = left <= 0 ? 0 : static_cast<int>(min(left, static_cast<int64_t>(8)) * sizeof(T));
+        const uint32_t to = slot + n % TILE_STAGES * TILE_STAGE;
 #pragma unroll
-    for (int j = 0; j < (COLUMNS ? 8 : 1); ++j) inverse[j] = inverse_s[COLUMNS ? col(j) : 0];
-    if (COLUMNS) {
-        if (tid < BLOCK && tid < cols) a.scales[blockIdx.x * a.cols + c0 + tid] = scale_s[tid];
-    } else if (tid == 0) {
-        a.scales[(static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x) * gridDim.y + blockIdx.y] = scale_s[0];
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 16 * i, some = r < p.rows ? bytes : 0;
+            copy_async(to + 16u * THREADS * i, some ? x + r * a.ldx + 8 * part : static_cast<const T *>(a.x), some);
+        }
+    };
+    Place here{-1, -1, -1, 0, 0, 0}, ahead = here;
+    if (LOAD == ASYNC) {
+        place(first, ahead);
+        fetch(ahead, 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    uint8_t *q = a.q + blockIdx.z * a.strideQ + at * a.ldq + c0;
+    for (unsigned u = first; u < last; ++u) {
+        constexpr int PER = 16 / sizeof(T);
+        Pack<T, PER> v[LOAD == ASYNC ? 1 : 8][8 / PER];
+        const uint8_t *from = staged + (u - first) % TILE_STAGES * TILE_STAGE + 16 * tid;
+        // Row i of the thread's values. ASYNC: from shared memory whenever they are
+        // needed: in registers from the maximum to the conversion they were 64 fp32
+        // values, spilled.
+        auto row = [&](int i, float (&w)[8]) {
+            if constexpr (LOAD == ASYNC) {
+                const Pack<T, 8> x = *reinterpret_cast<const Pack<T, 8> *>(from + 16 * THREADS * i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        const uint2 o = convert8<E5M2>(v[i], [&](int j) { return inverse[COLUMNS ? j : 0]; }, infinite);
-        if (VECTOR) {
-            uint8_t *to = q + r * a.ldq + 8 * part;
-            if (r >= kept) continue;
-            if (a.q_vector && 8 * part + 8 <= cols) {
-                *reinterpret_cast<uint2 *>(to) = o;
+                for (int j = 0; j < 8; ++j) w[j] = to_f32(x.v[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = to_f32(v[i][j / PER].v[j % PER]);
+            }
+        };
+        if constexpr (LOAD == ASYNC) {
+            static_assert(TILE_STAGES == 2, "the tile after this one is on its way");
+            here = ahead;
+            if (u + 1 < last) {
+                place(u + 1, ahead);
+                fetch(ahead, u + 1 - first);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            place(u, here);
+            const T *x = static_cast<const T *>(a.x) + here.item * a.strideX + here.begin * a.ldx +
+                         static_cast<int64_t>(here.col_block) * BLOCK;
+            const int64_t cols = a.cols - static_cast<int64_t>(here.col_block) * BLOCK;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + 16 * i;
+                const T *p = x + r * a.ldx;
+                if (LOAD == VECTOR && r < here.rows && 8 * part + 8 <= cols) {
+#pragma unroll
+                    for (int h = 0; h < 8 / PER; ++h) v[i][h] = load_pack<T, PER>(p + 8 * part + PER * h);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[i][j / PER].v[j % PER] = r < here.rows && col(j) < cols ? p[col(j)] : from_f32<T>(0.0f);
+                }
+            }
+        }
+        const int64_t c0 = static_cast<int64_t>(here.col_block) * BLOCK, cols = a.cols - c0;
+        float most[MAXIMA], inverse[MAXIMA];
+        // Joins the maxima of the block's threads, or of a column's; whether one of
+        // them is infinite.
+        auto join = [&](auto &&larger_of) {
+#pragma unroll
+            for (int j = 0; j < MAXIMA; ++j) most[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float w[8];
+                row(i, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) most[COLUMNS ? j : 0] = larger_of(most[COLUMNS ? j : 0], w[j]);
+            }
+            if (COLUMNS) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    most[j] = fmaxf(most[j], __shfl_xor_sync(0xffffffffu, most[j], 16));
+                    if (lane < 16) most_of[warp * BLOCK + col(j)] = most[j];
+                }
+            } else {
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], d));
+                if (lane == 0) most_of[warp] = most[0];
+            }
+            __syncthreads();
+            bool infinite = false;
+            if (COLUMNS ? tid < BLOCK : tid == 0) {
+                float m = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) m = fmaxf(m, most_of[COLUMNS ? w * BLOCK + tid : w]);
+                infinite = m == __int_as_float(0x7F800000);
+                const float s = scale_of<E5M2>(m, a.pow2);
+                inverse_s[COLUMNS ? tid : 0] = 1.0f / s;
+                if (!COLUMNS)
+                    a.scales[u] = s;
+                else if (tid < cols)
+                    a.scales[here.row_block * a.cols + c0 + tid] = s;
+            }
+            return __syncthreads_or(infinite) != 0;
+        };
+        const bool infinite = join(larger);
+        if (infinite) join(larger_finite);
+#pragma unroll
+        for (int j = 0; j < MAXIMA; ++j) inverse[j] = inverse_s[COLUMNS ? col(j) : 0];
+        uint8_t *q = a.q + here.item * a.strideQ + static_cast<int64_t>(here.row_block) * BLOCK * a.ldq + c0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 16 * i;
+            float w[8];
+            row(i, w);
+            const uint2 o = convert8<E5M2>(w, [&](int j) { return inverse[COLUMNS ? j : 0]; }, infinite);
+            if (LOAD != SCALAR) {
+                uint8_t *to = q + r * a.ldq + 8 * part;
+                if (r >= here.kept) continue;
+                if (a.q_vector && 8 * part + 8 <= cols) {
+                    *reinterpret_cast<uint2 *>(to) = o;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (8 * part + j < cols) to[j] = static_cast<uint8_t>((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (8 * part + j < cols) to[j] = static_cast<uint8_t>((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
+                    tile[r * (BLOCK + 16) + col(j)] = static_cast<uint8_t>((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                tile[r * (BLOCK + 16) + col(j)] = static_cast<uint8_t>((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
         }
-    }
-    if (VECTOR) return;
-    __syncthreads();
-    // Sixteen bytes a thread, eight threads a row.
-    for (int r = tid >> 3; r < kept; r += THREADS / 8) {
-        const int c = 16 * (tid & 7);
-        const uint8_t *from = tile + r * (BLOCK + 16) + c;
-        uint8_t *to = q + r * a.ldq + c;
-        if (a.q_vector && c + 16 <= cols) {
-            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
-        } else {
-            for (int j = 0; j < 16; ++j)
-                if (c + j < cols) to[j] = from[j];
+        if (LOAD != SCALAR) continue;
+        __syncthreads();
+        // Sixteen bytes a thread, eight threads a row.
+        for (int r = tid >> 3; r < here.kept; r += THREADS / 8) {
+            const int c = 16 * (tid & 7);
+            const uint8_t *from = tile + r * (BLOCK + 16) + c;
+            uint8_t *to = q + r * a.ldq + c;
+            if (a.q_vector && c + 16 <= cols) {
+                *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+            } else {
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < cols) to[j] = from[j];
+            }
         }
+        // The next tile's first write to `tile` comes after a barrier.
     }
 }
 
+template <class T, bool E5M2, bool COLUMNS>
+int launch_tiles(QArgs a, bool vector, const DeviceInfo &dev, cudaStream_t stream) {
+    if (!vector) {
+        quantize_tiles_kernel<T, E5M2, COLUMNS, SCALAR><<<static_cast<unsigned>(a.tiles), THREADS, 0, stream>>>(a);
+    } else if constexpr (sizeof(T) == 4) {
+        quantize_tiles_kernel<T, E5M2, COLUMNS, VECTOR><<<static_cast<unsigned>(a.tiles), THREADS, 0, stream>>>(a);
+    } else {
+        auto kernel = quantize_tiles_kernel<T, E5M2, COLUMNS, ASYNC>;
+        constexpr int bytes = TILE_STAGES * TILE_STAGE;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return SGEMM_ERR_LAUNCH;
+        const int64_t ctas = TILE_CTAS * static_cast<int64_t>(dev.sm_count);
+        kernel<<<static_cast<unsigned>(a.tiles < ctas ? a.tiles : ctas), THREADS, bytes, stream>>>(a);
+    }
+    return SGEMM_OK;
+}
+
 template <class T, bool E5M2>
-int launch_type(const QuantizeProblem &p, const QArgs &a, bool vector, cudaStream_t stream) {
+int launch_type(const QuantizeProblem &p, const QArgs &a, bool vector, const DeviceInfo &dev, cudaStream_t stream) {
     if (p.block == SGEMM_FP8_ROWS) {
         const int64_t warps = p.rows * ((p.cols + WARP_VALUES - 1) / WARP_VALUES), per = THREADS / 32;
         const int64_t blocks = (warps + per - 1) / per;
@@ -299,31 +403,31 @@ int launch_type(const QuantizeProblem &p, const QArgs &a, bool vector, cudaStrea
         auto kernel = vector ? quantize_rows_kernel<T, E5M2, true> : quantize_rows_kernel<T, E5M2, false>;
         kernel<<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(a);
     } else {
-        const int64_t wide = blocks_of(p.cols),
-                      high = p.offsets ? sgemm_fp8_blocks(p.rows, p.experts) : blocks_of(p.rows);
-        if (high > INT32_MAX || wide > 65535 || p.items > 65535) return SGEMM_ERR_UNSUPPORTED;
-        const dim3 grid(static_cast<unsigned>(high), static_cast<unsigned>(wide), static_cast<unsigned>(p.items));
-        auto kernel = p.block == SGEMM_FP8_COLUMNS
-                          ? (vector ? quantize_tiles_kernel<T, E5M2, true, true> : quantize_tiles_kernel<T, E5M2, true, false>)
-                          : (vector ? quantize_tiles_kernel<T, E5M2, false, true>
-                                    : quantize_tiles_kernel<T, E5M2, false, false>);
-        kernel<<<grid, THREADS, 0, stream>>>(a);
+        const int rc = p.block == SGEMM_FP8_COLUMNS ? launch_tiles<T, E5M2, true>(a, vector, dev, stream)
+                                                    : launch_tiles<T, E5M2, false>(a, vector, dev, stream);
+        if (rc != SGEMM_OK) return rc;
     }
     return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 
 template <class T>
-int launch_any(const QuantizeProblem &p, const QArgs &a, bool vector, cudaStream_t stream) {
-    return p.to == SGEMM_FP8_E5M2 ? launch_type<T, true>(p, a, vector, stream)
-                                  : launch_type<T, false>(p, a, vector, stream);
+int launch_any(const QuantizeProblem &p, const QArgs &a, bool vector, const DeviceInfo &dev, cudaStream_t stream) {
+    return p.to == SGEMM_FP8_E5M2 ? launch_type<T, true>(p, a, vector, dev, stream)
+                                  : launch_type<T, false>(p, a, vector, dev, stream);
 }
 
 }  // namespace
 
-int quantize_launch(const QuantizeProblem &p, const DeviceInfo &, cudaStream_t stream, int *launches) {
+int quantize_launch(const QuantizeProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     QArgs a{};
     a.rows = p.rows;
     a.cols = p.cols;
+    const int64_t high = p.offsets ? sgemm_fp8_blocks(p.rows, p.experts) : blocks_of(p.rows), wide = blocks_of(p.cols);
+    if (p.block != SGEMM_FP8_ROWS && (high > INT32_MAX || wide > INT32_MAX || high * wide > INT32_MAX / p.items))
+        return SGEMM_ERR_UNSUPPORTED;
+    a.high = static_cast<unsigned>(high);
+    a.wide = static_cast<unsigned>(wide);
+    a.tiles = high * wide * p.items;
     a.x = p.x;
     a.ldx = p.ldx;
     a.strideX = p.items > 1 ? p.strideX : 0;
@@ -339,11 +443,11 @@ int quantize_launch(const QuantizeProblem &p, const DeviceInfo &, cudaStream_t s
     const bool vector = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % per == 0 && a.strideX % per == 0;
     int rc;
     if (p.type == SGEMM_TYPE_F32)
-        rc = launch_any<float>(p, a, vector, stream);
+        rc = launch_any<float>(p, a, vector, dev, stream);
     else if (p.type == SGEMM_TYPE_BF16)
-        rc = launch_any<__nv_bfloat16>(p, a, vector, stream);
+        rc = launch_any<__nv_bfloat16>(p, a, vector, dev, stream);
     else
-        rc = launch_any<__half>(p, a, vector, stream);
+        rc = launch_any<__half>(p, a, vector, dev, stream);
     if (rc == SGEMM_OK)
         ++*launches;
     else

@@ -92,10 +92,12 @@ int64_t sgemm_fp8_blocks(int64_t rows, int64_t experts);
  * A and B are 16-byte aligned, lda, ldb and strideB multiples of 16; rows must
  * be below 2^31 - 1024. Every block of 128 products is summed on the tensor
  * cores in fp32 and scaled by the product of its two scales (which should
- * neither overflow nor fall below 2^-126), the blocks are added up in order in
- * fp32, and the sum is rounded once to C's type. A row's result depends on that
- * row and its matrix only. The gradient of A is the same call on C's
- * gradient, quantised in rows, with transB the other way round.
+ * neither overflow nor fall below 2^-126), the blocks are added up in fp32 in an
+ * order that is always the same, and the sum is rounded once to C's type. A row's
+ * result depends on that row and its matrix, and on whether the call takes the
+ * kernel for few rows (without offsets, SGEMM_OP_T, at most 16 rows, or 32 for a
+ * small N), which adds the blocks up in another order. The gradient of A is the
+ * same call on C's gradient, quantised in rows, with transB the other way round.
  */
 int sgemm_fp8_gemm(int out_type, int transB, int type_a, int type_b, int64_t rows, int64_t N, int64_t K,
                    int64_t experts, const int32_t *offsets, const void *A, int64_t lda, const float *sA,

@@ -185,6 +185,32 @@ def test_gemm(fp8, rows, N, K, trans):
         check_product(fp8.gemm(a, b, transB=trans, dtype=dtype), A, B, K, f"{dtype}")
 
 
+@pytest.mark.parametrize("rows", [1, 2, 8, 9, 16, 17, 32])
+@pytest.mark.parametrize("N,K", [(1, 1), (15, 128), (17, 127), (129, 1040), (260, 1153), (40, 3201)])
+def test_gemm_of_few_rows(fp8, rows, N, K):
+    for ta, tb in ((E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)):
+        a, b = operands(fp8, rows, N, K, True, ta, tb, seed=rows)
+        A, B = meaning(a, "rows"), meaning(b, "blocks").t()
+        for dtype in DTYPES.values():
+            room = torch.full((rows + 1, N + 3), 7.0, dtype=dtype, device="cuda")
+            check_product(fp8.gemm(a, b, out=room[:rows, :N], transB=True), A, B, K, f"{dtype}")
+            assert bool((room[rows:] == 7).all() and (room[:, N:] == 7).all())
+
+
+def test_gemm_of_few_rows_reads_no_padding(fp8):
+    """Bytes behind the last column, whatever they are, and NaN in one row."""
+    a, b = operands(fp8, 9, 50, 200, True)
+    want = fp8.gemm(a, b, transB=True)
+    wide = [torch.full((*t.shape[:-1], 208), 0x7F, dtype=torch.uint8, device="cuda") for t in (a.values, b.values)]
+    for w, t in zip(wide, (a.values, b.values)):
+        w[..., :200] = t.view(torch.uint8)
+    aw, bw = (fp8.Quantized(w.view(E4M3)[..., :200], t.scales) for w, t in zip(wide, (a, b)))
+    assert torch.equal(fp8.gemm(aw, bw, transB=True), want)
+    wide[0][4, 130] = 0x7F
+    got = fp8.gemm(aw, bw, transB=True)
+    assert bool(got[4].isnan().all()) and torch.equal(got[:4], want[:4]) and torch.equal(got[5:], want[5:])
+
+
 @pytest.mark.parametrize("ta", [E4M3, E5M2])
 @pytest.mark.parametrize("tb", [E4M3, E5M2])
 def test_gemm_types(fp8, ta, tb):
@@ -244,12 +270,19 @@ def test_wgrad(fp8, rows, M, N):
 
 
 def test_a_row_depends_on_itself(fp8):
-    """The same row gives the same bits alone, among others and in a group."""
-    a, b = operands(fp8, 700, 520, 384, True)
+    """The same row gives the same bits among others and in a group, and, where few rows have a kernel of their own,
+    the same bits among few."""
+    a, b = operands(fp8, 700, 520, 2000, True)
+
+    def some(r):
+        return fp8.gemm(fp8.Quantized(a.values[r], a.scales[:, r].contiguous()), b, transB=True, dtype=torch.float32)
+
     all_rows = fp8.gemm(a, b, transB=True, dtype=torch.float32)
-    for r in (slice(0, 1), slice(3, 50), slice(255, 600)):
-        some = fp8.Quantized(a.values[r], a.scales[:, r].contiguous())
-        assert torch.equal(fp8.gemm(some, b, transB=True, dtype=torch.float32), all_rows[r])
+    for r in (slice(3, 50), slice(255, 600)):
+        assert torch.equal(some(r), all_rows[r])
+    few = some(slice(40, 72))
+    for n in (1, 8, 9, 16, 17):
+        assert torch.equal(some(slice(40, 40 + n)), few[:n])
     stack = fp8.Quantized(b.values[None].repeat(3, 1, 1), b.scales[None].repeat(3, 1, 1))
     off = torch.tensor([0, 37, 37, 700], dtype=torch.int32, device="cuda")
     assert torch.equal(fp8.gemm(a, stack, off, transB=True, dtype=torch.float32), all_rows)
