@@ -36,7 +36,7 @@ constexpr float SMALLEST_SCALE = 1.17549435e-38f;  // 2^-126
 struct QArgs {
     int64_t rows, cols;
     unsigned high, wide;  // blocks of rows and of columns of an item
-    int64_t tiles;        // 128 x 128 tiles of all
+    unsigned tiles;       // 128 x 128 tiles of all
     const void *x;
     int64_t ldx, strideX;
     const int32_t *offsets;
@@ -188,7 +188,7 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void *from, int by
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
-// Tiles [first, last) of 128 x 128 values, in the order items, row blocks, columns.
+// Tiles of 128 x 128 values, in the order items, row blocks, columns.
 template <class T, bool E5M2, bool COLUMNS, Load LOAD>
 __global__ void __launch_bounds__(THREADS, LOAD == ASYNC || !COLUMNS ? TILE_CTAS : 2)
     quantize_tiles_kernel(const __grid_constant__ QArgs a) {
@@ -199,8 +199,9 @@ __global__ void __launch_bounds__(THREADS, LOAD == ASYNC || !COLUMNS ? TILE_CTAS
     extern __shared__ __align__(16) uint8_t staged[];
     const int tid = static_cast<int>(threadIdx.x), part = tid & 15, r0 = tid >> 4, warp = tid >> 5, lane = tid & 31;
     const unsigned high = a.high, wide = a.wide;
-    const unsigned first = static_cast<unsigned>(static_cast<uint64_t>(a.tiles) * blockIdx.x / gridDim.x),
-                   last = static_cast<unsigned>(static_cast<uint64_t>(a.tiles) * (blockIdx.x + 1) / gridDim.x);
+    // ASYNC: a run of tiles for each CTA, otherwise one.
+    const unsigned each = LOAD == ASYNC ? a.tiles / gridDim.x : 1, more = LOAD == ASYNC ? a.tiles % gridDim.x : 0;
+    const unsigned first = each * blockIdx.x + min(blockIdx.x, more), last = first + each + (blockIdx.x < more);
 
     struct Place {
         int item, row_block, col_block;
@@ -380,16 +381,16 @@ __global__ void __launch_bounds__(THREADS, LOAD == ASYNC || !COLUMNS ? TILE_CTAS
 template <class T, bool E5M2, bool COLUMNS>
 int launch_tiles(QArgs a, bool vector, const DeviceInfo &dev, cudaStream_t stream) {
     if (!vector) {
-        quantize_tiles_kernel<T, E5M2, COLUMNS, SCALAR><<<static_cast<unsigned>(a.tiles), THREADS, 0, stream>>>(a);
+        quantize_tiles_kernel<T, E5M2, COLUMNS, SCALAR><<<a.tiles, THREADS, 0, stream>>>(a);
     } else if constexpr (sizeof(T) == 4) {
-        quantize_tiles_kernel<T, E5M2, COLUMNS, VECTOR><<<static_cast<unsigned>(a.tiles), THREADS, 0, stream>>>(a);
+        quantize_tiles_kernel<T, E5M2, COLUMNS, VECTOR><<<a.tiles, THREADS, 0, stream>>>(a);
     } else {
         auto kernel = quantize_tiles_kernel<T, E5M2, COLUMNS, ASYNC>;
         constexpr int bytes = TILE_STAGES * TILE_STAGE;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
             return SGEMM_ERR_LAUNCH;
-        const int64_t ctas = TILE_CTAS * static_cast<int64_t>(dev.sm_count);
-        kernel<<<static_cast<unsigned>(a.tiles < ctas ? a.tiles : ctas), THREADS, bytes, stream>>>(a);
+        const unsigned ctas = static_cast<unsigned>(TILE_CTAS * dev.sm_count);
+        kernel<<<a.tiles < ctas ? a.tiles : ctas, THREADS, bytes, stream>>>(a);
     }
     return SGEMM_OK;
 }
@@ -427,7 +428,7 @@ int quantize_launch(const QuantizeProblem &p, const DeviceInfo &dev, cudaStream_
         return SGEMM_ERR_UNSUPPORTED;
     a.high = static_cast<unsigned>(high);
     a.wide = static_cast<unsigned>(wide);
-    a.tiles = high * wide * p.items;
+    a.tiles = static_cast<unsigned>(high * wide * p.items);
     a.x = p.x;
     a.ldx = p.ldx;
     a.strideX = p.items > 1 ? p.strideX : 0;
