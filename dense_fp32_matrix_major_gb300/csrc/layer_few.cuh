@@ -35,8 +35,8 @@
 // multiply-adds leave 0.2e-6). (tcgen05 wants its operands in shared memory and
 // 128 rows a tile for at most 16 columns of x here.) Which k a lane holds does not
 // matter to a matrix instruction as long as matrix and x agree, so a lane takes 16
-// bytes of a row that lie together. Rows that are not 16-byte aligned, or end in a
-// part of 16 bytes, are read value by value, and summed by multiply-adds.
+// bytes of a row that lie together. Of rows that are not 16-byte aligned it takes
+// them out of the 32 bytes around, 15 instructions for 16 bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -62,11 +62,12 @@ constexpr int WARPS = 16, THREADS = 32 * WARPS;
 constexpr int MEMBERS = 8;   // pairs of an entry, the columns of the matrix instructions
 constexpr int COLUMNS = 32;  // of y that a block of the second kernel makes at once
 static_assert(MAX_PAIRS <= THREADS, "a thread a pair");
-// A warp's ring: slices of 256 bytes of 16 rows, in 16-byte pieces by lane.
-constexpr int SLICE = 256, CHUNKS = SLICE / 64, STAGE = 2 * CHUNKS * 512, STAGES = 2;
+// A warp's ring: slices of 256 bytes of 16 rows, in 16-byte pieces by lane, and the
+// 16 bytes of each row that follow.
+constexpr int SLICE = 256, CHUNKS = SLICE / 64, FOLLOWING = 2 * CHUNKS * 512, STAGE = FOLLOWING + 16 * 16, STAGES = 2;
 constexpr int RING_BYTES = STAGES * STAGE;
-// Shared memory: the rings, a tile's sums of each warp, and in the second kernel
-// the pairs' sums.
+// Shared memory: the rings, 512 bytes of each warp (x of its chunk, then the sums of
+// a tile that it shares), and in the second kernel the pairs' sums.
 constexpr int SMEM = WARPS * (RING_BYTES + 512);
 constexpr int smem_out(int pairs) { return SMEM + pairs * COLUMNS * 4; }
 
@@ -157,15 +158,14 @@ struct Matrix {
 // bf16, or with h in two planes.
 enum Math { FMA, NATIVE, PLANES, HALF8, TF32_X, TF32_H };
 
-// 16 bytes of a row of K values from value k on, zeros past its end. whole: they
-// may be loaded at once where the row has them all (they are 16-byte aligned).
+// 16 bytes of a row of K values from value k on, zeros past its end. They are 16-byte aligned.
 template <int SIZE>
-__device__ __forceinline__ void load_piece(const uint8_t *row, int k, int K, bool whole, uint32_t (&v)[4]) {
+__device__ __forceinline__ void load_piece(const uint8_t *row, int k, int K, uint32_t (&v)[4]) {
     constexpr int PER = 16 / SIZE;
     v[0] = v[1] = v[2] = v[3] = 0;
     if (k >= K) return;
     const uint8_t *p = row + static_cast<int64_t>(k) * SIZE;
-    if (whole && k + PER <= K) {
+    if (k + PER <= K) {
         const uint4 x = *reinterpret_cast<const uint4 *>(p);
         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         return;
@@ -181,6 +181,46 @@ __device__ __forceinline__ void load_piece(const uint8_t *row, int k, int K, boo
         v[2] |= i * SIZE / 4 == 2 ? x : 0;
         v[3] |= i * SIZE / 4 == 3 ? x : 0;
     }
+}
+
+// The same of a row anywhere: the 32 bytes around them from the 16-byte boundary
+// before them on, for realign(). Nothing past the row's end is read.
+template <int SIZE>
+__device__ __forceinline__ void load_piece(const uint8_t *row, int k, int K, uint32_t (&v)[8]) {
+    constexpr int PER = 16 / SIZE;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v[w] = 0;
+    if (k >= K) return;
+    const uint8_t *p = row + static_cast<int64_t>(k) * SIZE;
+    const int before = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    if (k + 2 * PER - before / SIZE <= K) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p - before), y = *reinterpret_cast<const uint4 *>(p - before + 16);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < PER && k + i < K; ++i) {
+        uint32_t x;
+        if (SIZE == 4) x = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        if (SIZE == 2) x = __ldg(reinterpret_cast<const uint16_t *>(p) + i);
+        const int at = before + i * SIZE;
+        x <<= 8 * (at % 4);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v[w] |= at / 4 == w ? x : 0;
+    }
+}
+
+// 16 of 32 bytes, from byte `from` (0 .. 15, a multiple of SIZE) on.
+template <int SIZE>
+__device__ __forceinline__ void realign(const uint32_t (&w)[8], int from, uint32_t (&v)[4]) {
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) a[i] = from & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = from & 4 ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = SIZE == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], 8 * (from & 3));
 }
 
 __device__ __forceinline__ float half_of(uint32_t w, int i, bool bf16) {
@@ -255,17 +295,22 @@ struct Cursor {
     int item, entry, tile, slice;
 };
 
-// 16-byte asynchronous copy to shared memory, past the L1 cache; valid == false
-// writes zeros and reads nothing.
-__device__ __forceinline__ void copy_16(uint32_t dst, const void *src, bool valid) {
+// 16-byte asynchronous copy to shared memory, past the L1 cache: the first `bytes`
+// are read, the others zero.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(valid ? 16 : 0)
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes)
                  : "memory");
 }
 
-__device__ __forceinline__ void lds_128(uint32_t at, uint32_t (&v)[4]) {
+__device__ __forceinline__ void sts_128(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void lds_128(uint32_t at, uint32_t (&v)[N], int first = 0) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "=r"(v[first]), "=r"(v[first + 1]), "=r"(v[first + 2]), "=r"(v[first + 3])
                  : "r"(at)
                  : "memory");
 }
@@ -279,7 +324,7 @@ __device__ __forceinline__ void lds_128(uint32_t at, uint32_t (&v)[4]) {
 //   scale_row(c, i, g) where those of row 8 i + g begin
 //   members(c)         pairs
 //   x(c, m)            pair m's row of x or h
-//   whole()            whether those rows are 16-byte aligned
+//   ALIGNED            those rows always start on 16-byte boundaries
 //   finish(c, sum)     takes a tile's sums: sum[2 i + j] of lane 4 g + t is row 8 i + g, pair 2 t + j
 
 // The next slice; true where a tile starts.
@@ -339,14 +384,19 @@ __device__ __forceinline__ void gather_lanes(float (&f)[MEMBERS][2], int t, floa
         }
 }
 
-// Tiles whose rows are 16-byte aligned and a multiple of 16 bytes long. ring: this
-// lane's place in its warp's ring.
-template <int H, int MATH, class X, class Job>
+// ring: the warp's ring. ANY: rows of the matrix (8-bit ones excepted) and of x need
+// not start on 16-byte boundaries. Those of the matrix are then copied from the
+// boundary before them on (which lies in the same allocation), and a lane takes its
+// 16 bytes from its own piece and the next; x comes in 32 bytes that hold its 16.
+template <int H, int MATH, bool ANY, class X, class Job>
 __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint32_t ring, float4 *parts, int *part_of,
                                          Rest &rest) {
     using M = Matrix<H>;
+    constexpr bool SHIFT = ANY && !M::FP8, SPLIT = ANY && !Job::ALIGNED, TWO = MATH == PLANES || MATH == TF32_H;
     // 16-byte pieces of x in a lane's part of a chunk, and chunks of them on their way.
-    constexpr int PX = M::PER * static_cast<int>(sizeof(X)) / 16, PIECES = MATH == PLANES || MATH == TF32_H ? 2 * M::PER / 8 : PX, XP = PIECES > 2 ? 2 : 4;
+    constexpr int PX = M::PER * static_cast<int>(sizeof(X)) / 16, PIECES = TWO ? 2 * M::PER / 8 : PX,
+                  XP = SPLIT ? (PIECES > 1 ? 1 : 2) : (PIECES > 2 ? 2 : 4), XW = SPLIT ? 8 : 4;
+    constexpr int XSIZE = TWO ? 2 : static_cast<int>(sizeof(X));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const Share s = share_of(items, K, M::SLICE_K);
     rest.open = false;
@@ -354,24 +404,49 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
     if (s.mine == 0) return;
     Cursor load = first_of(job, s), use = load;
     const int64_t delta = job.delta();
-    const uint8_t *row;
-    bool there0, there1;
+    // Where rows g and g + 8 lie after the boundary before them, in bytes.
+    auto shifts = [&](const uint8_t *p, int (&shift)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) shift[i] = SHIFT ? static_cast<int>(reinterpret_cast<uintptr_t>(p + i * delta) & 15) : 0;
+    };
+    const uint8_t *row[2];
+    int left[2];  // values from this lane's first piece to the row's end
     auto enter = [&] {
-        row = job.base(load, g) + M::PER * t * M::SIZE;
-        there0 = job.there(load, 0, g);
-        there1 = job.there(load, 1, g);
+        const uint8_t *p = job.base(load, g);
+        int shift[2];
+        shifts(p, shift);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            row[i] = p + i * delta - shift[i] + 16 * t;
+            left[i] = job.there(load, i, g) ? K + shift[i] / M::SIZE - M::PER * t : 0;
+        }
     };
     enter();
     // Copies the next slice; one group of copies each, empty or not.
     auto fetch = [&](int stage, bool in) {
         if (in) {
-            const uint32_t to = ring + static_cast<uint32_t>(stage * STAGE);
+            const uint32_t to = ring + static_cast<uint32_t>(stage * STAGE + 16 * lane);
+            const int64_t at = static_cast<int64_t>(load.slice) * SLICE;
+            const int k = load.slice * M::SLICE_K;
+            const bool inner = k + M::SLICE_K <= K;  // the rows end later
+            auto bytes = [&](int n) { return max(min(n, M::PER), 0) * M::SIZE; };
 #pragma unroll
-            for (int q = 0; q < CHUNKS; ++q) {
-                const uint8_t *p = row + (load.slice * SLICE + q * 64);
-                const bool inside = load.slice * M::SLICE_K + q * M::CHUNK + M::PER * t < K;
-                copy_16(to + 1024 * q, p, there0 && inside);
-                copy_16(to + 1024 * q + 512, p + delta, there1 && inside);
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *p = row[i] + at;
+                if (inner) {
+                    const int all = left[i] > 0 ? 16 : 0;
+#pragma unroll
+                    for (int q = 0; q < CHUNKS; ++q) copy_16(to + 1024 * q + 512 * i, p + q * 64, all);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < CHUNKS; ++q)
+                        copy_16(to + 1024 * q + 512 * i, p + q * 64, bytes(left[i] - (k + q * M::CHUNK)));
+                }
+            }
+            if (SHIFT && t < 2) {
+                const int n = t == 0 ? left[0] : (left[1] > 0 ? left[1] + M::PER : 0);
+                copy_16(ring + static_cast<uint32_t>(stage * STAGE + FOLLOWING + 128 * t + 16 * g),
+                        (t == 0 ? row[0] : row[1] - 16) + at + SLICE, bytes(n - (k + M::SLICE_K)));
             }
             if (step(job, s, load)) enter();
         }
@@ -387,43 +462,48 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
     };
     float next_scale[2][BLOCKS] = {};
     auto fetch_scales = [&](bool in) {
-        if (!M::FP8 || !in) return;
+        if constexpr (M::FP8) {
+            if (!in) return;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) {
-                const int block = ahead.slice * BLOCKS + b;
-                next_scale[i][b] = block * SGEMM_FP8_BLOCK_SIZE < K ? __ldg(scale_at[i] + block) : 0.0f;
-            }
-        if (step(job, s, ahead)) enter_scales();
+                for (int b = 0; b < BLOCKS; ++b) {
+                    const int block = ahead.slice * BLOCKS + b;
+                    next_scale[i][b] = block * SGEMM_FP8_BLOCK_SIZE < K ? __ldg(scale_at[i] + block) : 0.0f;
+                }
+            if (step(job, s, ahead)) enter_scales();
+        }
     };
     // x of member g, XP chunks ahead of the sums.
     Cursor pre = use;
-    const uint8_t *x_row = nullptr;
-    auto enter_x = [&] {
-        const int n = job.members(pre);
-        x_row = static_cast<const uint8_t *>(job.x(pre, g < n ? g : 0));
+    auto x_of = [&](const Cursor &c) {
+        const int n = job.members(c);
+        return static_cast<const uint8_t *>(job.x(c, g < n ? g : 0));
     };
-    const bool whole = job.whole();
-    uint32_t xw[XP][PIECES][4];
+    const uint8_t *x_row = nullptr;
+    uint32_t xw[XP][PIECES][XW];
     auto load_x = [&](int q, bool in) {  // chunk q of slice `pre`
         if (!in) return;
         const int k = pre.slice * M::SLICE_K + q * M::CHUNK + M::PER * t;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            if (MATH == PLANES || MATH == TF32_H)  // plane i % 2
-                load_piece<2>(x_row + (i & 1) * job.plane(), k + i / 2 * 8, K, true, xw[q % XP][i]);
+            if (TWO)  // plane i % 2
+                load_piece<2>(x_row + (i & 1) * job.plane(), k + i / 2 * 8, K, xw[q % XP][i]);
             else
-                load_piece<sizeof(X)>(x_row, k + i * (16 / static_cast<int>(sizeof(X))), K, whole, xw[q % XP][i]);
+                load_piece<XSIZE>(x_row, k + i * (16 / XSIZE), K, xw[q % XP][i]);
         }
-        if (q == CHUNKS - 1 && step(job, s, pre)) enter_x();
+        if (q == CHUNKS - 1 && step(job, s, pre)) x_row = x_of(pre);
     };
     float sum[4], side[2][4], fma[MATH == FMA ? MEMBERS : 1][2];
-    int count = 0;
+    float part[4] = {};
+    int part_item = -1;
+    int count = 0, shift[2], x_shift = 0;
     bool started = false;  // the tile started in this share
     auto start = [&] {
         count = job.members(use);
         started = use.slice == 0;
+        if (SHIFT) shifts(job.base(use, g), shift);
+        if (SPLIT) x_shift = static_cast<int>(reinterpret_cast<uintptr_t>(x_of(use)) & 15);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = side[0][i] = side[1][i] = 0.0f;
 #pragma unroll
@@ -433,18 +513,18 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
     // of instructions that wait for their own sums only.
     auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&v)[PIECES][4],
                         float (&d)[2][4]) {
-        if (MATH == NATIVE || MATH == PLANES) {
+        if constexpr (MATH == NATIVE || MATH == PLANES) {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
                 mma_16<H == BF16>(d[0], lo[0], hi[0], lo[1], hi[1], v[i][0], v[i][1]);
                 mma_16<H == BF16>(d[1], lo[2], hi[2], lo[3], hi[3], v[i][2], v[i][3]);
             }
-        } else if (MATH == HALF8) {
+        } else if constexpr (MATH == HALF8) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 mma_16<false>(d[j & 1], fp8_halves<H>(lo[j]), fp8_halves<H>(hi[j]), fp8_halves<H>(lo[j] >> 16),
                               fp8_halves<H>(hi[j] >> 16), v[j / 2][2 * (j & 1)], v[j / 2][2 * (j & 1) + 1]);
-        } else if (MATH == TF32_X || MATH == TF32_H) {
+        } else if constexpr (MATH == TF32_X || MATH == TF32_H) {
 #pragma unroll
             for (int j = 0; j < M::PER / 2; ++j) {
                 const float2 a0 = two_of<H>(lo, j), a1 = two_of<H>(hi, j);
@@ -457,20 +537,48 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
             }
         }
     };
+    // The same by multiply-adds, with x by way of shared memory to all lanes.
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(parts + warp * 32));
+    auto multiply_add = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&v)[PIECES][4], float s0,
+                            float s1) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            float a0[4], a1[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a0[j] = value_of<H>(lo, 4 * i + j) * (M::FP8 ? s0 : 1.0f);
+                a1[j] = value_of<H>(hi, 4 * i + j) * (M::FP8 ? s1 : 1.0f);
+            }
+            __syncwarp();
+            sts_128(mine + 16 * lane, v[i]);
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < MEMBERS; ++m) {
+                if (m >= count) break;
+                uint32_t b[4];
+                lds_128(mine + 16 * (4 * m + t), b);
+                float(&f)[2] = fma[MATH == FMA ? m : 0];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[0] = fmaf(a0[j], __uint_as_float(b[j]), f[0]);
+                    f[1] = fmaf(a1[j], __uint_as_float(b[j]), f[1]);
+                }
+            }
+        }
+    };
 #pragma unroll
     for (int n = 0; n < STAGES; ++n) fetch(n, n < s.mine);
     if (M::FP8) enter_scales();
     fetch_scales(true);
-    if (MATH != FMA) {
-        enter_x();
+    x_row = x_of(pre);
 #pragma unroll
-        for (int q = 0; q < XP; ++q) load_x(q, true);
-    }
+    for (int q = 0; q < XP; ++q) load_x(q, true);
     start();
     for (int n = 0; n < s.mine; ++n) {
         const int stage = n % STAGES;
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        const uint32_t at = ring + static_cast<uint32_t>(stage * STAGE);
+        if (SHIFT) __syncwarp();  // the other lanes' copies
+        const uint32_t at = ring + static_cast<uint32_t>(stage * STAGE + 16 * lane);
         const bool last = n + 1 == s.mine;
         float scale[2][BLOCKS];
 #pragma unroll
@@ -479,36 +587,36 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
 #pragma unroll
         for (int q = 0; q < CHUNKS; ++q) {
             constexpr int PER_BLOCK = CHUNKS / BLOCKS;
-            uint32_t lo[4], hi[4];
-            lds_128(at + 1024 * q, lo);
-            lds_128(at + 1024 * q + 512, hi);
-            if (MATH == FMA) {
-                const int k0 = use.slice * M::SLICE_K + q * M::CHUNK + M::PER * t;
+            uint32_t a[2][4];
 #pragma unroll
-                for (int j0 = 0; j0 < M::PER; j0 += 4) {
-                    float a0[4], a1[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a0[j] = value_of<H>(lo, j0 + j) * (M::FP8 ? scale[0][q / PER_BLOCK] : 1.0f);
-                        a1[j] = value_of<H>(hi, j0 + j) * (M::FP8 ? scale[1][q / PER_BLOCK] : 1.0f);
-                    }
-#pragma unroll
-                    for (int m = 0; m < MEMBERS; ++m) {
-                        if (m >= count) break;
-                        uint32_t b[4];
-                        load_piece<4>(static_cast<const uint8_t *>(job.x(use, m)), k0 + j0, K, whole, b);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float(&f)[2] = fma[MATH == FMA ? m : 0];
-                            f[0] = fmaf(a0[j], __uint_as_float(b[j]), f[0]);
-                            f[1] = fmaf(a1[j], __uint_as_float(b[j]), f[1]);
-                        }
-                    }
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (SHIFT) {
+                    uint32_t w[8];
+                    lds_128(at + 1024 * q + 512 * i, w);
+                    lds_128(t < 3            ? at + 1024 * q + 512 * i + 16
+                            : q + 1 < CHUNKS ? at + 1024 * (q + 1) + 512 * i - 48
+                                             : ring + stage * STAGE + FOLLOWING + 128 * i + 16 * g,
+                            w, 4);
+                    realign<M::SIZE>(w, shift[i], a[i]);
+                } else {
+                    lds_128(at + 1024 * q + 512 * i, a[i]);
                 }
-            } else {
-                multiply(lo, hi, xw[q % XP], side);
-                load_x((q + XP) % CHUNKS, !last || q + XP < CHUNKS);
             }
+            auto sums = [&](const uint32_t(&v)[PIECES][4]) {
+                if constexpr (MATH == FMA)
+                    multiply_add(a[0], a[1], v, scale[0][q / PER_BLOCK], scale[1][q / PER_BLOCK]);
+                else
+                    multiply(a[0], a[1], v, side);
+            };
+            if constexpr (SPLIT) {
+                uint32_t v[PIECES][4];
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) realign<XSIZE>(xw[q % XP][i], x_shift, v[i]);
+                sums(v);
+            } else {
+                sums(xw[q % XP]);
+            }
+            load_x((q + XP) % CHUNKS, !last || q + XP < CHUNKS);
             if (M::FP8 && MATH != FMA && q % PER_BLOCK == PER_BLOCK - 1) {
                 // A block of an 8-bit matrix ends.
 #pragma unroll
@@ -518,6 +626,7 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
                 }
             }
         }
+        if (SHIFT) __syncwarp();  // the other lanes have read this stage
         fetch(stage, n + STAGES < s.mine);
         const bool done = use.slice + 1 == s.slices;
         if (last || done) {
@@ -534,6 +643,11 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
                 rest.at = use;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rest.sum[i] = sum[i];
+            } else if constexpr (MATH == FMA) {
+                // parts' place is x's: later.
+                part_item = use.item;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[i] = sum[i];
             } else {
                 parts[warp * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
                 if (lane == 0) part_of[warp] = use.item;
@@ -542,127 +656,24 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
         if (step(job, s, use) && !last) start();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-// Tiles whose rows are anywhere: value by value, multiply-adds. A lane takes
-// every fourth k of a slice of 32.
-template <int H, class X, class Job>
-__device__ __forceinline__ void sum_values(const Job &job, int items, int K, float4 *parts, int *part_of, Rest &rest) {
-    using M = Matrix<H>;
-    constexpr int N = 8, D = 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const Share s = share_of(items, K, 4 * N);
-    rest.open = false;
-    if (lane == 0) part_of[warp] = -1;
-    if (s.mine == 0) return;
-    Cursor load = first_of(job, s), use = load;
-    const int64_t delta = job.delta();
-    const uint8_t *row;
-    const float *scale_at[2];
-    bool there[2];
-    auto enter = [&] {
-        row = job.base(load, g);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            there[r] = job.there(load, r, g);
-            if (M::FP8) scale_at[r] = job.scales(load) + job.scale_row(load, r, g);
-        }
-    };
-    enter();
-    uint32_t w[D][2][N];
-    float sw[D][2];
-    auto load_w = [&](int d, bool in) {
-        const int k0 = load.slice * 4 * N + t;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int k = k0 + 4 * j;
-                w[d][r][j] = 0;
-                if (!in || !there[r] || k >= K) continue;
-                const uint8_t *p = row + r * delta + static_cast<int64_t>(k) * M::SIZE;
-                if (M::SIZE == 4) w[d][r][j] = __ldg(reinterpret_cast<const uint32_t *>(p));
-                if (M::SIZE == 2) w[d][r][j] = __ldg(reinterpret_cast<const uint16_t *>(p));
-                if (M::SIZE == 1) w[d][r][j] = __ldg(p);
-            }
-            if (M::FP8) sw[d][r] = in ? __ldg(scale_at[r] + load.slice * 4 * N / SGEMM_FP8_BLOCK_SIZE) : 0.0f;
-        }
-        if (in && step(job, s, load)) enter();
-    };
-    float fma[MEMBERS][2];
-    int count = 0;
-    bool started = false;
-    auto start = [&] {
-        count = job.members(use);
-        started = use.slice == 0;
-#pragma unroll
-        for (int m = 0; m < MEMBERS; ++m) fma[m][0] = fma[m][1] = 0.0f;
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(d, d < s.mine);
-    start();
-    for (int i0 = 0; i0 < s.mine; i0 += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (i0 + d >= s.mine) break;
-            const int k0 = use.slice * 4 * N + t;
-            float a[2][N];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const uint32_t one[4] = {w[d][r][j], 0, 0, 0};
-                    a[r][j] = value_of<H>(one, 0) * (M::FP8 ? sw[d][r] : 1.0f);
-                }
-#pragma unroll
-            for (int m = 0; m < MEMBERS; ++m) {
-                if (m >= count) break;
-                const X *x = static_cast<const X *>(job.x(use, m));
-                float b[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) b[j] = k0 + 4 * j < K ? to_f32(x[k0 + 4 * j]) : 0.0f;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    fma[m][0] = fmaf(a[0][j], b[j], fma[m][0]);
-                    fma[m][1] = fmaf(a[1][j], b[j], fma[m][1]);
-                }
-            }
-            load_w(d, i0 + d + D < s.mine);
-            const bool last = i0 + d + 1 == s.mine, done = use.slice + 1 == s.slices;
-            if (last || done) {
-                float sum[4];
-                gather_lanes(fma, t, sum);
-                if (done && started) {
-                    job.finish(use, sum);
-                } else if (started) {
-                    rest.open = true;
-                    rest.at = use;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rest.sum[i] = sum[i];
-                } else {
-                    parts[warp * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-                    if (lane == 0) part_of[warp] = use.item;
-                }
-            }
-            if (step(job, s, use) && !last) start();
-        }
+    if constexpr (MATH == FMA) {
+        if (part_item < 0) return;
+        __syncwarp();  // x there is read
+        parts[warp * 32 + lane] = make_float4(part[0], part[1], part[2], part[3]);
+        if (lane == 0) part_of[warp] = part_item;
     }
 }
 
 extern __shared__ __align__(16) uint8_t dynamic_smem[];
 
-// Sums and finishes a block's tiles. VALUES: rows that the ring cannot take.
-template <int H, int MATH, bool VALUES, class X, class Job>
+// Sums and finishes a block's tiles.
+template <int H, int MATH, bool ANY, class X, class Job>
 __device__ __forceinline__ void sum_tiles(const Job &job, int items, int K, int *part_of) {
     float4 *parts = reinterpret_cast<float4 *>(dynamic_smem + WARPS * RING_BYTES);
     Rest rest;
-    if constexpr (VALUES)
-        sum_values<H, X>(job, items, K, parts, part_of, rest);
-    else
-        sum_ring<H, MATH, X>(job, items, K,
-                             static_cast<uint32_t>(__cvta_generic_to_shared(dynamic_smem)) +
-                                 (threadIdx.x >> 5) * RING_BYTES + (threadIdx.x & 31) * 16,
-                             parts, part_of, rest);
+    sum_ring<H, MATH, ANY, X>(job, items, K,
+                              static_cast<uint32_t>(__cvta_generic_to_shared(dynamic_smem)) + (threadIdx.x >> 5) * RING_BYTES,
+                              parts, part_of, rest);
     join(job, rest, parts, part_of);
 }
 
@@ -704,10 +715,10 @@ struct HiddenJob {
         return static_cast<const uint8_t *>(a.x) + pair(c, m) / a.top_k * a.ldx * a.x_size;
     }
     __device__ __forceinline__ int64_t plane() const { return 0; }
-    __device__ __forceinline__ bool whole() const { return a.x_vector; }
+    static constexpr bool ALIGNED = false;
     __device__ __forceinline__ void write(const Cursor &c, int m, int feature, float v) const {
         float *to = a.h + pair(c, m) * a.ldh;
-        if (a.planes) {
+        if (a.x_type != SGEMM_TYPE_F32) {
             // Two bf16 terms, 16 bits of v: what a 16-bit y rounds away is 2^7 times as large.
             const __nv_bfloat16 hi = __float2bfloat16_rn(v);
             __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(to) + feature;
@@ -768,7 +779,7 @@ struct OutJob {
         return a.h + l.order[l.begin[c.entry] + m] * a.ldh;
     }
     __device__ __forceinline__ int64_t plane() const { return a.ldh * 2; }
-    __device__ __forceinline__ bool whole() const { return true; }
+    static constexpr bool ALIGNED = true;
     __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const {
         const int lane = threadIdx.x & 31, count = members(c);
 #pragma unroll
@@ -790,7 +801,7 @@ __device__ __forceinline__ OutJob<H> out_job(const LArgs &a, const Lists &l, int
                      static_cast<int64_t>(nblocks) * kblocks};
 }
 
-template <int H, int MATH, bool VALUES, class X>
+template <int H, int MATH, bool ANY, class X>
 __global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_constant__ LArgs a) {
     __shared__ Lists l;
     __shared__ int part_of[WARPS];
@@ -805,10 +816,10 @@ __global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_c
     const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
     job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
     const int items = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) - job.first;
-    sum_tiles<H, MATH, VALUES, X>(job, items, a.width, part_of);
+    sum_tiles<H, MATH, ANY, X>(job, items, a.width, part_of);
 }
 
-template <int H, int MATH, bool VALUES>
+template <int H, int MATH, bool ANY>
 __global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_constant__ LArgs a) {
     __shared__ Lists l;
     __shared__ int part_of[WARPS];
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_cons
     OutJob<H> job = out_job<H>(a, l, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), &n1);
     for (; job.at < n1; job.at += COLUMNS) {
         job.cols = min(COLUMNS, n1 - job.at);
-        sum_tiles<H, MATH, VALUES, float>(job, a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0, a.hidden, part_of);
+        sum_tiles<H, MATH, ANY, float>(job, a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0, a.hidden, part_of);
         __syncthreads();
         for (int i = threadIdx.x; i < a.tokens * COLUMNS; i += THREADS) {
             const int n = i % COLUMNS, token = i / COLUMNS;
@@ -873,12 +884,11 @@ int enqueue_kernel(const LArgs &a, int grid, int smem, const DeviceInfo &dev, cu
     return SGEMM_OK;
 }
 
-// Rows of K values that the ring can take: they start on 16-byte boundaries and
-// are a multiple of 16 bytes long.
+// Whether all rows start on 16-byte boundaries. Those of 8-bit matrices always do.
 template <int H>
-bool ring_takes(const void *w, int64_t ld, int64_t stride, int64_t K) {
+bool rows_aligned(const void *w, int64_t ld, int64_t stride) {
     constexpr int64_t per = Matrix<H>::PER;
-    return reinterpret_cast<uintptr_t>(w) % 16 == 0 && ld % per == 0 && stride % per == 0 && K % per == 0;
+    return Matrix<H>::FP8 || (reinterpret_cast<uintptr_t>(w) % 16 == 0 && ld % per == 0 && stride % per == 0);
 }
 
 // Blocks of the second kernel: four columns of y a block at least.
@@ -887,19 +897,20 @@ inline int out_grid(const LArgs &a, const DeviceInfo &dev) {
     return most < dev.sm_count ? most : dev.sm_count;
 }
 
-// Both kernels. HIDDEN, OUT: how their sums are made where the ring takes the rows.
+// Both kernels. HIDDEN, OUT: how their sums are made.
 template <int H, int HIDDEN, int OUT, class X>
-int launch_layer(const LayerProblem &p, LArgs a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
-    const bool out_ring = ring_takes<H>(p.w2, p.ld2, a.stride2, p.hidden);
-    a.planes = (OUT == PLANES || OUT == TF32_H) && out_ring;
+int launch_layer(const LayerProblem &p, const LArgs &a, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const bool in = a.x_vector && rows_aligned<H>(p.w1, p.ld1, a.stride1), out = rows_aligned<H>(p.w2, p.ld2, a.stride2);
+    const int smem = smem_out(a.pairs);
     int rc = SGEMM_OK;
     if (p.hidden > 0)
-        rc = ring_takes<H>(p.w1, p.ld1, a.stride1, p.width)
-                 ? enqueue_kernel<layer_hidden_kernel<H, HIDDEN, false, X>>(a, dev.sm_count, SMEM, dev, stream, launches)
-                 : enqueue_kernel<layer_hidden_kernel<H, FMA, true, X>>(a, dev.sm_count, SMEM, dev, stream, launches);
+        rc = in ? enqueue_kernel<layer_hidden_kernel<H, HIDDEN, false, X>>(a, dev.sm_count, SMEM, dev, stream, launches)
+                : enqueue_kernel<layer_hidden_kernel<H, HIDDEN, true, X>>(a, dev.sm_count, SMEM, dev, stream, launches);
     if (rc != SGEMM_OK) return rc;
-    return out_ring ? enqueue_kernel<layer_out_kernel<H, OUT, false>>(a, out_grid(a, dev), smem_out(a.pairs), dev, stream, launches)
-                    : enqueue_kernel<layer_out_kernel<H, FMA, true>>(a, out_grid(a, dev), smem_out(a.pairs), dev, stream, launches);
+    if (out) return enqueue_kernel<layer_out_kernel<H, OUT, false>>(a, out_grid(a, dev), smem, dev, stream, launches);
+    if constexpr (!Matrix<H>::FP8)
+        rc = enqueue_kernel<layer_out_kernel<H, OUT, true>>(a, out_grid(a, dev), smem, dev, stream, launches);
+    return rc;
 }
 
 }  // namespace

@@ -58,8 +58,7 @@ struct LArgs {
     void *y;
     int64_t ldy;
     float *h;
-    int64_t ldh;
-    int planes;  // h as two bf16 terms, the rows' first halves and second halves, in place of fp32
+    int64_t ldh;  // rows of h: fp32, or with x of 16 bits two bf16 terms, the first ones and then the second
 };
 
 int layer_launch(const LayerProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);

@@ -51,10 +51,12 @@ enum sgemm_layer_weights {
  *               sgemm_experts_layer_workspace(tokens, top_k, hidden). Contents
  *               need not be set. Not to be shared by calls that may run at once.
  * tokens * top_k is SGEMM_LAYER_PAIRS_MAX at most. Sums are fp32; h is held in
- * fp32 (with x of 16 bits as two bf16 terms, 16 bits of it), y is rounded once. Each expert's matrices are read
- * once per 16 pairs that share it, so every width, alignment and stride is
- * served, fastest where rows are 16-byte aligned. Infinities and NaN follow IEEE
- * arithmetic, except that an infinite matrix element gives NaN.
+ * fp32 (with x of 16 bits as two bf16 terms, 16 bits of it), y is rounded once.
+ * Each expert's matrices are read once per 8 pairs that share it. 8-bit ones
+ * start on 16-byte boundaries, with ld1, ld2, stride1 and stride2 multiples of 16;
+ * otherwise every width, alignment and stride is served, fastest where rows are
+ * 16-byte aligned. Infinities and NaN follow IEEE arithmetic, except that an
+ * infinite matrix element gives NaN.
  */
 int sgemm_experts_layer(int type, int held, int activation, int gated, int64_t tokens, int64_t top_k,
                         int64_t experts, int64_t width, int64_t hidden, const void *x, int64_t ldx, const void *ids,

@@ -118,6 +118,39 @@ def test_strides(layer, name, pad, offset):
         assert torch.equal(y, want)
 
 
+def among_nan(t, pitch, offset):
+    """t's values in rows of `pitch` from value `offset` of a buffer on, NaN (0x7F in 8 bits) everywhere else."""
+    rows = t.flatten(0, -2)
+    bits = t.element_size() == 1
+    room = torch.full((offset + rows.shape[0] * pitch + 64,), 0x7F if bits else float("nan"),
+                      dtype=torch.uint8 if bits else t.dtype, device="cuda")
+    strides = (t.shape[-2] * pitch, pitch, 1)[-t.dim():]
+    view = room.as_strided(t.shape, strides, offset)
+    view.copy_(t.view(torch.uint8) if bits else t)
+    return view.view(t.dtype) if bits else view
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("width,hidden", [(133, 71), (8, 3), (1, 1), (520, 261), (300, 640)])
+def test_what_lies_around_rows_is_not_read_as_values(layer, fp8, name, width, hidden):
+    """Rows on 16-byte boundaries that end anywhere, and rows anywhere, with NaN before, between and behind them."""
+    dtype = DTYPES[name]
+    for gated in (False, True):
+        c = case(9, 2, 3, width, hidden, dtype, gated, drop=0.1)
+        d1, d2 = c["w1"].double(), c["w2"].double()
+        for p1, p2, px, o in ((-(-width // 8) * 8, -(-hidden // 8) * 8 + 8, -(-width // 8) * 8, 0), (width, hidden, width, 5), (width + 3, hidden + 1, width + 5, 1),
+                              (width + 7, hidden + 2, -(-width // 8) * 8, 8)):
+            y = layer.forward(among_nan(c["x"], px, o), c["ids"], c["weights"], among_nan(c["w1"], p1, o),
+                              among_nan(c["w2"], p2, o), gated=gated, activation="gelu")
+            check_layer(y, c["x"], c["ids"], c["weights"], d1, d2, gated, "gelu", f"{gated} {p1} {p2} {px} {o}")
+        q1, q2 = fp8.quantize(c["w1"], "blocks"), fp8.quantize(c["w2"], "blocks")
+        e1, e2 = meaning(q1, "blocks"), meaning(q2, "blocks")
+        w1, w2 = (fp8.Quantized(among_nan(q.values, -(-q.values.shape[-1] // 16) * 16 + 16, 32), q.scales) for q in (q1, q2))
+        for px, o in ((width, 0), (width + 1, 3), (-(-width // 8) * 8, 8)):
+            y = layer.forward(among_nan(c["x"], px, o), c["ids"], c["weights"], w1, w2, gated=gated, activation="gelu")
+            check_layer(y, c["x"], c["ids"], c["weights"], e1, e2, gated, "gelu", f"8 bits {gated} {px} {o}")
+
+
 @pytest.mark.parametrize("name", list(DTYPES))
 def test_infinities_and_nan(layer, fp8, name):
     """What is not finite stays with its token, and infinities are what IEEE arithmetic makes of them."""
