@@ -3,16 +3,20 @@
 //
 //     C[s][n] = sum over blocks b of sA[b][s] sB[n / 128][b] P_b[s][n]
 //
-// Bound by reading B once. A tile of fp8_gemm.cu covers 256 columns, which
-// leaves most of the SMs without one; here a CTA takes 16 columns and its eight
-// warps every eighth block of K, so that there are eight warps for every 16
-// columns and each has its loads of several blocks on their way at once. A warp's
-// sums over its blocks, in order, are joined in the warps' order.
+// Bound by reading B once, and in short calls by the latency of that. A tile of
+// fp8_gemm.cu covers 256 columns, which leaves most of the SMs without one; here
+// a CTA takes 16 columns and its eight warps every eighth block of K, so that
+// there are eight warps for every 16 columns, each with the next blocks' loads on
+// their way (three blocks with 8 rows; one with more, whose registers A takes:
+// 16 rows of 4096 x 4096 6.7 us, with two 7.4). A warp's sums over its blocks, in
+// order, are joined in the warps' order. 8 rows of 16384 x 8192: 26 us, 5.1 TB/s
+// of B. With loads that may meet the rows' end, each under a branch of its own, 35.
 //
 // Matrix instructions m16n8k32: 16 columns of C by 8 rows. The 32 values of k may
 // be taken in any order that A and B share, so a thread's fragments are 16
 // consecutive bytes of a row, loaded from memory straight into registers: 64
-// bytes a row and load, each byte of B read once; A comes from L2.
+// bytes a row and load, each byte of B read once; A comes from L2. (tcgen05 wants
+// both staged in shared memory and 128 columns of C a tile.)
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -12,19 +12,27 @@
 // Two CTAs on two SMs of a cluster make a tile of 256 rows by up to 256 columns
 // of C. The MMA's first operand gives C's rows (A, 128 of them staged by each
 // CTA: the lanes of tensor memory), its second C's columns (B, half of them
-// staged by each CTA). Two buffers of 256 columns fill tensor memory: the
-// epilogue empties one while the tensor core fills the other.
+// staged by each CTA). Four buffers of 128 columns fill tensor memory, two for
+// each half of the tile: four warps empty a half's sums while the tensor core
+// makes the other's. (Two buffers of 256 columns, emptied by all eight warps at
+// once: 276 us in place of 259 for 16384 x 4096 x 4096, whose rate is 2130
+// TFLOP/s.)
 //
-// What bounds it. A k-block's MMAs take 512 cycles, in which shared memory takes
-// in 32 KB from TMA and gives 32 KB to the MMA, all it can. So nothing else may
-// go through shared memory while blocks are summed: in rows a lane needs one
-// factor a block, its row's scale times the scale of the 128 columns that the warp
-// sums, and gets it from global memory two blocks ahead. (With C's columns as
-// the lanes, which charges short groups less, every thread needs a factor for
-// each of its 32 columns: 319 us for 16384 x 4096 x 4096.) In wgrad both factors
-// vary; the columns' come through a ring in shared memory that warp 2 fills, in
-// the order in which the threads read them, and loads of 16 lanes x 4 columns
-// (16x128b) leave a thread a quarter of the columns.
+// What bounds it. The sums that leave tensor memory: a CTA's 128 x 256 of them a
+// block of 128 are 1 load, 1 multiply-add and the waits for each, 8 warps' work
+// for as long as the MMAs take. Without the MMAs the same kernel takes 206 us,
+// without the sums 145, without both TMA and sums 127. A k-block's MMAs take 512 cycles, in
+// which shared memory takes in 32 KB from TMA and gives 32 KB to the MMA, all it
+// can. So nothing else may go through shared memory while blocks are summed: in
+// rows a lane needs one factor a block, its row's scale times the scale of the
+// 128 columns that the warp sums, and gets it from global memory two blocks
+// ahead. (With C's columns as the lanes, which charges short groups less, every
+// thread needs a factor for each of its 32 columns: 319 us.) In wgrad both
+// factors vary; the columns' come through a ring in shared memory that warp 2
+// fills, in the order in which the threads read them, and loads of 16 lanes x 4
+// columns (16x128b) leave a thread a quarter of the columns (4096 x 2048 over
+// 8192 rows: 115 us). Tried without gain: 16 warps for the sums 276 us, one SM a
+// tile 274, multiply-adds in pairs 265.
 //
 // Layouts. An operand whose summed direction is contiguous in memory is staged
 // K-major, otherwise MN-major, both in 128-byte swizzled rows as TMA writes
@@ -35,7 +43,14 @@
 // robin, each role of a worker walking the bounds for itself. Rows staged past a
 // tile's end belong to the next and change only sums that are not written; a CTA
 // whose rows all lie past it stages none. In wgrad every group's rows start in a
-// block of their own and end in zeros.
+// block of their own and end in zeros. 16384 rows in 32 even groups, 2048 -> 4096:
+// 152 us; ragged 178: a group's last tile costs as much as a full one.
+//
+// C leaves through shared memory and TMA stores, 32 rows of 128 bytes at a time,
+// while the next tile is summed; where TMA cannot address it or a warp has fewer
+// than 32 rows, by 16-byte or single stores (all tiles that way: 276 us).
+//
+// A matrix and a few rows: fp8_few.cu.
 //
 // Roles in each CTA (12 warps): warp 0 loads the first operand and warp 3 the
 // second (TMA), warp 1 of the even CTA issues the MMAs, warp 2 prepares wgrad's
@@ -190,8 +205,7 @@ __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t a_desc, uint
 }
 
 // 32 lanes x 32 columns of 32 bits from tensor memory, waited for: r[i] is this
-// lane's column i. (The wait in a statement of its own, with the registers tied to
-// it, cost a hundred moves a k-block and warp.)
+// lane's column i.
 __device__ __forceinline__ void tmem_load_32x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -244,8 +258,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
 
 // Arrives on the mbarrier at this offset in the even CTA. Relaxed: what went
 // before is reads of tensor memory, complete when their wait returned. (With
-// release semantics at cluster scope 578 us in place of 354 for 16384 x 4096 x
-// 4096: the arrival waits out the thread's memory operations.)
+// release semantics at cluster scope an earlier form took 578 us in place of 354 for
+// 16384 x 4096 x 4096: the arrival waits out the thread's memory operations.)
 __device__ __forceinline__ void arrive_even(uint32_t bar) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(0));
