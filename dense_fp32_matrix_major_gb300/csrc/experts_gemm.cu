@@ -206,18 +206,25 @@ int sliced_launch(const GroupedProblem &p, int split, float *sums, const DeviceI
     GroupedProblem q = p;
     q.split = split;
     q.C = sums;
-    q.ldc = (p.N + 3) / 4 * 4;
+    q.ldc = slice_ld(p.N);
     q.strideC = p.M * q.ldc;
     const int rc = tensor_launch(q, dev, stream, launches);
     if (rc != SGEMM_OK) return rc;
-    const int64_t size = type_size(p.type);
-    Join j{sums, p.C, p.experts * p.M, p.M, p.N, q.ldc, p.ldc, p.experts > 1 ? p.strideC : 0, split, 0};
-    j.vector = (reinterpret_cast<uintptr_t>(p.C) % (4 * size) | (p.ldc % 4) | (j.strideC % 4)) == 0;
-    const int64_t blocks = (j.rows * (j.ld / 4) + JOIN_THREADS - 1) / JOIN_THREADS, most = 8LL * dev.sm_count;
+    return join_slices_launch(p.type, sums, split, p.experts, p.M, p.N, p.C, p.ldc, p.strideC, dev, stream, launches);
+}
+
+}  // namespace
+
+int join_slices_launch(int type, const float *sums, int split, int64_t experts, int64_t M, int64_t N, void *C,
+                       int64_t ldc, int64_t strideC, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
+    const int64_t size = type_size(type), ld = slice_ld(N);
+    Join j{sums, C, experts * M, M, N, ld, ldc, experts > 1 ? strideC : 0, split, 0};
+    j.vector = (reinterpret_cast<uintptr_t>(C) % (4 * size) | (ldc % 4) | (j.strideC % 4)) == 0;
+    const int64_t blocks = (j.rows * (ld / 4) + JOIN_THREADS - 1) / JOIN_THREADS, most = 8LL * dev.sm_count;
     const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-    if (p.type == SGEMM_TYPE_F32)
+    if (type == SGEMM_TYPE_F32)
         join_slices_kernel<float><<<grid, JOIN_THREADS, 0, stream>>>(j);
-    else if (p.type == SGEMM_TYPE_BF16)
+    else if (type == SGEMM_TYPE_BF16)
         join_slices_kernel<__nv_bfloat16><<<grid, JOIN_THREADS, 0, stream>>>(j);
     else
         join_slices_kernel<__half><<<grid, JOIN_THREADS, 0, stream>>>(j);
@@ -225,8 +232,6 @@ int sliced_launch(const GroupedProblem &p, int split, float *sums, const DeviceI
     ++*launches;
     return SGEMM_OK;
 }
-
-}  // namespace
 
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     // fp32 on the tensor cores is the three-term TF32 split; a caller who wants
@@ -237,7 +242,7 @@ int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t 
         int rc = SGEMM_ERR_UNSUPPORTED;
         const int split = p.wgrad ? slices_of(p, dev) : 1;
         if (split > 1) {
-            const int64_t bytes = split * p.experts * p.M * ((p.N + 3) / 4 * 4) * 4;
+            const int64_t bytes = split * p.experts * p.M * slice_ld(p.N) * 4;
             if (float *sums = scratch_alloc(dev, static_cast<size_t>(bytes), stream)) {
                 rc = sliced_launch(p, split, sums, dev, stream, launches);
                 scratch_free(sums, stream);

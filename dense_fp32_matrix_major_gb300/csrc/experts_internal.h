@@ -52,6 +52,11 @@ struct GroupedProblem {
     int split = 1;  // wgrad: slices of a group's rows; C is then fp32, an item per slice, rows 16-byte aligned
 };
 int grouped_launch(const GroupedProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
+// Matrices whose rows were summed in slices: C[e] = the sum over s of the fp32
+// matrices sums[e * split + s], M x N in rows of slice_ld(N), in that order.
+inline int64_t slice_ld(int64_t N) { return (N + 3) / 4 * 4; }
+int join_slices_launch(int type, const float *sums, int split, int64_t experts, int64_t M, int64_t N, void *C,
+                       int64_t ldc, int64_t strideC, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 // fp32 on SM pairs (experts_gemm_f32.cu).
 bool grouped_f32_supports(const GroupedProblem &p);
 void grouped_f32_tile(const GroupedProblem &p, int64_t *high, int64_t *wide);  // of C

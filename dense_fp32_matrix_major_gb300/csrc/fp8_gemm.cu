@@ -105,6 +105,7 @@ enum Form { ROWS_N, ROWS_T, WGRAD };
 struct Args {
     const int32_t *offsets;  // NULL: one group
     int rows, experts;
+    int split;         // wgrad: slices of a group's rows, whole blocks but the last; the "groups" are then slices
     int tiles_n;
     int blocks;        // wgrad: of A and B
     int k_blocks;      // rows
@@ -127,14 +128,24 @@ struct Tile {
     int group, row0, row_end, n0, k0, k_blocks;
 };
 
-__device__ __forceinline__ int start_of(const Args &a, int e) {
+__device__ __forceinline__ int group_of_rows(const Args &a, int e) {
     return a.offsets ? ex::group_start(a.offsets, e, a.rows) : (e == 0 ? 0 : a.rows);
+}
+
+template <Form FORM>
+__device__ __forceinline__ int start_of(const Args &a, int e) {
+    if (FORM != WGRAD || a.split == 1) return group_of_rows(a, e);
+    const int g = e / a.split, s = e - g * a.split, begin = group_of_rows(a, g);
+    if (s == 0) return begin;
+    const int end = max(begin, group_of_rows(a, g + 1));
+    const int slice = ((end - begin + KB - 1) / KB + a.split - 1) / a.split * KB;
+    return begin + min(s * slice, end - begin);
 }
 
 template <Form FORM, class F>
 __device__ __forceinline__ void for_each_tile(const Args &a, volatile int *abort_flag, int index, int count, F &&f) {
     int e = 0, begin = 0, base = 0, first = 0;  // base: tiles (rows: of rows) before group e; first: blocks
-    int next = start_of(a, 1), end = max(begin, next);
+    int next = start_of<FORM>(a, 1), end = max(begin, next);
     const int tiles_m = static_cast<int>((a.M + PM - 1) / PM);  // wgrad
     int tiles = FORM == WGRAD ? tiles_m : (end - begin + PM - 1) / PM;
     for (int64_t u = index;; u += count) {
@@ -147,7 +158,7 @@ __device__ __forceinline__ void for_each_tile(const Args &a, volatile int *abort
             ++e;
             if (FORM == WGRAD && e == a.experts) return;
             begin = next;
-            next = e < a.experts ? start_of(a, e + 1) : a.rows;
+            next = e < a.experts ? start_of<FORM>(a, e + 1) : a.rows;
             end = max(begin, next);
             if (FORM != WGRAD) tiles = (end - begin + PM - 1) / PM;
         }
@@ -819,13 +830,15 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
     }
+    const int64_t matrices = p.experts * p.split;  // of C
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     alignas(64) CUtensorMap map1{}, map2{}, few{}, out{};
     Args a{};
     a.offsets = p.offsets;
     a.rows = static_cast<int>(p.rows);
-    a.experts = static_cast<int>(p.experts);
+    a.experts = static_cast<int>(matrices);
+    a.split = p.split;
     a.N = p.N;
     a.C = p.C;
     a.ldc = p.ldc;
@@ -833,7 +846,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     a.out_type = p.out_type;
     const int64_t per = p.out_type == SGEMM_TYPE_F32 ? 4 : 8;
     a.vector = reinterpret_cast<uintptr_t>(p.C) % 16 == 0 && p.ldc % per == 0 &&
-               (!p.wgrad || p.experts == 1 || p.strideC % per == 0);
+               (!p.wgrad || matrices == 1 || p.strideC % per == 0);
     a.scale_rows = p.sA;
     a.scale_cols = p.sB;
     bool ok;
@@ -843,7 +856,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
         a.M = p.M;
         a.ld_rows = p.M;
         a.b_cols = p.N;
-        row_tiles = (p.M + PM - 1) / PM * p.experts;
+        row_tiles = (p.M + PM - 1) / PM * matrices;
         ok = encode_map_typed(&map1, type, 1, p.A, p.rows, p.M, p.lda, 1, 0, HALF, KB, sw) &&
              encode_map_typed(&map2, type, 1, p.B, p.rows, p.N, p.ldb, 1, 0, HALF, KB, sw);
         few = map1;  // not read by the kernel
@@ -862,7 +875,7 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
                              : encode_map_typed(&map2, type, 1, p.B, p.K, p.N, p.ldb, p.experts, strideB, HALF, KB, sw));
     }
     if (!ok) return SGEMM_ERR_LAUNCH;
-    const int64_t size = ex::type_size(p.out_type), items = p.wgrad ? p.experts : 1;
+    const int64_t size = ex::type_size(p.out_type), items = p.wgrad ? matrices : 1;
     const CUtensorMapDataType out_type = p.out_type == SGEMM_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                          : p.out_type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -891,12 +904,48 @@ int launch_form(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream
     return SGEMM_OK;
 }
 
+// Slices of the groups' rows in wgrad that pay, where the tiles leave half of the
+// SM pairs idle: a block of 128 rows takes a pair 0.87 us; the sums are written
+// and read at 5 TB/s, the second launch and its wait take 6 us. Groups are taken
+// as even. In slices and whole: 1024 x 2048 over 16384 rows 68 and 111 us, 1024 x
+// 1024 over 4096 23 and 33, 256 x 256 over 30000 32 and 196 (slices of 3 blocks in
+// place of 8: 50, for the join reads more and each role steps over more of them).
+int slices_of(const GemmProblem &p, const DeviceInfo &dev) {
+    const int64_t tiles = (p.M + PM - 1) / PM * ((p.N + PN - 1) / PN) * p.experts, pairs = dev.sm_count / 2;
+    if (2 * tiles > pairs) return 1;
+    const double blocks = static_cast<double>(p.rows) / static_cast<double>(p.experts * KB);
+    int64_t split = pairs / tiles;
+    if (split > blocks / 8) split = static_cast<int64_t>(blocks / 8);
+    if (split < 2) return 1;
+    const double sums = 8.0 * static_cast<double>(split * p.experts * p.M * p.N) / 5e6;
+    const double saved = blocks * (1.0 - 1.0 / static_cast<double>(split)) * 0.87;
+    return saved > 6.0 + sums ? static_cast<int>(split) : 1;
+}
+
 }  // namespace
 
 int gemm_launch(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches) {
     if (gemm_few(p, dev)) return gemm_few_launch(p, stream, launches);
     if (dev.device < 0 || dev.device >= kMaxDevices) return SGEMM_ERR_DEVICE;
-    if (p.wgrad) return launch_form<WGRAD>(p, dev, stream, launches);
+    if (p.wgrad) {
+        const int split = slices_of(p, dev);
+        float *sums = nullptr;
+        if (split > 1)
+            sums = scratch_alloc(dev, static_cast<size_t>(split * p.experts * p.M * ex::slice_ld(p.N)) * 4, stream);
+        if (!sums) return launch_form<WGRAD>(p, dev, stream, launches);
+        GemmProblem q = p;
+        q.split = split;
+        q.out_type = SGEMM_TYPE_F32;
+        q.C = sums;
+        q.ldc = ex::slice_ld(p.N);
+        q.strideC = p.M * q.ldc;
+        int rc = launch_form<WGRAD>(q, dev, stream, launches);
+        if (rc == SGEMM_OK)
+            rc = ex::join_slices_launch(p.out_type, sums, split, p.experts, p.M, p.N, p.C, p.ldc, p.strideC, dev, stream,
+                                        launches);
+        scratch_free(sums, stream);
+        return rc;
+    }
     return p.transB == SGEMM_OP_T ? launch_form<ROWS_T>(p, dev, stream, launches)
                                   : launch_form<ROWS_N>(p, dev, stream, launches);
 }

@@ -45,6 +45,7 @@ struct GemmProblem {
     const float *sB;
     void *C;
     int64_t ldc, strideC;
+    int split = 1;  // wgrad: slices of a group's rows; C is then fp32, an item per slice
 };
 int gemm_launch(const GemmProblem &p, const DeviceInfo &dev, cudaStream_t stream, int *launches);
 

@@ -7,8 +7,10 @@
  * Conventions are those of sgemm.h and experts.h: sizes and strides are int64_t
  * element counts, pointers are device pointers owned by the caller, calls
  * enqueue on `stream` and return, status codes are sgemm_status values and on
- * an error nothing is enqueued. Nothing is kept between calls, no memory is
- * allocated. Outputs must not overlap inputs.
+ * an error nothing is enqueued. Nothing is kept between calls; the gradient of few
+ * matrices over many rows takes sums of slices of them from the library's
+ * stream-ordered pool, otherwise no memory is allocated. Outputs must not overlap
+ * inputs.
  *
  * Values. E4M3 (4 exponent bits, 3 digits, largest value 448, no infinity) and
  * E5M2 (largest finite value 57344). An element stands for its 8-bit value

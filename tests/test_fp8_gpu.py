@@ -269,6 +269,29 @@ def test_wgrad(fp8, rows, M, N):
     check_product(fp8.gemm_wgrad(a, b), meaning(a, "columns").t(), meaning(b, "columns"), rows)
 
 
+@pytest.mark.parametrize("counts,tail", [(None, 0), ([3000], 0), ([8000, 0, 130, 301], 5), ([3000, 2500, 900], 0)])
+@pytest.mark.parametrize("M,N", [(1, 1), (130, 270), (64, 96)])
+def test_wgrad_in_slices(fp8, counts, tail, M, N):
+    """Few matrices over many rows, whose rows are summed in slices."""
+    rows = 5003 if counts is None else sum(counts) + tail
+    g = torch.Generator(device="cuda").manual_seed(rows + M)
+    x, y = (torch.randn((rows, n), generator=g, device="cuda") for n in (M, N))
+    off = None if counts is None else offsets_of(counts).cuda()
+    a, b = fp8.quantize(x, "columns", offsets=off), fp8.quantize(y, "columns", dtype=E5M2, offsets=off)
+    A, B = meaning(a, "columns"), meaning(b, "columns")
+    for dtype in DTYPES.values():
+        shape = (M, N) if counts is None else (len(counts), M, N)
+        room = torch.full((*shape[:-2], M + 1, N + 3), 7.0, dtype=dtype, device="cuda")
+        c = fp8.gemm_wgrad(a, b, off, room[..., :M, :N])
+        assert bool((room[..., M:, :] == 7).all() and (room[..., N:] == 7).all())
+        assert torch.equal(fp8.gemm_wgrad(a, b, off, dtype=dtype), c)
+        at = 0
+        for e, n in enumerate([rows] if counts is None else counts):
+            end = at + -(-n // 128) * 128
+            check_product(c if counts is None else c[e], A[at:end].t(), B[at:end], max(n, 1), f"{dtype} group {e}")
+            at = end
+
+
 def test_a_row_depends_on_itself(fp8):
     """The same row gives the same bits among others and in a group, and, where few rows have a kernel of their own,
     the same bits among few."""
