@@ -54,9 +54,10 @@ __device__ __forceinline__ uint4 load_once(const uint8_t *p) {
 
 // The first n of 16 bytes, zeros for the others.
 __device__ __forceinline__ uint4 load_part(const uint8_t *p, int64_t n) {
+    if (n >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
     uint64_t lo = 0, hi = 0;
 #pragma unroll 1
-    for (int i = static_cast<int>(min(n, static_cast<int64_t>(16))) - 1; i >= 0; --i) {
+    for (int i = static_cast<int>(n) - 1; i >= 0; --i) {
         hi = (hi << 8) | (lo >> 56);
         lo = (lo << 8) | p[i];
     }

@@ -719,8 +719,10 @@ struct HiddenJob {
     __device__ __forceinline__ void write(const Cursor &c, int m, int feature, float v) const {
         float *to = a.h + pair(c, m) * a.ldh;
         if (a.x_type != SGEMM_TYPE_F32) {
-            // Two bf16 terms, 16 bits of v: what a 16-bit y rounds away is 2^7 times as large.
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+            // Two bf16 terms, 16 bits of v: what a 16-bit y rounds away is 2^7 times as
+            // large. The first of a finite v is finite.
+            constexpr float most = 3.38953139e38f;  // bf16's largest
+            const __nv_bfloat16 hi = __float2bfloat16_rn(isfinite(v) ? fminf(fmaxf(v, -most), most) : v);
             __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(to) + feature;
             p[0] = hi;
             p[a.ldh] = __float2bfloat16_rn(isfinite(v) ? v - __bfloat162float(hi) : 0.0f);

@@ -192,6 +192,22 @@ def test_hidden_values_past_fp16(layer):
     check(layer, c, True, None)
 
 
+def test_hidden_values_past_bf16(layer):
+    """h between bf16's largest number and fp32's, which is finite in both."""
+    x = torch.ones((1, 8), dtype=torch.bfloat16, device="cuda")
+    w1, w2 = torch.zeros((1, 8, 8), device="cuda"), torch.zeros((1, 8, 8), device="cuda")
+    w1[0, :, 0], w1[0, :, 1] = torch.finfo(torch.bfloat16).max, 1.2e36
+    w1[0, 4:] *= -1
+    w2[0] = 2.0 ** -100
+    w2[0, :, 4:] *= -1
+    one = torch.ones((1, 1), device="cuda")
+    ids = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    h = x.double() @ w1[0].bfloat16().double().t()
+    assert float(h.abs().max()) > torch.finfo(torch.bfloat16).max
+    y = layer.forward(x, ids, one, w1.bfloat16(), w2.bfloat16(), activation=None)
+    check_layer(y, x, ids, one, w1.bfloat16().double(), w2.bfloat16().double(), False, None)
+
+
 def test_nothing(layer):
     f = lambda t, k, w, h: layer.forward(  # noqa: E731
         torch.zeros((t, w), device="cuda"), torch.zeros((t, k), dtype=torch.int64, device="cuda"),
