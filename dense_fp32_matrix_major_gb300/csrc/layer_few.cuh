@@ -20,23 +20,34 @@
 // ring in shared memory (cp.async), two slices ahead: 128 KB on their way to an SM
 // at no cost in registers, and no lane waits for another's copies. (Slices of 128
 // bytes, four ahead: 203 us in place of 185 for 32 tokens through 8 of 128 experts
-// of 2048 x 768.) (Bulk copies
-// of 256 bytes a row take 38 cycles each: 274 us for the 8-bit layer of 16 experts
-// of 4096 x 4096.) x and h come by plain loads two to four chunks ahead, mostly from
-// the caches.
+// of 2048 x 768. Bulk copies of 256 bytes a row take 38 cycles each: 274 us for the
+// 8-bit layer of 16 experts of 4096 x 4096.) x and h come by plain loads one to four
+// chunks ahead, mostly from the caches.
 //
-// Arithmetic. Where x is 16-bit and the matrices' rows are 16-byte aligned, warp
-// matrix instructions (16 rows of the matrix x k x 8 pairs, fp32 sums) on the
-// values as they are: bf16 and fp16 with x of the same type; 8-bit ones as fp16
-// with fp16 x, as tf32 with bf16 x. h enters as two bf16 terms, 16 of its 24 bits (y
-// is rounded to 11 at most), which the first kernel stores apart: as they are with
-// bf16 matrices, as tf32 with fp16 and 8-bit ones. With fp32 x fp32 multiply-adds, because the
-// instruction cuts its running sums (1.3e-6 of the result's norm where
-// multiply-adds leave 0.2e-6). (tcgen05 wants its operands in shared memory and
-// 128 rows a tile for at most 16 columns of x here.) Which k a lane holds does not
-// matter to a matrix instruction as long as matrix and x agree, so a lane takes 16
-// bytes of a row that lie together. Of rows that are not 16-byte aligned it takes
-// them out of the 32 bytes around, 15 instructions for 16 bytes.
+// Rows that do not start on 16-byte boundaries are copied from the boundary before
+// them on, and a lane takes its 16 bytes out of the 32 around them in registers, 15
+// instructions. (Value by value, with multiply-adds: 404 us in place of 97 for 32
+// tokens through 4 of 32 experts of 1537 x 1023, gated, bf16.)
+//
+// Arithmetic. Where x is 16-bit, warp matrix instructions (16 rows of the matrix x
+// k x 8 pairs, fp32 sums) on the values as they are: bf16 and fp16 with x of the
+// same type; 8-bit ones as x's type, exactly. h enters as two bf16 terms, 16 of its
+// 24 bits (y is rounded to 11 at most), which the first kernel stores apart: as they are with
+// bf16 matrices and with 8-bit ones made bf16, as tf32 with fp16 ones. (8-bit ones as tf32 with bf16
+// x and with h, fewer steps for a value but twice the instructions that multiply:
+// 140 us in place of 127 for 8 tokens, 2 of 16 experts of 4096 x 4096.) With fp32 x
+// fp32 multiply-adds, because the instruction cuts its running sums (1.3e-6 of the
+// result's norm where multiply-adds leave 0.2e-6); x then goes through 512 bytes of
+// shared memory, from the lane that loaded it to all. (Loaded by every lane: 449 us in
+// place of 121 for 32 tokens, 4 of 32 experts of 1536 x 1024.) (tcgen05 wants its operands in
+// shared memory and 128 rows a tile for at most 16 columns of x here.) Which k a
+// lane holds does not matter as long as matrix and x agree, so a lane takes 16 bytes
+// of a row that lie together.
+//
+// What it reaches: 32 tokens through 8 of 128 experts of 2048 x 768, gated, fp16, 180
+// us, 5.8 TB/s. One token through 8 of 64 experts of 2048 x 1024 takes 29 us for 100 MB:
+// the start and the end of two kernels. 8-bit matrices are bound by the instructions
+// that a byte takes: 4.2 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -154,9 +165,9 @@ struct Matrix {
 };
 
 // How sums are made: fp32 multiply-adds; matrix instructions on 16-bit values,
-// with x, or with h in two planes; on fp16 made of 8-bit values; on tf32 with x of
-// bf16, or with h in two planes.
-enum Math { FMA, NATIVE, PLANES, HALF8, TF32_X, TF32_H };
+// with x, or with h in two planes; on fp16 or bf16 made of 8-bit values, with x of
+// that type, or with h; on tf32 with h.
+enum Math { FMA, NATIVE, PLANES, HALF8, BF8, BF8_H, TF32_H };
 
 // 16 bytes of a row of K values from value k on, zeros past its end. They are 16-byte aligned.
 template <int SIZE>
@@ -235,6 +246,15 @@ __device__ __forceinline__ uint32_t fp8_halves(uint32_t w) {
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w)));
     return h2;
+}
+
+// The same as bf16, exactly too.
+template <int H>
+__device__ __forceinline__ uint32_t fp8_bf16(uint32_t w) {
+    const uint32_t h = fp8_halves<H>(w);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // Values 2 i and 2 i + 1 of 16 bytes of 16- or 8-bit values as fp32.
@@ -392,7 +412,7 @@ template <int H, int MATH, bool ANY, class X, class Job>
 __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint32_t ring, float4 *parts, int *part_of,
                                          Rest &rest) {
     using M = Matrix<H>;
-    constexpr bool SHIFT = ANY && !M::FP8, SPLIT = ANY && !Job::ALIGNED, TWO = MATH == PLANES || MATH == TF32_H;
+    constexpr bool SHIFT = ANY && !M::FP8, SPLIT = ANY && !Job::ALIGNED, TWO = MATH == PLANES || MATH == BF8_H || MATH == TF32_H;
     // 16-byte pieces of x in a lane's part of a chunk, and chunks of them on their way.
     constexpr int PX = M::PER * static_cast<int>(sizeof(X)) / 16, PIECES = TWO ? 2 * M::PER / 8 : PX,
                   XP = SPLIT ? (PIECES > 1 ? 1 : 2) : (PIECES > 2 ? 2 : 4), XW = SPLIT ? 8 : 4;
@@ -524,15 +544,25 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
             for (int j = 0; j < 4; ++j)
                 mma_16<false>(d[j & 1], fp8_halves<H>(lo[j]), fp8_halves<H>(hi[j]), fp8_halves<H>(lo[j] >> 16),
                               fp8_halves<H>(hi[j] >> 16), v[j / 2][2 * (j & 1)], v[j / 2][2 * (j & 1) + 1]);
-        } else if constexpr (MATH == TF32_X || MATH == TF32_H) {
+        } else if constexpr (MATH == BF8 || MATH == BF8_H) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = fp8_bf16<H>(lo[j]), a1 = fp8_bf16<H>(hi[j]), a2 = fp8_bf16<H>(lo[j] >> 16),
+                               a3 = fp8_bf16<H>(hi[j] >> 16);
+#pragma unroll
+                for (int i = 0; i < (MATH == BF8_H ? 2 : 1); ++i) {
+                    const uint32_t(&x)[4] = v[MATH == BF8_H ? j / 2 * 2 + i : j / 2];
+                    mma_16<true>(d[MATH == BF8_H ? i : j & 1], a0, a1, a2, a3, x[2 * (j & 1)], x[2 * (j & 1) + 1]);
+                }
+            }
+        } else if constexpr (MATH == TF32_H) {
 #pragma unroll
             for (int j = 0; j < M::PER / 2; ++j) {
                 const float2 a0 = two_of<H>(lo, j), a1 = two_of<H>(hi, j);
 #pragma unroll
-                for (int i = 0; i < (MATH == TF32_H ? 2 : 1); ++i) {
-                    const uint32_t two = v[MATH == TF32_H ? j / 4 * 2 + i : j / 4][j % 4];
-                    mma_tf32(d[MATH == TF32_H ? i : j & 1], a0.x, a1.x, a0.y, a1.y, half_of(two, 0, true),
-                             half_of(two, 1, true));
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t two = v[j / 4 * 2 + i][j % 4];
+                    mma_tf32(d[i], a0.x, a1.x, a0.y, a1.y, half_of(two, 0, true), half_of(two, 1, true));
                 }
             }
         }
