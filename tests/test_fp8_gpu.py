@@ -105,6 +105,36 @@ def test_quantize_special_values(fp8, block):
             assert bool(torch.isfinite(q.scales).all()) and bool((q.scales >= 2.0 ** -126).all())
 
 
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("block", ["rows", "columns", "blocks"])
+def test_quantize_special_values_of_16_bits(fp8, block, pad, name):
+    """The same, in rows that are 16-byte aligned and in others."""
+    dtype = DTYPES[name]
+    big, small = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal
+    x = rows_of(300, 264, dtype, 6)
+    x[0:128, 0:128] = 0.0
+    x[3, 200] = float("inf")
+    x[4, 201] = float("-inf")
+    x[5, 202] = float("nan")
+    x[6, 203] = -float("nan")
+    x[128:256, 5] = float("nan")
+    x[130, :] = torch.linspace(-small, small, 264)
+    x[131, 0:64] = big
+    x[132, :] = float("nan")
+    x[133, 5] = -0.0
+    x[134, :] = float("inf")
+    x[256:, 128:256] = float("-inf")
+    x[299, 130] = -big
+    room = torch.zeros((300, 264 + pad), dtype=dtype, device="cuda")
+    room[:, :264] = x.cuda()
+    for to in (E4M3, E5M2):
+        q = fp8.quantize(room[:, :264], block, dtype=to)
+        values, scales = quantize64(x, block, to)
+        same(q.values, values)
+        same(q.scales, scales.astype(np.float64))
+
+
 def test_quantize_every_border(fp8):
     """All 8-bit values, the borders between them and their neighbours in fp32, at a scale of 1."""
     for to in (E4M3, E5M2):
