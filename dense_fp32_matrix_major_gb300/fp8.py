@@ -65,39 +65,57 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _pitch(cols):
+    """Row stride of a matrix of these sizes whose own says nothing (one row, no elements)."""
+    return max(-(-cols // 16) * 16, 16)
+
+
 def _strides(t, name, dtypes, dims):
     """Row and item stride of a 2-D or 3-D CUDA tensor of row-major matrices."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() not in dims or not t.is_cuda:
         raise TypeError(f"{name} must be a {' or '.join(f'{d}-D' for d in dims)} CUDA tensor of "
                         f"{' or '.join(str(d) for d in dtypes)}")
+    strides = t.stride()
     rows, cols = t.shape[-2:]
-    if cols > 1 and t.stride(-1) != 1:
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
     if rows == 0 or cols == 0:
-        return max(-(-cols // 16) * 16, 16), 0
-    return (t.stride(-2) if rows > 1 else max(-(-cols // 16) * 16, 16)), (t.stride(0) if t.dim() == 3 else 0)
+        return _pitch(cols), 0
+    return (strides[-2] if rows > 1 else _pitch(cols)), (strides[0] if len(strides) == 3 else 0)
 
 
-def _operand(t, name, dims, shape_of_scales):
+def _operand(t, name, dims, block):
     """(type, row stride, item stride, values pointer, scales pointer) of a product's operand."""
     if not isinstance(t, Quantized):
         raise TypeError(f"{name} must be a fp8.Quantized")
-    ld, stride = _strides(t.values, name, FP8_TYPES, dims)
-    ptr = t.values.data_ptr()
-    if ld % 16 or ptr % 16 or (t.values.dim() == 3 and t.values.shape[0] > 1 and stride % 16):
+    values, scales = t
+    ld, stride = _strides(values, name, FP8_TYPES, dims)
+    shape = values.shape
+    ptr = values.data_ptr()
+    if ld % 16 or ptr % 16 or (stride % 16 and shape[0] > 1):
         raise ValueError(f"{name}'s rows must start on 16-byte boundaries (as fp8.quantize lays them out)")
-    sp = _contiguous(t.scales, f"{name}'s scales", _FP32, shape_of_scales(t.values.shape))
-    return FP8_TYPES[t.values.dtype], ld, stride, ptr, sp
+    if block == "rows":
+        want = (_blocks(shape[1]), shape[0])
+    elif block == "columns":
+        want = (_blocks(shape[0]), shape[1])
+    else:
+        want = (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1]))
+    return FP8_TYPES[values.dtype], ld, stride, ptr, _contiguous(scales, f"{name}'s scales", _FP32, want)
 
 
-def _out(out, shape, dtype, device, stream):
-    if dtype not in TYPES:
-        raise TypeError("dtype must be float32, bfloat16 or float16")
+def _out(out, shape, dtype, like, stream):
+    """(tensor, row stride, item stride) of a product's result, ``out`` or a new tensor."""
+    rows, cols = shape[-2:]
     if out is None:
-        return _empty(shape, dtype, device, stream)
-    if tuple(out.shape) != tuple(shape):
+        if dtype not in TYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16")
+        return (_empty(shape, dtype, like.device, stream), cols if rows > 1 and cols else _pitch(cols),
+                rows * cols if len(shape) == 3 else 0)
+    if not isinstance(out, torch.Tensor) or out.dtype not in TYPES:
+        raise TypeError("out must be a float32, bfloat16 or float16 tensor")
+    if tuple(out.shape) != shape:
         raise ValueError("out has the wrong shape")
-    return out
+    return (out, *_strides(out, "out", TYPES, (len(shape),)))
 
 
 def quantize(x, block="rows", *, dtype=torch.float8_e4m3fn, pow2=False, offsets=None, out=None, stream=None):
@@ -130,23 +148,27 @@ def quantize(x, block="rows", *, dtype=torch.float8_e4m3fn, pow2=False, offsets=
             raise ValueError("offsets must be experts + 1 long")
         experts = offsets.shape[0] - 1
         stored = 128 * lib.sgemm_fp8_blocks(rows, experts)
-    lead = tuple(x.shape[:-2])
+    lead = x.shape[:-2]
+    pow2 = 1 if pow2 else 0
     shape = (_blocks(cols), rows) if block == "rows" else \
         (_blocks(stored), cols) if block == "columns" else (*lead, _blocks(rows), _blocks(cols))
     if out is None:
-        wide = -(-cols // 16) * 16
-        values = _empty((*lead, stored, wide), dtype, x.device, stream)
-        out = Quantized(values if wide == cols else values[..., :cols], _empty(shape, torch.float32, x.device, stream))
+        ldq = max(-(-cols // 16) * 16, 16)
+        values = _empty((*lead, stored, ldq), dtype, x.device, stream)
+        scales = _empty(shape, torch.float32, x.device, stream)
+        out = Quantized(values if ldq == cols else values[..., :cols], scales)
+        stride_q, sp = (stored * ldq if lead else 0), scales.data_ptr()
     else:
         if not isinstance(out, Quantized) or out.values.dtype != dtype:
             raise TypeError(f"out must be a fp8.Quantized of {dtype}")
-        if tuple(out.values.shape) != (*lead, stored, cols):
+        values, scales = out
+        if tuple(values.shape) != (*lead, stored, cols):
             raise ValueError("out has the wrong shape")
-    ldq, stride_q = _strides(out.values, "out", FP8_TYPES, (x.dim(),))
-    sp = _contiguous(out.scales, "out's scales", _FP32, shape)
-    _check(lib.sgemm_fp8_quantize(TYPES[x.dtype], BLOCK_SHAPES[block], FP8_TYPES[dtype], int(bool(pow2)), items, rows,
-                                  cols, x.data_ptr(), ldx, stride_x, experts, off, out.values.data_ptr(), ldq,
-                                  stride_q, sp, _stream_handle(stream, x, offsets, out.values, out.scales)),
+        ldq, stride_q = _strides(values, "out", FP8_TYPES, (x.dim(),))
+        sp = _contiguous(scales, "out's scales", _FP32, shape)
+    _check(lib.sgemm_fp8_quantize(TYPES[x.dtype], BLOCK_SHAPES[block], FP8_TYPES[dtype], pow2, items, rows, cols,
+                                  x.data_ptr(), ldx, stride_x, experts, off, values.data_ptr(), ldq, stride_q, sp,
+                                  _stream_handle(stream, x, offsets, values, scales)),
            "sgemm_fp8_quantize")
     return out
 
@@ -158,19 +180,20 @@ def gemm(a, b, offsets=None, out=None, *, transB=False, dtype=torch.bfloat16, st
     "blocks". The result is of ``dtype`` (float32, bfloat16 or float16), or ``out``'s. The gradient of ``a`` is the
     same call on the output's gradient with ``transB`` the other way round.
     """
-    dims = (2,) if offsets is None else (3,)
-    ta, lda, _, ap, sa = _operand(a, "a", (2,), lambda s: (_blocks(s[1]), s[0]))
-    tb, ldb, stride, bp, sb = _operand(b, "b", dims, lambda s: (*s[:-2], _blocks(s[-2]), _blocks(s[-1])))
+    ta, lda, _, ap, sa = _operand(a, "a", (2,), "rows")
+    tb, ldb, stride, bp, sb = _operand(b, "b", (2,) if offsets is None else (3,), "blocks")
     rows, K = a.values.shape
-    N, K2 = b.values.shape[-2:] if transB else b.values.shape[:-3:-1]
+    shape = b.values.shape
+    N, K2 = shape[-2:] if transB else shape[:-3:-1]
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    E = 1 if offsets is None else b.values.shape[0]
-    off = 0 if offsets is None else _contiguous(offsets, "offsets", _INT32, (E + 1,))
-    out = _out(out, (rows, N), dtype if out is None else out.dtype, a.values.device, stream)
-    ldc, _ = _strides(out, "out", TYPES, (2,))
-    _check(lib.sgemm_fp8_gemm(TYPES[out.dtype], int(transB), ta, tb, rows, N, K, E, off, ap, lda, sa, bp, ldb, stride,
-                              sb, out.data_ptr(), ldc, _stream_handle(stream, *a, *b, offsets, out)),
+    E, off = 1, 0
+    if offsets is not None:
+        E = shape[0]
+        off = _contiguous(offsets, "offsets", _INT32, (E + 1,))
+    out, ldc, _ = _out(out, (rows, N), dtype, a.values, stream)
+    _check(lib.sgemm_fp8_gemm(TYPES[out.dtype], 1 if transB else 0, ta, tb, rows, N, K, E, off, ap, lda, sa, bp, ldb,
+                              stride, sb, out.data_ptr(), ldc, _stream_handle(stream, *a, *b, offsets, out)),
            "sgemm_fp8_gemm")
     return out
 
@@ -182,8 +205,8 @@ def gemm_wgrad(a, b, offsets=None, out=None, *, dtype=torch.float32, stream=None
     :func:`gemm`'s b is ``gemm_wgrad(a, dout)``, or ``gemm_wgrad(dout, a)`` for ``transB``. The result is of
     ``dtype``, or ``out``'s.
     """
-    ta, lda, _, ap, sa = _operand(a, "a", (2,), lambda s: (_blocks(s[0]), s[1]))
-    tb, ldb, _, bp, sb = _operand(b, "b", (2,), lambda s: (_blocks(s[0]), s[1]))
+    ta, lda, _, ap, sa = _operand(a, "a", (2,), "columns")
+    tb, ldb, _, bp, sb = _operand(b, "b", (2,), "columns")
     rows, M = a.values.shape
     if b.values.shape[0] != rows:
         raise ValueError(f"a has {rows} rows, b {b.values.shape[0]}")
@@ -196,9 +219,7 @@ def gemm_wgrad(a, b, offsets=None, out=None, *, dtype=torch.float32, stream=None
         if rows % 128:
             raise ValueError("operands with offsets hold whole blocks of 128 rows (as fp8.quantize lays them out)")
         E = offsets.shape[0] - 1
-    shape = (M, N) if offsets is None else (E, M, N)
-    out = _out(out, shape, dtype if out is None else out.dtype, a.values.device, stream)
-    ldc, stride = _strides(out, "out", TYPES, (len(shape),))
+    out, ldc, stride = _out(out, (M, N) if offsets is None else (E, M, N), dtype, a.values, stream)
     _check(lib.sgemm_fp8_gemm_wgrad(TYPES[out.dtype], ta, tb, rows, M, N, E, off, ap, lda, sa, bp, ldb, sb,
                                     out.data_ptr(), ldc, stride, _stream_handle(stream, *a, *b, offsets, out)),
            "sgemm_fp8_gemm_wgrad")

@@ -80,10 +80,11 @@ def forward(x, ids, weights, w1, w2, *, gated=False, activation="silu", out=None
     if cols != width or (gated and rows % 2) or tuple(m2.shape) != (E, width, hidden):
         raise ValueError(f"w1 {tuple(m1.shape)} and w2 {tuple(m2.shape)} do not fit x {tuple(x.shape)}")
     if out is None:
-        out = _empty((tokens, width), x.dtype, x.device, stream)
-    _, ldo = _rows(out, "out", x.dtype)
-    if tuple(out.shape) != (tokens, width):
-        raise ValueError("out has the wrong shape")
+        out, ldo = _empty((tokens, width), x.dtype, x.device, stream), max(width, 1)
+    else:
+        _, ldo = _rows(out, "out", x.dtype)
+        if tuple(out.shape) != (tokens, width):
+            raise ValueError("out has the wrong shape")
     need = lib.sgemm_experts_layer_workspace(tokens, top_k, hidden)
     space = _empty((need // 4,), torch.float32, x.device, stream) if need else None
     _check(lib.sgemm_experts_layer(code, held, ACTIVATIONS[activation], int(bool(gated)), tokens, top_k, E, width,
