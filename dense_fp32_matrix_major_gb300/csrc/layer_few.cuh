@@ -429,16 +429,20 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
 #pragma unroll
         for (int i = 0; i < 2; ++i) shift[i] = SHIFT ? static_cast<int>(reinterpret_cast<uintptr_t>(p + i * delta) & 15) : 0;
     };
+    // Pieces past a row's end, and rows past the matrix's, are copies of no bytes
+    // from the start of a row that is there.
     const uint8_t *row[2];
     int left[2];  // values from this lane's first piece to the row's end
     auto enter = [&] {
-        const uint8_t *p = job.base(load, g);
-        int shift[2];
+        const uint8_t *first = job.base(load, 0), *p = job.base(load, g);
+        int shift[2], none[2];
         shifts(p, shift);
+        shifts(first, none);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            row[i] = p + i * delta - shift[i] + 16 * t;
-            left[i] = job.there(load, i, g) ? K + shift[i] / M::SIZE - M::PER * t : 0;
+            const bool there = job.there(load, i, g);
+            row[i] = (there ? p + i * delta - shift[i] : first - none[0]) + 16 * t;
+            left[i] = there ? K + shift[i] / M::SIZE - M::PER * t : 0;
         }
     };
     enter();
@@ -449,7 +453,9 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
             const int64_t at = static_cast<int64_t>(load.slice) * SLICE;
             const int k = load.slice * M::SLICE_K;
             const bool inner = k + M::SLICE_K <= K;  // the rows end later
-            auto bytes = [&](int n) { return max(min(n, M::PER), 0) * M::SIZE; };
+            auto copy_part = [&](uint32_t dst, const uint8_t *from, const uint8_t *start, int n) {
+                copy_16(dst, n > 0 ? from : start, max(min(n, M::PER), 0) * M::SIZE);
+            };
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint8_t *p = row[i] + at;
@@ -460,13 +466,14 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
                 } else {
 #pragma unroll
                     for (int q = 0; q < CHUNKS; ++q)
-                        copy_16(to + 1024 * q + 512 * i, p + q * 64, bytes(left[i] - (k + q * M::CHUNK)));
+                        copy_part(to + 1024 * q + 512 * i, p + q * 64, row[i] - 16 * t, left[i] - (k + q * M::CHUNK));
                 }
             }
             if (SHIFT && t < 2) {
                 const int n = t == 0 ? left[0] : (left[1] > 0 ? left[1] + M::PER : 0);
-                copy_16(ring + static_cast<uint32_t>(stage * STAGE + FOLLOWING + 128 * t + 16 * g),
-                        (t == 0 ? row[0] : row[1] - 16) + at + SLICE, bytes(n - (k + M::SLICE_K)));
+                const uint8_t *start = t == 0 ? row[0] : row[1] - 16;
+                copy_part(ring + static_cast<uint32_t>(stage * STAGE + FOLLOWING + 128 * t + 16 * g), start + at + SLICE,
+                          start, n - (k + M::SLICE_K));
             }
             if (step(job, s, load)) enter();
         }
