@@ -234,10 +234,8 @@ __device__ __forceinline__ void realign(const uint32_t (&w)[8], int from, uint32
     for (int i = 0; i < 4; ++i) v[i] = SIZE == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], 8 * (from & 3));
 }
 
-__device__ __forceinline__ float half_of(uint32_t w, int i, bool bf16) {
-    if (bf16) return __uint_as_float(i ? w & 0xFFFF0000u : w << 16);
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(i ? w >> 16 : w)));
-}
+// Value i of two bf16 ones.
+__device__ __forceinline__ float bf16_of(uint32_t w, int i) { return __uint_as_float(i ? w & 0xFFFF0000u : w << 16); }
 
 // Two 8-bit values (the low 16 bits of w) as fp16, exactly.
 template <int H>
@@ -257,10 +255,9 @@ __device__ __forceinline__ uint32_t fp8_bf16(uint32_t w) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Values 2 i and 2 i + 1 of 16 bytes of 16- or 8-bit values as fp32.
+// Values 2 i and 2 i + 1 of 16 bytes of fp16 or 8-bit values as fp32.
 template <int H>
 __device__ __forceinline__ float2 two_of(const uint32_t (&w)[4], int i) {
-    if (H == BF16) return make_float2(half_of(w[i], 0, true), half_of(w[i], 1, true));
     const uint32_t h = H == F16 ? w[i] : fp8_halves<H>(w[i / 2] >> (16 * (i & 1)));
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
@@ -569,7 +566,7 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t two = v[j / 4 * 2 + i][j % 4];
-                    mma_tf32(d[i], a0.x, a1.x, a0.y, a1.y, half_of(two, 0, true), half_of(two, 1, true));
+                    mma_tf32(d[i], a0.x, a1.x, a0.y, a1.y, bf16_of(two, 0), bf16_of(two, 1));
                 }
             }
         }
