@@ -697,10 +697,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const uint32_t x[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
+                                // The scales first: one of them alone may take a sum out of range.
                                 const uint64_t xx = pack2(x[i], x[i]);
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
-                                    fma2(acc[c][i][h], mul2(pack2(p[16 * h + 2 * i], p[16 * h + 2 * i + 1]), of_lane[h]), xx);
+                                    fma2(acc[c][i][h], pack2(p[16 * h + 2 * i], p[16 * h + 2 * i + 1]), mul2(of_lane[h], xx));
                             }
                         }
                     }

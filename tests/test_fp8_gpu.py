@@ -322,6 +322,33 @@ def test_wgrad_in_slices(fp8, counts, tail, M, N):
             at = end
 
 
+@pytest.mark.parametrize("a,b", [(2.0 ** 100, 2.0 ** -100), (2.0 ** -100, 2.0 ** 100), (2.0 ** -126, 2.0 ** 120)])
+def test_scales_far_from_one(fp8, a, b):
+    """Two scales whose product is in range, where a block's sum times one of them would not be."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+
+    def far(shape, block, dtype, size, experts=0):
+        s = {"rows": (-(-shape[1] // 128), shape[0]), "columns": (-(-shape[0] // 128), shape[1]),
+             "blocks": (-(-shape[0] // 128), -(-shape[1] // 128))}[block]
+        lead = (experts,) if experts else ()
+        q = fp8.quantize(torch.randn((*lead, *shape), generator=g, device="cuda"), block, dtype=dtype)
+        return fp8.Quantized(q.values, size * (1 + torch.rand((*lead, *s), generator=g, device="cuda") / 2))
+
+    for ta, tb in ((E4M3, E4M3), (E5M2, E5M2), (E5M2, E4M3)):
+        for rows, trans in ((8, True), (300, True), (300, False)):
+            x, w = far((rows, 700), "rows", ta, a), far((260, 700) if trans else (700, 260), "blocks", tb, b)
+            check_product(fp8.gemm(x, w, transB=trans, dtype=torch.float32), meaning(x, "rows"),
+                          op(meaning(w, "blocks"), trans), 700, f"rows {rows} {trans}")
+        off = torch.tensor([0, 100, 384], dtype=torch.int32, device="cuda")
+        x, w = far((384, 200), "rows", ta, a), far((140, 200), "blocks", tb, b, 2)
+        c = fp8.gemm(x, w, off, transB=True, dtype=torch.float32)
+        for e, r in enumerate((slice(0, 100), slice(100, 384))):
+            check_product(c[r], meaning(x, "rows")[r], meaning(w, "blocks")[e].t(), 200, f"group {e}")
+        for rows, M, N in ((300, 130, 270), (5003, 130, 270)):  # the second in slices
+            x, y = far((rows, M), "columns", ta, a), far((rows, N), "columns", tb, b)
+            check_product(fp8.gemm_wgrad(x, y), meaning(x, "columns").t(), meaning(y, "columns"), rows, f"wgrad {rows}")
+
+
 def test_a_row_depends_on_itself(fp8):
     """The same row gives the same bits among others and in a group, and, where few rows have a kernel of their own,
     the same bits among few."""
