@@ -92,6 +92,7 @@ struct Lists {
     int expert[MAX_PAIRS], begin[MAX_PAIRS], count[MAX_PAIRS];  // of an entry
     int total[WARPS];
     int entries;
+    mutable int late;  // h has places to be made again (see sums_again)
 };
 
 __device__ __forceinline__ int id_of(const LArgs &a, int p) {
@@ -144,7 +145,10 @@ __device__ __forceinline__ void build_lists(const LArgs &a, Lists &l) {
         all += l.total[w];
     }
     l.entry_at[p] = before + __popc(ballot & (0xffffffffu >> (31 - lane))) - 1;
-    if (p == 0) l.entries = all;
+    if (p == 0) {
+        l.entries = all;
+        l.late = 0;
+    }
     __syncthreads();
     if (used && rank % MEMBERS == 0) {
         const int e = l.entry_at[place];
@@ -343,6 +347,11 @@ __device__ __forceinline__ void lds_128(uint32_t at, uint32_t (&v)[N], int first
 //   x(c, m)            pair m's row of x or h
 //   ALIGNED            those rows always start on 16-byte boundaries
 //   finish(c, sum)     takes a tile's sums: sum[2 i + j] of lane 4 g + t is row 8 i + g, pair 2 t + j
+// and where they may be made again:
+//   late(c)            which of the lane's sums, bit 2 i + j
+//   settle(c, sum, n)  takes those of bits n
+//   length()           values of a row
+//   value(x, k)        value k of a pair's row of x or h
 
 // The next slice; true where a tile starts.
 template <class Job>
@@ -711,9 +720,66 @@ __device__ __forceinline__ void sum_tiles(const Job &job, int items, int K, int 
     join(job, rest, parts, part_of);
 }
 
+// The matrix instructions sum a block of an 8-bit matrix before its scale: values
+// of x from 2^105 on (128 times 57344 is 2^22.8) may overflow where the scaled
+// products do not. Sums that are not finite are made again, of scaled values, when
+// the block's tiles are done; those of a pair with a NaN are not, which explains
+// them. (8 tokens, 2 of 16 experts of 4096 x 4096: 130 us, without this code 128,
+// which deals the registers out otherwise; made again as soon as a tile is done
+// 132; with the scale's power of two in the values from the start 138.) Called by
+// the whole block.
+template <int H, class Job>
+__device__ __forceinline__ void sums_again(const Job &job, int items) {
+    const int lane = threadIdx.x & 31, K = job.length();
+#pragma unroll 1
+    for (int item = threadIdx.x >> 5; item < items; item += WARPS) {
+        const Cursor c = job.cursor(item);
+        const unsigned late = job.late(c);
+        if (!__any_sync(0xffffffffu, late)) continue;
+        const int count = job.members(c);
+        unsigned with_nan = 0;  // pairs
+#pragma unroll 1
+        for (int m = 0; m < count; ++m) {
+            const void *x = job.x(c, m);
+            bool any = false;
+#pragma unroll 4
+            for (int k = lane; k < K; k += 32) any |= isnan(job.value(x, k));
+            with_nan |= __any_sync(0xffffffffu, any) ? 1u << m : 0;
+        }
+        float sum[4] = {};
+        unsigned made = 0;
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+            unsigned lanes = __ballot_sync(0xffffffffu, late >> n & 1);
+#pragma unroll 1
+            for (; lanes; lanes &= lanes - 1) {
+                const int to = __ffs(lanes) - 1, m = 2 * (to & 3) + (n & 1);
+                if (with_nan >> m & 1) continue;
+                const void *x = job.x(c, m);
+                const uint8_t *row = job.base(c, to >> 2) + (n >> 1) * job.delta();
+                const float *scale = job.scales(c) + job.scale_row(c, n >> 1, to >> 2);
+                float v = 0.0f;
+#pragma unroll 2
+                for (int k = lane; k < K; k += 32) {
+                    const uint32_t h = fp8_halves<H>(row[k]);
+                    v = fmaf(__low2float(*reinterpret_cast<const __half2 *>(&h)) * __ldg(scale + k / SGEMM_FP8_BLOCK_SIZE),
+                             job.value(x, k), v);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+                if (lane != to) continue;
+                made |= 1u << n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = i == n ? v : sum[i];
+            }
+        }
+        job.settle(c, sum, made);
+    }
+}
+
 // h of the entries' tiles of features: 16 rows of W1, 8 features with their gates
-// or 16 without.
-template <int H>
+// or 16 without. AGAIN: sums_again() follows.
+template <int H, bool AGAIN>
 struct HiddenJob {
     using M = Matrix<H>;
     const LArgs &a;
@@ -764,20 +830,51 @@ struct HiddenJob {
             to[feature] = v;
         }
     }
-    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const {
+    // Where a feature's sums are to be made again h is this NaN, which no rounding gives.
+    static constexpr uint16_t LATE = 0x7FC1;
+    __device__ __forceinline__ uint16_t *place(const Cursor &c, int m, int feature) const {
+        return reinterpret_cast<uint16_t *>(a.h + pair(c, m) * a.ldh) + feature;
+    }
+    template <bool MARK>
+    __device__ __forceinline__ void take(const Cursor &c, const float (&sum)[4], unsigned which) const {
         const int lane = threadIdx.x & 31, f = feature(c) + (lane >> 2), count = members(c);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int m = 2 * (lane & 3) + j;
             if (m >= count) continue;
-            const float v = activate(sum[j], a.activation);
             if (a.gated) {
-                if (f < a.hidden) write(c, m, f, v * sum[2 + j]);
+                if (f >= a.hidden || !(which >> j & 1)) continue;
+                write(c, m, f, activate(sum[j], a.activation) * sum[2 + j]);
+                if (MARK && !(isfinite(sum[j]) && isfinite(sum[2 + j]))) *place(c, m, f) = LATE, l.late = 1;
             } else {
-                if (f < a.hidden) write(c, m, f, v);
-                if (f + 8 < a.hidden) write(c, m, f + 8, activate(sum[2 + j], a.activation));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (f + 8 * i >= a.hidden || !(which >> (2 * i + j) & 1)) continue;
+                    write(c, m, f + 8 * i, activate(sum[2 * i + j], a.activation));
+                    if (MARK && !isfinite(sum[2 * i + j])) *place(c, m, f + 8 * i) = LATE, l.late = 1;
+                }
             }
         }
+    }
+    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const { take<AGAIN>(c, sum, 15); }
+    __device__ __forceinline__ void settle(const Cursor &c, const float (&sum)[4], unsigned which) const {
+        take<false>(c, sum, which);
+    }
+    __device__ __forceinline__ unsigned late(const Cursor &c) const {
+        const int lane = threadIdx.x & 31, f = feature(c) + (lane >> 2), count = members(c);
+        unsigned which = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int m = 2 * (lane & 3) + j;
+            if (m >= count) continue;
+            if (f < a.hidden && *place(c, m, f) == LATE) which |= (a.gated ? 5u : 1u) << j;
+            if (!a.gated && f + 8 < a.hidden && *place(c, m, f + 8) == LATE) which |= 4u << j;
+        }
+        return which;
+    }
+    __device__ __forceinline__ int length() const { return a.width; }
+    __device__ __forceinline__ float value(const void *x, int k) const {
+        return __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[k]);
     }
 };
 
@@ -816,13 +913,40 @@ struct OutJob {
     }
     __device__ __forceinline__ int64_t plane() const { return a.ldh * 2; }
     static constexpr bool ALIGNED = true;
-    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const {
+    __device__ __forceinline__ void finish(const Cursor &c, const float (&sum)[4]) const { settle(c, sum, 15); }
+    __device__ __forceinline__ void settle(const Cursor &c, const float (&sum)[4], unsigned which) const {
         const int lane = threadIdx.x & 31, count = members(c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int m = 2 * (lane & 3) + (i & 1), n = 16 * c.tile + 8 * (i >> 1) + (lane >> 2);
-            if (m < count) sums[(l.begin[c.entry] + m) * COLUMNS + n] = sum[i];
+            const int m = 2 * (lane & 3) + (i & 1);
+            if (m < count && (which >> i & 1)) *place(c, i) = sum[i];
         }
+    }
+    // Of sum i of the lane.
+    __device__ __forceinline__ float *place(const Cursor &c, int i) const {
+        const int lane = threadIdx.x & 31, m = 2 * (lane & 3) + (i & 1), n = 16 * c.tile + 8 * (i >> 1) + (lane >> 2);
+        return sums + (l.begin[c.entry] + m) * COLUMNS + n;
+    }
+    // Whether one of the thread's share of the block's sums is not finite.
+    __device__ __forceinline__ bool any_late() const {
+        bool any = false;
+        if (l.entries == 0) return false;
+        const int all = (l.begin[l.entries - 1] + l.count[l.entries - 1]) * COLUMNS;
+        for (int i = threadIdx.x; i < all; i += THREADS) any |= i % COLUMNS < cols && !isfinite(sums[i]);
+        return any;
+    }
+    __device__ __forceinline__ unsigned late(const Cursor &c) const {
+        const int lane = threadIdx.x & 31, count = members(c);
+        unsigned which = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * (lane & 3) + (i & 1) < count && there(c, i >> 1, lane >> 2) && !isfinite(*place(c, i))) which |= 1u << i;
+        return which;
+    }
+    __device__ __forceinline__ int length() const { return a.hidden; }
+    __device__ __forceinline__ float value(const void *x, int k) const {
+        const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(x) + k;
+        return __bfloat162float(h[0]) + __bfloat162float(h[a.ldh]);
     }
 };
 
@@ -846,13 +970,17 @@ __global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_c
     build_lists(a, l);
     const int per_tile = a.gated ? 8 : 16;  // features
     const int rows1 = a.gated ? 2 * a.hidden : a.hidden;
-    HiddenJob<H> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
+    HiddenJob<H, MATH == BF8> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
                      (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
     job.item_scales = static_cast<int64_t>((rows1 + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
     const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
     job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
     const int items = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) - job.first;
     sum_tiles<H, MATH, ANY, X>(job, items, a.width, part_of);
+    if constexpr (MATH == BF8) {
+        __syncthreads();
+        if (l.late) sums_again<H>(job, items);
+    }
 }
 
 template <int H, int MATH, bool ANY>
@@ -866,8 +994,15 @@ __global__ void __launch_bounds__(THREADS, 1) layer_out_kernel(const __grid_cons
     OutJob<H> job = out_job<H>(a, l, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), &n1);
     for (; job.at < n1; job.at += COLUMNS) {
         job.cols = min(COLUMNS, n1 - job.at);
-        sum_tiles<H, MATH, ANY, float>(job, a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0, a.hidden, part_of);
+        const int items = a.hidden > 0 ? l.entries * ((job.cols + 15) / 16) : 0;
+        sum_tiles<H, MATH, ANY, float>(job, items, a.hidden, part_of);
         __syncthreads();
+        if constexpr (MATH == BF8_H) {
+            if (__syncthreads_or(items > 0 && job.any_late())) {
+                sums_again<H>(job, items);
+                __syncthreads();
+            }
+        }
         for (int i = threadIdx.x; i < a.tokens * COLUMNS; i += THREADS) {
             const int n = i % COLUMNS, token = i / COLUMNS;
             if (n >= job.cols) continue;

@@ -208,6 +208,37 @@ def test_hidden_values_past_bf16(layer):
     check_layer(y, x, ids, one, w1.bfloat16().double(), w2.bfloat16().double(), False, None)
 
 
+@pytest.mark.parametrize("to", [E4M3, E5M2])
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_8_bit_sums_that_overflow_before_their_scale(layer, fp8, name, to):
+    """x or h so large that a block's values times it leave fp32, where scaled ones do not; a pair of an expert or more
+    than an entry has, sums that one warp has and that several share, and a NaN in another token."""
+    dtype = DTYPES[name]
+    for tokens, width, hidden in ((2, 300, 260), (20, 140, 130), (3, 2000, 2100)):
+        for gated in (False, True):
+            c = case(tokens, 2, 3, width, hidden, torch.float32, False)
+            gate = [torch.full_like(c["w1"], width ** -0.5)] if gated else []  # the second half: near one
+
+            def w1(first, second):
+                return torch.cat([c["w1"] * 2.0 ** first, *(w * 2.0 ** second for w in gate)], 1)
+
+            x = c["x"].to(dtype)
+            jobs = [(x, w1(117, 0), c["w2"] * 2.0 ** -114)]  # h
+            if dtype != torch.float16:
+                jobs.append((x * 2.0 ** 122, w1(-64, -64) if gated else w1(-30, 0), c["w2"]))  # x
+            for t, u1, u2 in jobs:
+                q1, q2 = fp8.quantize(u1, "blocks", dtype=to), fp8.quantize(u2, "blocks", dtype=to)
+                d1, d2 = meaning(q1, "blocks"), meaning(q2, "blocks")
+                y = layer.forward(t, c["ids"], c["weights"], q1, q2, gated=gated, activation=None)
+                assert bool(torch.isfinite(y).all())
+                check_layer(y, t, c["ids"], c["weights"], d1, d2, gated, None, f"{tokens} {gated}")
+                bad = t.clone()
+                bad[1, 7] = float("nan")
+                z = layer.forward(bad, c["ids"], c["weights"], q1, q2, gated=gated, activation=None)
+                rest = [i for i in range(tokens) if i != 1]
+                assert bool(z[1].isnan().all()) and torch.equal(z[rest], y[rest])
+
+
 def test_nothing(layer):
     f = lambda t, k, w, h: layer.forward(  # noqa: E731
         torch.zeros((t, w), device="cuda"), torch.zeros((t, k), dtype=torch.int64, device="cuda"),
