@@ -37,7 +37,8 @@
 // x and with h, fewer steps for a value but twice the instructions that multiply:
 // 140 us in place of 127 for 8 tokens, 2 of 16 experts of 4096 x 4096.) With fp32 x
 // fp32 multiply-adds, because the instruction cuts its running sums (1.3e-6 of the
-// result's norm where multiply-adds leave 0.2e-6); x then goes through 512 bytes of
+// result's norm where multiply-adds leave 0.2e-6), which is also why 16-bit values'
+// sums leave it after every slice of 128 (at no cost); x then goes through 512 bytes of
 // shared memory, from the lane that loaded it to all. (Loaded by every lane: 449 us in
 // place of 121 for 32 tokens, 4 of 32 experts of 1536 x 1024.) (tcgen05 wants its operands in
 // shared memory and 128 rows a tile for at most 16 columns of x here.) Which k a
@@ -660,11 +661,12 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
                 sums(xw[q % XP]);
             }
             load_x((q + XP) % CHUNKS, !last || q + XP < CHUNKS);
-            if (M::FP8 && MATH != FMA && q % PER_BLOCK == PER_BLOCK - 1) {
-                // A block of an 8-bit matrix ends.
+            if (MATH != FMA && q % PER_BLOCK == PER_BLOCK - 1) {
+                // A block of an 8-bit matrix ends, or a slice of another.
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sum[i] = fmaf(side[0][i] + side[1][i], scale[i >> 1][q / PER_BLOCK], sum[i]);
+                    const float more = side[0][i] + side[1][i];
+                    sum[i] = M::FP8 ? fmaf(more, scale[i >> 1][q / PER_BLOCK], sum[i]) : sum[i] + more;
                     side[0][i] = side[1][i] = 0.0f;
                 }
             }
@@ -673,12 +675,7 @@ __device__ __forceinline__ void sum_ring(const Job &job, int items, int K, uint3
         fetch(stage, n + STAGES < s.mine);
         const bool done = use.slice + 1 == s.slices;
         if (last || done) {
-            if constexpr (MATH == FMA) {
-                gather_lanes(fma, t, sum);
-            } else if constexpr (!M::FP8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = side[0][i] + side[1][i];
-            }
+            if constexpr (MATH == FMA) gather_lanes(fma, t, sum);
             if (done && started) {
                 job.finish(use, sum);
             } else if (started) {

@@ -239,6 +239,29 @@ def test_8_bit_sums_that_overflow_before_their_scale(layer, fp8, name, to):
                 assert bool(z[1].isnan().all()) and torch.equal(z[rest], y[rest])
 
 
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_small_terms_beside_a_large_sum(layer, name):
+    """A running sum of 2^24 that the last term takes back, with terms between whose sum over an instruction's 16 values
+    is half of the sum's last place: what an instruction cuts off is lost for the slice of 128 that holds a large
+    term, and not for the whole row. Enough features that a warp has whole rows of W1."""
+    dtype, width, hidden = DTYPES[name], 16384, 16 * 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    row = torch.full((width,), 0.25)
+    row[0] = row[-1] = 2.0 ** 12
+    x = row.to(dtype).cuda()[None]
+    row[-1] *= -1
+    w1 = row.to(dtype).cuda().expand(1, hidden, width).contiguous()
+    w2 = torch.zeros((1, width, hidden), dtype=dtype, device="cuda")
+    w2[0].fill_diagonal_(1)
+    y = layer.forward(x, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones((1, 1), device="cuda"), w1, w2,
+                      activation=None)
+    exact = (width - 2) / 16
+    # Two slices with a large term: 65 additions of a chain, each off by 2^-23 of 2^24; 128 slices added, half a last
+    # place of 2^24 each. Then y's rounding.
+    limit = 2 * 65 * 2 + 128
+    assert limit < exact / 2
+    assert float((y.double() - exact).abs().max()) <= limit + 2.0 ** -8 * 2 * exact
+
+
 def test_nothing(layer):
     f = lambda t, k, w, h: layer.forward(  # noqa: E731
         torch.zeros((t, w), device="cuda"), torch.zeros((t, k), dtype=torch.int64, device="cuda"),
