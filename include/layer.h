@@ -56,7 +56,8 @@ enum sgemm_layer_weights {
  * start on 16-byte boundaries, with ld1, ld2, stride1 and stride2 multiples of 16;
  * otherwise every width, alignment and stride is served, fastest where rows are
  * 16-byte aligned. Infinities and NaN follow IEEE arithmetic, except that an
- * infinite matrix element gives NaN.
+ * infinite element of a 16-bit W2, which meets both terms of h, may give NaN in
+ * place of an infinity.
  */
 int sgemm_experts_layer(int type, int held, int activation, int gated, int64_t tokens, int64_t top_k,
                         int64_t experts, int64_t width, int64_t hidden, const void *x, int64_t ldx, const void *ids,

@@ -170,6 +170,40 @@ def test_infinities_and_nan(layer, fp8, name):
     assert bool((y[4] == float("inf")).all()) and bool(torch.isfinite(y[rest]).all())
 
 
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("held", ["same", "e5m2"])
+def test_infinite_matrix_elements(layer, fp8, name, held):
+    """An infinity in W1 or W2, times positive values: infinities of its sign where its expert is used, for a 16-bit W2
+    perhaps NaN, and nothing elsewhere."""
+    dtype = DTYPES[name]
+    c = case(6, 2, 4, 136, 72, dtype, False)
+    c["ids"] = torch.tensor([[0, 1], [1, 2], [2, 0], [3, 3], [0, 0], [-1, 1]], dtype=torch.int32, device="cuda")
+    x, w1, w2 = (c[k].abs() + 0.125 for k in ("x", "w1", "w2"))
+    run = lambda a, b: layer.forward(x, c["ids"], c["weights"] + 0.5, a, b, activation="relu")  # noqa: E731
+
+    def matrices(w, at=None, sign=1):
+        w = w.clone() if held == "same" else fp8.quantize(w, "blocks", dtype=E5M2)
+        if at is not None and held == "same":
+            w[at] = sign * float("inf")
+        elif at is not None:
+            w.values.view(torch.uint8)[at] = 0x7C if sign > 0 else 0xFC
+        return w
+
+    fine = run(matrices(w1), matrices(w2))
+    assert bool(torch.isfinite(fine).all())
+    has, rest = [0, 1, 5], [2, 3, 4]  # tokens of expert 1
+    y = run(matrices(w1, (1, 30, 100)), matrices(w2))
+    assert bool((y[has] == float("inf")).all()) and torch.equal(y[rest], fine[rest])
+    y = run(matrices(w1), matrices(w2, (1, 90, 40), -1))
+    assert torch.equal(y[rest], fine[rest])
+    other = torch.arange(136, device="cuda") != 90
+    assert torch.equal(y[:, other], fine[:, other])
+    if held == "same" and dtype != torch.float32:
+        assert not bool(torch.isfinite(y[has, 90]).any()) and not bool((y[has, 90] == float("inf")).any())
+    else:
+        assert bool((y[has, 90] == -float("inf")).all())
+
+
 def test_outliers_at_zero_weights(layer, fp8):
     """A value of x far above the rest, at weights that are zero, costs the rest no digits."""
     for dtype in DTYPES.values():
