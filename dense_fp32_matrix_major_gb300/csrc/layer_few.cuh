@@ -1059,7 +1059,8 @@ bool rows_aligned(const void *w, int64_t ld, int64_t stride) {
     return Matrix<H>::FP8 || (reinterpret_cast<uintptr_t>(w) % 16 == 0 && ld % per == 0 && stride % per == 0);
 }
 
-// Blocks of the second kernel: four columns of y a block at least.
+// Blocks of the second kernel: one an SM, or about four columns of y each where
+// that makes fewer.
 inline int out_grid(const LArgs &a, const DeviceInfo &dev) {
     const int most = (a.width + 3) / 4;
     return most < dev.sm_count ? most : dev.sm_count;
