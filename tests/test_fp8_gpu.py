@@ -178,6 +178,45 @@ def test_quantize_groups_of_bad_offsets(fp8):
         assert bool(torch.isfinite(q.scales).all())
 
 
+def limited(off, rows):
+    """The groups that offsets stand for, and the first row behind them: bounds limited to 0 .. rows, the first taken as
+    0, a group that would end before it starts empty."""
+    o = [0] + [min(max(i, 0), rows) for i in off[1:]]
+    return [(b, max(b, e)) for b, e in zip(o, o[1:])], o[-1]
+
+
+BAD_OFFSETS = [[0, 1000, 2000], [0, -5, 300], [0, 200, 100], [7, 8, 9], [0, 2 ** 31 - 1, -2 ** 31], [0, 150, 20, 290],
+               [5, 100, 100, 2 ** 31 - 1]]
+
+
+@pytest.mark.parametrize("off", BAD_OFFSETS, ids=str)
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_quantize_groups_of_limited_offsets(fp8, off, name):
+    """Offsets past the rows, below zero or decreasing give the groups that they are limited to; large values around x
+    reach neither values nor scales, and nothing around q and the scales is written."""
+    rows, cols, experts = 300, 136, len(off) - 1
+    x = rows_of(rows, cols, DTYPES[name])
+    room = torch.full((rows + 400, cols + 8), 3e4, dtype=x.dtype, device="cuda")
+    room[200:500, :cols] = x.cuda()
+    stored = (rows + 127 * min(rows, experts)) // 128 * 128
+    values = torch.full((stored + 256, 144), 0x5A, dtype=torch.uint8, device="cuda")
+    scales = torch.full((stored // 128 + 2, cols), 77.0, device="cuda")
+    out = fp8.Quantized(values.view(E4M3)[128:128 + stored, :cols], scales[1:-1])
+    offsets = torch.tensor([2 ** 30, *off, 2 ** 30], dtype=torch.int32, device="cuda")[1:-1]
+    fp8.quantize(room[200:500, :cols], "columns", offsets=offsets, out=out)
+    at = 0
+    for b, e in limited(off, rows)[0]:
+        if b < e:
+            v, s = quantize64(x[b:e], "columns", E4M3)
+            same(out.values[at:at + e - b], v)
+            same(out.scales[at // 128:at // 128 + len(s)], s.astype(np.float64))
+            assert not out.values[at + e - b:at + 128 * len(s)].view(torch.uint8).any()
+            at += 128 * len(s)
+    assert not out.values[at:].view(torch.uint8).any() and bool((out.scales[at // 128:] == 2.0 ** -126).all())
+    out.values.view(torch.uint8).fill_(0x5A)
+    assert bool((values == 0x5A).all()) and bool((scales[0] == 77).all() and (scales[-1] == 77).all())
+
+
 def test_quantize_nothing(fp8):
     for shape in ((0, 64), (64, 0), (0, 0)):
         for block in ("rows", "columns", "blocks"):
@@ -431,6 +470,37 @@ def test_offsets_are_limited(fp8):
         assert bool(torch.isfinite(fp8.gemm(a, b, t, transB=True)).all())
         x = fp8.quantize(torch.randn((200, 64), device="cuda"), "columns", offsets=t)
         assert bool(torch.isfinite(fp8.gemm_wgrad(x, x, t)).all())
+
+
+@pytest.mark.parametrize("off", BAD_OFFSETS, ids=str)
+def test_products_of_limited_offsets(fp8, off):
+    """Products of the groups that offsets are limited to, into outputs that hold NaN. Rows that decreasing bounds give
+    to two groups may hold either's."""
+    rows, N, K, E = 300, 200, 140, len(off) - 1
+    t = torch.tensor(off, dtype=torch.int32, device="cuda")
+    groups, behind = limited(off, rows)
+    for trans in (False, True):
+        a, b = operands(fp8, rows, N, K, trans, experts=E)
+        room = torch.full((rows + 64, N), float("nan"), device="cuda")
+        c = fp8.gemm(a, b, t, room[32:-32], transB=trans)
+        A, B = meaning(a, "rows"), op(meaning(b, "blocks"), trans)
+        of = [[e for e, (x, y) in enumerate(groups) if x <= r < y] + ([E] if r >= behind else []) for r in range(rows)]
+        for r in range(rows):
+            if len(of[r]) == 1:
+                check_product(c[r:r + 1], A[r:r + 1], B[of[r][0]] if of[r][0] < E else torch.zeros_like(B[0]), K, f"{r}")
+        assert all(of) and bool(torch.isfinite(c).all())
+        assert bool(room[:32].isnan().all() and room[-32:].isnan().all())
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, y = (fp8.quantize(torch.randn((rows, n), generator=g, device="cuda"), "columns", offsets=t) for n in (130, 70))
+    room = torch.full((E + 2, 130, 70), float("nan"), device="cuda")
+    c = fp8.gemm_wgrad(x, y, t, room[1:-1])
+    X, Y, at = meaning(x, "columns"), meaning(y, "columns"), 0
+    for e, (b, end) in enumerate(groups):
+        blocks = -(-(end - b) // 128)
+        r = slice(128 * at, 128 * (at + blocks))
+        check_product(c[e], X[r].t(), Y[r], end - b, f"matrix {e}")
+        at += blocks
+    assert bool(room[0].isnan().all() and room[-1].isnan().all())
 
 
 def test_gradients_against_differences(fp8):
