@@ -149,6 +149,53 @@ def test_quantize_every_border(fp8):
         assert bool((q.scales == 1).all())
 
 
+def reference8(x, block, to):
+    """Values (as bytes) and scales of finite x, whole blocks at a time: PyTorch's fp32 arithmetic and cast."""
+    high, wide = {"rows": (1, 128), "columns": (128, 1), "blocks": (128, 128)}[block]
+    R, C = x.shape[-2:]
+    t = torch.nn.functional.pad(x.float(), (0, -C % wide, 0, -R % high))
+    t = t.reshape(*x.shape[:-2], t.shape[-2] // high, high, t.shape[-1] // wide, wide)
+    most = t.abs().amax((-3, -1), keepdim=True)
+    s = (most / torch.full_like(most, LARGEST[to])).clamp(min=2.0 ** -126)  # (a number's reciprocal would be rounded first)
+    q = (t * (1 / s)).to(to).view(torch.uint8)
+    s = s[..., 0, :, 0]
+    return (q.reshape(*x.shape[:-2], q.shape[-4] * high, -1)[..., :R, :C],
+            (s.transpose(-1, -2) if block == "rows" else s).contiguous())
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("block,shape", [("columns", (6001, 2600)), ("blocks", (6001, 2600)), ("blocks", (11, 900, 1300)),
+                                         ("rows", (6001, 2600))], ids=str)
+def test_quantize_many_tiles(fp8, name, block, shape):
+    """More tiles than blocks of threads are resident, so that each takes several."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = (torch.randn(shape, generator=g, device="cuda") * torch.exp(torch.randn(shape[-1:], generator=g, device="cuda")))
+    x = x.to(DTYPES[name])
+    for to in (E4M3, E5M2):
+        q = fp8.quantize(x, block, dtype=to)
+        values, scales = reference8(x, block, to)
+        assert torch.equal(q.values.view(torch.uint8), values) and torch.equal(q.scales, scales)
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_quantize_many_tiles_in_groups(fp8, name):
+    g = torch.Generator(device="cuda").manual_seed(6)
+    counts = [300, 0, 1, 128, 129, 700, 0, 513] * 5
+    rows, cols = sum(counts) + 77, 2600
+    x = torch.randn((rows, cols), generator=g, device="cuda").to(DTYPES[name])
+    q = fp8.quantize(x, "columns", offsets=offsets_of(counts).cuda())
+    at = first = 0
+    for n in counts:
+        if n:
+            values, scales = reference8(x[first:first + n], "columns", E4M3)
+            whole = len(scales) * 128
+            assert torch.equal(q.values[at:at + n].view(torch.uint8), values)
+            assert not q.values[at + n:at + whole].view(torch.uint8).any()
+            assert torch.equal(q.scales[at // 128:at // 128 + len(scales)], scales)
+            at, first = at + whole, first + n
+    assert not q.values[at:].view(torch.uint8).any() and bool((q.scales[at // 128:] == 2.0 ** -126).all())
+
+
 @pytest.mark.parametrize("counts,tail", [([5, 0, 128, 129, 0], 0), ([300], 7), ([0, 0, 0], 3), ([1] * 40, 0),
                                          ([128, 128], 0), ([0] * 100 + [1, 200], 50)])
 def test_quantize_groups(fp8, counts, tail):
