@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.experts_harness import DTYPES, canaries_intact, offsets_of, strided
+from tests.experts_harness import DTYPES, ROUNDING, TINY, canaries_intact, offsets_of, strided
 from tests.fp8_harness import E4M3, E5M2, LARGEST, check_product, meaning, quantize64
 
 pytestmark = pytest.mark.gpu
@@ -433,6 +433,53 @@ def test_scales_far_from_one(fp8, a, b):
         for rows, M, N in ((300, 130, 270), (5003, 130, 270)):  # the second in slices
             x, y = far((rows, M), "columns", ta, a), far((rows, N), "columns", tb, b)
             check_product(fp8.gemm_wgrad(x, y), meaning(x, "columns").t(), meaning(y, "columns"), rows, f"wgrad {rows}")
+
+
+def near(got, a, b, terms, what):
+    """check_product on the GPU, for large results."""
+    exact, size = a @ b, a.abs() @ b.abs()
+    limit = 2 * (terms + 1) * 2.0 ** -23 * size + ROUNDING[got.dtype] * exact.abs() + TINY[got.dtype]
+    bad = ~((got.double() - exact).abs() <= limit)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} out of bound"
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+@pytest.mark.parametrize("trans", [False, True])
+def test_gemm_many_tiles(fp8, name, trans):
+    """More tiles than SM pairs, so that a pair takes several: dense, and in groups with ends of any size."""
+    a, b = operands(fp8, 4100, 4200, 260, trans)
+    out = torch.full((4100, 4200), float("nan"), dtype=DTYPES[name], device="cuda")
+    near(fp8.gemm(a, b, out=out, transB=trans), meaning(a, "rows"), op(meaning(b, "blocks"), trans), 260, "dense")
+    counts = [270, 0, 5, 256, 300, 700, 31, 128] * 5
+    rows = sum(counts) + 300
+    a, b = operands(fp8, rows, 600, 390, trans, experts=len(counts))
+    out = torch.full((rows, 600), float("nan"), dtype=DTYPES[name], device="cuda")
+    fp8.gemm(a, b, offsets_of(counts).cuda(), out, transB=trans)
+    A, B, at = meaning(a, "rows"), op(meaning(b, "blocks"), trans), 0
+    for e, n in enumerate(counts):
+        near(out[at:at + n], A[at:at + n], B[e], 390, f"group {e}")
+        at += n
+    assert not out[at:].any()
+
+
+@pytest.mark.parametrize("name", list(DTYPES))
+def test_wgrad_many_tiles(fp8, name):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, y = (torch.randn((1100, n), generator=g, device="cuda") for n in (2600, 2500))
+    a, b = fp8.quantize(x, "columns"), fp8.quantize(y, "columns", dtype=E5M2)
+    out = torch.full((2600, 2500), float("nan"), dtype=DTYPES[name], device="cuda")
+    near(fp8.gemm_wgrad(a, b, out=out), meaning(a, "columns").t(), meaning(b, "columns"), 1100, "dense")
+    counts = [270, 0, 5, 256, 300, 1700, 31, 128] * 5
+    off = offsets_of(counts).cuda()
+    x, y = (torch.randn((sum(counts) + 50, n), generator=g, device="cuda") for n in (300, 500))
+    a, b = fp8.quantize(x, "columns", offsets=off), fp8.quantize(y, "columns", dtype=E5M2, offsets=off)
+    out = torch.full((len(counts), 300, 500), float("nan"), dtype=DTYPES[name], device="cuda")
+    fp8.gemm_wgrad(a, b, off, out)
+    A, B, at = meaning(a, "columns"), meaning(b, "columns"), 0
+    for e, n in enumerate(counts):
+        end = at + -(-n // 128) * 128
+        near(out[e], A[at:end].t(), B[at:end], n, f"matrix {e}")
+        at = end
 
 
 def test_a_row_depends_on_itself(fp8):
