@@ -149,6 +149,30 @@ def test_quantize_every_border(fp8):
         assert bool((q.scales == 1).all())
 
 
+def test_quantize_against_the_quotient(fp8):
+    """x times the rounded reciprocal of the scale, two roundings of 2^-24, against x / scale rounded once to 8 bits: the
+    same but where the quotient lies within 2^-23 (and the roundings' product) of a border between two 8-bit values."""
+    g = torch.Generator().manual_seed(21)
+    for to in (E4M3, E5M2):
+        v = torch.arange(127 if to == E4M3 else 124, dtype=torch.uint8).view(to).double()
+        x = torch.randn((400, 128), generator=g, dtype=torch.float64)
+        scale = torch.exp(3 * torch.randn((400, 1), generator=g, dtype=torch.float64))
+        at = torch.randint(1, len(v) - 1, (400, 127), generator=g)
+        close = (v[at] + v[at + 1]) / 2 * (1 + torch.randint(-4, 5, at.shape, generator=g) * 2.0 ** -24)
+        x[:, 1:] = torch.where(torch.rand(at.shape, generator=g) < 0.7, close * x[:, 1:].sign(), x[:, 1:])
+        x[:, 0] = LARGEST[to]
+        x = (x * scale).float()
+        q = fp8.quantize(x.cuda(), "rows", dtype=to)
+        t = x.double() / q.scales.cpu().double().t()
+        codes = v.numpy()
+        want = codes[np.abs(np.abs(t.numpy())[..., None] - codes).argmin(-1)] * np.sign(t.numpy())
+        got = q.values.double().cpu().numpy()
+        differ = got != want
+        border = (got[differ] + want[differ]) / 2
+        assert (np.abs(t.numpy()[differ] - border) <= 2.0 ** -23 * (1 + 2.0 ** -20) * np.abs(border)).all()
+        assert 0 < differ.mean() < 0.3
+
+
 def reference8(x, block, to):
     """Values (as bytes) and scales of finite x, whole blocks at a time: PyTorch's fp32 arithmetic and cast."""
     high, wide = {"rows": (1, 128), "columns": (128, 1), "blocks": (128, 128)}[block]
