@@ -114,6 +114,56 @@ def test_two_streams_at_once(mods):
             equal(o, w, "stream")
 
 
+def test_gradients_in_slices_captured_and_on_two_streams(mods):
+    """Few matrices over many rows, whose sums of slices lie in pool memory: in two graphs that are replayed at once, and
+    eagerly on two streams."""
+    fp8 = mods[1]
+    off = [None, torch.tensor([0, 3000, 3000, 8100], dtype=torch.int32, device="cuda")]
+
+    def operands(seed, offsets):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        return [fp8.quantize(torch.randn((8200, n), generator=g, device="cuda"), "columns", offsets=offsets)
+                for n in (130, 270)]
+
+    from dense_fp32_matrix_major_gb300 import sgemm
+
+    fixed, graphs, outs = [operands(i, o) for i, o in enumerate(off)], [], []
+    for (a, b), o in zip(fixed, off):
+        fp8.gemm_wgrad(a, b, o)
+        assert sgemm.last_launch_count() == 2  # slices, and their join
+    torch.cuda.synchronize()
+    for (a, b), o in zip(fixed, off):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(fp8.gemm_wgrad(a, b, o))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for n in range(4):
+        for i, (pair, o) in enumerate(zip(fixed, off)):
+            for mine, new in zip(pair, operands(10 + 2 * n + i, o)):
+                mine.values.view(torch.uint8).copy_(new.values.view(torch.uint8))
+                mine.scales.copy_(new.scales)
+        want = [fp8.gemm_wgrad(a, b, o) for (a, b), o in zip(fixed, off)]
+        torch.cuda.synchronize()
+        for out in outs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        equal(outs, want, n)
+        got = [[], []]
+        for _ in range(6):
+            for i, stream in enumerate(streams):
+                with torch.cuda.stream(stream):
+                    got[i].append(fp8.gemm_wgrad(*fixed[i], off[i]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            equal(got[i], [want[i]] * 6, (n, "eager"))
+
+
 def test_stream_argument(mods):
     experts, fp8, layer = mods
     s = make(4, 64, 264, 136)
