@@ -581,6 +581,51 @@ def test_products_of_nothing(fp8):
     assert not out.any()
 
 
+def test_products_of_nothing_into_rows_far_apart(fp8):
+    """A sum of nothing is zero in rows more than 2^31 bytes apart, too."""
+    q = lambda r, c, block: fp8.quantize(torch.zeros((r, c), device="cuda"), block)  # noqa: E731
+    pitch = 2 ** 29 + 16
+    store = torch.full((2 * pitch,), 5.0, device="cuda")
+    out = store.as_strided((2, 32), (pitch, 1))
+    fp8.gemm(q(2, 0, "rows"), q(32, 0, "blocks"), out=out, transB=True)
+    assert not out.any() and bool((store[32:64] == 5).all()) and bool((store[pitch + 32:] == 5).all())
+    out.fill_(5.0)
+    fp8.gemm_wgrad(q(0, 2, "columns"), q(0, 32, "columns"), out=out)
+    assert not out.any()
+
+
+def test_elements_past_32_bits(fp8):
+    """Operands and results of more than 2^31 elements: their last rows and columns."""
+    rows, wide, last = 270000, 8192, 300
+    x = torch.empty((rows, wide), dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+    by_row, by_column = fp8.quantize(x, "rows"), fp8.quantize(x, "columns")
+    assert torch.equal(fp8.quantize(x, "blocks").scales[-3:], fp8.quantize(x[rows // 128 * 128 - 256:], "blocks").scales)
+    end = fp8.quantize(x[-last:], "rows")
+    assert torch.equal(by_row.values[-last:].view(torch.uint8), end.values.view(torch.uint8))
+    assert torch.equal(by_row.scales[:, -last:], end.scales)
+    whole = rows // 128 * 128 - 256
+    values, scales = reference8(x[whole:], "columns", E4M3)
+    assert torch.equal(by_column.values[whole:].view(torch.uint8), values)
+    assert torch.equal(by_column.scales[whole // 128:], scales)
+    w = fp8.quantize(torch.randn((128, wide), device="cuda"), "blocks")
+    assert torch.equal(fp8.gemm(by_row, w, transB=True)[-last:], fp8.gemm(end, w, transB=True))
+    # A result of as many, from a short sum.
+    short = fp8.Quantized(by_row.values[:, :128], by_row.scales[:1].contiguous())
+    of_end = fp8.Quantized(end.values[:, :128], end.scales[:1].contiguous())
+    w = fp8.quantize(torch.randn((wide, 128), device="cuda"), "blocks")
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(fp8.gemm(short, w, transB=True, dtype=dtype)[-last:], fp8.gemm(of_end, w, transB=True, dtype=dtype))
+    # The gradient's sum over all rows, of which only the last ones are not zero.
+    y = torch.zeros((rows, 64), device="cuda")
+    y[-last:] = torch.randn((last, 64), device="cuda")
+    dy = fp8.quantize(y, "columns")
+    near(fp8.gemm_wgrad(by_column, dy), meaning(fp8.Quantized(by_column.values[whole:], by_column.scales[whole // 128:]),
+                                                "columns").t(),
+         meaning(fp8.Quantized(dy.values[whole:], dy.scales[whole // 128:]), "columns"), rows - whole, "gradient")
+
+
 def test_offsets_are_limited(fp8):
     a, b = operands(fp8, 200, 64, 128, True, experts=2)
     for off in ([0, 1000, 2000], [0, 150, 100], [0, -3, 200]):
