@@ -134,7 +134,10 @@ int sgemm_experts_gemm(int type, int transB, int64_t rows, int64_t N, int64_t K,
  *   B, ldb     rows x N.
  *   C, ldc     out, experts matrices of M x N, strideC elements apart.
  * The gradient of sgemm_experts_gemm's B: with A its A and B its C's
- * gradient for SGEMM_OP_N, the two exchanged for SGEMM_OP_T.
+ * gradient for SGEMM_OP_N, the two exchanged for SGEMM_OP_T. Few matrices over
+ * many rows are summed in slices of the rows, which are then added in order; when
+ * the scratch pool has no memory for their sums the rows are summed in one piece,
+ * which rounds otherwise.
  */
 int sgemm_experts_gemm_wgrad(int type, int64_t rows, int64_t M, int64_t N, int64_t experts, const int32_t *offsets,
                              const void *A, int64_t lda, const void *B, int64_t ldb, void *C, int64_t ldc,

@@ -115,7 +115,11 @@ int sgemm_fp8_gemm(int out_type, int transB, int type_a, int type_b, int64_t row
  *              a multiple of 128.
  *   B, ldb     rows x N of type_b, sB, likewise.
  *   C, ldc     out, experts matrices of M x N, strideC elements apart.
- * Alignment, limits and sums as for sgemm_fp8_gemm.
+ * Alignment, limits and sums as for sgemm_fp8_gemm, except that few matrices over
+ * many rows are summed in slices of the rows, whose fp32 sums are then added in
+ * order. The sizes (and the device's number of SMs) say into how many. Only when
+ * the pool has no memory for them are the rows summed in one piece, which rounds
+ * otherwise.
  */
 int sgemm_fp8_gemm_wgrad(int out_type, int type_a, int type_b, int64_t rows, int64_t M, int64_t N, int64_t experts,
                          const int32_t *offsets, const void *A, int64_t lda, const float *sA, const void *B,
