@@ -15,7 +15,7 @@
 // staged by each CTA). Four buffers of 128 columns fill tensor memory, two for
 // each half of the tile: four warps empty a half's sums while the tensor core
 // makes the other's. (Two buffers of 256 columns, emptied by all eight warps at
-// once: 276 us in place of 259 for 16384 x 4096 x 4096, whose rate is 2130
+// once: 276 us in place of 260 for 16384 x 4096 x 4096, whose rate is 2110
 // TFLOP/s.)
 //
 // What bounds it. The sums that leave tensor memory: a CTA's 128 x 256 of them a
@@ -44,7 +44,7 @@
 // tile's end belong to the next and change only sums that are not written; a CTA
 // whose rows all lie past it stages none. In wgrad every group's rows start in a
 // block of their own and end in zeros. 16384 rows in 32 even groups, 2048 -> 4096:
-// 152 us; ragged 178: a group's last tile costs as much as a full one.
+// 152 us; ragged 184: a group's last tile costs as much as a full one.
 //
 // C leaves through shared memory and TMA stores, 32 rows of 128 bytes at a time,
 // while the next tile is summed; where TMA cannot address it or a warp has fewer
