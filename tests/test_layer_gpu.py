@@ -246,9 +246,10 @@ def test_hidden_values_past_bf16(layer):
 @pytest.mark.parametrize("name", list(DTYPES))
 def test_8_bit_sums_that_overflow_before_their_scale(layer, fp8, name, to):
     """x or h so large that a block's values times it leave fp32, where scaled ones do not; a pair of an expert or more
-    than an entry has, sums that one warp has and that several share, and a NaN in another token."""
+    than an entry has, sums that one warp has and that several share, more columns of y than a block makes at once, and
+    a NaN in another token."""
     dtype = DTYPES[name]
-    for tokens, width, hidden in ((2, 300, 260), (20, 140, 130), (3, 2000, 2100)):
+    for tokens, width, hidden in ((2, 300, 260), (20, 140, 130), (3, 2000, 2100), (2, 6000, 130)):
         for gated in (False, True):
             c = case(tokens, 2, 3, width, hidden, torch.float32, False)
             gate = [torch.full_like(c["w1"], width ** -0.5)] if gated else []  # the second half: near one
