@@ -35,8 +35,9 @@
 // 24 bits (y is rounded to 11 at most; a third term took 141 us in place of 128 for 8
 // tokens, 2 of 16 experts of 4096 x 4096 in 8 bits, 193 in place of 180 in bf16 and
 // 203 in place of 183 in fp16 for 32 tokens, 8 of 128 of 2048 x 768, and left the
-// error of y against 64 bits as it was, 1.66693e-3 of the norm in the first), which the first kernel stores apart: as they are with
-// bf16 matrices and with 8-bit ones made bf16, as tf32 with fp16 ones. (8-bit ones as tf32 with bf16
+// error of y against 64 bits as it was, 1.66693e-3 of the norm in the first), which
+// the first kernel stores apart: as they are with bf16 matrices and with 8-bit ones
+// made bf16, as tf32 with fp16 ones. (8-bit ones as tf32 with bf16
 // x and with h, fewer steps for a value but twice the instructions that multiply:
 // 140 us in place of 127 for 8 tokens, 2 of 16 experts of 4096 x 4096.) With fp32 x
 // fp32 multiply-adds, because the instruction cuts its running sums (1.3e-6 of the
@@ -729,8 +730,9 @@ __device__ __forceinline__ void sum_tiles(const Job &job, int items, int K, int 
 // the block's tiles are done; those of a pair with a NaN are not, which explains
 // them. (8 tokens, 2 of 16 experts of 4096 x 4096: 130 us, without this code 128,
 // which deals the registers out otherwise; made again as soon as a tile is done
-// 132; with the scale's power of two in the values from the start 138.) Called by
-// the whole block.
+// 132; with the scale's power of two in the values from the start 138. Made again
+// for all of one token's sums: 0.8 ms for an infinity in its x, 1.1 for values near
+// 2^125, and 0.16 with a NaN.) Called by the whole block.
 template <int H, class Job>
 __device__ __forceinline__ void sums_again(const Job &job, int items) {
     const int lane = threadIdx.x & 31, K = job.length();
@@ -974,7 +976,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_hidden_kernel(const __grid_c
     const int per_tile = a.gated ? 8 : 16;  // features
     const int rows1 = a.gated ? 2 * a.hidden : a.hidden;
     HiddenJob<H, MATH == BF8> job{a, l, 0, per_tile, (a.hidden + per_tile - 1) / per_tile,
-                     (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
+                                  (a.width + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE, 0};
     job.item_scales = static_cast<int64_t>((rows1 + SGEMM_FP8_BLOCK_SIZE - 1) / SGEMM_FP8_BLOCK_SIZE) * job.kblocks;
     const int64_t tiles = static_cast<int64_t>(l.entries) * job.per_entry;
     job.first = static_cast<int>(tiles * blockIdx.x / gridDim.x);
